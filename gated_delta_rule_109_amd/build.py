@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libkda.so")
 BUILD_DIR = os.path.join(HERE, "_build")
-SOURCES = ["kda_api.hip", "kda_decode.hip", "kda_prefill.hip"]
+SOURCES = ["kda_api.hip", "kda_decode.hip", "kda_prefill.hip", "kda_tree.hip", "kda_verify.hip", "kda_cache.hip"]
 PEAK_SOURCE = os.path.join(CSRC, "measure", "peak_mfma.hip")
 PEAK_LIB = os.path.join(HERE, "libkda_peak.so")
 ARCH = "gfx950"

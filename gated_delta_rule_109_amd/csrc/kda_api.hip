@@ -312,4 +312,142 @@ kda_status kda_decode_tokens(const void* q, const void* k, const void* v, kda_dt
   return from_hip(kda::launch_decode(a));
 }
 
+// Tree step: the checks kda_decode_tree and kda_commit_path share, in the order
+// of kda_decode_tokens.
+namespace {
+kda_status tree_args_ok(int dt, const kda_options* opt, int32_t N, int32_t T, int32_t H, int32_t Dk,
+                        int32_t Dv, float g_min) {
+  if (dt != KDA_BF16 && dt != KDA_F32) return KDA_ERR_UNSUPPORTED;
+  if (!options_ok(opt)) return KDA_ERR_INVALID_ARG;
+  if (!supported_dims(Dk, Dv)) return KDA_ERR_UNSUPPORTED;
+  if (T < 1 || T > KDA_TREE_MAX_NODES) return KDA_ERR_INVALID_ARG;
+  if (!decode_floor_ok(g_min)) return KDA_ERR_INVALID_ARG;
+  if (N < 0 || H <= 0 || (int64_t)N * T > INT32_MAX || (int64_t)N * T * H > INT32_MAX)
+    return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+}  // namespace
+
+kda_status kda_decode_tree(const void* q, const void* k, const void* v, kda_dtype dtype,
+                           const float* g, const float* beta, const float* state,
+                           const int32_t* parents, const int32_t* num_nodes, void* o, int32_t N,
+                           int32_t T, int32_t H, int32_t Dk, int32_t Dv, float scale, float g_min,
+                           const kda_options* opt, hipStream_t stream) {
+  const int dt = enum_code(dtype);
+  const kda_status st = tree_args_ok(dt, opt, N, T, H, Dk, Dv, g_min);
+  if (st != KDA_OK || N == 0) return st;
+  const bool need_g = gate_of(opt) != KDA_GATE_NONE;
+  if (!q || !k || !v || (need_g && !g) || !beta || !state || !o) return KDA_ERR_INVALID_ARG;
+  if (!aligned16({q, k, v, g, beta, state, o, parents, num_nodes})) return KDA_ERR_INVALID_ARG;
+  kda::TreeArgs a;
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.state = const_cast<float*>(state); a.o = o;
+  a.parents = parents; a.num_nodes = num_nodes;
+  a.path = nullptr; a.accept = nullptr;
+  a.N = N; a.T = T; a.H = H; a.D = Dk;
+  a.scale = scale; a.g_min = g_min;
+  a.fe_flags = opt ? opt->flags : 0u; a.fe_eps = opt ? opt->norm_eps : 0.f;
+  a.gate = gate_of(opt);
+  a.bf16 = dt == KDA_BF16;
+  a.stream = stream;
+  return from_hip(kda::launch_tree(a));
+}
+
+kda_status kda_commit_path(const void* k, const void* v, kda_dtype dtype, const float* g,
+                           const float* beta, float* state, const int32_t* path,
+                           const int32_t* accept, int32_t N, int32_t T, int32_t H, int32_t Dk,
+                           int32_t Dv, float g_min, const kda_options* opt, hipStream_t stream) {
+  const int dt = enum_code(dtype);
+  const kda_status st = tree_args_ok(dt, opt, N, T, H, Dk, Dv, g_min);
+  if (st != KDA_OK || N == 0) return st;
+  const bool need_g = gate_of(opt) != KDA_GATE_NONE;
+  if (!k || !v || (need_g && !g) || !beta || !state || !path || !accept) return KDA_ERR_INVALID_ARG;
+  if (!aligned16({k, v, g, beta, state, path, accept})) return KDA_ERR_INVALID_ARG;
+  kda::TreeArgs a;
+  a.q = nullptr; a.k = k; a.v = v; a.g = g; a.beta = beta; a.state = state; a.o = nullptr;
+  a.parents = nullptr; a.num_nodes = nullptr;
+  a.path = path; a.accept = accept;
+  a.N = N; a.T = T; a.H = H; a.D = Dk;
+  a.scale = 1.f; a.g_min = g_min;
+  a.fe_flags = opt ? opt->flags : 0u; a.fe_eps = opt ? opt->norm_eps : 0.f;
+  a.gate = gate_of(opt);
+  a.bf16 = dt == KDA_BF16;
+  a.stream = stream;
+  return from_hip(kda::launch_commit(a));
+}
+
+size_t kda_verify_workspace_size(int32_t N, int32_t T, int32_t V) {
+  if (N < 0 || T < 1 || T > KDA_TREE_MAX_NODES || V < 1 ||
+      V > KDA_VERIFY_MAX_VOCAB || (int64_t)N * T > INT32_MAX) return 0;
+  return kda::verify_workspace(N, T, V);
+}
+
+kda_status kda_verify_drafts(const void* target, const void* draft, kda_dtype dtype,
+                             const int32_t* tokens, const int32_t* parents,
+                             const int32_t* num_nodes, const float* uniforms, int32_t* accept,
+                             int32_t* path, int32_t* next_token, int32_t N, int32_t T, int32_t V,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const int dt = enum_code(dtype);
+  if (dt != KDA_BF16 && dt != KDA_F32) return KDA_ERR_UNSUPPORTED;
+  if (N < 0 || T < 1 || T > KDA_TREE_MAX_NODES || V < 1 ||
+      V > KDA_VERIFY_MAX_VOCAB || (int64_t)N * T > INT32_MAX)
+    return KDA_ERR_INVALID_ARG;
+  if (N == 0) return KDA_OK;
+  if (!target || !tokens || !uniforms || !accept || !path || !next_token) return KDA_ERR_INVALID_ARG;
+  if (!aligned16({target, draft, tokens, parents, num_nodes, uniforms, accept, path, next_token}))
+    return KDA_ERR_INVALID_ARG;
+  if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < kda::verify_workspace(N, T, V))
+    return KDA_ERR_WORKSPACE;
+  kda::VerifyArgs a;
+  a.target = target; a.draft = draft;
+  a.tokens = tokens; a.parents = parents; a.num_nodes = num_nodes; a.uniforms = uniforms;
+  a.accept = accept; a.path = path; a.next_token = next_token;
+  a.N = N; a.T = T; a.V = V;
+  a.workspace = workspace;
+  a.bf16 = dt == KDA_BF16;
+  a.stream = stream;
+  return from_hip(kda::launch_verify(a));
+}
+
+namespace {
+// Checks and arguments of both directions of the state cache; KDA_OK with
+// a->N == 0 when there is nothing to do.
+kda_status cache_args(const void* states, const int32_t* slots, const void* values, const uint8_t* scales,
+                      int format, int32_t N, int32_t num_slots, int32_t H, int32_t Dk, int32_t Dv,
+                      hipStream_t stream, kda::CacheArgs* a) {
+  if (format != KDA_CACHE_INT8 && format != KDA_CACHE_E4M3) return KDA_ERR_UNSUPPORTED;
+  if (!supported_dims(Dk, Dv)) return KDA_ERR_UNSUPPORTED;
+  if (N < 0 || num_slots < 0 || H <= 0 || (int64_t)N * H > INT32_MAX) return KDA_ERR_INVALID_ARG;
+  if (!slots && N > num_slots) return KDA_ERR_INVALID_ARG;
+  if (N > 0 && (!states || (num_slots > 0 && (!values || !scales)))) return KDA_ERR_INVALID_ARG;
+  if (!aligned16({states, slots, values, scales})) return KDA_ERR_INVALID_ARG;
+  a->states = (float*)states; a->slots = slots;
+  a->values = (void*)values; a->scales = (uint8_t*)scales;
+  a->N = N; a->num_slots = num_slots; a->H = H; a->D = Dk;
+  a->e4m3 = format == KDA_CACHE_E4M3;
+  a->stream = stream;
+  return KDA_OK;
+}
+}  // namespace
+
+kda_status kda_state_store(const float* states, const int32_t* slots, void* values,
+                           uint8_t* scales, kda_cache_format format, int32_t N,
+                           int32_t num_slots, int32_t H, int32_t Dk, int32_t Dv,
+                           hipStream_t stream) {
+  kda::CacheArgs a;
+  const kda_status st =
+      cache_args(states, slots, values, scales, enum_code(format), N, num_slots, H, Dk, Dv, stream, &a);
+  if (st != KDA_OK || N == 0 || num_slots == 0) return st;
+  return from_hip(kda::launch_cache_store(a));
+}
+
+kda_status kda_state_load(const void* values, const uint8_t* scales, const int32_t* slots,
+                          float* states, kda_cache_format format, int32_t N, int32_t num_slots,
+                          int32_t H, int32_t Dk, int32_t Dv, hipStream_t stream) {
+  kda::CacheArgs a;
+  const kda_status st =
+      cache_args(states, slots, values, scales, enum_code(format), N, num_slots, H, Dk, Dv, stream, &a);
+  if (st != KDA_OK || N == 0) return st;
+  return from_hip(kda::launch_cache_load(a));
+}
+
 }  // extern "C"

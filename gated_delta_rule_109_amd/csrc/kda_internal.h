@@ -31,6 +31,46 @@ struct DecodeArgs {
   hipStream_t stream;
 };
 
+// A tree of T nodes per sequence over the state (out), or the commit of a path
+// (path, accept; q, o and parents unused).
+struct TreeArgs {
+  const void *q, *k, *v;
+  const float *g, *beta;
+  float* state;               // read only unless a commit
+  const int32_t *parents;     // device [N, T], or NULL (chains)
+  const int32_t *num_nodes;   // device [N], or NULL (T each)
+  const int32_t *path, *accept;
+  void* o;
+  int32_t N, T, H, D;
+  float scale, g_min;
+  uint32_t fe_flags = 0;
+  float fe_eps = 0.f;
+  int32_t gate = KDA_GATE_CHANNEL;
+  bool bf16;
+  hipStream_t stream;
+};
+
+struct VerifyArgs {
+  const void *target, *draft;
+  const int32_t *tokens, *parents, *num_nodes;
+  const float* uniforms;
+  int32_t *accept, *path, *next_token;
+  int32_t N, T, V;
+  void* workspace;
+  bool bf16;
+  hipStream_t stream;
+};
+
+struct CacheArgs {
+  float* states;              // read only when storing
+  const int32_t* slots;       // device [N], or NULL (slot n)
+  void* values;
+  uint8_t* scales;
+  int32_t N, num_slots, H, D;
+  bool e4m3;
+  hipStream_t stream;
+};
+
 struct PrefillArgs {
   const void *q, *k, *v;
   const float *g, *beta;
@@ -93,6 +133,14 @@ int32_t auto_segments(int32_t num_seqs, int32_t H, int32_t D, int64_t max_blocks
 
 hipError_t launch_decode(const DecodeArgs& a);
 hipError_t launch_prefill(const PrefillArgs& a);
+hipError_t launch_tree(const TreeArgs& a);
+hipError_t launch_commit(const TreeArgs& a);
+hipError_t launch_verify(const VerifyArgs& a);
+hipError_t launch_cache_store(const CacheArgs& a);
+hipError_t launch_cache_load(const CacheArgs& a);
+
+// Workspace of a verification (bytes; N, T, V validated).
+size_t verify_workspace(int32_t N, int32_t T, int32_t V);
 
 // Device address of the static scratch (KDA_NOALLOC_SCRATCH_BYTES) on the
 // current device, looked up on the first call per device and kept.

@@ -1,0 +1,468 @@
+// Verification of drafted tokens by rejection sampling on gfx950.
+//
+// At node `cur` with target row p and draft row q, after rejecting children
+// 1 .. m the residual is r = max(p - C q, 0), C the sum of the masses so far:
+// subtracting one more multiple of q from a row that is already clamped at 0
+// gives the same as subtracting the total at once, so one number per node
+// replaces a row of V. Every test needs p and q at one token only; a whole row
+// is summed only for the mass after a rejection that another child follows,
+// and for the draw of the next token.
+//
+// All sums are fp64: a token is chosen where a running sum of up to V values
+// passes a threshold, and in fp32 the sum's rounding would be as wide as many
+// tokens. Bound by the bytes of the rows p and q of the last node.
+//
+// Three steps: the walk down the tree (alone in its kernel only when masses
+// are summed), the partial sums of the last node's r over chunks of the
+// vocabulary, and the choice of the token inside one chunk.
+#include "kda_device.h"
+#include "kda_internal.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int kMaxChunks = 64;
+
+// Per-sequence workspace record.
+struct Walk {
+  double spent;      // C of the last node
+  int32_t node;      // the last node, -1: no nodes
+  int32_t pad;
+};
+
+struct VerifyPlan {
+  int chunks, chunk;        // chunks of the vocabulary, elements in each
+  size_t walks, sums, total;
+};
+
+// (V <= KDA_VERIFY_MAX_VOCAB, so element indices of a row stay far inside 32 bits.)
+// At most 64 chunks (one lane each when they are joined), of 4096 elements or
+// more; of 1024 or more where there are too few sequences to fill the GPU.
+VerifyPlan verify_plan(int32_t N, int32_t V) {
+  VerifyPlan p;
+  const int least = N >= 64 ? 4096 : 1024;
+  const int chunk = ((V + kMaxChunks - 1) / kMaxChunks + 7) / 8 * 8;
+  p.chunk = chunk < least ? least : chunk;
+  p.chunks = (V + p.chunk - 1) / p.chunk;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  p.walks = 0;
+  p.sums = up(sizeof(Walk) * (size_t)N);
+  p.total = p.sums + up(2 * sizeof(double) * (size_t)N * p.chunks);
+  return p;
+}
+
+// A stored probability; whatever is no finite positive number counts as 0.
+template <typename T>
+__device__ __forceinline__ double weight(T raw) {
+  const float x = Elem<T>::load(&raw);
+  return x > 0.f && x < __builtin_inff() ? (double)x : 0.0;
+}
+
+__device__ __forceinline__ double lane_xor64(double x, int m) { return __shfl_xor(x, m); }
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+  for (int m = 1; m < kWave; m *= 2) x += lane_xor64(x, m);
+  return x;
+}
+
+// The tree of one sequence as a wave holds it: lane t is node t.
+template <typename T>
+struct Nodes {
+  int parent, token;
+  double p, q, u;     // target and draft probability of the node's token at its parent
+};
+
+template <typename T>
+__device__ __forceinline__ Nodes<T> load_nodes(const T* target, const T* draft, const int32_t* tokens,
+                                               const int32_t* parents, const float* uniforms, size_t n, int T_, int nt,
+                                               int V, int lane) {
+  Nodes<T> d;
+  d.parent = -1; d.token = -1; d.p = 0.0; d.q = draft ? 0.0 : 1.0; d.u = 1.0;
+  if (lane >= 1 && lane < nt) {
+    const size_t at = n * T_ + lane;
+    d.token = tokens[at];
+    d.parent = parents ? parents[at] : lane - 1;
+    d.u = (double)uniforms[at];
+    if (d.parent < 0 || d.parent >= lane) d.parent = -1;
+    if (d.parent >= 0 && d.token >= 0 && d.token < V) {
+      const size_t e = (n * T_ + d.parent) * (size_t)V + d.token;
+      d.p = weight<T>(target[e]);
+      if (draft) d.q = weight<T>(draft[e]);
+    } else if (d.parent >= 0 && draft == nullptr) {
+      d.q = 1.0;
+    }
+  }
+  return d;
+}
+
+// One element's residual weight. Mode without draft: the rejected tokens are
+// taken out by the callers.
+__device__ __forceinline__ double residual(double p, double q, double spent) { return fmax(p - spent * q, 0.0); }
+
+// Walks one sequence's tree; every lane of the calling wave returns the same.
+// mass(cur, spent): sum of the residual row of node cur, for a node with
+// another child to test (only with draft rows).
+template <typename T, typename Mass>
+__device__ __forceinline__ void walk(const Nodes<T>& d, bool has_draft, int nt, int lane, int& cur, int& count,
+                                     double& spent, uint64_t& accepted, Mass&& mass) {
+  cur = 0; count = 1; spent = 0.0;
+  accepted = 1;
+  double c = 1.0;
+  uint64_t gone = 0;            // rejected children of cur
+  uint64_t kids = __ballot(d.parent == 0);
+  while (kids) {
+    const int t = __builtin_ctzll(kids);
+    kids &= kids - 1;
+    const double p = __shfl(d.p, t), q = __shfl(d.q, t), u = __shfl(d.u, t);
+    const int x = __shfl(d.token, t);
+    double r;
+    if (has_draft) r = residual(p, q, spent);
+    else r = __ballot(d.token == x) & gone ? 0.0 : p;
+    if (u * q * c < r) {
+      cur = t;
+      ++count;
+      accepted |= 1ull << t;
+      spent = 0.0; c = 1.0; gone = 0;
+      kids = __ballot(d.parent == t);
+    } else if (has_draft) {
+      spent += c;
+      if (kids) c = mass(cur, spent);
+    } else {
+      c -= r;
+      gone |= 1ull << t;
+    }
+  }
+}
+
+__device__ __forceinline__ int node_count(const int32_t* num_nodes, uint32_t n, int T) {
+  return num_nodes ? min(max(num_nodes[n], 0), T) : T;
+}
+
+// Results of the walk: accept, path, and the record for the later kernels.
+__device__ __forceinline__ void write_walk(int lane, size_t n, int T, int nt, int cur, int count, double spent,
+                                           uint64_t accepted, int32_t* accept, int32_t* path, int32_t* next_token,
+                                           Walk* walks) {
+  if (nt == 0) { cur = -1; count = 0; accepted = 0; }
+  if (lane < T) {
+    // lane's accepted node goes to the place of its rank; places past the path hold -1
+    if (accepted >> lane & 1) path[n * T + __builtin_popcountll(accepted & ((1ull << lane) - 1))] = lane;
+    if (lane >= count) path[n * T + lane] = -1;
+  }
+  if (lane == 0) {
+    accept[n] = count;
+    if (nt == 0) next_token[n] = -1;
+    walks[n].spent = spent;
+    walks[n].node = cur;
+  }
+}
+
+// Rows start at any element (V may be odd). They are read in groups of 16
+// bytes at aligned addresses: group i of a range [a, b) starts at element
+// a - skew(a) + i * kPer, and elements outside [a, b) are never read.
+template <typename T>
+constexpr int kPer = 16 / sizeof(T);
+template <typename T>
+__device__ __forceinline__ int skew(const T* at) { return (int)(((uintptr_t)at / sizeof(T)) % kPer<T>); }
+
+template <typename T>
+__device__ __forceinline__ void load_group(const T* row, int first, int a, int b, double (&w)[kPer<T>]) {
+  if (first >= a && first <= b - kPer<T>) {
+    T x[kPer<T>];
+    *(u32x4*)x = *(const u32x4*)(row + first);
+#pragma unroll
+    for (int j = 0; j < kPer<T>; ++j) w[j] = weight<T>(x[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPer<T>; ++j) w[j] = first + j >= a && first + j < b ? weight<T>(row[first + j]) : 0.0;
+  }
+}
+
+// f(element, p, q) for the elements of [a, b) that fall to this thread (and,
+// with weights 0, for some outside); q = NULL reads as 0.
+template <typename T, typename F>
+__device__ __forceinline__ void for_range(const T* p, const T* q, int a, int b, int tid, int threads, F&& f) {
+  const int begin = a - skew(p + a);
+  const int groups = (b - begin + kPer<T> - 1) / kPer<T>;
+  for (int i = tid; i < groups; i += threads) {
+    double x[kPer<T>], y[kPer<T>] = {};
+    const int first = begin + i * kPer<T>;
+    load_group<T>(p, first, a, b, x);
+    if (q) load_group<T>(q, first, a, b, y);
+#pragma unroll
+    for (int j = 0; j < kPer<T>; ++j) f(first + j, x[j], y[j]);
+  }
+}
+
+// The rejected tokens of the last node without draft rows: the tokens of its
+// children (had one been accepted, it would be the last node).
+struct Gone {
+  int count;
+  int token[kWave];
+};
+// Called by one wave; other waves read `gone` after a barrier.
+__device__ __forceinline__ void list_gone(Gone& gone, const int32_t* tokens, const int32_t* parents, size_t n, int T,
+                                          int nt, int cur, int lane) {
+  int x = -1;
+  if (lane > cur && lane < nt) {
+    const size_t at = n * T + lane;
+    if ((parents ? parents[at] : lane - 1) == cur) x = tokens[at];
+  }
+  const uint64_t mask = __ballot(x >= 0);
+  if (x >= 0) gone.token[__builtin_popcountll(mask & ((1ull << lane) - 1))] = x;
+  if (lane == 0) gone.count = __builtin_popcountll(mask);
+}
+__device__ __forceinline__ bool is_gone(const Gone& gone, int x) {
+  for (int i = 0; i < gone.count; ++i)
+    if (gone.token[i] == x) return true;
+  return false;
+}
+
+// The walk of a tree with draft rows: a workgroup per sequence, since masses
+// are sums over rows. Every wave walks; the sums are shared through LDS in a
+// fixed order, so all waves take the same turns.
+constexpr int kWalkThreads = 1024;
+template <typename T>
+__global__ __launch_bounds__(kWalkThreads) void walk_kernel(
+    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
+    const int32_t* __restrict__ parents, const int32_t* __restrict__ num_nodes,
+    const float* __restrict__ uniforms, int32_t* __restrict__ accept, int32_t* __restrict__ path,
+    int32_t* __restrict__ next_token, int T_, int V, Walk* __restrict__ walks) {
+  const uint32_t n = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int nt = node_count(num_nodes, n, T_);
+  __shared__ double s_sum[2][kWalkThreads / kWave];
+  const Nodes<T> d = load_nodes<T>(target, draft, tokens, parents, uniforms, n, T_, nt, V, lane);
+  int cur, count, turn = 0;
+  double spent;
+  uint64_t accepted;
+  walk<T>(d, true, nt, lane, cur, count, spent, accepted, [&](int at, double C) {
+    const size_t row = ((size_t)n * T_ + at) * (size_t)V;
+    double sum = 0.0;
+    for_range<T>(target + row, draft + row, 0, V, tid, kWalkThreads,
+                 [&](int, double p, double q) { sum += residual(p, q, C); });
+    sum = wave_sum(sum);
+    // two buffers in turn: a wave may start the next sum while another still
+    // reads this one, but not the one after it
+    if (lane == 0) s_sum[turn][wave] = sum;
+    __syncthreads();
+    double total = 0.0;
+#pragma unroll
+    for (int w = 0; w < kWalkThreads / kWave; ++w) total += s_sum[turn][w];
+    turn ^= 1;
+    return total;
+  });
+  if (wave == 0) write_walk(lane, n, T_, nt, cur, count, spent, accepted, accept, path, next_token, walks);
+}
+
+// Partial sums of the last node's r (and of p, for the case that r is 0
+// everywhere) over one chunk. kWalk: no masses are needed (chains, or no draft
+// rows), so every wave walks by itself and the sequence's first workgroup
+// writes the results.
+template <typename T, bool kDraft, bool kWalk>
+__global__ __launch_bounds__(256) void sums_kernel(
+    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
+    const int32_t* __restrict__ parents, const int32_t* __restrict__ num_nodes,
+    const float* __restrict__ uniforms, int32_t* __restrict__ accept, int32_t* __restrict__ path,
+    int32_t* __restrict__ next_token, int T_, int V, int chunk, int chunks, Walk* __restrict__ walks,
+    double* __restrict__ sums) {
+  const uint32_t n = blockIdx.x / (uint32_t)chunks;
+  const int part = blockIdx.x % (uint32_t)chunks, tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int nt = node_count(num_nodes, n, T_);
+  __shared__ double s_sum[2][4];
+  __shared__ Gone s_gone;
+  int cur;
+  double spent;
+  if constexpr (kWalk) {
+    const Nodes<T> d = load_nodes<T>(target, draft, tokens, parents, uniforms, n, T_, nt, V, lane);
+    int count;
+    uint64_t accepted;
+    walk<T>(d, kDraft, nt, lane, cur, count, spent, accepted, [](int, double) { return 0.0; });
+    if (part == 0 && wave == 0)
+      write_walk(lane, n, T_, nt, cur, count, spent, accepted, accept, path, next_token, walks);
+  } else {
+    cur = walks[n].node;
+    spent = walks[n].spent;
+  }
+  if (nt == 0) return;
+  if constexpr (!kDraft) {
+    if (wave == 0) list_gone(s_gone, tokens, parents, n, T_, nt, cur, lane);
+    __syncthreads();
+  }
+  const size_t row = ((size_t)n * T_ + cur) * (size_t)V;
+  const int a = part * chunk, b = min(V - a, chunk) + a;
+  double rs = 0.0, ps = 0.0;
+  // the row of q matters only after a rejection
+  const T* q = kDraft && spent > 0.0 ? draft + row : nullptr;
+  for_range<T>(target + row, q, a, b, tid, 256, [&](int x, double p, double qv) {
+    if constexpr (kDraft) rs += residual(p, qv, spent);
+    else rs += is_gone(s_gone, x) ? 0.0 : p;
+    ps += p;
+  });
+  rs = wave_sum(rs);
+  ps = wave_sum(ps);
+  if (lane == 0) { s_sum[0][wave] = rs; s_sum[1][wave] = ps; }
+  __syncthreads();
+  if (tid < 2)
+    sums[((size_t)n * chunks + part) * 2 + tid] = (s_sum[tid][0] + s_sum[tid][1]) + (s_sum[tid][2] + s_sum[tid][3]);
+}
+
+// Inclusive sums over the lanes of a wave.
+__device__ __forceinline__ double wave_scan(double x, int lane) {
+#pragma unroll
+  for (int m = 1; m < kWave; m *= 2) {
+    const double y = __shfl_up(x, m);
+    if (lane >= m) x += y;
+  }
+  return x;
+}
+
+// The next token: the chunk where the running sum of r passes u * sum(r), then
+// the token inside it. One workgroup per sequence; a tile of the chunk is kRun
+// consecutive elements per thread. Where rounding leaves the threshold past
+// the last sum, the last token with r > 0 is taken.
+template <typename T, bool kDraft>
+__global__ __launch_bounds__(256) void choose_kernel(
+    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
+    const int32_t* __restrict__ parents, const int32_t* __restrict__ num_nodes,
+    const float* __restrict__ uniforms, int32_t* __restrict__ next_token, int T_, int V, int chunk, int chunks,
+    const Walk* __restrict__ walks, const double* __restrict__ sums) {
+  constexpr int kRun = 16;
+  const uint32_t n = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int nt = node_count(num_nodes, n, T_);
+  if (nt == 0) return;
+  __shared__ double s_sum[4];
+  __shared__ int s_last[4];
+  __shared__ int s_token;
+  __shared__ Gone s_gone;
+  const int cur = walks[n].node;
+  double spent = walks[n].spent;
+  // every wave: the chunk sums, their total and the chunk of the threshold
+  double r = 0.0, p = 0.0;
+  if (lane < chunks) {
+    r = sums[((size_t)n * chunks + lane) * 2];
+    p = sums[((size_t)n * chunks + lane) * 2 + 1];
+  }
+  const bool plain = !(wave_sum(r) > 0.0);     // r is 0 everywhere: draw from p
+  if (plain) { r = p; spent = 0.0; }
+  const double upto = wave_scan(r, lane);
+  const uint64_t some = __ballot(r > 0.0);
+  if (!some) {
+    if (tid == 0) next_token[n] = -1;
+    return;
+  }
+  const double goal = fmax((double)uniforms[(size_t)n * T_], 0.0) * __shfl(upto, kWave - 1);
+  const uint64_t past = __ballot(upto > goal) & some;
+  const int part = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);
+  double left = goal - __shfl(upto - r, part);
+
+  if constexpr (!kDraft) {
+    if (wave == 0) {
+      list_gone(s_gone, tokens, parents, n, T_, nt, cur, lane);
+      if (plain && lane == 0) s_gone.count = 0;
+    }
+  }
+  if (tid == 0) s_token = -1;
+  __syncthreads();
+  const size_t row = ((size_t)n * T_ + cur) * (size_t)V;
+  const T* tp = target + row;
+  const T* tq = kDraft && spent > 0.0 ? draft + row : nullptr;
+  const int a = part * chunk, b = min(V - a, chunk) + a;
+  int last = -1;                                // last token with r > 0 so far
+  for (int tile = a - skew(tp + a); tile < b; tile += 256 * kRun) {
+    const int first = tile + tid * kRun;
+    double w[kRun], sum = 0.0;
+    int mine = -1;
+#pragma unroll
+    for (int gr = 0; gr < kRun / kPer<T>; ++gr) {
+      double x[kPer<T>] = {}, y[kPer<T>] = {};
+      const int at = first + gr * kPer<T>;
+      if (at < b) {
+        load_group<T>(tp, at, a, b, x);
+        if (tq) load_group<T>(tq, at, a, b, y);
+      }
+#pragma unroll
+      for (int j = 0; j < kPer<T>; ++j) {
+        double& z = w[gr * kPer<T> + j];
+        z = kDraft ? residual(x[j], y[j], spent) : x[j] > 0.0 && is_gone(s_gone, at + j) ? 0.0 : x[j];
+        if (z > 0.0) mine = at + j;
+        sum += z;
+      }
+    }
+    const double incl = wave_scan(sum, lane);
+    int top = mine;                             // last token with r > 0 in the wave
+#pragma unroll
+    for (int m = 1; m < kWave; m *= 2) top = max(top, __shfl_xor(top, m));
+    if (lane == kWave - 1) s_sum[wave] = incl;
+    if (lane == 0) s_last[wave] = top;
+    __syncthreads();
+    double before = 0.0;
+    for (int x = 0; x < wave; ++x) before += s_sum[x];
+    const double total = ((s_sum[0] + s_sum[1]) + s_sum[2]) + s_sum[3];
+    for (int x = 0; x < 4; ++x) last = max(last, s_last[x]);
+    // the first thread whose running sum passes the threshold finds the token
+    double run = before + (incl - sum);
+    const bool here = before + incl > left;
+    const uint64_t ok = __ballot(here && sum > 0.0);
+    if (ok && lane == __builtin_ctzll(ok)) {
+      int token = mine;
+#pragma unroll
+      for (int j = kRun - 1; j >= 0; --j) {
+        // from the end: the lowest element at which the sum has passed
+        double upto_j = run;
+#pragma unroll
+        for (int x = 0; x <= j; ++x) upto_j += w[x];
+        if (upto_j > left && w[j] > 0.0) token = first + j;
+      }
+      atomicMin((unsigned*)&s_token, (unsigned)token);   // waves in order of tokens
+    }
+    __syncthreads();
+    if (s_token != -1) break;
+    left -= total;
+    __syncthreads();
+  }
+  if (tid == 0) next_token[n] = s_token != -1 ? s_token : last;
+}
+
+template <typename T>
+hipError_t launch_verify_t(const VerifyArgs& a) {
+  const VerifyPlan p = verify_plan(a.N, a.V);
+  Walk* walks = (Walk*)((char*)a.workspace + p.walks);
+  double* sums = (double*)((char*)a.workspace + p.sums);
+  const T *target = (const T*)a.target, *draft = (const T*)a.draft;
+  const dim3 grid((unsigned)((int64_t)a.N * p.chunks));
+#define KDA_SUMS(DRAFT, WALK)                                                                                       \
+  hipLaunchKernelGGL((sums_kernel<T, DRAFT, WALK>), grid, dim3(256), 0, a.stream, target, draft, a.tokens, a.parents, \
+                     a.num_nodes, a.uniforms, a.accept, a.path, a.next_token, a.T, a.V, p.chunk, p.chunks, walks,   \
+                     sums)
+#define KDA_CHOOSE(DRAFT)                                                                                           \
+  hipLaunchKernelGGL((choose_kernel<T, DRAFT>), dim3((unsigned)a.N), dim3(256), 0, a.stream, target, draft,         \
+                     a.tokens, a.parents, a.num_nodes, a.uniforms, a.next_token, a.T, a.V, p.chunk, p.chunks,       \
+                     walks, sums)
+  if (draft && a.parents) {
+    hipLaunchKernelGGL((walk_kernel<T>), dim3((unsigned)a.N), dim3(kWalkThreads), 0, a.stream, target, draft,
+                       a.tokens, a.parents, a.num_nodes, a.uniforms, a.accept, a.path, a.next_token, a.T, a.V, walks);
+    KDA_SUMS(true, false);
+    KDA_CHOOSE(true);
+  } else if (draft) {
+    KDA_SUMS(true, true);
+    KDA_CHOOSE(true);
+  } else {
+    KDA_SUMS(false, true);
+    KDA_CHOOSE(false);
+  }
+#undef KDA_SUMS
+#undef KDA_CHOOSE
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t verify_workspace(int32_t N, int32_t T, int32_t V) { return verify_plan(N, V).total; }
+
+hipError_t launch_verify(const VerifyArgs& a) {
+  return a.bf16 ? launch_verify_t<bf16_bits>(a) : launch_verify_t<float>(a);
+}
+
+}  // namespace kda

@@ -25,8 +25,12 @@ LN_HALF = math.log(0.5)
 
 EXPORTED = ("kda_status_string", "kda_prefill_num_checkpoints", "kda_prefill_workspace_size",
             "kda_prefill_workspace_size_window", "kda_prefill_chunked", "kda_prefill_chunked_ex", "kda_prefill_chunked_noalloc",
-            "kda_decode_step", "kda_decode_tokens")
+            "kda_decode_step", "kda_decode_tokens", "kda_decode_tree", "kda_commit_path",
+            "kda_verify_workspace_size", "kda_verify_drafts", "kda_state_store", "kda_state_load")
 DECODE_MAX_TOKENS = 16
+TREE_MAX_NODES = 64
+CACHE_INT8, CACHE_E4M3 = 0, 1
+CACHE_BLOCK = 32                                 # values that share a scale
 FE_L2NORM_QK, FE_GATE_LOGITS, FE_BETA_LOGITS = 1, 2, 4
 FE_ALL = FE_L2NORM_QK | FE_GATE_LOGITS | FE_BETA_LOGITS
 GATE_CHANNEL, GATE_HEAD, GATE_NONE = 0, 1, 2     # KDA, Gated DeltaNet, DeltaNet
@@ -92,6 +96,21 @@ def lib():
         L.kda_prefill_chunked_noalloc.restype = ctypes.c_int
         L.kda_prefill_chunked_noalloc.argtypes = L.kda_prefill_chunked.argtypes[:-3] + [
             ctypes.POINTER(Options), _vp]
+        L.kda_decode_tree.restype = ctypes.c_int
+        L.kda_decode_tree.argtypes = [_vp, _vp, _vp, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
+                                      _i32, _i32, ctypes.c_float, ctypes.c_float, ctypes.POINTER(Options), _vp]
+        L.kda_commit_path.restype = ctypes.c_int
+        L.kda_commit_path.argtypes = [_vp, _vp, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                      ctypes.c_float, ctypes.POINTER(Options), _vp]
+        L.kda_verify_workspace_size.restype = ctypes.c_size_t
+        L.kda_verify_workspace_size.argtypes = [_i32, _i32, _i32]
+        L.kda_verify_drafts.restype = ctypes.c_int
+        L.kda_verify_drafts.argtypes = [_vp, _vp, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
+                                        _vp, ctypes.c_size_t, _vp]
+        L.kda_state_store.restype = ctypes.c_int
+        L.kda_state_store.argtypes = [_vp, _vp, _vp, _vp, ctypes.c_int, _i32, _i32, _i32, _i32, _i32, _vp]
+        L.kda_state_load.restype = ctypes.c_int
+        L.kda_state_load.argtypes = [_vp, _vp, _vp, _vp, ctypes.c_int, _i32, _i32, _i32, _i32, _i32, _vp]
         _lib = L
     return _lib
 
@@ -306,3 +325,174 @@ def decode_tokens(q, k, v, g, beta, state, accept=None, scale=1.0, g_min=LN_HALF
     if st != KDA_OK:
         raise KdaError(st, "kda_decode_tokens")
     return o
+
+
+# ---- one speculative step over trees of drafted tokens ---------------------------
+
+def _check_step(*ts):
+    """Every given tensor is contiguous and on one device (the first one's),
+    which becomes the current device if it is not."""
+    _check_dev(*ts)
+    dev = next(t.device for t in ts if t is not None)
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one call takes one device")
+    return dev
+
+
+def _call(dev, where, fn, *args):
+    """fn(*args, stream) with dev current and its current stream."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(dev))
+    else:
+        st = fn(*args, _stream(dev))
+    if st != KDA_OK:
+        raise KdaError(st, where)
+
+
+def decode_tree(q, k, v, g, beta, state, parents=None, num_nodes=None, scale=1.0, g_min=LN_HALF, o=None,
+                options: Optional[Options] = None):
+    """kda_decode_tree: the outputs of T drafted tokens per sequence that form
+    a tree (parents, device int32 [N,T]; None: a chain), each over the state
+    [N,H,D,D] and its own path; the state is only read. q,k,g,v [N,T,H,D] and
+    beta [N,T,H] as in decode_tokens; num_nodes (device int32 [N]) gives each
+    sequence its own number of nodes, whose other rows of o stay as they are.
+    Returns o [N,T,H,D]."""
+    N, T, H, D = q.shape
+    g = _check_inputs(q, k, v, g, beta, (N, T), H, D, options, (N, T, H))
+    _expect(state, "state", (N, H, D, D), torch.float32)
+    _expect(parents, "parents", (N, T), torch.int32)
+    _expect(num_nodes, "num_nodes", (N,), torch.int32)
+    _expect(o, "o", (N, T, H, D), q.dtype)
+    dev = _check_step(q, k, v, g, beta, state, parents, num_nodes, o)
+    if o is None:
+        o = torch.empty_like(v) if num_nodes is None else torch.zeros_like(v)
+    _call(dev, "kda_decode_tree", lib().kda_decode_tree, _ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(g),
+          _ptr(beta), _ptr(state), _ptr(parents), _ptr(num_nodes), _ptr(o), N, T, H, D, v.shape[3], float(scale),
+          float(g_min), _opt_ptr(options))
+    return o
+
+
+def commit_path(k, v, g, beta, state, path, accept, g_min=LN_HALF, options: Optional[Options] = None):
+    """kda_commit_path: the recurrence over nodes path[n, :accept[n]] (device
+    int32 [N,T] and [N], as verify_drafts returns them) on state [N,H,D,D], in
+    place; k, v, g, beta and options are those of decode_tree. Returns state."""
+    N, T, H, D = k.shape
+    g = _check_inputs(k, k, v, g, beta, (N, T), H, D, options, (N, T, H))
+    _expect(state, "state", (N, H, D, D), torch.float32)
+    _expect(path, "path", (N, T), torch.int32)
+    _expect(accept, "accept", (N,), torch.int32)
+    if path is None or accept is None:
+        raise ValueError("path and accept are required")
+    dev = _check_step(k, v, g, beta, state, path, accept)
+    _call(dev, "kda_commit_path", lib().kda_commit_path, _ptr(k), _ptr(v), _dtype_code(k), _ptr(g), _ptr(beta),
+          _ptr(state), _ptr(path), _ptr(accept), N, T, H, D, v.shape[3], float(g_min), _opt_ptr(options))
+    return state
+
+
+def verify_workspace(N: int, T: int, V: int, device) -> torch.Tensor:
+    """A workspace for verify_drafts calls of these sizes, one after another."""
+    size = int(lib().kda_verify_workspace_size(int(N), int(T), int(V)))
+    if size == 0 and N != 0:
+        raise KdaError(KDA_ERR_INVALID_ARG, "kda_verify_workspace_size")
+    return torch.empty(max(size, 256), dtype=torch.uint8, device=device)
+
+
+def verify_drafts(target, draft, tokens, uniforms, parents=None, num_nodes=None,
+                  workspace: Optional[torch.Tensor] = None, accept=None, path=None, next_token=None):
+    """kda_verify_drafts: rejection sampling of drafted tokens. target [N,T,V]
+    (bfloat16 or float32) holds the target's probabilities after each node,
+    draft [N,T,V] those that a node's children were drawn from (None: chosen
+    without sampling); tokens int32 [N,T]; uniforms float32 [N,T], entry i >= 1
+    for node i's test and entry 0 for the next token; parents and num_nodes as
+    in decode_tree. workspace (verify_workspace) is allocated when None.
+    Returns (accept [N], path [N,T], next_token [N]), int32: accept is that of
+    decode_tokens (chains) and, with path, of commit_path."""
+    N, T, V = target.shape
+    code = _dtype_code(target)
+    _expect(draft, "draft", (N, T, V), target.dtype)
+    _expect(tokens, "tokens", (N, T), torch.int32)
+    _expect(uniforms, "uniforms", (N, T), torch.float32)
+    _expect(parents, "parents", (N, T), torch.int32)
+    _expect(num_nodes, "num_nodes", (N,), torch.int32)
+    _expect(accept, "accept", (N,), torch.int32)
+    _expect(path, "path", (N, T), torch.int32)
+    _expect(next_token, "next_token", (N,), torch.int32)
+    if tokens is None or uniforms is None:
+        raise ValueError("tokens and uniforms are required")
+    if workspace is not None and workspace.dtype != torch.uint8:
+        raise TypeError(f"workspace: expected torch.uint8, got {workspace.dtype}")
+    dev = _check_step(target, draft, tokens, uniforms, parents, num_nodes, workspace, accept, path, next_token)
+    if workspace is None:
+        workspace = verify_workspace(N, T, V, dev)
+    if accept is None:
+        accept = torch.empty(N, dtype=torch.int32, device=dev)
+    if path is None:
+        path = torch.empty(N, T, dtype=torch.int32, device=dev)
+    if next_token is None:
+        next_token = torch.empty(N, dtype=torch.int32, device=dev)
+    _call(dev, "kda_verify_drafts", lib().kda_verify_drafts, _ptr(target), _ptr(draft), code, _ptr(tokens),
+          _ptr(parents), _ptr(num_nodes), _ptr(uniforms), _ptr(accept), _ptr(path), _ptr(next_token), N, T, V,
+          _ptr(workspace), workspace.numel())
+    return accept, path, next_token
+
+
+# ---- 8-bit cache of recurrent states -----------------------------------------------
+
+@dataclass
+class StateCache:
+    """values [num_slots,H,D,D] (int8, or float8_e4m3fn) and scales
+    [num_slots,H,D*D/32] (uint8: the step's exponent + 127)."""
+    values: torch.Tensor
+    scales: torch.Tensor
+
+    def __post_init__(self):
+        if self.values.dtype not in (torch.int8, torch.float8_e4m3fn):
+            raise TypeError(f"values: expected torch.int8 or torch.float8_e4m3fn, got {self.values.dtype}")
+        if self.values.dim() != 4 or self.values.shape[2] != self.values.shape[3]:
+            raise ValueError(f"values: expected shape [num_slots, H, D, D], got {tuple(self.values.shape)}")
+        S, H, D, _ = self.values.shape
+        _expect(self.scales, "scales", (S, H, D * D // CACHE_BLOCK), torch.uint8)
+
+    @property
+    def format(self) -> int:
+        return CACHE_INT8 if self.values.dtype == torch.int8 else CACHE_E4M3
+
+
+def make_state_cache(num_slots: int, H: int, D: int, device, dtype=torch.int8) -> StateCache:
+    """A cache of num_slots states, every slot the zero state."""
+    return StateCache(torch.zeros(num_slots, H, D, D, dtype=dtype, device=device),
+                      torch.zeros(num_slots, H, D * D // CACHE_BLOCK, dtype=torch.uint8, device=device))
+
+
+def _cache_call(where, fn, first, cache: StateCache, slots, states):
+    S, H, D, _ = cache.values.shape
+    N = states.shape[0]
+    _expect(states, "states", (N, H, D, D), torch.float32)
+    _expect(slots, "slots", (N,), torch.int32)
+    dev = _check_step(cache.values, cache.scales, slots, states)
+    if S >= 2 ** 31:
+        raise ValueError(f"num_slots: {S} is above INT32_MAX")
+    if first == "states":
+        args = (_ptr(states), _ptr(slots), _ptr(cache.values), _ptr(cache.scales))
+    else:
+        args = (_ptr(cache.values), _ptr(cache.scales), _ptr(slots), _ptr(states))
+    _call(dev, where, fn, *args, cache.format, N, S, H, D, D)
+
+
+def state_store(states, cache: StateCache, slots=None):
+    """kda_state_store: states [N,H,D,D] into the cache's slots (device int32
+    [N]; None: slot n), quantised to 8 bits. A state whose slot is outside the
+    cache is not written; of two states for one slot the later one is."""
+    _cache_call("kda_state_store", lib().kda_state_store, "states", cache, slots, states)
+
+
+def state_load(cache: StateCache, slots=None, states=None):
+    """kda_state_load: the states of the given slots (None: all), float32
+    [N,H,D,D]; a slot outside the cache reads as the zero state."""
+    if states is None:
+        N = cache.values.shape[0] if slots is None else slots.shape[0]
+        states = torch.empty(N, *cache.values.shape[1:], dtype=torch.float32, device=cache.values.device)
+    _cache_call("kda_state_load", lib().kda_state_load, "cache", cache, slots, states)
+    return states

@@ -333,6 +333,150 @@ kda_status kda_decode_tokens(const void* q, const void* k, const void* v, kda_dt
                              int32_t Dk, int32_t Dv, float scale, float g_min,
                              const kda_options* opt, hipStream_t stream);
 
+/* ---- one speculative step over trees of drafted tokens ---------------------------
+ *
+ * A step drafts up to KDA_TREE_MAX_NODES tokens per sequence, as a chain or as
+ * a tree, evaluates them against the sequence's state (kda_decode_tree), checks
+ * them against the target model's probabilities (kda_verify_drafts) and commits
+ * the accepted path (kda_commit_path; a chain's accepted prefix also by
+ * kda_decode_tokens). The three calls share these conventions:
+ *   - Node 0 of a sequence is the root: the last token already decided, whose
+ *     state update is still to come. The other nodes are drafts.
+ *   - parents [N, T] int32 (device): the node that node i follows. A parent
+ *     comes before its node (parents[i] < i); -1, and any value outside
+ *     [-1, i - 1], means the node follows the sequence's state directly.
+ *     NULL means chains: node i follows node i - 1.
+ *   - num_nodes [N] int32 (device), or NULL for T nodes each: sequence n uses
+ *     its first num_nodes[n] nodes (clamped to [0, T]). Nothing of the others
+ *     is read, and their rows of o are left as they were. */
+#define KDA_TREE_MAX_NODES 64
+
+/* Attention of a tree of T drafted tokens per sequence over its recurrent
+ * state. Every node's output is the recurrence's output after the tokens on
+ * its path from the state (ancestors first, itself last); siblings do not see
+ * each other. The state is only read, once, whatever the tree.
+ *   With a_i the decay of node i, E_i the product of the decays on its path
+ *   (per channel) and anc(i) its ancestors:
+ *     d_i = beta_i (v_i - S^T (E_i k_i) - sum_{j in anc(i)} (sum_c k_ic k_jc E_ic / E_jc) d_j)
+ *     o_i = scale (S^T (E_i q_i) + sum_{j in anc(i), i} (sum_c q_ic k_jc E_ic / E_jc) d_j)
+ *   q, k, v [N, T, H, D] dtype, g, beta and opt as in kda_decode_tokens
+ *   state   [N, H, Dk, Dv] fp32, read only
+ *   o       [N, T, H, Dv] dtype; must not overlap the inputs
+ * A node whose inputs are not finite, or overflow, makes outputs of itself and
+ * its descendants non-finite, and no others.
+ * T outside [1, KDA_TREE_MAX_NODES] is KDA_ERR_INVALID_ARG; the other errors
+ * are those of kda_decode_tokens. */
+kda_status kda_decode_tree(const void* q, const void* k, const void* v, kda_dtype dtype,
+                           const float* g, const float* beta, const float* state,
+                           const int32_t* parents, const int32_t* num_nodes, void* o, int32_t N,
+                           int32_t T, int32_t H, int32_t Dk, int32_t Dv, float scale, float g_min,
+                           const kda_options* opt, hipStream_t stream);
+
+/* The state after an accepted path, in place: the recurrence over the nodes
+ * path[n][0 .. accept[n] - 1] of sequence n, in that order.
+ *   k, v, g, beta, opt  the step's inputs, as in kda_decode_tree
+ *   state   [N, H, Dk, Dv] fp32, read and updated in place
+ *   path    [N, T] int32 (device), as kda_verify_drafts writes it; a value
+ *           outside [0, T) ends the path
+ *   accept  [N] int32 (device), clamped to [0, T]; 0 leaves the state untouched
+ * Only the listed nodes are read. Errors as kda_decode_tree. */
+kda_status kda_commit_path(const void* k, const void* v, kda_dtype dtype, const float* g,
+                           const float* beta, float* state, const int32_t* path,
+                           const int32_t* accept, int32_t N, int32_t T, int32_t H, int32_t Dk,
+                           int32_t Dv, float g_min, const kda_options* opt, hipStream_t stream);
+
+/* Largest vocabulary kda_verify_drafts takes. */
+#define KDA_VERIFY_MAX_VOCAB (1 << 24)
+
+/* Bytes of device workspace kda_verify_drafts needs (0 for sizes it refuses).
+ * It needs no initialisation; calls that may overlap need one each. */
+size_t kda_verify_workspace_size(int32_t N, int32_t T, int32_t V);
+
+/* Verification of drafted tokens against the target model's probabilities, by
+ * rejection sampling from given random numbers: the tokens it returns are
+ * distributed as the target's own samples.
+ *   target    [N, T, V] dtype: row i is the target's distribution after node i
+ *   draft     [N, T, V] dtype: row i is the distribution that the children of
+ *             node i were drawn from (independently); or NULL when the drafts
+ *             were chosen without sampling (each stands for a distribution
+ *             that has it alone)
+ *   tokens    [N, T] int32: the token of each node (tokens[n][0] is not read)
+ *   parents, num_nodes   as above (NULL parents: chains)
+ *   uniforms  [N, T] fp32 in [0, 1): entry i >= 1 tests node i, entry 0 draws
+ *             the next token
+ * From the root, with p and q the rows of the current node, r = p, c = 1 and
+ * C = 0, its children are tried in the order of their indices. A child with
+ * token x is accepted, and becomes the current node, iff
+ *     u q(x) c < r(x);
+ * else, with draft given, C grows by c, r becomes max(p - C q, 0) and c its
+ * sum; without draft (q(x) = 1), c shrinks by r(x) and r(x) becomes 0. When no
+ * child is accepted the next token is the lowest x with
+ *     r(0) + .. + r(x) > uniforms[n][0] * sum(r)
+ * (r = p if the whole of r is 0). Everything is computed in fp64 from the
+ * stored values. Entries of target and draft that are negative, infinite or
+ * NaN, and tokens outside [0, V), count as probability 0.
+ * Outputs:
+ *   accept      [N] int32: nodes on the accepted path, the root included (so at
+ *               least 1, and 0 only where num_nodes[n] is 0)
+ *   path        [N, T] int32: their indices from the root on, then -1
+ *   next_token  [N] int32: the token after the path; -1 where num_nodes[n] is
+ *               0 or the target's row has no positive entry
+ * For chains, accept is the accept of kda_decode_tokens.
+ *   workspace   256-byte aligned device scratch of
+ *               kda_verify_workspace_size(N, T, V) bytes
+ * target and draft must be 16-byte aligned, as every tensor; V may be odd.
+ * Errors: KDA_ERR_INVALID_ARG (null required pointer, N < 0, T outside
+ * [1, KDA_TREE_MAX_NODES], V outside [1, KDA_VERIFY_MAX_VOCAB], N * T above
+ * INT32_MAX), KDA_ERR_UNSUPPORTED
+ * (dtype), KDA_ERR_WORKSPACE, KDA_ERR_HIP. */
+kda_status kda_verify_drafts(const void* target, const void* draft, kda_dtype dtype,
+                             const int32_t* tokens, const int32_t* parents,
+                             const int32_t* num_nodes, const float* uniforms, int32_t* accept,
+                             int32_t* path, int32_t* next_token, int32_t N, int32_t T, int32_t V,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---- 8-bit cache of recurrent states ------------------------------------------------
+ *
+ * A cache holds num_slots states of H heads at 8.25 bits per value (a quarter
+ * of the fp32 state): states kept for prefix reuse (a prefill's checkpoints or
+ * final states) or of sequences set aside. Each run of KDA_CACHE_BLOCK
+ * consecutive values of a head (row-major) shares the power-of-two step 2^e,
+ * e the least integer >= -127 with max|x| <= qmax 2^e over the run's finite
+ * values; a value is stored as x 2^-e rounded to the nearest (ties to even):
+ *   KDA_CACHE_INT8  int8 in [-127, 127] (qmax 127): at most half a step off,
+ *                   i.e. within max|x| / 127 over the run
+ *   KDA_CACHE_E4M3  8-bit float, 4 exponent and 3 mantissa bits, no
+ *                   infinities (qmax 448): within 2^-4 of each value, down to
+ *                   2^-10 steps
+ * Infinite values are stored as the largest of their sign; NaN as 0 (int8) or
+ * NaN (e4m3). A stored value whose product with the step passes FLT_MAX reads
+ * as FLT_MAX of its sign. */
+#define KDA_CACHE_BLOCK 32
+typedef enum { KDA_CACHE_INT8 = 0, KDA_CACHE_E4M3 = 1 } kda_cache_format;
+
+/* Writes N states into the cache.
+ *   states  [N, H, Dk, Dv] fp32
+ *   slots   [N] int32 (device): the slot of each state, or NULL for slot n. A
+ *           state whose slot is outside [0, num_slots) is not written. Where
+ *           two states name one slot, the later one is written.
+ *   values  [num_slots, H, Dk, Dv] 8-bit;  scales [num_slots, H, Dk * Dv / 32]
+ *           uint8, e + 127. Slots that are not named are left as they were.
+ * Errors: KDA_ERR_INVALID_ARG (null required pointer, N or num_slots < 0,
+ * H <= 0, N * H above INT32_MAX, without slots N > num_slots),
+ * KDA_ERR_UNSUPPORTED (head size or format), KDA_ERR_HIP. */
+kda_status kda_state_store(const float* states, const int32_t* slots, void* values,
+                           uint8_t* scales, kda_cache_format format, int32_t N,
+                           int32_t num_slots, int32_t H, int32_t Dk, int32_t Dv,
+                           hipStream_t stream);
+
+/* Reads N states from the cache: states[n] = the values of slot slots[n]. A
+ * slot outside [0, num_slots) reads as the zero state (a sequence without a
+ * cached prefix). The states serve as initial_state of a prefill or as the
+ * state of a decode. Arguments and errors as kda_state_store. */
+kda_status kda_state_load(const void* values, const uint8_t* scales, const int32_t* slots,
+                          float* states, kda_cache_format format, int32_t N, int32_t num_slots,
+                          int32_t H, int32_t Dk, int32_t Dv, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

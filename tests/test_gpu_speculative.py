@@ -1,0 +1,532 @@
+"""The speculative step (tree attention over the state, draft verification,
+path commit) and the 8-bit state cache on the GPU, against the fp64 oracle.
+
+Tolerances:
+  tree outputs   element by element: the oracle's error bound for the arithmetic
+                 (oracle.speculative.tree_bound; fp32 products, or two-term bf16
+                 operands of 3 * 2^-18 relative error each for bf16 tensors) plus,
+                 for bf16 outputs, the rounding to bf16, 2^-8 |o|
+  committed states  a step rounds its sums of D terms and a few products, at most
+                 (D + 16) 2^-24 of the sizes involved; for unit keys and write
+                 strengths in [0, 1] a step does not enlarge a column's error
+                 (I - b k k^T and the decays have norm <= 1), so over a path of L
+                 tokens a column is at most L (D + 16) 2^-24 (|S column| + |d|) off
+  verification and cache   equal
+"""
+import numpy as np
+import pytest
+import torch
+
+from gated_delta_rule_109_amd import kda
+from gated_delta_rule_109_amd.workloads import make_inputs
+from oracle import frontend, speculative
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+LN_HALF = float(np.log(0.5))
+BF16, F32 = torch.bfloat16, torch.float32
+# relative error of one product of the unrolled form, by the tensors' type
+PRODUCT = {BF16: 3 * 3 * 2.0 ** -18, F32: 0.0}
+# hardware rcp, rsqrt and exp2 of the front end: a few units of 2^-23 on each input
+FRONT_END = 16 * 2.0 ** -23
+
+
+def dev(a, dt=F32):
+    return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).to(dt).to(DEV)
+
+
+def host(x):
+    return x.float().cpu().numpy()
+
+
+def random_parents(N, T, kind, seed):
+    rng = np.random.default_rng(seed)
+    if kind == "chain":
+        return np.tile(np.arange(T) - 1, (N, 1)).astype(np.int32)
+    if kind == "star":
+        return np.tile(np.minimum(np.arange(T), 1) - 1, (N, 1)).astype(np.int32)
+    p = np.array([[-1] + [int(rng.integers(0, i)) for i in range(1, T)] for _ in range(N)], np.int32)
+    if kind == "forest":
+        p[rng.random((N, T)) < 0.3] = -1
+    if kind == "bad":          # values that count as -1
+        for n in range(N):
+            for i in range(T):
+                p[n, i] = rng.choice([p[n, i], -7, i, T + 3, 2 ** 31 - 1, -2 ** 31])
+    return p
+
+
+class Step:
+    """Inputs of a step on the host (values as the device holds them) and on the device."""
+
+    def __init__(self, N, T, H, D, dtype, seed, gate=kda.GATE_CHANNEL, flags=0, g_min=LN_HALF):
+        raw = flags != 0
+        inp = make_inputs(N * T, H, D, seed=seed, lengths=[T] * N, initial_state=True, bf16=dtype is BF16, raw=raw)
+        self.s0 = inp.initial_state
+        q, k, v, g, b = (x.reshape(N, T, *x.shape[1:]) for x in (inp.q, inp.k, inp.v, inp.g, inp.beta))
+        if g_min != LN_HALF and not raw:
+            g = (g * np.float32(g_min / LN_HALF)).astype(np.float32)
+        if gate == kda.GATE_HEAD:
+            g = np.ascontiguousarray(g[..., 0])
+        elif gate == kda.GATE_NONE:
+            g = None
+        self.args = [dev(q, dtype), dev(k, dtype), dev(v, dtype), dev(g), dev(b)]
+        if raw:
+            z = np.zeros((N, T, H)) if g is None else g
+            q, k, z, b = frontend.apply(q, k, z, b, flags, 1e-6)
+            g = None if g is None else z
+        self.q, self.k, self.v, self.g, self.b = q, k, v, g, b
+        self.state = dev(self.s0)
+        self.g_min = g_min
+        self.product = PRODUCT[dtype] + (FRONT_END if raw else 0.0)
+        self.options = kda.Options(flags=flags, gate=gate) if raw or gate != kda.GATE_CHANNEL else None
+
+    def check_tree(self, o, parents, num_nodes=None, scale=1.0):
+        ref = speculative.decode_tree(self.q, self.k, self.v, self.g, self.b, self.s0, parents, num_nodes, scale,
+                                      self.g_min)
+        N, T = ref.shape[:2]
+        out = host(o)
+        for n in range(N):
+            nt = T if num_nodes is None else int(np.clip(num_nodes[n], 0, T))
+            par = speculative.parents_of(None if parents is None else parents[n], T)
+            tol = speculative.tree_bound(self.q[n], self.k[n], self.v[n], None if self.g is None else self.g[n],
+                                         self.b[n], self.s0[n], par, nt, scale, self.g_min, self.product)
+            if o.dtype is BF16:
+                tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref[n, :nt])
+            err = np.abs(out[n, :nt] - ref[n, :nt])
+            assert (err <= tol).all(), f"sequence {n}: {np.nanmax(err / tol):.2f} of the tolerance"
+
+
+TREES = [
+    # N, T, H, D, dtype, tree, gate, flags, g_min
+    (1, 1, 1, 128, BF16, "chain", 0, 0, LN_HALF),
+    (2, 8, 3, 128, BF16, "bushy", 0, 0, LN_HALF),
+    (3, 16, 2, 128, BF16, "bushy", 0, 0, LN_HALF),
+    (2, 17, 2, 128, BF16, "chain", 0, 0, LN_HALF),
+    (2, 31, 1, 128, F32, "forest", 0, 0, LN_HALF),
+    (1, 33, 2, 128, F32, "bushy", 1, 0, LN_HALF),
+    (1, 48, 1, 128, BF16, "star", 2, 0, LN_HALF),
+    (1, 64, 2, 128, BF16, "bushy", 0, kda.FE_ALL, LN_HALF),
+    (1, 64, 1, 128, BF16, "chain", 0, 0, LN_HALF),
+    (1, 64, 1, 128, F32, "chain", 0, 0, LN_HALF),
+    (2, 16, 2, 128, F32, "bushy", 0, kda.FE_ALL, LN_HALF),
+    (2, 12, 2, 128, BF16, "bad", 1, kda.FE_ALL, LN_HALF),
+    (1, 64, 2, 128, BF16, "chain", 0, 0, -5.0),
+    (2, 5, 1, 128, F32, "chain", 0, 0, -40.0),
+    (1, 20, 1, 128, BF16, "bushy", 0, kda.FE_ALL, -1e30),
+    (3, 1, 2, 16, F32, "chain", 0, 0, LN_HALF),
+    (2, 23, 3, 16, BF16, "bushy", 0, 0, LN_HALF),
+    (1, 64, 2, 16, F32, "chain", 0, kda.FE_ALL, -5.0),
+    (1, 64, 2, 16, BF16, "bad", 2, kda.FE_L2NORM_QK | kda.FE_BETA_LOGITS, LN_HALF),
+]
+
+
+@pytest.mark.parametrize("N,T,H,D,dtype,tree,gate,flags,g_min", TREES)
+def test_tree(N, T, H, D, dtype, tree, gate, flags, g_min):
+    s = Step(N, T, H, D, dtype, 100 + T, gate, flags, g_min)
+    par = random_parents(N, T, tree, T)
+    before = s.state.clone()
+    o = kda.decode_tree(*s.args, s.state, dev(par, torch.int32), scale=0.7, g_min=g_min, options=s.options)
+    s.check_tree(o, par, scale=0.7)
+    assert torch.equal(s.state, before)
+    if tree == "chain":
+        assert torch.equal(o, kda.decode_tree(*s.args, s.state, None, scale=0.7, g_min=g_min, options=s.options))
+
+
+@pytest.mark.parametrize("T,D,dtype", [(16, 128, BF16), (40, 128, F32), (16, 128, F32), (64, 128, BF16), (19, 16, BF16)])
+def test_tree_of_each_sequences_own_size(T, D, dtype):
+    nodes = np.array([0, 1, T, T + 9, -3, T // 2], np.int32)
+    N, H = len(nodes), 2
+    s = Step(N, T, H, D, dtype, 7)
+    par = random_parents(N, T, "bushy", 3)
+    # what lies behind a sequence's last node is never read
+    live = torch.arange(T, device=DEV) < dev(nodes, torch.int32)[:, None]
+    for x in s.args:
+        x[~live] = float("nan")
+    o = torch.full((N, T, H, D), 42.0, device=DEV, dtype=dtype)
+    kda.decode_tree(*s.args, s.state, dev(par, torch.int32), dev(nodes, torch.int32), o=o)
+    s.check_tree(o, par, nodes)
+    assert (o[~live] == 42.0).all()
+
+
+@pytest.mark.parametrize("T,D,dtype", [(16, 128, BF16), (50, 128, BF16), (21, 128, F32), (16, 16, F32)])
+@pytest.mark.parametrize("what", ["v", "k", "q", "beta"])
+def test_a_nodes_nan_reaches_its_descendants_only(T, D, dtype, what):
+    s = Step(1, T, 2, D, dtype, 21)
+    par = random_parents(1, T, "bushy", 8)
+    p = dev(par, torch.int32)
+    clean = kda.decode_tree(*s.args, s.state, p)
+    i = 3
+    x = s.args[["q", "k", "v", "g", "beta"].index(what)]
+    if what == "beta":
+        x[0, i, 1] = float("inf")
+    else:
+        x[0, i, 1, 5] = float("nan")
+    o = kda.decode_tree(*s.args, s.state, p)
+    below = {i}
+    for t in range(i + 1, T):
+        if int(par[0, t]) in below:
+            below.add(t)
+    hit = torch.zeros(1, T, 2, dtype=torch.bool, device=DEV)
+    hit[0, [i] if what == "q" else sorted(below), 1] = True
+    assert torch.equal(o[~hit], clean[~hit])
+    bad = ~torch.isfinite(o[hit])
+    # a value's NaN stays in its column, the others reach every one
+    assert bad[:, 5].all() if what == "v" else bad.all()
+    if what == "v":
+        rest = torch.ones(D, dtype=torch.bool, device=DEV)
+        rest[5] = False
+        assert torch.equal(o[hit][:, rest], clean[hit][:, rest])
+
+
+def test_tree_of_a_chain_is_the_token_decode():
+    """The tree's outputs of a chain against kda_decode_tokens, which runs the
+    recurrence: both within their bounds of the exact value, so within twice."""
+    s = Step(3, 16, 2, 128, F32, 9)
+    o = kda.decode_tree(*s.args, s.state, None)
+    ref = kda.decode_tokens(*s.args, s.state.clone())
+    s.check_tree(o, None)
+    s.check_tree(ref, None)
+
+
+@pytest.mark.parametrize("N,T,H,D,dtype,gate,flags,g_min", [
+    (3, 1, 2, 128, BF16, 0, 0, LN_HALF), (4, 16, 2, 128, BF16, 0, 0, LN_HALF), (2, 64, 1, 128, F32, 0, 0, LN_HALF),
+    (5, 23, 2, 128, F32, 1, 0, -5.0), (3, 9, 2, 128, BF16, 2, kda.FE_L2NORM_QK | kda.FE_BETA_LOGITS, LN_HALF),
+    (3, 12, 1, 128, BF16, 0, kda.FE_ALL, -1e30), (4, 8, 3, 16, F32, 0, 0, LN_HALF), (3, 40, 2, 16, BF16, 0, kda.FE_ALL, LN_HALF),
+])
+def test_commit(N, T, H, D, dtype, gate, flags, g_min):
+    s = Step(N, T, H, D, dtype, 300 + T, gate, flags, g_min)
+    rng = np.random.default_rng(T)
+    accept = rng.integers(0, T + 1, N).astype(np.int32)
+    accept[0] = 0
+    accept[-1] = T + 5                                       # counts as T
+    path = rng.integers(0, T, (N, T)).astype(np.int32)       # any order, with repeats
+    if N > 2:
+        path[1, T // 2:] = -1                                # ends the path
+        path[2, T - 1] = T
+    out = kda.commit_path(*s.args[1:], s.state, dev(path, torch.int32), dev(accept, torch.int32), g_min=g_min,
+                          options=s.options)
+    assert out is s.state
+    ref, size, lengths = speculative.commit_path(s.k, s.v, s.g, s.b, s.s0, path, accept, g_min)
+    tol = lengths[:, None, None] * ((D + 16) * 2.0 ** -24 + (FRONT_END if flags else 0)) * size
+    err = np.sqrt(((host(s.state) - ref) ** 2).sum(-2))
+    assert (err <= tol).all(), f"{np.nanmax(err / np.maximum(tol, 1e-30)):.2f} of the tolerance"
+    assert torch.equal(s.state[0], dev(s.s0)[0])             # bit for bit
+    assert lengths[0] == 0
+
+
+def test_commit_reads_listed_nodes_only():
+    s = Step(2, 6, 2, 128, BF16, 5)
+    path, accept = np.array([[0, 3, 5, -1, -1, -1]] * 2, np.int32), np.array([3, 2], np.int32)
+    want = kda.commit_path(*s.args[1:], s.state.clone(), dev(path, torch.int32), dev(accept, torch.int32))
+    for x in s.args:
+        x[:, [1, 2, 4]] = float("nan")
+        x[1, 5] = float("nan")
+    got = kda.commit_path(*s.args[1:], s.state, dev(path, torch.int32), dev(accept, torch.int32))
+    assert torch.equal(got, want) and torch.isfinite(got).all()
+
+
+def probabilities(rng, N, T, V, dtype, peak=3.0, drift=1.0):
+    z = peak * rng.standard_normal((N, T, V))
+    p = np.exp(z - z.max(-1, keepdims=True))
+    z = z + drift * rng.standard_normal((N, T, V))
+    q = np.exp(z - z.max(-1, keepdims=True))
+    return [torch.from_numpy((x / x.sum(-1, keepdims=True)).astype(np.float32)).to(dtype) for x in (p, q)]
+
+
+def check_verify(target, draft, tokens, u, parents, nodes=None, **more):
+    got = kda.verify_drafts(target.to(DEV), None if draft is None else draft.to(DEV), dev(tokens, torch.int32), dev(u),
+                            dev(parents, torch.int32), dev(nodes, torch.int32), **more)
+    want = speculative.verify(target.float().numpy(), None if draft is None else draft.float().numpy(), tokens, u, parents,
+                              nodes)
+    for a, b, name in zip(got, want, ("accept", "path", "next_token")):
+        assert a.cpu().numpy().tolist() == b.tolist(), name
+    return want
+
+
+VERIFY = [
+    # N, T, V, dtype, tree, draft
+    (1, 1, 1, F32, "chain", False), (3, 4, 7, BF16, "chain", True), (1, 5, 1024, F32, "chain", True),
+    (5, 8, 1025, F32, "chain", True), (4, 6, 4099, BF16, "chain", False), (2, 9, 9001, BF16, "bushy", True),
+    (6, 16, 2049, F32, "bushy", True), (3, 64, 1000, F32, "bushy", True), (3, 64, 501, BF16, "star", False),
+    (2, 33, 5003, F32, "bushy", False), (70, 5, 4097, F32, "chain", True), (66, 7, 8209, BF16, "bushy", True),
+    (65, 3, 65537, F32, "chain", True), (2, 3, 300001, BF16, "star", True), (4, 12, 777, F32, "forest", True),
+    (4, 12, 777, F32, "bad", False),
+]
+
+
+@pytest.mark.parametrize("N,T,V,dtype,tree,with_draft", VERIFY)
+def test_verify(N, T, V, dtype, tree, with_draft):
+    rng = np.random.default_rng(V + T)
+    target, draft = probabilities(rng, N, T, V, dtype)
+    par = random_parents(N, T, tree, V)
+    tokens = np.zeros((N, T), np.int32)
+    for n in range(N):
+        for i in range(1, T):
+            w = draft[n, max(0, min(int(par[n, i]), T - 1))].double().numpy()
+            tokens[n, i] = rng.choice(V, p=w / w.sum())
+    u = rng.random((N, T)).astype(np.float32)
+    nodes = None if N == 1 else rng.integers(0, T + 1, N).astype(np.int32)
+    acc, _, _ = check_verify(target, draft if with_draft else None, tokens, u, None if tree == "chain" else par, nodes)
+    if N >= 65 and with_draft:
+        assert len(set(acc.tolist())) > 2           # the drafts are taken to different depths
+    # low uniforms accept more, and draw from the first tokens
+    check_verify(target, draft if with_draft else None, tokens, u * 0.1, None if tree == "chain" else par, nodes)
+
+
+def test_verify_edges():
+    """u at the ends of its range and outside it, rows of one token, rows with no
+    weight, residuals that are 0, tokens out of range, repeated siblings, and
+    entries that are no probabilities."""
+    T, V = 4, 5000
+    star = np.array([[-1, 0, 0, 0]], np.int32)
+    p = torch.zeros(1, T, V)
+    p[0, :, 4999] = 1.0
+    tok = np.array([[0, 4999, 1, 2]], np.int32)
+    for u0 in (0.0, 0.5, np.float32(1 - 2.0 ** -24), 1.0, 7.0, -1.0, np.nan):
+        u = np.array([[u0, 0.0, 0.0, 0.0]], np.float32)
+        un = np.where(np.isnan(u), 0.0, u)                  # NaN draws as 0
+        for draft in (None, p):
+            got = check_verify(p, draft, tok, u if not np.isnan(u0) else un, star)
+            assert got[0][0] == 2 and got[2][0] == 4999
+    # no child of weight, draft equal to target: the residual is 0, the draw is from the target
+    tok = np.array([[0, 1, 1, 1]], np.int32)
+    u = np.full((1, T), 0.5, np.float32)
+    for draft in (None, p):
+        got = check_verify(p, draft, tok, u, star)
+        assert got[0][0] == 1 and got[2][0] == 4999
+    # without draft rows, all of the target's weight rejected: the draw is from the target after all
+    u[0, 1:] = 1.0
+    got = check_verify(p, None, np.array([[0, 4999, 4999, 4999]], np.int32), u, star)
+    assert got[0][0] == 1 and got[2][0] == 4999
+    # no weight anywhere
+    got = check_verify(torch.zeros(1, T, V), p, tok, u, star)
+    assert got[2][0] == -1
+    # out-of-range tokens are rejected and take nothing out
+    w = torch.full((1, T, V), 1.0 / V)
+    for bad in (-1, V, 2 ** 31 - 1, -2 ** 31):
+        check_verify(w, None, np.array([[0, bad, bad, 3]], np.int32), np.array([[0.3, 0.0, 0.0, 0.9]], np.float32), star)
+        check_verify(w, w * 2, np.array([[0, bad, bad, 3]], np.int32), np.array([[0.3, 0.0, 0.0, 0.9]], np.float32), star)
+    # what is no probability counts as 0, in both
+    x = w.clone()
+    x[0, :, 10:20] = float("nan"); x[0, :, 20:30] = float("inf"); x[0, :, 30:40] = -1.0
+    x[0, :, 40:50] = float("-inf")
+    for u0 in (0.0, 0.0021, 0.4):
+        for t in (15, 25, 35, 45, 60):
+            u = np.array([[u0, 0.5, 0.5, 0.5]], np.float32)
+            check_verify(x, w, np.array([[0, t, t, t]], np.int32), u, star)
+            check_verify(w, x, np.array([[0, t, t, t]], np.int32), u, star)
+            check_verify(x, None, np.array([[0, t, t, t]], np.int32), u, star)
+
+
+def test_verify_rejects_a_near_certain_token_exactly():
+    """One token holds all but 2^-60 of a row: without it the residual is the
+    rest, which no subtraction of sums may lose."""
+    V = 4096
+    p = torch.full((1, 2, V), 2.0 ** -72)
+    p[0, :, 77] = 1.0
+    for u0 in (0.0, 0.25, 0.75):
+        got = check_verify(p, None, np.array([[0, 77]], np.int32), np.array([[u0, 1.0]], np.float32), None)
+        assert got[0][0] == 1 and got[2][0] != 77
+        assert abs(int(got[2][0]) - u0 * V) <= 1
+
+
+def states(N, H, D, seed):
+    rng = np.random.default_rng(seed)
+    return (rng.standard_normal((N, H, D, D)) * 10.0 ** rng.uniform(-5, 4, (N, H, D, 1))).astype(np.float32)
+
+
+def check_cache(cache, x, slots):
+    """Slots hold exactly what the oracle's rounding of x gives."""
+    y, code = speculative.quantise(x, cache.format == kda.CACHE_E4M3)
+    got_v = cache.values.float().cpu().numpy().reshape(cache.values.shape[0], cache.values.shape[1], -1)
+    got_c = cache.scales.cpu().numpy()
+    for n, slot in enumerate(slots):
+        np.testing.assert_array_equal(got_c[slot], code[n])
+        np.testing.assert_array_equal(got_v[slot], y[n])
+    return y, code
+
+
+@pytest.mark.parametrize("fmt", [torch.int8, torch.float8_e4m3fn])
+@pytest.mark.parametrize("N,H,D", [(1, 1, 128), (5, 3, 128), (1, 1, 16), (7, 2, 16)])
+def test_cache_round_trip(N, H, D, fmt):
+    x = states(N, H, D, N + D)
+    x[0, 0, 0] = 0.0                                          # blocks of zeros
+    x[0, 0, 1, :8] = [1e-45, -1e-45, 1e-38, 3e-39, 0, -0.0, 1e-40, 1e-44]
+    x[-1, -1, 5, 3] = 3.4e38                                  # near the largest
+    x[-1, 0, 7, :4] = np.float32([127, 126.5, 63.5, -0.5]) * 2.0 ** -9
+    cache = kda.make_state_cache(N + 4, H, D, DEV, dtype=fmt)
+    slots = np.random.default_rng(1).permutation(N + 4)[:N].astype(np.int32)
+    kda.state_store(dev(x), cache, dev(slots, torch.int32))
+    y, code = check_cache(cache, x, slots)
+    others = sorted(set(range(N + 4)) - set(slots.tolist()))
+    assert not cache.values.view(torch.uint8)[others].any() and not cache.scales[others].any()
+    back = kda.state_load(cache, dev(slots, torch.int32))
+    want = speculative.dequantise(y, code).astype(np.float32).reshape(x.shape)
+    np.testing.assert_array_equal(back.cpu().numpy(), want)
+    # within half a step of each value
+    b = np.abs(back.cpu().numpy().astype(np.float64) - x).reshape(N, H, -1, 32)
+    top = np.abs(x).reshape(N, H, -1, 32).max(-1, keepdims=True).astype(np.float64)
+    half = (2.0 ** (code.astype(np.float64) - 128))[..., None]
+    if fmt is torch.int8:
+        assert (b <= half).all() and (b <= np.maximum(top / 127, 2.0 ** -127)).all()
+    else:
+        assert (b <= np.maximum(2.0 ** -4 * np.abs(x.reshape(b.shape)), half * 2.0 ** -9)).all()
+    # all slots, without a list
+    everything = kda.state_load(cache)
+    assert torch.equal(everything[torch.from_numpy(slots).long().to(DEV)], back)
+
+
+@pytest.mark.parametrize("fmt", [torch.int8, torch.float8_e4m3fn])
+def test_cache_slots_outside_twice_and_without_a_list(fmt):
+    N, H, D = 6, 2, 128
+    x = states(N, H, D, 3)
+    cache = kda.make_state_cache(4, H, D, DEV, dtype=fmt)
+    # 1 is named three times: the last state wins; -1, 4 and INT32_MAX are outside
+    slots = np.array([1, -1, 1, 4, 1, 2 ** 31 - 1], np.int32)
+    kda.state_store(dev(x), cache, dev(slots, torch.int32))
+    check_cache(cache, x[4:5], [1])
+    assert not cache.values.view(torch.uint8)[[0, 2, 3]].any()
+    back = torch.full((N, H, D, D), 5.0, device=DEV)
+    kda.state_load(cache, dev(slots, torch.int32), states=back)
+    want = kda.state_load(cache)[1]
+    for n, slot in enumerate(slots):
+        assert torch.equal(back[n], want if slot == 1 else torch.zeros_like(want))
+    kda.state_store(dev(x[:3]), cache)
+    check_cache(cache, x[:3], [0, 1, 2])
+
+
+@pytest.mark.parametrize("fmt", [torch.int8, torch.float8_e4m3fn])
+def test_cache_of_values_that_are_not_finite(fmt):
+    x = states(1, 1, 16, 8)
+    x[0, 0, 0, :3] = [np.inf, -np.inf, np.nan]                # other values of the block keep their step
+    x[0, 0, 4:6] = np.nan
+    x[0, 0, 8:10] = np.inf
+    cache = kda.make_state_cache(1, 1, 16, DEV, dtype=fmt)
+    kda.state_store(dev(x), cache)
+    check_cache(cache, x, [0])
+
+
+def test_cache_reads_every_code():
+    """All 256 codes under steps from 2^-127 to 2^128, through the load."""
+    for fmt in (torch.int8, torch.float8_e4m3fn):
+        cache = kda.make_state_cache(1, 8, 16, DEV, dtype=fmt)
+        cache.values.view(torch.uint8).copy_(torch.arange(256, dtype=torch.uint8).reshape(16, 16).expand(1, 8, 16, 16))
+        codes = torch.tensor([0, 1, 2, 100, 127, 200, 240, 255], dtype=torch.uint8)
+        cache.scales.copy_(codes[None, :, None].expand(1, 8, 8))
+        got = kda.state_load(cache).cpu().numpy()
+        vals = cache.values.cpu().float().numpy().reshape(1, 8, -1)
+        with np.errstate(over="ignore", invalid="ignore"):
+            want = speculative.dequantise(vals, cache.scales.cpu().numpy()).astype(np.float32).reshape(got.shape)
+        np.testing.assert_array_equal(got, want)
+
+
+def full_step(s, par, target, draft, tokens, u, nodes, cache, slots, ws):
+    """Cached states in, tree, verification, commit, cached states out."""
+    state = kda.state_load(cache, slots)
+    o = kda.decode_tree(*s.args, state, par, nodes)
+    accept, path, token = kda.verify_drafts(target, draft, tokens, u, par, nodes, workspace=ws)
+    kda.commit_path(*s.args[1:], state, path, accept)
+    kda.state_store(state, cache, slots)
+    return o, accept, path, token, state
+
+
+def step_setup(N=5, T=12, H=2, D=128, V=3001):
+    rng = np.random.default_rng(77)
+    s = Step(N, T, H, D, BF16, 77)
+    par = random_parents(N, T, "bushy", 4)
+    target, draft = probabilities(rng, N, T, V, F32)
+    tokens = np.zeros((N, T), np.int32)
+    for n in range(N):
+        for i in range(1, T):
+            w = draft[n, par[n, i]].double().numpy()
+            tokens[n, i] = rng.choice(V, p=w / w.sum())
+    u = rng.random((N, T)).astype(np.float32)
+    nodes = np.array([T, T, 0, T - 5, T], np.int32)[:N]
+    cache = kda.make_state_cache(N + 2, H, D, DEV)
+    slots = dev(np.arange(N)[::-1].astype(np.int32), torch.int32)
+    kda.state_store(s.state, cache, slots)
+    return (s, dev(par, torch.int32), target.to(DEV), draft.to(DEV), dev(tokens, torch.int32), dev(u),
+            dev(nodes, torch.int32), cache, slots, kda.verify_workspace(N, T, V, DEV)), par, tokens, u, nodes
+
+
+def test_a_step_from_cache_to_cache():
+    a, par, tokens, u, nodes = step_setup()
+    s, target, draft, cache, slots = a[0], a[2], a[3], a[7], a[8]
+    s.s0 = kda.state_load(cache, slots).cpu().numpy()
+    o, accept, path, token, state = full_step(*a)
+    s.check_tree(o, par, nodes)
+    acc, pth, nxt = speculative.verify(target.cpu().numpy(), draft.cpu().numpy(), tokens, u, par, nodes)
+    assert accept.tolist() == acc.tolist() and path.tolist() == pth.tolist() and token.tolist() == nxt.tolist()
+    ref, size, lengths = speculative.commit_path(s.k, s.v, s.g, s.b, s.s0, pth, acc)
+    assert lengths.tolist() == acc.tolist() and lengths.max() > 1
+    err = np.sqrt(((host(state) - ref) ** 2).sum(-2))
+    assert (err <= lengths[:, None, None] * 144 * 2.0 ** -24 * size).all()
+    # the outputs are those of the accepted path run as tokens on the committed prefix
+    n = int(np.argmax(acc))
+    idx = torch.from_numpy(pth[n, :acc[n]]).long().to(DEV)
+    st = dev(s.s0[n:n + 1])
+    chain = kda.decode_tokens(*(x[n:n + 1, idx].contiguous() for x in s.args), st)
+    s.check_tree(o, par, nodes)
+    assert (chain[0].float() - o[n, idx].float()).abs().max() <= 2.0 ** -6 * o[n, idx].float().abs().max()
+    # committing the accepted path and decoding its tokens one after the other are the same recurrence
+    assert (st[0] - state[n]).norm() <= 2 * acc[n] * 144 * 2.0 ** -24 * float(np.linalg.norm(size[n]))
+    check_cache(cache, state.cpu().numpy(), slots.tolist())
+
+
+def test_a_step_captured_and_replayed():
+    """The whole step in one graph, replayed over refreshed inputs with eager
+    work between the replays; each replay equals the eager step."""
+    a, par, tokens, u, nodes = step_setup()
+    s, us, cache = a[0], a[5], a[7]
+    first = [cache.values.clone(), cache.scales.clone()]
+
+    def reset():
+        cache.values.copy_(first[0])
+        cache.scales.copy_(first[1])
+
+    full_step(*a)                                             # loads the kernels
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = full_step(*a)
+    for turn in range(4):
+        us.copy_(torch.rand(us.shape, generator=torch.Generator().manual_seed(turn)))
+        reset()
+        want = [x.clone() for x in full_step(*a)]
+        kept = [cache.values.clone(), cache.scales.clone()]
+        reset()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(out, want):
+            assert torch.equal(x, y)
+        assert torch.equal(cache.values, kept[0]) and torch.equal(cache.scales, kept[1])
+
+
+def test_on_another_stream_and_twice_the_same():
+    a, *_ = step_setup()
+    cache = a[7]
+    first = [cache.values.clone(), cache.scales.clone()]
+    want = [x.clone() for x in full_step(*a)]
+    for _ in range(3):
+        cache.values.copy_(first[0]); cache.scales.copy_(first[1])
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            got = full_step(*a)
+        torch.cuda.current_stream().wait_stream(stream)
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+
+
+def test_empty_calls():
+    x = torch.empty(0, 4, 2, 128, device=DEV, dtype=BF16)
+    g, b, st = torch.empty(0, 4, 2, 128, device=DEV), torch.empty(0, 4, 2, device=DEV), torch.empty(0, 2, 128, 128, device=DEV)
+    assert kda.decode_tree(x, x, x, g, b, st).shape == x.shape
+    i = torch.empty(0, 4, device=DEV, dtype=torch.int32)
+    kda.commit_path(x, x, g, b, st, i, torch.empty(0, device=DEV, dtype=torch.int32))
+    p = torch.empty(0, 4, 100, device=DEV)
+    assert kda.verify_drafts(p, p, i, torch.empty(0, 4, device=DEV))[1].shape == (0, 4)
+    cache = kda.make_state_cache(2, 2, 128, DEV)
+    kda.state_store(st, cache, torch.empty(0, device=DEV, dtype=torch.int32))
+    assert kda.state_load(cache, torch.empty(0, device=DEV, dtype=torch.int32)).shape == (0, 2, 128, 128)
