@@ -40,6 +40,27 @@ __device__ __forceinline__ int clean_parent(const int32_t* parents, size_t first
   return p >= 0 && p < i ? p : -1;
 }
 
+// The tree of one sequence as a wave holds it (lane i is node i): every node's
+// ancestors and itself as a bit mask, by doubling the distance looked back.
+__device__ __forceinline__ uint64_t ancestors(int parent, int lane) {
+  uint64_t anc = 1ull << lane;
+  for (int jump = parent; __ballot(jump >= 0);) {
+    const uint64_t up = __shfl((unsigned long long)anc, max(jump, 0));
+    const int next = __shfl(jump, max(jump, 0));
+    if (jump >= 0) { anc |= up; jump = next; }
+  }
+  return anc;
+}
+
+// Whether a sequence takes the tile kernel: it forms decays between nodes as
+// quotients E_i / E_j, so the smallest E, at least exp(depth * g_min), must stay
+// far inside the range of fp32 and of a two-term bf16 split. `reach` is
+// kMaxSpan / -g_min, the deepest tree allowed.
+constexpr float kMaxSpan = 60.f;
+__device__ __forceinline__ bool shallow(uint64_t anc, bool live, int reach) {
+  return __ballot(live && __builtin_popcountll(anc) > reach) == 0;
+}
+
 // ---- any decays, any head size -------------------------------------------------
 // One 256-thread workgroup per (sequence, head). A_ij and B_ij are summed pair
 // by pair along each node's path, with the decay between the two nodes built
@@ -56,11 +77,15 @@ __global__ __launch_bounds__(256) void tree_path_kernel(
     const TIn* __restrict__ q, const TIn* __restrict__ k, const TIn* __restrict__ v,
     const float* __restrict__ g, const float* __restrict__ beta, const float* __restrict__ state,
     const int32_t* __restrict__ parents, const int32_t* __restrict__ num_nodes, TIn* __restrict__ o, int H,
-    int T, float scale, float g_min, uint32_t fe_flags, float fe_eps, int gate) {
+    int T, float scale, float g_min, uint32_t fe_flags, float fe_eps, int gate, int skip_reach) {
   const uint32_t n = blockIdx.x / (uint32_t)H, h = blockIdx.x % (uint32_t)H;
   const int nt = num_nodes ? min(max(num_nodes[n], 0), T) : T;
   if (nt == 0) return;
   const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+  if (skip_reach > 0) {   // the tile kernel takes the shallow ones
+    const int p = lane < nt ? clean_parent(parents, (size_t)n * T, lane) : -1;
+    if (shallow(ancestors(p, lane), lane < nt, skip_reach)) return;
+  }
   extern __shared__ float smem[];
   float* s_k = smem;
   float* s_q = s_k + T * D;
@@ -174,18 +199,461 @@ __global__ __launch_bounds__(256) void tree_path_kernel(
   }
 }
 
+// ---- D = 128, decays of moderate span ---------------------------------------------
+// The same products as tiles of 16 nodes on the matrix cores. One workgroup of
+// kWaves waves per (sequence, head); wave w owns the 128 / kWaves value columns
+// from there on, and nothing of S, d or o leaves its registers:
+//   1. E by products along the paths (doubling), k E, q E and k / E to LDS;
+//   2. U = (k E) S and W = (q E) S, S straight from memory in operand layout;
+//      A = (k E)(k / E)^T and B = (q E)(k / E)^T, masked to ancestors, to LDS;
+//   3. (I + beta A)^-1 of the 16 x 16 diagonal blocks, one column per lane;
+//   4. d by blocks of 16 nodes, then o = W + B d. The accumulator layout of a
+//      16 x 16 tile is the K = 16 operand layout, so d feeds the products as it is.
+// Operands of bf16 tensors are split in two bf16 terms (16 bits of mantissa,
+// 2^-17 relative, far below the bf16 rounding of o), three products each; fp32
+// tensors use the fp32 matrix instructions, at an eighth of the rate.
+//
+// Values that are not finite: a product over nodes would carry one node's NaN
+// to nodes that do not descend from it (0 * NaN). So they are replaced by 0
+// before such a product and remembered as bits, per node where they reach every
+// column (A, B) and per node and column (d); the outputs of their nodes and
+// descendants are then set to NaN.
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+struct SplitOp {                 // two bf16 terms
+  static constexpr int kRowBytes = 2 * 272;      // a row of 128: hi, lo, each padded by 16 bytes
+  struct F8 { bf16x8 hi, lo; };
+  struct F4 { bf16x4 hi, lo; };
+  static __device__ __forceinline__ F8 make8(const float (&x)[8]) {
+    F8 f;
+    bf16x4 h0, l0, h1, l1;
+    split_bf16(f32x4{x[0], x[1], x[2], x[3]}, h0, l0);
+    split_bf16(f32x4{x[4], x[5], x[6], x[7]}, h1, l1);
+    f.hi = cat(h0, h1);
+    f.lo = cat(l0, l1);
+    return f;
+  }
+  static __device__ __forceinline__ F4 make4(f32x4 x) {
+    F4 f;
+    split_bf16(x, f.hi, f.lo);
+    return f;
+  }
+  // channels 2 lane, 2 lane + 1 of a row
+  static __device__ __forceinline__ void put2(char* row, int lane, float a, float b) {
+    bf16x4 hi, lo;
+    split_bf16(f32x4{a, b, 0.f, 0.f}, hi, lo);
+    ((uint32_t*)row)[lane] = __builtin_bit_cast(uint2, hi).x;
+    ((uint32_t*)(row + 272))[lane] = __builtin_bit_cast(uint2, lo).x;
+  }
+  static __device__ __forceinline__ F8 get8(const char* row, int c) {
+    return {*(const bf16x8*)(row + 2 * c), *(const bf16x8*)(row + 272 + 2 * c)};
+  }
+  // element (i, j) of a matrix with rows of `stride` elements
+  static __device__ __forceinline__ void put1(char* m, int stride, int i, int j, float x) {
+    const __bf16 hi = f32_to_bf16(x);
+    ((__bf16*)m)[2 * i * stride + j] = hi;
+    ((__bf16*)m)[(2 * i + 1) * stride + j] = f32_to_bf16(x - bf16v_to_f32(hi));
+  }
+  static __device__ __forceinline__ F4 get4(const char* m, int stride, int i, int j) {
+    return {*(const bf16x4*)(m + 2 * (2 * i * stride + j)), *(const bf16x4*)(m + 2 * ((2 * i + 1) * stride + j))};
+  }
+  static __device__ __forceinline__ f32x4 mma(const F8& a, const F8& b, f32x4 c) {
+    c = mfma32(a.lo, b.hi, c);
+    c = mfma32(a.hi, b.lo, c);
+    return mfma32(a.hi, b.hi, c);
+  }
+  static __device__ __forceinline__ f32x4 mma16(bf16x4 a, bf16x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, a), __builtin_bit_cast(s16x4, b), c, 0,
+                                                     0, 0);
+  }
+  static __device__ __forceinline__ f32x4 mma(const F4& a, const F4& b, f32x4 c) {
+    c = mma16(a.lo, b.hi, c);
+    c = mma16(a.hi, b.lo, c);
+    return mma16(a.hi, b.hi, c);
+  }
+};
+
+struct FloatOp {
+  static constexpr int kRowBytes = 528;
+  struct F8 { float x[8]; };
+  struct F4 { f32x4 x; };
+  static __device__ __forceinline__ F8 make8(const float (&x)[8]) {
+    F8 f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.x[j] = x[j];
+    return f;
+  }
+  static __device__ __forceinline__ F4 make4(f32x4 x) { return {x}; }
+  static __device__ __forceinline__ void put2(char* row, int lane, float a, float b) {
+    ((f32x2*)row)[lane] = f32x2{a, b};
+  }
+  static __device__ __forceinline__ F8 get8(const char* row, int c) {
+    F8 f;
+    *(f32x4*)f.x = *(const f32x4*)(row + 4 * c);
+    *(f32x4*)(f.x + 4) = *(const f32x4*)(row + 4 * c + 16);
+    return f;
+  }
+  static __device__ __forceinline__ void put1(char* m, int stride, int i, int j, float x) {
+    ((float*)m)[i * stride + j] = x;
+  }
+  static __device__ __forceinline__ F4 get4(const char* m, int stride, int i, int j) {
+    return {*(const f32x4*)(m + 4 * (i * stride + j))};
+  }
+  // K is walked in four lane groups an instruction; which of the fragment's
+  // elements go together is free as long as both operands agree
+  static __device__ __forceinline__ f32x4 mma(const F8& a, const F8& b, f32x4 c) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x[j], b.x[j], c, 0, 0, 0);
+    return c;
+  }
+  static __device__ __forceinline__ f32x4 mma(const F4& a, const F4& b, f32x4 c) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x[j], b.x[j], c, 0, 0, 0);
+    return c;
+  }
+};
+
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) < __builtin_inff(); }
+
+// kTB: tiles of 16 nodes; kWaves: 4 or 8.
+template <int kTB, int kWaves, typename Op>
+struct TileLds {
+  static constexpr int kT = 16 * kTB;
+  static constexpr int kStride = kT + 4;                 // row of A or B, elements
+  static constexpr size_t kRows = (size_t)kT * Op::kRowBytes;
+  static constexpr size_t kMat = (size_t)kT * kStride * 4;
+  static constexpr size_t kE = (size_t)kT * 128 * 4;
+  static constexpr size_t kDiag = (size_t)kTB * 16 * 20 * 4;
+  // E lies under A, B, the diagonal blocks and their inverses, which come later
+  static constexpr size_t kTail = 2 * kMat + 2 * kDiag > kE ? 2 * kMat + 2 * kDiag : kE;
+  static constexpr size_t kBytes = 3 * kRows + kTail;
+};
+
+template <int kTB, int kWaves, typename TIn, typename Op>
+__global__ __launch_bounds__(64 * kWaves) void tree_tile_kernel(
+    const TIn* __restrict__ q, const TIn* __restrict__ k, const TIn* __restrict__ v,
+    const float* __restrict__ g, const float* __restrict__ beta, const float* __restrict__ state,
+    const int32_t* __restrict__ parents, const int32_t* __restrict__ num_nodes, TIn* __restrict__ o, int H,
+    int T, float scale, float g_min, uint32_t fe_flags, float fe_eps, int gate, int reach) {
+  constexpr int D = 128;
+  using L = TileLds<kTB, kWaves, Op>;
+  constexpr int kT = L::kT, kNT = 8 / kWaves;            // n-tiles of a wave
+  constexpr int kRowsPerWave = kT / kWaves;
+  const uint32_t n = blockIdx.x / (uint32_t)H, h = blockIdx.x % (uint32_t)H;
+  const int nt = num_nodes ? min(max(num_nodes[n], 0), T) : T;
+  if (nt == 0) return;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
+  const int lr = lane % 16, lg = lane / 16;              // operand row / column, lane group
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  char* s_ke = lds;                                      // k E, q E, k / E: [kT] rows each
+  char* s_qe = s_ke + L::kRows;
+  char* s_kq = s_qe + L::kRows;
+  float* s_E = (float*)(s_kq + L::kRows);                // [kT][128]
+  char* s_A = s_kq + L::kRows;                           // -beta A
+  char* s_B = s_A + L::kMat;
+  float* s_diag = (float*)(s_B + L::kMat);               // [kTB][16][20] diagonal blocks of -beta A
+  char* s_inv = (char*)s_diag + L::kDiag;                // [kTB] 16 rows of stride 20
+  __shared__ uint64_t s_anc[kMaxNodes];
+  __shared__ __attribute__((aligned(16))) float s_b[kMaxNodes];
+  __shared__ unsigned long long s_bad[2];                // nodes with d, with o not finite in every column
+  auto row = [&](int t) __attribute__((always_inline)) { return ((size_t)n * T + t) * H + h; };
+
+  const int parent = lane < nt ? clean_parent(parents, (size_t)n * T, lane) : -1;
+  const float braw = beta[row(min(lane, nt - 1))];
+  // this wave's nodes: wave + kWaves x, two channels per lane
+  float tk[kRowsPerWave][2], tq[kRowsPerWave][2], te[kRowsPerWave][2];
+#pragma unroll
+  for (int x = 0; x < kRowsPerWave; ++x) {
+    const size_t r = row(min(wave + kWaves * x, nt - 1));
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      tk[x][c] = Elem<TIn>::load(k + r * D + 2 * lane + c);
+      tq[x][c] = Elem<TIn>::load(q + r * D + 2 * lane + c);
+      te[x][c] = gate == KDA_GATE_NONE ? 0.f : g[gate == KDA_GATE_CHANNEL ? r * D + 2 * lane + c : r];
+    }
+  }
+  // S in operand layout: rows 32 ks + 8 lg + j, columns col0 + kNT lr + {0 ..}
+  const int col0 = wave * 16 * kNT;
+  const float* S = state + (size_t)blockIdx.x * D * D + col0 + kNT * lr;
+  float sreg[4][8][kNT];
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int c = 0; c < kNT; ++c) sreg[ks][j][c] = S[(32 * ks + 8 * lg + j) * D + c];
+  TIn vreg[kTB][4][kNT];
+#pragma unroll
+  for (int I = 0; I < kTB; ++I)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int c = 0; c < kNT; ++c)
+        vreg[I][r][c] = v[row(min(16 * I + 4 * lg + r, nt - 1)) * D + col0 + kNT * lr + c];
+
+  // the tree: ancestors, and whether this kernel takes it
+  const uint64_t anc = ancestors(parent, lane);
+  if (reach > 0 && !shallow(anc, lane < nt, reach)) return;
+  if (wave == 0) {
+    s_anc[lane] = anc;
+    s_b[lane] = lane >= nt ? 0.f : fe_flags & KDA_FE_BETA_LOGITS ? beta_logit(braw) : braw;
+    if (lane < 2) s_bad[lane] = 0;
+  }
+  // decays, normalised rows
+  const float alpha_min = __builtin_amdgcn_exp2f(g_min * kLog2e);
+#pragma unroll
+  for (int x = 0; x < kRowsPerWave; ++x) {
+    const int i = wave + kWaves * x;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float a = gate == KDA_GATE_NONE              ? 1.f
+                      : fe_flags & KDA_FE_GATE_LOGITS ? gate_alpha_logit(te[x][c], alpha_min)
+                                                      : gate_alpha(te[x][c], g_min);
+      te[x][c] = i < nt ? a : 1.f;
+      if (i >= nt) tk[x][c] = tq[x][c] = 0.f;
+    }
+    if (fe_flags & KDA_FE_L2NORM_QK) {
+      const float rk = inv_norm(wave_sum(tk[x][0] * tk[x][0] + tk[x][1] * tk[x][1]), fe_eps);
+      const float rq = inv_norm(wave_sum(tq[x][0] * tq[x][0] + tq[x][1] * tq[x][1]), fe_eps);
+      if (i < nt) { tk[x][0] *= rk; tk[x][1] *= rk; tq[x][0] *= rq; tq[x][1] *= rq; }
+    }
+  }
+  // E by doubling: after r rounds the product over the last 2^r nodes of the path
+  if (gate != KDA_GATE_NONE)
+    for (int jump = parent; __ballot(jump >= 0);) {
+#pragma unroll
+      for (int x = 0; x < kRowsPerWave; ++x)
+        *(f32x2*)(s_E + (wave + kWaves * x) * D + 2 * lane) = f32x2{te[x][0], te[x][1]};
+      lds_barrier();
+#pragma unroll
+      for (int x = 0; x < kRowsPerWave; ++x) {
+        const int p = __builtin_amdgcn_readlane(jump, wave + kWaves * x);
+        if (p >= 0) {
+          const f32x2 e = *(const f32x2*)(s_E + p * D + 2 * lane);
+          te[x][0] *= e[0];
+          te[x][1] *= e[1];
+        }
+      }
+      const int next = __shfl(jump, max(jump, 0));
+      jump = jump >= 0 ? next : -1;
+      lds_barrier();
+    }
+#pragma unroll
+  for (int x = 0; x < kRowsPerWave; ++x) {
+    const int i = wave + kWaves * x;
+    const float e0 = te[x][0], e1 = te[x][1];
+    Op::put2(s_ke + i * Op::kRowBytes, lane, tk[x][0] * e0, tk[x][1] * e1);
+    Op::put2(s_qe + i * Op::kRowBytes, lane, tq[x][0] * e0, tq[x][1] * e1);
+    Op::put2(s_kq + i * Op::kRowBytes, lane, tk[x][0] * __builtin_amdgcn_rcpf(e0), tk[x][1] * __builtin_amdgcn_rcpf(e1));
+  }
+  lds_barrier();
+
+  // A and B: tiles (I, J <= I) of either, shared out over the waves
+  constexpr int kPairs = kTB * (kTB + 1) / 2;
+  f32x4 mat[(2 * kPairs + kWaves - 1) / kWaves];
+  static_for<0, (2 * kPairs + kWaves - 1) / kWaves>([&](auto X) __attribute__((always_inline)) {
+    constexpr int x = decltype(X)::value;
+    const int unit = wave + kWaves * x;
+    mat[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (unit < 2 * kPairs) {
+      const int pair = unit >> 1;
+      int I = 0;
+      while ((I + 1) * (I + 2) / 2 <= pair) ++I;
+      const int J = pair - I * (I + 1) / 2;
+      const char* rows = unit & 1 ? s_qe : s_ke;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        mat[x] = Op::mma(Op::get8(rows + (16 * I + lr) * Op::kRowBytes, 32 * ks + 8 * lg),
+                         Op::get8(s_kq + (16 * J + lr) * Op::kRowBytes, 32 * ks + 8 * lg), mat[x]);
+    }
+  });
+  // U and W
+  f32x4 U[kTB][kNT], W[kTB][kNT];
+#pragma unroll
+  for (int I = 0; I < kTB; ++I)
+#pragma unroll
+    for (int c = 0; c < kNT; ++c) U[I][c] = W[I][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) {
+    typename Op::F8 sf[kNT];
+#pragma unroll
+    for (int c = 0; c < kNT; ++c) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = sreg[ks][j][c];
+      sf[c] = Op::make8(x);
+    }
+#pragma unroll
+    for (int I = 0; I < kTB; ++I) {
+      const typename Op::F8 a = Op::get8(s_ke + (16 * I + lr) * Op::kRowBytes, 32 * ks + 8 * lg);
+      const typename Op::F8 b = Op::get8(s_qe + (16 * I + lr) * Op::kRowBytes, 32 * ks + 8 * lg);
+#pragma unroll
+      for (int c = 0; c < kNT; ++c) {
+        U[I][c] = Op::mma(a, sf[c], U[I][c]);
+        W[I][c] = Op::mma(b, sf[c], W[I][c]);
+      }
+    }
+  }
+  // masked A and B to LDS (over E, which nobody reads any more)
+  static_for<0, (2 * kPairs + kWaves - 1) / kWaves>([&](auto X) __attribute__((always_inline)) {
+    constexpr int x = decltype(X)::value;
+    const int unit = wave + kWaves * x;
+    if (unit < 2 * kPairs) {
+      const int pair = unit >> 1;
+      int I = 0;
+      while ((I + 1) * (I + 2) / 2 <= pair) ++I;
+      const int J = pair - I * (I + 1) / 2;
+      const bool is_b = unit & 1;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * I + 4 * lg + r, j = 16 * J + lr;
+        const bool on = (s_anc[i] >> j & 1) && (is_b || i != j);
+        float y = is_b ? mat[x][r] : -s_b[i] * mat[x][r];
+        y = on ? y : 0.f;
+        if (!is_finite(y)) {
+          atomicOr(&s_bad[is_b], 1ull << i);
+          y = 0.f;
+        }
+        Op::put1(is_b ? s_B : s_A, L::kStride, i, j, y);
+        if (!is_b && I == J) s_diag[(I * 16 + 4 * lg + r) * 20 + lr] = y;
+      }
+    }
+  });
+  lds_barrier();
+
+  // inverses of I + beta A on the diagonal, lane (block lg, column lr):
+  // x_i = (i == column) + sum_j (-beta A)_ij x_j
+  if (wave == 0 && lg < kTB) {
+    float x[16];
+    const float* m = s_diag + lg * 16 * 20;
+    static_for<0, 16>([&](auto I) __attribute__((always_inline)) {
+      constexpr int i = decltype(I)::value;
+      f32x4 part = {i == lr ? 1.f : 0.f, 0.f, 0.f, 0.f};
+      static_for<0, (i + 3) / 4>([&](auto J) __attribute__((always_inline)) {
+        constexpr int j4 = decltype(J)::value;
+        const f32x4 a = *(const f32x4*)(m + i * 20 + 4 * j4);
+        static_for<0, 4>([&](auto R) __attribute__((always_inline)) {
+          constexpr int j = 4 * j4 + decltype(R)::value;
+          if constexpr (j < i) part[j % 4] += a[j % 4] * x[j];
+        });
+      });
+      x[i] = (part[0] + part[1]) + (part[2] + part[3]);
+      Op::put1(s_inv, 20, 16 * lg + i, lr, x[i]);
+    });
+  }
+  lds_barrier();
+
+  // d and o, block by block; bit 16 I + 4 lg + r of bad[c]: that row of the
+  // lane's column is not finite
+  typename Op::F4 d[kTB][kNT];
+  uint64_t bad[kNT] = {};
+  auto clean = [&](f32x4& x, int I, int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (!is_finite(x[r])) {
+        bad[c] |= 1ull << (16 * I + 4 * lg + r);
+        x[r] = 0.f;
+      }
+  };
+#pragma unroll
+  for (int I = 0; I < kTB; ++I) {
+    if (16 * I < nt) {
+      const f32x4 b4 = *(const f32x4*)(s_b + 16 * I + 4 * lg);
+#pragma unroll
+      for (int c = 0; c < kNT; ++c) {
+        f32x4 x;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          x[r] = 16 * I + 4 * lg + r < nt ? b4[r] * (Elem<TIn>::load(&vreg[I][r][c]) - U[I][c][r]) : 0.f;
+#pragma unroll
+        for (int J = 0; J < I; ++J)
+          x = Op::mma(Op::get4(s_A, L::kStride, 16 * I + lr, 16 * J + 4 * lg), d[J][c], x);
+        clean(x, I, c);
+        f32x4 y = {0.f, 0.f, 0.f, 0.f};
+        y = Op::mma(Op::get4(s_inv, 20, 16 * I + lr, 4 * lg), Op::make4(x), y);
+        clean(y, I, c);
+        d[I][c] = Op::make4(y);
+      }
+    }
+  }
+  const uint64_t bad_d = s_bad[0], bad_o = s_bad[1];
+  bool any = bad_d | bad_o;
+#pragma unroll
+  for (int c = 0; c < kNT; ++c) any |= bad[c] != 0;
+  any = __ballot(any) != 0;
+  if (any) {
+#pragma unroll
+    for (int c = 0; c < kNT; ++c) {
+      bad[c] |= __shfl_xor((unsigned long long)bad[c], 16);
+      bad[c] |= __shfl_xor((unsigned long long)bad[c], 32);
+      bad[c] |= bad_d;
+    }
+  }
+#pragma unroll
+  for (int I = 0; I < kTB; ++I) {
+    if (16 * I < nt) {
+#pragma unroll
+      for (int c = 0; c < kNT; ++c)
+#pragma unroll
+        for (int J = 0; J <= I; ++J)
+          W[I][c] = Op::mma(Op::get4(s_B, L::kStride, 16 * I + lr, 16 * J + 4 * lg), d[J][c], W[I][c]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * I + 4 * lg + r;
+        if (i < nt) {
+#pragma unroll
+          for (int c = 0; c < kNT; ++c) {
+            float y = scale * W[I][c][r];
+            if (any && ((s_anc[i] & bad[c]) || (bad_o >> i & 1))) y = __builtin_nanf("");
+            Elem<TIn>::store(o + row(i) * D + col0 + kNT * lr + c, y);
+          }
+        }
+      }
+    }
+  }
+}
+
 template <int D, typename TIn>
-static hipError_t launch_tree_t(const TreeArgs& a) {
+static hipError_t launch_paths(const TreeArgs& a, int skip_reach) {
   const unsigned blocks = (unsigned)((int64_t)a.N * a.H);
   hipLaunchKernelGGL((tree_path_kernel<D, TIn>), dim3(blocks), dim3(256), path_lds_bytes<D>(a.T), a.stream,
                      (const TIn*)a.q, (const TIn*)a.k, (const TIn*)a.v, a.g, a.beta, a.state, a.parents,
-                     a.num_nodes, (TIn*)a.o, a.H, a.T, a.scale, a.g_min, a.fe_flags, a.fe_eps, (int)a.gate);
+                     a.num_nodes, (TIn*)a.o, a.H, a.T, a.scale, a.g_min, a.fe_flags, a.fe_eps, (int)a.gate,
+                     skip_reach);
   return hipGetLastError();
 }
 
+template <int kTB, int kWaves, typename TIn, typename Op>
+static hipError_t launch_tiles(const TreeArgs& a, int reach) {
+  const unsigned blocks = (unsigned)((int64_t)a.N * a.H);
+  constexpr size_t lds = TileLds<kTB, kWaves, Op>::kBytes;
+  hipLaunchKernelGGL((tree_tile_kernel<kTB, kWaves, TIn, Op>), dim3(blocks), dim3(64 * kWaves), lds, a.stream,
+                     (const TIn*)a.q, (const TIn*)a.k, (const TIn*)a.v, a.g, a.beta, a.state, a.parents, a.num_nodes, (TIn*)a.o, a.H, a.T, a.scale, a.g_min, a.fe_flags,
+                     a.fe_eps, (int)a.gate, reach);
+  return hipGetLastError();
+}
+
+template <typename TIn, typename Op>
+static hipError_t launch_tree_128(const TreeArgs& a) {
+  // the deepest path whose decays span at most kMaxSpan; every tree if T does
+  const float deepest = a.gate == KDA_GATE_NONE || a.g_min == 0.f ? (float)kMaxNodes : kMaxSpan / -a.g_min;
+  const int reach = deepest >= (float)a.T ? 0 : (int)deepest;
+  if (reach == 0 && deepest < 1.f) return launch_paths<128, TIn>(a, 0);
+  hipError_t e;
+  switch ((a.T + 15) / 16) {
+    case 1: e = launch_tiles<1, 4, TIn, Op>(a, reach); break;
+    case 2: e = launch_tiles<2, 8, TIn, Op>(a, reach); break;
+    case 3: e = launch_tiles<3, 8, TIn, Op>(a, reach); break;
+    default: e = launch_tiles<4, 8, TIn, Op>(a, reach);
+  }
+  if (e != hipSuccess || reach == 0) return e;
+  return launch_paths<128, TIn>(a, reach);
+}
+
 hipError_t launch_tree(const TreeArgs& a) {
-  if (a.D == 128) return a.bf16 ? launch_tree_t<128, bf16_bits>(a) : launch_tree_t<128, float>(a);
-  return a.bf16 ? launch_tree_t<16, bf16_bits>(a) : launch_tree_t<16, float>(a);
+  if (a.D == 128) return a.bf16 ? launch_tree_128<bf16_bits, SplitOp>(a) : launch_tree_128<float, FloatOp>(a);
+  return a.bf16 ? launch_paths<16, bf16_bits>(a, 0) : launch_paths<16, float>(a, 0);
 }
 
 // ---- commit of a path -------------------------------------------------------------
