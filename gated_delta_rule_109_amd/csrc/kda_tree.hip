@@ -18,12 +18,52 @@ namespace kda {
 
 constexpr int kMaxNodes = KDA_TREE_MAX_NODES;
 
+// Lane rotations and broadcasts inside rows of 16 lanes, as operand modifiers
+// of vector instructions (no LDS crossbar, which all waves of a CU share).
+template <int kCtrl>
+__device__ __forceinline__ float row_dpp(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), kCtrl, 0xF, 0xF, true));
+}
+template <int R> __device__ __forceinline__ float row_ror(float x) { return row_dpp<0x120 + R>(x); }
+template <int L> __device__ __forceinline__ float row_bcast(float x) { return row_dpp<0x150 + L>(x); }
+
 // Sum over the 64 lanes, in every lane.
 __device__ __forceinline__ float wave_sum(float x) {
-  x += lane_xor<1>(x); x += lane_xor<2>(x); x += lane_xor<4>(x);
-  x += lane_xor<8>(x); x += lane_xor<16>(x); x += lane_xor<32>(x);
-  return x;
+  x += row_ror<8>(x); x += row_ror<4>(x); x += row_ror<2>(x); x += row_ror<1>(x);
+  const int b = __builtin_bit_cast(int, x);
+  return (__builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 0)) +
+          __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 16))) +
+         (__builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 32)) +
+          __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 48)));
 }
+
+// Two consecutive elements in one load (p even-aligned), as floats when needed.
+template <typename T> struct Pair;
+template <> struct Pair<bf16_bits> {
+  uint32_t w;
+  __device__ __forceinline__ void load(const bf16_bits* p) { w = *(const uint32_t*)p; }
+  __device__ __forceinline__ float get(int c) const {
+    return __builtin_bit_cast(float, c ? w & 0xffff0000u : w << 16);
+  }
+  static __device__ __forceinline__ void store(bf16_bits* p, float a, float b) {
+    const bf16x4 y = to_bf16x4(f32x4{a, b, 0.f, 0.f});
+    *(uint32_t*)p = __builtin_bit_cast(uint2, y).x;
+  }
+};
+template <> struct Pair<float> {
+  f32x2 w;
+  __device__ __forceinline__ void load(const float* p) { w = *(const f32x2*)p; }
+  __device__ __forceinline__ float get(int c) const { return w[c]; }
+  static __device__ __forceinline__ void store(float* p, float a, float b) { *(f32x2*)p = f32x2{a, b}; }
+};
+
+// One element, with the interface of Pair.
+template <typename T> struct One {
+  T w;
+  __device__ __forceinline__ void load(const T* p) { w = *p; }
+  __device__ __forceinline__ float get(int) const { return Elem<T>::load(&w); }
+  static __device__ __forceinline__ void store(T* p, float a, float) { Elem<T>::store(p, a); }
+};
 
 // Decay of one channel of token row `row` (a row of the [N, T, H] grid).
 __device__ __forceinline__ float load_alpha(const float* g, int gate, size_t row, int D, int c, uint32_t fe_flags,
@@ -316,22 +356,29 @@ struct FloatOp {
 
 __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) < __builtin_inff(); }
 
-// kTB: tiles of 16 nodes; kWaves: 4 or 8.
+// kTB: tiles of 16 nodes; kWaves: 4 or 8. With three or four tiles the three
+// operand planes would leave room for one workgroup per compute unit, which
+// then either loads or computes: q E takes the place of k E once A and U are
+// formed, and the matrices lie over the planes (two workgroups; 64 nodes on 64
+// x 32 heads: FIGURE). With one or two tiles all lie side by side and two
+// barriers are saved.
 template <int kTB, int kWaves, typename Op>
 struct TileLds {
   static constexpr int kT = 16 * kTB;
+  static constexpr bool kTwo = kTB >= 3;
   static constexpr int kStride = kT + 4;                 // row of A or B, elements
   static constexpr size_t kRows = (size_t)kT * Op::kRowBytes;
   static constexpr size_t kMat = (size_t)kT * kStride * 4;
   static constexpr size_t kE = (size_t)kT * 128 * 4;
   static constexpr size_t kDiag = (size_t)kTB * 16 * 20 * 4;
-  // E lies under A, B, the diagonal blocks and their inverses, which come later
   static constexpr size_t kTail = 2 * kMat + 2 * kDiag > kE ? 2 * kMat + 2 * kDiag : kE;
-  static constexpr size_t kBytes = 3 * kRows + kTail;
+  static constexpr size_t kTailAt = kTwo ? 0 : 3 * kRows;   // E, then A, B, diagonal blocks and inverses
+  static constexpr size_t kBytes = kTwo ? 2 * kRows : 3 * kRows + kTail;
+  static_assert(!kTwo || kTail <= 2 * kRows, "matrices lie inside the planes");
 };
 
 template <int kTB, int kWaves, typename TIn, typename Op>
-__global__ __launch_bounds__(64 * kWaves) void tree_tile_kernel(
+__global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
     const TIn* __restrict__ q, const TIn* __restrict__ k, const TIn* __restrict__ v,
     const float* __restrict__ g, const float* __restrict__ beta, const float* __restrict__ state,
     const int32_t* __restrict__ parents, const int32_t* __restrict__ num_nodes, TIn* __restrict__ o, int H,
@@ -346,11 +393,11 @@ __global__ __launch_bounds__(64 * kWaves) void tree_tile_kernel(
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
   const int lr = lane % 16, lg = lane / 16;              // operand row / column, lane group
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  char* s_ke = lds;                                      // k E, q E, k / E: [kT] rows each
-  char* s_qe = s_ke + L::kRows;
-  char* s_kq = s_qe + L::kRows;
-  float* s_E = (float*)(s_kq + L::kRows);                // [kT][128]
-  char* s_A = s_kq + L::kRows;                           // -beta A
+  char* s_ke = lds;                                      // planes: k E, k / E, q E, [kT] rows each
+  char* s_kq = s_ke + L::kRows;
+  char* s_qe = L::kTwo ? s_ke : s_kq + L::kRows;
+  float* s_E = (float*)(lds + L::kTailAt);               // [kT][128]
+  char* s_A = lds + L::kTailAt;                          // -beta A
   char* s_B = s_A + L::kMat;
   float* s_diag = (float*)(s_B + L::kMat);               // [kTB][16][20] diagonal blocks of -beta A
   char* s_inv = (char*)s_diag + L::kDiag;                // [kTB] 16 rows of stride 20
@@ -362,35 +409,44 @@ __global__ __launch_bounds__(64 * kWaves) void tree_tile_kernel(
   const int parent = lane < nt ? clean_parent(parents, (size_t)n * T, lane) : -1;
   const float braw = beta[row(min(lane, nt - 1))];
   // this wave's nodes: wave + kWaves x, two channels per lane
-  float tk[kRowsPerWave][2], tq[kRowsPerWave][2], te[kRowsPerWave][2];
+  Pair<TIn> lk[kRowsPerWave], lq[kRowsPerWave];
+  float te[kRowsPerWave][2];
 #pragma unroll
   for (int x = 0; x < kRowsPerWave; ++x) {
     const size_t r = row(min(wave + kWaves * x, nt - 1));
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      tk[x][c] = Elem<TIn>::load(k + r * D + 2 * lane + c);
-      tq[x][c] = Elem<TIn>::load(q + r * D + 2 * lane + c);
-      te[x][c] = gate == KDA_GATE_NONE ? 0.f : g[gate == KDA_GATE_CHANNEL ? r * D + 2 * lane + c : r];
+    lk[x].load(k + r * D + 2 * lane);
+    lq[x].load(q + r * D + 2 * lane);
+    if (gate == KDA_GATE_CHANNEL) {
+      const f32x2 e = *(const f32x2*)(g + r * D + 2 * lane);
+      te[x][0] = e[0];
+      te[x][1] = e[1];
+    } else {
+      te[x][0] = te[x][1] = gate == KDA_GATE_HEAD ? g[r] : 0.f;
     }
   }
   // S in operand layout: rows 32 ks + 8 lg + j, columns col0 + kNT lr + {0 ..}
   const int col0 = wave * 16 * kNT;
-  const float* S = state + (size_t)blockIdx.x * D * D + col0 + kNT * lr;
+  // (a uniform base and one 32-bit lane offset: no 64-bit address per load)
+  const uint32_t lane_off = (uint32_t)(8 * lg * D + kNT * lr) * 4;
   float sreg[4][8][kNT];
 #pragma unroll
-  for (int ks = 0; ks < 4; ++ks)
+  for (int ks = 0; ks < 4; ++ks) {
+    const char* base = (const char*)(state + (size_t)blockIdx.x * D * D + col0 + 32 * ks * D) + lane_off;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
-      for (int c = 0; c < kNT; ++c) sreg[ks][j][c] = S[(32 * ks + 8 * lg + j) * D + c];
-  TIn vreg[kTB][4][kNT];
+      for (int c = 0; c < kNT; ++c) sreg[ks][j][c] = ((const float*)base)[j * D + c];
+  }
+  using Cols = std::conditional_t<kNT == 2, Pair<TIn>, One<TIn>>;
+  Cols vreg[kTB][4];
+  auto load_v = [&]() __attribute__((always_inline)) {
 #pragma unroll
-  for (int I = 0; I < kTB; ++I)
+    for (int I = 0; I < kTB; ++I)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int c = 0; c < kNT; ++c)
-        vreg[I][r][c] = v[row(min(16 * I + 4 * lg + r, nt - 1)) * D + col0 + kNT * lr + c];
+      for (int r = 0; r < 4; ++r)
+        vreg[I][r].load(v + row(min(16 * I + 4 * lg + r, nt - 1)) * D + col0 + kNT * lr);
+  };
+  if constexpr (!L::kTwo) load_v();
 
   // the tree: ancestors, and whether this kernel takes it
   const uint64_t anc = ancestors(parent, lane);
@@ -402,23 +458,36 @@ __global__ __launch_bounds__(64 * kWaves) void tree_tile_kernel(
   }
   // decays, normalised rows
   const float alpha_min = __builtin_amdgcn_exp2f(g_min * kLog2e);
+  if (gate == KDA_GATE_NONE) {
 #pragma unroll
-  for (int x = 0; x < kRowsPerWave; ++x) {
-    const int i = wave + kWaves * x;
+    for (int x = 0; x < kRowsPerWave; ++x) te[x][0] = te[x][1] = 1.f;
+  } else if (fe_flags & KDA_FE_GATE_LOGITS) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const float a = gate == KDA_GATE_NONE              ? 1.f
-                      : fe_flags & KDA_FE_GATE_LOGITS ? gate_alpha_logit(te[x][c], alpha_min)
-                                                      : gate_alpha(te[x][c], g_min);
-      te[x][c] = i < nt ? a : 1.f;
-      if (i >= nt) tk[x][c] = tq[x][c] = 0.f;
-    }
-    if (fe_flags & KDA_FE_L2NORM_QK) {
-      const float rk = inv_norm(wave_sum(tk[x][0] * tk[x][0] + tk[x][1] * tk[x][1]), fe_eps);
-      const float rq = inv_norm(wave_sum(tq[x][0] * tq[x][0] + tq[x][1] * tq[x][1]), fe_eps);
-      if (i < nt) { tk[x][0] *= rk; tk[x][1] *= rk; tq[x][0] *= rq; tq[x][1] *= rq; }
-    }
+    for (int x = 0; x < kRowsPerWave; ++x)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) te[x][c] = gate_alpha_logit(te[x][c], alpha_min);
+  } else {
+#pragma unroll
+    for (int x = 0; x < kRowsPerWave; ++x)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) te[x][c] = gate_alpha(te[x][c], g_min);
   }
+  // scales of k and q: 1, the inverse norms, or 0 for rows past the last node
+  float rk[kRowsPerWave], rq[kRowsPerWave];
+#pragma unroll
+  for (int x = 0; x < kRowsPerWave; ++x) rk[x] = rq[x] = 1.f;
+  if (fe_flags & KDA_FE_L2NORM_QK) {
+#pragma unroll
+    for (int x = 0; x < kRowsPerWave; ++x) {
+      rk[x] = wave_sum(lk[x].get(0) * lk[x].get(0) + lk[x].get(1) * lk[x].get(1));
+      rq[x] = wave_sum(lq[x].get(0) * lq[x].get(0) + lq[x].get(1) * lq[x].get(1));
+    }
+#pragma unroll
+    for (int x = 0; x < kRowsPerWave; ++x) { rk[x] = inv_norm(rk[x], fe_eps); rq[x] = inv_norm(rq[x], fe_eps); }
+  }
+#pragma unroll
+  for (int x = 0; x < kRowsPerWave; ++x)
+    if (wave + kWaves * x >= nt) te[x][0] = te[x][1] = 1.f, rk[x] = rq[x] = 0.f;
   // E by doubling: after r rounds the product over the last 2^r nodes of the path
   if (gate != KDA_GATE_NONE)
     for (int jump = parent; __ballot(jump >= 0);) {
@@ -426,135 +495,194 @@ __global__ __launch_bounds__(64 * kWaves) void tree_tile_kernel(
       for (int x = 0; x < kRowsPerWave; ++x)
         *(f32x2*)(s_E + (wave + kWaves * x) * D + 2 * lane) = f32x2{te[x][0], te[x][1]};
       lds_barrier();
+      f32x2 e[kRowsPerWave];
+      int p[kRowsPerWave];
 #pragma unroll
       for (int x = 0; x < kRowsPerWave; ++x) {
-        const int p = __builtin_amdgcn_readlane(jump, wave + kWaves * x);
-        if (p >= 0) {
-          const f32x2 e = *(const f32x2*)(s_E + p * D + 2 * lane);
-          te[x][0] *= e[0];
-          te[x][1] *= e[1];
-        }
+        p[x] = __builtin_amdgcn_readlane(jump, wave + kWaves * x);
+        e[x] = *(const f32x2*)(s_E + max(p[x], 0) * D + 2 * lane);
+      }
+      __builtin_amdgcn_sched_barrier(0);   // all reads in flight before the first is waited for
+#pragma unroll
+      for (int x = 0; x < kRowsPerWave; ++x) {
+        te[x][0] *= p[x] >= 0 ? e[x][0] : 1.f;
+        te[x][1] *= p[x] >= 0 ? e[x][1] : 1.f;
       }
       const int next = __shfl(jump, max(jump, 0));
       jump = jump >= 0 ? next : -1;
       lds_barrier();
     }
+  auto put_q = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int x = 0; x < kRowsPerWave; ++x)
+      Op::put2(s_qe + (wave + kWaves * x) * Op::kRowBytes, lane, lq[x].get(0) * rq[x] * te[x][0],
+               lq[x].get(1) * rq[x] * te[x][1]);
+  };
 #pragma unroll
   for (int x = 0; x < kRowsPerWave; ++x) {
     const int i = wave + kWaves * x;
-    const float e0 = te[x][0], e1 = te[x][1];
-    Op::put2(s_ke + i * Op::kRowBytes, lane, tk[x][0] * e0, tk[x][1] * e1);
-    Op::put2(s_qe + i * Op::kRowBytes, lane, tq[x][0] * e0, tq[x][1] * e1);
-    Op::put2(s_kq + i * Op::kRowBytes, lane, tk[x][0] * __builtin_amdgcn_rcpf(e0), tk[x][1] * __builtin_amdgcn_rcpf(e1));
+    const float e0 = te[x][0], e1 = te[x][1], k0 = lk[x].get(0) * rk[x], k1 = lk[x].get(1) * rk[x];
+    Op::put2(s_ke + i * Op::kRowBytes, lane, k0 * e0, k1 * e1);
+    Op::put2(s_kq + i * Op::kRowBytes, lane, k0 * __builtin_amdgcn_rcpf(e0), k1 * __builtin_amdgcn_rcpf(e1));
   }
+  if constexpr (!L::kTwo) put_q();
   lds_barrier();
 
-  // A and B: tiles (I, J <= I) of either, shared out over the waves
+  // U = (k E) S and W = (q E) S; A and B by tiles (I, J <= I), shared out over
+  // the waves. Units of tiles: A and B alternate, or (kTwo) A's, then B's.
   constexpr int kPairs = kTB * (kTB + 1) / 2;
-  f32x4 mat[(2 * kPairs + kWaves - 1) / kWaves];
-  static_for<0, (2 * kPairs + kWaves - 1) / kWaves>([&](auto X) __attribute__((always_inline)) {
-    constexpr int x = decltype(X)::value;
-    const int unit = wave + kWaves * x;
-    mat[x] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (unit < 2 * kPairs) {
-      const int pair = unit >> 1;
-      int I = 0;
-      while ((I + 1) * (I + 2) / 2 <= pair) ++I;
-      const int J = pair - I * (I + 1) / 2;
-      const char* rows = unit & 1 ? s_qe : s_ke;
+  constexpr int kTurns = L::kTwo ? (kPairs + kWaves - 1) / kWaves : (2 * kPairs + kWaves - 1) / kWaves;
+  constexpr int kSets = L::kTwo ? 2 : 1;
+  f32x4 mat[kSets][kTurns];
+  auto tile_of = [&](int set, int turn, bool& is_b, int& I, int& J) __attribute__((always_inline)) {
+    const int unit = wave + kWaves * turn, pair = L::kTwo ? unit : unit >> 1;
+    is_b = L::kTwo ? set == 1 : unit & 1;
+    I = (pair >= 1) + (pair >= 3) + (pair >= 6);
+    J = pair - I * (I + 1) / 2;
+    return pair < kPairs;
+  };
+  auto tiles = [&](auto Set) __attribute__((always_inline)) {
+    constexpr int set = decltype(Set)::value;
+    static_for<0, kTurns>([&](auto X) __attribute__((always_inline)) {
+      constexpr int x = decltype(X)::value;
+      f32x4 y = {0.f, 0.f, 0.f, 0.f};
+      bool is_b;
+      int I, J;
+      if (tile_of(set, x, is_b, I, J)) {
+        const char* rows = is_b ? s_qe : s_ke;
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        mat[x] = Op::mma(Op::get8(rows + (16 * I + lr) * Op::kRowBytes, 32 * ks + 8 * lg),
-                         Op::get8(s_kq + (16 * J + lr) * Op::kRowBytes, 32 * ks + 8 * lg), mat[x]);
-    }
-  });
-  // U and W
+        for (int ks = 0; ks < 4; ++ks)
+          y = Op::mma(Op::get8(rows + (16 * I + lr) * Op::kRowBytes, 32 * ks + 8 * lg),
+                      Op::get8(s_kq + (16 * J + lr) * Op::kRowBytes, 32 * ks + 8 * lg), y);
+      }
+      mat[set][x] = y;
+    });
+  };
   f32x4 U[kTB][kNT], W[kTB][kNT];
 #pragma unroll
   for (int I = 0; I < kTB; ++I)
 #pragma unroll
     for (int c = 0; c < kNT; ++c) U[I][c] = W[I][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto times_s = [&](bool u, bool w) __attribute__((always_inline)) {
 #pragma unroll
-  for (int ks = 0; ks < 4; ++ks) {
-    typename Op::F8 sf[kNT];
-#pragma unroll
-    for (int c = 0; c < kNT; ++c) {
-      float x[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = sreg[ks][j][c];
-      sf[c] = Op::make8(x);
-    }
-#pragma unroll
-    for (int I = 0; I < kTB; ++I) {
-      const typename Op::F8 a = Op::get8(s_ke + (16 * I + lr) * Op::kRowBytes, 32 * ks + 8 * lg);
-      const typename Op::F8 b = Op::get8(s_qe + (16 * I + lr) * Op::kRowBytes, 32 * ks + 8 * lg);
+    for (int ks = 0; ks < 4; ++ks) {
+      typename Op::F8 sf[kNT];
 #pragma unroll
       for (int c = 0; c < kNT; ++c) {
-        U[I][c] = Op::mma(a, sf[c], U[I][c]);
-        W[I][c] = Op::mma(b, sf[c], W[I][c]);
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = sreg[ks][j][c];
+        sf[c] = Op::make8(x);
+      }
+#pragma unroll
+      for (int I = 0; I < kTB; ++I) {
+        if (u) {
+          const typename Op::F8 a = Op::get8(s_ke + (16 * I + lr) * Op::kRowBytes, 32 * ks + 8 * lg);
+#pragma unroll
+          for (int c = 0; c < kNT; ++c) U[I][c] = Op::mma(a, sf[c], U[I][c]);
+        }
+        if (w) {
+          const typename Op::F8 a = Op::get8(s_qe + (16 * I + lr) * Op::kRowBytes, 32 * ks + 8 * lg);
+#pragma unroll
+          for (int c = 0; c < kNT; ++c) W[I][c] = Op::mma(a, sf[c], W[I][c]);
+        }
       }
     }
+  };
+  tiles(std::integral_constant<int, 0>{});
+  if constexpr (L::kTwo) {
+    times_s(true, false);
+    lds_barrier();
+    put_q();
+    lds_barrier();
+    tiles(std::integral_constant<int, 1>{});
+    times_s(false, true);
+    load_v();                              // (no registers to spare for it before)
+    lds_barrier();
+  } else {
+    times_s(true, true);
   }
-  // masked A and B to LDS (over E, which nobody reads any more)
-  static_for<0, (2 * kPairs + kWaves - 1) / kWaves>([&](auto X) __attribute__((always_inline)) {
-    constexpr int x = decltype(X)::value;
-    const int unit = wave + kWaves * x;
-    if (unit < 2 * kPairs) {
-      const int pair = unit >> 1;
-      int I = 0;
-      while ((I + 1) * (I + 2) / 2 <= pair) ++I;
-      const int J = pair - I * (I + 1) / 2;
-      const bool is_b = unit & 1;
+  // masked A and B to LDS (over E, or over the planes)
+  static_for<0, kSets * kTurns>([&](auto X) __attribute__((always_inline)) {
+    constexpr int set = decltype(X)::value / kTurns, x = decltype(X)::value % kTurns;
+    bool is_b;
+    int I, J;
+    if (tile_of(set, x, is_b, I, J)) {
+      const int j = 16 * J + lr;
+      f32x4 y;
+      bool odd = false;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = 16 * I + 4 * lg + r, j = 16 * J + lr;
+        const int i = 16 * I + 4 * lg + r;
         const bool on = (s_anc[i] >> j & 1) && (is_b || i != j);
-        float y = is_b ? mat[x][r] : -s_b[i] * mat[x][r];
-        y = on ? y : 0.f;
-        if (!is_finite(y)) {
-          atomicOr(&s_bad[is_b], 1ull << i);
-          y = 0.f;
-        }
-        Op::put1(is_b ? s_B : s_A, L::kStride, i, j, y);
-        if (!is_b && I == J) s_diag[(I * 16 + 4 * lg + r) * 20 + lr] = y;
+        y[r] = on ? (is_b ? mat[set][x][r] : -s_b[i] * mat[set][x][r]) : 0.f;
+        odd |= !is_finite(y[r]);
+      }
+      if (__ballot(odd)) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (!is_finite(y[r])) {
+            atomicOr(&s_bad[is_b], 1ull << (16 * I + 4 * lg + r));
+            y[r] = 0.f;
+          }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        Op::put1(is_b ? s_B : s_A, L::kStride, 16 * I + 4 * lg + r, j, y[r]);
+        if (!is_b && I == J) s_diag[(16 * I + 4 * lg + r) * 20 + lr] = y[r];
       }
     }
   });
   lds_barrier();
 
-  // inverses of I + beta A on the diagonal, lane (block lg, column lr):
-  // x_i = (i == column) + sum_j (-beta A)_ij x_j
-  if (wave == 0 && lg < kTB) {
-    float x[16];
-    const float* m = s_diag + lg * 16 * 20;
-    static_for<0, 16>([&](auto I) __attribute__((always_inline)) {
-      constexpr int i = decltype(I)::value;
-      f32x4 part = {i == lr ? 1.f : 0.f, 0.f, 0.f, 0.f};
-      static_for<0, (i + 3) / 4>([&](auto J) __attribute__((always_inline)) {
-        constexpr int j4 = decltype(J)::value;
-        const f32x4 a = *(const f32x4*)(m + i * 20 + 4 * j4);
-        static_for<0, 4>([&](auto R) __attribute__((always_inline)) {
-          constexpr int j = 4 * j4 + decltype(R)::value;
-          if constexpr (j < i) part[j % 4] += a[j % 4] * x[j];
-        });
+  // Inverses X of I + beta A = I - N on the diagonal blocks, row lr of block lg
+  // in lane (lg, lr), last column first: X = I + X N, so
+  // x_j = (j == lr) + sum_{i > j} x_i N_ij, with N_ij broadcast from lane j of
+  // its row of lanes. (Substitution: powers of N would lose digits where keys repeat.)
+  f32x4 inv = {0.f, 0.f, 0.f, 0.f};                       // kTB = 1: X[lr][4 lg ..]
+  if (kTB == 1 || wave == 0) {
+    const float* m = s_diag + (kTB == 1 ? 0 : min(lg, kTB - 1)) * 16 * 20 + lr;
+    float nr[16], x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) nr[i] = m[i * 20];
+    static_for<0, 16>([&](auto JJ) __attribute__((always_inline)) {
+      constexpr int j = 15 - decltype(JJ)::value;
+      float s0 = j == lr ? 1.f : 0.f, s1 = 0.f;
+      static_for<j + 1, 16>([&](auto I) __attribute__((always_inline)) {
+        constexpr int i = decltype(I)::value;
+        // the newest x last, so that it is waited for last
+        if constexpr ((i - j) % 2) s1 += row_bcast<j>(nr[16 + j - i]) * x[16 + j - i];
+        else s0 += row_bcast<j>(nr[16 + j - i]) * x[16 + j - i];
       });
-      x[i] = (part[0] + part[1]) + (part[2] + part[3]);
-      Op::put1(s_inv, 20, 16 * lg + i, lr, x[i]);
+      x[j] = s0 + s1;
+      // formed here: the compiler would move the sums to their use and leave all
+      // 120 broadcasts in registers until then
+      asm volatile("" : "+v"(x[j]));
     });
+    if constexpr (kTB == 1) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        inv[r] = lg < 2 ? (lg == 0 ? x[r] : x[4 + r]) : (lg == 2 ? x[8 + r] : x[12 + r]);
+    } else if (lg < kTB) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) Op::put1(s_inv, 20, 16 * lg + lr, j, x[j]);
+    }
   }
-  lds_barrier();
+  if constexpr (kTB > 1) lds_barrier();
 
   // d and o, block by block; bit 16 I + 4 lg + r of bad[c]: that row of the
   // lane's column is not finite
   typename Op::F4 d[kTB][kNT];
   uint64_t bad[kNT] = {};
   auto clean = [&](f32x4& x, int I, int c) __attribute__((always_inline)) {
+    if (__ballot(!(is_finite(x[0]) && is_finite(x[1]) && is_finite(x[2]) && is_finite(x[3])))) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (!is_finite(x[r])) {
-        bad[c] |= 1ull << (16 * I + 4 * lg + r);
-        x[r] = 0.f;
-      }
+      for (int r = 0; r < 4; ++r)
+        if (!is_finite(x[r])) {
+          bad[c] |= 1ull << (16 * I + 4 * lg + r);
+          x[r] = 0.f;
+        }
+    }
   };
 #pragma unroll
   for (int I = 0; I < kTB; ++I) {
@@ -565,13 +693,16 @@ __global__ __launch_bounds__(64 * kWaves) void tree_tile_kernel(
         f32x4 x;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          x[r] = 16 * I + 4 * lg + r < nt ? b4[r] * (Elem<TIn>::load(&vreg[I][r][c]) - U[I][c][r]) : 0.f;
+          x[r] = 16 * I + 4 * lg + r < nt ? b4[r] * (vreg[I][r].get(c) - U[I][c][r]) : 0.f;
 #pragma unroll
         for (int J = 0; J < I; ++J)
           x = Op::mma(Op::get4(s_A, L::kStride, 16 * I + lr, 16 * J + 4 * lg), d[J][c], x);
         clean(x, I, c);
         f32x4 y = {0.f, 0.f, 0.f, 0.f};
-        y = Op::mma(Op::get4(s_inv, 20, 16 * I + lr, 4 * lg), Op::make4(x), y);
+        typename Op::F4 a;
+        if constexpr (kTB == 1) a = Op::make4(inv);
+        else a = Op::get4(s_inv, 20, 16 * I + lr, 4 * lg);
+        y = Op::mma(a, Op::make4(x), y);
         clean(y, I, c);
         d[I][c] = Op::make4(y);
       }
@@ -602,12 +733,13 @@ __global__ __launch_bounds__(64 * kWaves) void tree_tile_kernel(
       for (int r = 0; r < 4; ++r) {
         const int i = 16 * I + 4 * lg + r;
         if (i < nt) {
+          float y[kNT];
 #pragma unroll
           for (int c = 0; c < kNT; ++c) {
-            float y = scale * W[I][c][r];
-            if (any && ((s_anc[i] & bad[c]) || (bad_o >> i & 1))) y = __builtin_nanf("");
-            Elem<TIn>::store(o + row(i) * D + col0 + kNT * lr + c, y);
+            y[c] = scale * W[I][c][r];
+            if (any && ((s_anc[i] & bad[c]) || (bad_o >> i & 1))) y[c] = __builtin_nanf("");
           }
+          Cols::store(o + row(i) * D + col0 + kNT * lr, y[0], y[kNT - 1]);
         }
       }
     }

@@ -148,7 +148,7 @@ def _expect(t, name, shape, dtype):
     before any call."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:      # torch.Size compares as the tuple it is
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -330,23 +330,33 @@ def decode_tokens(q, k, v, g, beta, state, accept=None, scale=1.0, g_min=LN_HALF
 # ---- one speculative step over trees of drafted tokens ---------------------------
 
 def _check_step(*ts):
-    """Every given tensor is contiguous and on one device (the first one's),
-    which becomes the current device if it is not."""
-    _check_dev(*ts)
-    dev = next(t.device for t in ts if t is not None)
+    """Every given tensor is contiguous and on one device, whose index is
+    returned."""
+    dev = None
     for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one call takes one device")
+        if t is None:
+            continue
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("tensors must be contiguous device tensors")
+        if dev is None:
+            dev = t.get_device()
+        elif t.get_device() != dev:
+            raise ValueError(f"tensors on devices {dev} and {t.get_device()}: one call takes one device")
     return dev
 
 
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def _call(dev, where, fn, *args):
-    """fn(*args, stream) with dev current and its current stream."""
-    if torch.cuda.current_device() != dev.index:
+    """fn(*args, stream) on device dev's current stream, with dev current. These
+    calls take microseconds, so the stream's handle is read without building
+    a torch.cuda.Stream around it (2.2 us of a call's 13)."""
+    if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
-            st = fn(*args, _stream(dev))
-    else:
-        st = fn(*args, _stream(dev))
+            return _call(dev, where, fn, *args)
+    st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st != KDA_OK:
         raise KdaError(st, where)
 
@@ -368,8 +378,8 @@ def decode_tree(q, k, v, g, beta, state, parents=None, num_nodes=None, scale=1.0
     dev = _check_step(q, k, v, g, beta, state, parents, num_nodes, o)
     if o is None:
         o = torch.empty_like(v) if num_nodes is None else torch.zeros_like(v)
-    _call(dev, "kda_decode_tree", lib().kda_decode_tree, _ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(g),
-          _ptr(beta), _ptr(state), _ptr(parents), _ptr(num_nodes), _ptr(o), N, T, H, D, v.shape[3], float(scale),
+    _call(dev, "kda_decode_tree", lib().kda_decode_tree, _addr(q), _addr(k), _addr(v), _dtype_code(q), _addr(g),
+          _addr(beta), _addr(state), _addr(parents), _addr(num_nodes), _addr(o), N, T, H, D, v.shape[3], float(scale),
           float(g_min), _opt_ptr(options))
     return o
 
@@ -386,8 +396,8 @@ def commit_path(k, v, g, beta, state, path, accept, g_min=LN_HALF, options: Opti
     if path is None or accept is None:
         raise ValueError("path and accept are required")
     dev = _check_step(k, v, g, beta, state, path, accept)
-    _call(dev, "kda_commit_path", lib().kda_commit_path, _ptr(k), _ptr(v), _dtype_code(k), _ptr(g), _ptr(beta),
-          _ptr(state), _ptr(path), _ptr(accept), N, T, H, D, v.shape[3], float(g_min), _opt_ptr(options))
+    _call(dev, "kda_commit_path", lib().kda_commit_path, _addr(k), _addr(v), _dtype_code(k), _addr(g), _addr(beta),
+          _addr(state), _addr(path), _addr(accept), N, T, H, D, v.shape[3], float(g_min), _opt_ptr(options))
     return state
 
 
@@ -425,16 +435,16 @@ def verify_drafts(target, draft, tokens, uniforms, parents=None, num_nodes=None,
         raise TypeError(f"workspace: expected torch.uint8, got {workspace.dtype}")
     dev = _check_step(target, draft, tokens, uniforms, parents, num_nodes, workspace, accept, path, next_token)
     if workspace is None:
-        workspace = verify_workspace(N, T, V, dev)
+        workspace = verify_workspace(N, T, V, target.device)
     if accept is None:
-        accept = torch.empty(N, dtype=torch.int32, device=dev)
+        accept = tokens.new_empty(N)
     if path is None:
-        path = torch.empty(N, T, dtype=torch.int32, device=dev)
+        path = torch.empty_like(tokens)
     if next_token is None:
-        next_token = torch.empty(N, dtype=torch.int32, device=dev)
-    _call(dev, "kda_verify_drafts", lib().kda_verify_drafts, _ptr(target), _ptr(draft), code, _ptr(tokens),
-          _ptr(parents), _ptr(num_nodes), _ptr(uniforms), _ptr(accept), _ptr(path), _ptr(next_token), N, T, V,
-          _ptr(workspace), workspace.numel())
+        next_token = tokens.new_empty(N)
+    _call(dev, "kda_verify_drafts", lib().kda_verify_drafts, _addr(target), _addr(draft), code, _addr(tokens),
+          _addr(parents), _addr(num_nodes), _addr(uniforms), _addr(accept), _addr(path), _addr(next_token), N, T, V,
+          _addr(workspace), workspace.numel())
     return accept, path, next_token
 
 
@@ -475,9 +485,9 @@ def _cache_call(where, fn, first, cache: StateCache, slots, states):
     if S >= 2 ** 31:
         raise ValueError(f"num_slots: {S} is above INT32_MAX")
     if first == "states":
-        args = (_ptr(states), _ptr(slots), _ptr(cache.values), _ptr(cache.scales))
+        args = (_addr(states), _addr(slots), _addr(cache.values), _addr(cache.scales))
     else:
-        args = (_ptr(cache.values), _ptr(cache.scales), _ptr(slots), _ptr(states))
+        args = (_addr(cache.values), _addr(cache.scales), _addr(slots), _addr(states))
     _call(dev, where, fn, *args, cache.format, N, S, H, D, D)
 
 
