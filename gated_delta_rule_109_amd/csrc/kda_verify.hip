@@ -37,8 +37,9 @@ struct VerifyPlan {
 };
 
 // (V <= KDA_VERIFY_MAX_VOCAB, so element indices of a row stay far inside 32 bits.)
-// At most 64 chunks (one lane each when they are joined), of 4096 elements or
-// more; of 1024 or more where there are too few sequences to fill the GPU.
+// A chunk is one wave's work. At most 64 of them (a lane each when they are
+// joined), of 4096 elements or more, or of 1024 where there are too few
+// sequences to fill the GPU otherwise.
 VerifyPlan verify_plan(int32_t N, int32_t V) {
   VerifyPlan p;
   const int least = N >= 64 ? 4096 : 1024;
@@ -56,7 +57,10 @@ VerifyPlan verify_plan(int32_t N, int32_t V) {
 template <typename T>
 __device__ __forceinline__ double weight(T raw) {
   const float x = Elem<T>::load(&raw);
-  return x > 0.f && x < __builtin_inff() ? (double)x : 0.0;
+  constexpr int kPositive = 1 << 7 | 1 << 8;            // classes: subnormal and normal above 0
+  float y = __builtin_amdgcn_classf(x, kPositive) ? x : 0.f;
+  asm("" : "+v"(y));             // selected in 32 bits, not after the conversion in 64
+  return (double)y;
 }
 
 __device__ __forceinline__ double lane_xor64(double x, int m) { return __shfl_xor(x, m); }
@@ -178,36 +182,62 @@ __device__ __forceinline__ void load_group(const T* row, int first, int a, int b
   }
 }
 
-// f(element, p, q) for the elements of [a, b) that fall to this thread (and,
-// with weights 0, for some outside); q = NULL reads as 0.
-template <typename T, typename F>
+// f(element, p, q) for the elements of [a, b) that fall to thread tid of
+// `threads` (kQ = false: q is 0). Aligned groups run kUnroll at a time with
+// all their loads in flight; a group past the end is loaded again from the last one with
+// its values dropped, so there is no branch between the loads.
+template <bool kQ, int kUnroll = 4, typename T, typename F>
 __device__ __forceinline__ void for_range(const T* p, const T* q, int a, int b, int tid, int threads, F&& f) {
-  const int begin = a - skew(p + a);
-  const int groups = (b - begin + kPer<T> - 1) / kPer<T>;
-  for (int i = tid; i < groups; i += threads) {
-    double x[kPer<T>], y[kPer<T>] = {};
-    const int first = begin + i * kPer<T>;
-    load_group<T>(p, first, a, b, x);
-    if (q) load_group<T>(q, first, a, b, y);
+  const int head = min((kPer<T> - skew(p + a)) % kPer<T>, b - a);
+  const int groups = (b - a - head) / kPer<T>;
+  const T *pg = p + a + head, *qg = kQ ? q + a + head : nullptr;
+  for (int base = 0; base < groups; base += threads * kUnroll) {
+    const int i = base + tid;
+    u32x4 x[kUnroll], y[kUnroll];
 #pragma unroll
-    for (int j = 0; j < kPer<T>; ++j) f(first + j, x[j], y[j]);
+    for (int k = 0; k < kUnroll; ++k) {
+      const int at = min(i + k * threads, groups - 1);
+      x[k] = *(const u32x4*)(pg + at * kPer<T>);
+      if (kQ) y[k] = *(const u32x4*)(qg + at * kPer<T>);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const bool on = i + k * threads < groups;
+      if (!on) x[k] = u32x4{0, 0, 0, 0};
+      T u[kPer<T>], w[kPer<T>];
+      *(u32x4*)u = x[k];
+      if (kQ) *(u32x4*)w = y[k];
+#pragma unroll
+      for (int j = 0; j < kPer<T>; ++j)
+        f(a + head + (i + k * threads) * kPer<T> + j, weight<T>(u[j]), kQ ? weight<T>(w[j]) : 0.0);
+    }
   }
+  const int tail = a + head + groups * kPer<T>;
+  const int x = tid < head ? a + tid : tail + (tid - head);     // fewer than 2 kPer, all in one turn
+  double wp = 0.0, wq = 0.0;
+  if (x < b && tid < 2 * kPer<T>) {
+    wp = weight<T>(p[x]);
+    if (kQ) wq = weight<T>(q[x]);
+  }
+  f(x, wp, wq);
 }
 
 // The rejected tokens of the last node without draft rows: the tokens of its
-// children (had one been accepted, it would be the last node).
+// children (had one been accepted, it would be the last node). Lane t: node
+// t's token, or -1.
+__device__ __forceinline__ int gone_token(const int32_t* tokens, const int32_t* parents, size_t n, int T, int nt,
+                                          int cur, int lane) {
+  if (lane <= cur || lane >= nt) return -1;
+  const size_t at = n * T + lane;
+  return (parents ? parents[at] : lane - 1) == cur ? tokens[at] : -1;
+}
 struct Gone {
   int count;
   int token[kWave];
 };
 // Called by one wave; other waves read `gone` after a barrier.
-__device__ __forceinline__ void list_gone(Gone& gone, const int32_t* tokens, const int32_t* parents, size_t n, int T,
-                                          int nt, int cur, int lane) {
-  int x = -1;
-  if (lane > cur && lane < nt) {
-    const size_t at = n * T + lane;
-    if ((parents ? parents[at] : lane - 1) == cur) x = tokens[at];
-  }
+__device__ __forceinline__ void list_gone(Gone& gone, int x, int lane) {
   const uint64_t mask = __ballot(x >= 0);
   if (x >= 0) gone.token[__builtin_popcountll(mask & ((1ull << lane) - 1))] = x;
   if (lane == 0) gone.count = __builtin_popcountll(mask);
@@ -239,8 +269,8 @@ __global__ __launch_bounds__(kWalkThreads) void walk_kernel(
   walk<T>(d, true, nt, lane, cur, count, spent, accepted, [&](int at, double C) {
     const size_t row = ((size_t)n * T_ + at) * (size_t)V;
     double sum = 0.0;
-    for_range<T>(target + row, draft + row, 0, V, tid, kWalkThreads,
-                 [&](int, double p, double q) { sum += residual(p, q, C); });
+    for_range<true, 8>(target + row, draft + row, 0, V, tid, kWalkThreads,
+                       [&](int, double p, double q) { sum += residual(p, q, C); });
     sum = wave_sum(sum);
     // two buffers in turn: a wave may start the next sum while another still
     // reads this one, but not the one after it
@@ -256,8 +286,8 @@ __global__ __launch_bounds__(kWalkThreads) void walk_kernel(
 }
 
 // Partial sums of the last node's r (and of p, for the case that r is 0
-// everywhere) over one chunk. kWalk: no masses are needed (chains, or no draft
-// rows), so every wave walks by itself and the sequence's first workgroup
+// everywhere), one chunk per wave. kWalk: no masses are needed (chains, or no
+// draft rows), so every wave walks by itself, and the sequence's first one
 // writes the results.
 template <typename T, bool kDraft, bool kWalk>
 __global__ __launch_bounds__(256) void sums_kernel(
@@ -266,11 +296,11 @@ __global__ __launch_bounds__(256) void sums_kernel(
     const float* __restrict__ uniforms, int32_t* __restrict__ accept, int32_t* __restrict__ path,
     int32_t* __restrict__ next_token, int T_, int V, int chunk, int chunks, Walk* __restrict__ walks,
     double* __restrict__ sums) {
-  const uint32_t n = blockIdx.x / (uint32_t)chunks;
-  const int part = blockIdx.x % (uint32_t)chunks, tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const uint32_t groups = (uint32_t)(chunks + 3) / 4, n = blockIdx.x / groups;
+  const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int part = (int)(blockIdx.x % groups) * 4 + wave;
+  if (part >= chunks) return;
   const int nt = node_count(num_nodes, n, T_);
-  __shared__ double s_sum[2][4];
-  __shared__ Gone s_gone;
   int cur;
   double spent;
   if constexpr (kWalk) {
@@ -278,33 +308,42 @@ __global__ __launch_bounds__(256) void sums_kernel(
     int count;
     uint64_t accepted;
     walk<T>(d, kDraft, nt, lane, cur, count, spent, accepted, [](int, double) { return 0.0; });
-    if (part == 0 && wave == 0)
-      write_walk(lane, n, T_, nt, cur, count, spent, accepted, accept, path, next_token, walks);
+    if (part == 0) write_walk(lane, n, T_, nt, cur, count, spent, accepted, accept, path, next_token, walks);
   } else {
     cur = walks[n].node;
     spent = walks[n].spent;
   }
   if (nt == 0) return;
-  if constexpr (!kDraft) {
-    if (wave == 0) list_gone(s_gone, tokens, parents, n, T_, nt, cur, lane);
-    __syncthreads();
-  }
   const size_t row = ((size_t)n * T_ + cur) * (size_t)V;
   const int a = part * chunk, b = min(V - a, chunk) + a;
   double rs = 0.0, ps = 0.0;
-  // the row of q matters only after a rejection
-  const T* q = kDraft && spent > 0.0 ? draft + row : nullptr;
-  for_range<T>(target + row, q, a, b, tid, 256, [&](int x, double p, double qv) {
-    if constexpr (kDraft) rs += residual(p, qv, spent);
-    else rs += is_gone(s_gone, x) ? 0.0 : p;
-    ps += p;
-  });
+  if constexpr (kDraft) {
+    // the row of q matters only after a rejection
+    if (spent > 0.0)
+      for_range<true>(target + row, draft + row, a, b, lane, kWave, [&](int, double p, double q) {
+        rs += residual(p, q, spent);
+        ps += p;
+      });
+    else
+      for_range<false>(target + row, (const T*)nullptr, a, b, lane, kWave, [&](int, double p, double) { ps += p; });
+    if (!(spent > 0.0)) rs = ps;
+  } else {
+    const int gone = gone_token(tokens, parents, n, T_, nt, cur, lane);
+    const uint64_t here = __ballot(gone >= a && gone < b);
+    if (here)
+      for_range<false>(target + row, (const T*)nullptr, a, b, lane, kWave, [&](int x, double p, double) {
+        bool out = false;
+        for (uint64_t m = here; m; m &= m - 1) out |= x == __builtin_amdgcn_readlane(gone, __builtin_ctzll(m));
+        rs += out ? 0.0 : p;
+        ps += p;
+      });
+    else
+      for_range<false>(target + row, (const T*)nullptr, a, b, lane, kWave, [&](int, double p, double) { ps += p; });
+    if (!here) rs = ps;
+  }
   rs = wave_sum(rs);
   ps = wave_sum(ps);
-  if (lane == 0) { s_sum[0][wave] = rs; s_sum[1][wave] = ps; }
-  __syncthreads();
-  if (tid < 2)
-    sums[((size_t)n * chunks + part) * 2 + tid] = (s_sum[tid][0] + s_sum[tid][1]) + (s_sum[tid][2] + s_sum[tid][3]);
+  if (lane < 2) sums[((size_t)n * chunks + part) * 2 + lane] = lane ? ps : rs;
 }
 
 // Inclusive sums over the lanes of a wave.
@@ -359,8 +398,7 @@ __global__ __launch_bounds__(256) void choose_kernel(
 
   if constexpr (!kDraft) {
     if (wave == 0) {
-      list_gone(s_gone, tokens, parents, n, T_, nt, cur, lane);
-      if (plain && lane == 0) s_gone.count = 0;
+      list_gone(s_gone, plain ? -1 : gone_token(tokens, parents, n, T_, nt, cur, lane), lane);
     }
   }
   if (tid == 0) s_token = -1;
@@ -431,7 +469,7 @@ hipError_t launch_verify_t(const VerifyArgs& a) {
   Walk* walks = (Walk*)((char*)a.workspace + p.walks);
   double* sums = (double*)((char*)a.workspace + p.sums);
   const T *target = (const T*)a.target, *draft = (const T*)a.draft;
-  const dim3 grid((unsigned)((int64_t)a.N * p.chunks));
+  const dim3 grid((unsigned)((int64_t)a.N * ((p.chunks + 3) / 4)));
 #define KDA_SUMS(DRAFT, WALK)                                                                                       \
   hipLaunchKernelGGL((sums_kernel<T, DRAFT, WALK>), grid, dim3(256), 0, a.stream, target, draft, a.tokens, a.parents, \
                      a.num_nodes, a.uniforms, a.accept, a.path, a.next_token, a.T, a.V, p.chunk, p.chunks, walks,   \

@@ -329,20 +329,37 @@ def decode_tokens(q, k, v, g, beta, state, accept=None, scale=1.0, g_min=LN_HALF
 
 # ---- one speculative step over trees of drafted tokens ---------------------------
 
-def _check_step(*ts):
-    """Every given tensor is contiguous and on one device, whose index is
-    returned."""
-    dev = None
-    for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError("tensors must be contiguous device tensors")
-        if dev is None:
-            dev = t.get_device()
-        elif t.get_device() != dev:
-            raise ValueError(f"tensors on devices {dev} and {t.get_device()}: one call takes one device")
-    return dev
+def _check_step(*specs):
+    """Every given tensor (name, tensor or None, shape, dtype) has its shape and
+    dtype, is contiguous, and all are on one device, whose index is returned.
+    One pass over what is right; the first thing wrong is looked up after it."""
+    dev = next(t for _, t, _, _ in specs if t is not None).get_device()
+    for _, t, shape, dtype in specs:
+        if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()
+                              or t.get_device() != dev):
+            break
+    else:
+        if dev >= 0:
+            return dev
+    for name, t, shape, dtype in specs:
+        _expect(t, name, shape, dtype)
+    _check_dev(*(t for _, t, _, _ in specs))
+    raise ValueError("tensors on more than one device: one call takes one device")
+
+
+def _step_inputs(q, k, v, g, beta, lead, H, D, options):
+    """Specifications of a step's q, k, v, g and beta."""
+    dt = q.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise TypeError(f"q/k/v must be bfloat16 or float32, got {dt}")
+    shape = (*lead, H, D)
+    gshape = _gate_shape(lead, H, D, options)
+    if gshape is None:
+        g = None
+    elif g is None:
+        raise ValueError("g is required by this gate layout")
+    return (("q", q, shape, dt), ("k", k, shape, dt), ("v", v, shape, dt), ("g", g, gshape, torch.float32),
+            ("beta", beta, (*lead, H), torch.float32)), g
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -370,12 +387,10 @@ def decode_tree(q, k, v, g, beta, state, parents=None, num_nodes=None, scale=1.0
     sequence its own number of nodes, whose other rows of o stay as they are.
     Returns o [N,T,H,D]."""
     N, T, H, D = q.shape
-    g = _check_inputs(q, k, v, g, beta, (N, T), H, D, options, (N, T, H))
-    _expect(state, "state", (N, H, D, D), torch.float32)
-    _expect(parents, "parents", (N, T), torch.int32)
-    _expect(num_nodes, "num_nodes", (N,), torch.int32)
-    _expect(o, "o", (N, T, H, D), q.dtype)
-    dev = _check_step(q, k, v, g, beta, state, parents, num_nodes, o)
+    specs, g = _step_inputs(q, k, v, g, beta, (N, T), H, D, options)
+    dev = _check_step(*specs, ("state", state, (N, H, D, D), torch.float32),
+                      ("parents", parents, (N, T), torch.int32), ("num_nodes", num_nodes, (N,), torch.int32),
+                      ("o", o, (N, T, H, D), q.dtype))
     if o is None:
         o = torch.empty_like(v) if num_nodes is None else torch.zeros_like(v)
     _call(dev, "kda_decode_tree", lib().kda_decode_tree, _addr(q), _addr(k), _addr(v), _dtype_code(q), _addr(g),
@@ -389,13 +404,11 @@ def commit_path(k, v, g, beta, state, path, accept, g_min=LN_HALF, options: Opti
     int32 [N,T] and [N], as verify_drafts returns them) on state [N,H,D,D], in
     place; k, v, g, beta and options are those of decode_tree. Returns state."""
     N, T, H, D = k.shape
-    g = _check_inputs(k, k, v, g, beta, (N, T), H, D, options, (N, T, H))
-    _expect(state, "state", (N, H, D, D), torch.float32)
-    _expect(path, "path", (N, T), torch.int32)
-    _expect(accept, "accept", (N,), torch.int32)
     if path is None or accept is None:
         raise ValueError("path and accept are required")
-    dev = _check_step(k, v, g, beta, state, path, accept)
+    specs, g = _step_inputs(k, k, v, g, beta, (N, T), H, D, options)
+    dev = _check_step(*specs[1:], ("state", state, (N, H, D, D), torch.float32), ("path", path, (N, T), torch.int32),
+                      ("accept", accept, (N,), torch.int32))
     _call(dev, "kda_commit_path", lib().kda_commit_path, _addr(k), _addr(v), _dtype_code(k), _addr(g), _addr(beta),
           _addr(state), _addr(path), _addr(accept), N, T, H, D, v.shape[3], float(g_min), _opt_ptr(options))
     return state
@@ -421,19 +434,14 @@ def verify_drafts(target, draft, tokens, uniforms, parents=None, num_nodes=None,
     decode_tokens (chains) and, with path, of commit_path."""
     N, T, V = target.shape
     code = _dtype_code(target)
-    _expect(draft, "draft", (N, T, V), target.dtype)
-    _expect(tokens, "tokens", (N, T), torch.int32)
-    _expect(uniforms, "uniforms", (N, T), torch.float32)
-    _expect(parents, "parents", (N, T), torch.int32)
-    _expect(num_nodes, "num_nodes", (N,), torch.int32)
-    _expect(accept, "accept", (N,), torch.int32)
-    _expect(path, "path", (N, T), torch.int32)
-    _expect(next_token, "next_token", (N,), torch.int32)
     if tokens is None or uniforms is None:
         raise ValueError("tokens and uniforms are required")
-    if workspace is not None and workspace.dtype != torch.uint8:
-        raise TypeError(f"workspace: expected torch.uint8, got {workspace.dtype}")
-    dev = _check_step(target, draft, tokens, uniforms, parents, num_nodes, workspace, accept, path, next_token)
+    i32 = torch.int32
+    dev = _check_step(("target", target, (N, T, V), target.dtype), ("draft", draft, (N, T, V), target.dtype),
+                      ("tokens", tokens, (N, T), i32), ("uniforms", uniforms, (N, T), torch.float32),
+                      ("parents", parents, (N, T), i32), ("num_nodes", num_nodes, (N,), i32),
+                      ("workspace", workspace, None if workspace is None else (workspace.numel(),), torch.uint8),
+                      ("accept", accept, (N,), i32), ("path", path, (N, T), i32), ("next_token", next_token, (N,), i32))
     if workspace is None:
         workspace = verify_workspace(N, T, V, target.device)
     if accept is None:
@@ -479,9 +487,9 @@ def make_state_cache(num_slots: int, H: int, D: int, device, dtype=torch.int8) -
 def _cache_call(where, fn, first, cache: StateCache, slots, states):
     S, H, D, _ = cache.values.shape
     N = states.shape[0]
-    _expect(states, "states", (N, H, D, D), torch.float32)
-    _expect(slots, "slots", (N,), torch.int32)
-    dev = _check_step(cache.values, cache.scales, slots, states)
+    dev = _check_step(("values", cache.values, (S, H, D, D), cache.values.dtype),
+                      ("scales", cache.scales, (S, H, D * D // CACHE_BLOCK), torch.uint8),
+                      ("slots", slots, (N,), torch.int32), ("states", states, (N, H, D, D), torch.float32))
     if S >= 2 ** 31:
         raise ValueError(f"num_slots: {S} is above INT32_MAX")
     if first == "states":
