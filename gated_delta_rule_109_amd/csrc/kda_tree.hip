@@ -27,14 +27,13 @@ __device__ __forceinline__ float row_dpp(float x) {
 template <int R> __device__ __forceinline__ float row_ror(float x) { return row_dpp<0x120 + R>(x); }
 template <int L> __device__ __forceinline__ float row_bcast(float x) { return row_dpp<0x150 + L>(x); }
 
-// Sum over the 64 lanes, in every lane.
+// Sum over the 64 lanes, as a wave-uniform value.
 __device__ __forceinline__ float wave_sum(float x) {
   x += row_ror<8>(x); x += row_ror<4>(x); x += row_ror<2>(x); x += row_ror<1>(x);
-  const int b = __builtin_bit_cast(int, x);
-  return (__builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 0)) +
-          __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 16))) +
-         (__builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 32)) +
-          __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 48)));
+  // rows 1 and 3 take rows 0 and 2 in, then rows 2 and 3 row 1's sum
+  x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x142, 0xA, 0xF, false));
+  x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x143, 0xC, 0xF, false));
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
 }
 
 // Two consecutive elements in one load (p even-aligned), as floats when needed.
@@ -261,33 +260,49 @@ __global__ __launch_bounds__(256) void tree_path_kernel(
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+// Two floats to packed bf16, round to nearest even, as the dword they are
+// stored in (bf16 vector types would be taken apart and packed again).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
+}
+// x = hi + lo, both packed
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16(a, b);
+  asm("" : "+v"(hi));
+  lo = pack_bf16(a - __builtin_bit_cast(float, hi << 16), b - __builtin_bit_cast(float, hi & 0xffff0000u));
+}
+
 struct SplitOp {                 // two bf16 terms
   static constexpr int kRowBytes = 2 * 272;      // a row of 128: hi, lo, each padded by 16 bytes
-  struct F8 { bf16x8 hi, lo; };
-  struct F4 { bf16x4 hi, lo; };
+  struct F8 { u32x4 hi, lo; };
+  struct F4 { uint2 hi, lo; };
   static __device__ __forceinline__ F8 make8(const float (&x)[8]) {
     F8 f;
-    bf16x4 h0, l0, h1, l1;
-    split_bf16(f32x4{x[0], x[1], x[2], x[3]}, h0, l0);
-    split_bf16(f32x4{x[4], x[5], x[6], x[7]}, h1, l1);
-    f.hi = cat(h0, h1);
-    f.lo = cat(l0, l1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t h, l;
+      split2(x[2 * j], x[2 * j + 1], h, l);
+      f.hi[j] = h;
+      f.lo[j] = l;
+    }
     return f;
   }
   static __device__ __forceinline__ F4 make4(f32x4 x) {
     F4 f;
-    split_bf16(x, f.hi, f.lo);
+    split2(x[0], x[1], f.hi.x, f.lo.x);
+    split2(x[2], x[3], f.hi.y, f.lo.y);
     return f;
   }
   // channels 2 lane, 2 lane + 1 of a row
   static __device__ __forceinline__ void put2(char* row, int lane, float a, float b) {
-    bf16x4 hi, lo;
-    split_bf16(f32x4{a, b, 0.f, 0.f}, hi, lo);
-    ((uint32_t*)row)[lane] = __builtin_bit_cast(uint2, hi).x;
-    ((uint32_t*)(row + 272))[lane] = __builtin_bit_cast(uint2, lo).x;
+    uint32_t hi, lo;
+    split2(a, b, hi, lo);
+    ((uint32_t*)row)[lane] = hi;
+    ((uint32_t*)(row + 272))[lane] = lo;
   }
   static __device__ __forceinline__ F8 get8(const char* row, int c) {
-    return {*(const bf16x8*)(row + 2 * c), *(const bf16x8*)(row + 272 + 2 * c)};
+    return {*(const u32x4*)(row + 2 * c), *(const u32x4*)(row + 272 + 2 * c)};
   }
   // element (i, j) of a matrix with rows of `stride` elements
   static __device__ __forceinline__ void put1(char* m, int stride, int i, int j, float x) {
@@ -296,14 +311,17 @@ struct SplitOp {                 // two bf16 terms
     ((__bf16*)m)[(2 * i + 1) * stride + j] = f32_to_bf16(x - bf16v_to_f32(hi));
   }
   static __device__ __forceinline__ F4 get4(const char* m, int stride, int i, int j) {
-    return {*(const bf16x4*)(m + 2 * (2 * i * stride + j)), *(const bf16x4*)(m + 2 * ((2 * i + 1) * stride + j))};
+    return {*(const uint2*)(m + 2 * (2 * i * stride + j)), *(const uint2*)(m + 2 * ((2 * i + 1) * stride + j))};
+  }
+  static __device__ __forceinline__ f32x4 mma32(u32x4 a, u32x4 b, f32x4 c) {
+    return mfma32(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c);
   }
   static __device__ __forceinline__ f32x4 mma(const F8& a, const F8& b, f32x4 c) {
-    c = mfma32(a.lo, b.hi, c);
-    c = mfma32(a.hi, b.lo, c);
-    return mfma32(a.hi, b.hi, c);
+    c = mma32(a.lo, b.hi, c);
+    c = mma32(a.hi, b.lo, c);
+    return mma32(a.hi, b.hi, c);
   }
-  static __device__ __forceinline__ f32x4 mma16(bf16x4 a, bf16x4 b, f32x4 c) {
+  static __device__ __forceinline__ f32x4 mma16(uint2 a, uint2 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, a), __builtin_bit_cast(s16x4, b), c, 0,
                                                      0, 0);
   }
@@ -404,39 +422,59 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
   __shared__ uint64_t s_anc[kMaxNodes];
   __shared__ __attribute__((aligned(16))) float s_b[kMaxNodes];
   __shared__ unsigned long long s_bad[2];                // nodes with d, with o not finite in every column
-  auto row = [&](int t) __attribute__((always_inline)) { return ((size_t)n * T + t) * H + h; };
+  // Rows of this head inside the sequence by 32-bit byte offsets from uniform
+  // bases (the launcher sees to 4 H D < 2^24): one instruction an address.
+  const uint32_t row_bytes = (uint32_t)H * D * sizeof(TIn);
+  const size_t first = ((size_t)n * T * H + h) * D;
+  auto off = [&](int t) __attribute__((always_inline)) { return __umul24((uint32_t)t, row_bytes); };
 
   const int parent = lane < nt ? clean_parent(parents, (size_t)n * T, lane) : -1;
-  const float braw = beta[row(min(lane, nt - 1))];
+  const float braw = beta[((size_t)n * T + min(lane, nt - 1)) * H + h];
   // this wave's nodes: wave + kWaves x, two channels per lane
   Pair<TIn> lk[kRowsPerWave], lq[kRowsPerWave];
   float te[kRowsPerWave][2];
 #pragma unroll
   for (int x = 0; x < kRowsPerWave; ++x) {
-    const size_t r = row(min(wave + kWaves * x, nt - 1));
-    lk[x].load(k + r * D + 2 * lane);
-    lq[x].load(q + r * D + 2 * lane);
-    if (gate == KDA_GATE_CHANNEL) {
-      const f32x2 e = *(const f32x2*)(g + r * D + 2 * lane);
+    const size_t at = (size_t)min(wave + kWaves * x, nt - 1) * H * D;   // uniform
+    const uint32_t mine = 2 * lane * sizeof(TIn);
+    lk[x].load((const TIn*)((const char*)(k + first + at) + mine));
+    lq[x].load((const TIn*)((const char*)(q + first + at) + mine));
+  }
+  if (gate == KDA_GATE_CHANNEL) {
+#pragma unroll
+    for (int x = 0; x < kRowsPerWave; ++x) {
+      const size_t at = (size_t)min(wave + kWaves * x, nt - 1) * H * D;
+      const f32x2 e = *(const f32x2*)((const char*)(g + first + at) + 8u * lane);
       te[x][0] = e[0];
       te[x][1] = e[1];
-    } else {
-      te[x][0] = te[x][1] = gate == KDA_GATE_HEAD ? g[r] : 0.f;
     }
+  } else if (gate == KDA_GATE_HEAD) {
+    const float mine = g[((size_t)n * T + min(lane, nt - 1)) * H + h];    // lane t: node t
+#pragma unroll
+    for (int x = 0; x < kRowsPerWave; ++x)
+      te[x][0] = te[x][1] =
+          __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine), wave + kWaves * x));
+  } else {
+#pragma unroll
+    for (int x = 0; x < kRowsPerWave; ++x) te[x][0] = te[x][1] = 0.f;
   }
   // S in operand layout: rows 32 ks + 8 lg + j, columns col0 + kNT lr + {0 ..}
   const int col0 = wave * 16 * kNT;
   // (a uniform base and one 32-bit lane offset: no 64-bit address per load)
   const uint32_t lane_off = (uint32_t)(8 * lg * D + kNT * lr) * 4;
   float sreg[4][8][kNT];
+  auto load_s = [&]() __attribute__((always_inline)) {
 #pragma unroll
-  for (int ks = 0; ks < 4; ++ks) {
-    const char* base = (const char*)(state + (size_t)blockIdx.x * D * D + col0 + 32 * ks * D) + lane_off;
+    for (int ks = 0; ks < 4; ++ks) {
+      const char* base = (const char*)(state + (size_t)blockIdx.x * D * D + col0 + 32 * ks * D) + lane_off;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-      for (int c = 0; c < kNT; ++c) sreg[ks][j][c] = ((const float*)base)[j * D + c];
-  }
+        for (int c = 0; c < kNT; ++c) sreg[ks][j][c] = ((const float*)base)[j * D + c];
+    }
+  };
+  if constexpr (!L::kTwo) load_s();
+  const uint32_t cols = kNT * lr * sizeof(TIn);
   using Cols = std::conditional_t<kNT == 2, Pair<TIn>, One<TIn>>;
   Cols vreg[kTB][4];
   auto load_v = [&]() __attribute__((always_inline)) {
@@ -444,7 +482,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
     for (int I = 0; I < kTB; ++I)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        vreg[I][r].load(v + row(min(16 * I + 4 * lg + r, nt - 1)) * D + col0 + kNT * lr);
+        vreg[I][r].load((const TIn*)((const char*)(v + first + col0) + off(min(16 * I + 4 * lg + r, nt - 1)) + cols));
   };
   if constexpr (!L::kTwo) load_v();
 
@@ -488,6 +526,10 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
 #pragma unroll
   for (int x = 0; x < kRowsPerWave; ++x)
     if (wave + kWaves * x >= nt) te[x][0] = te[x][1] = 1.f, rk[x] = rq[x] = 0.f;
+  if constexpr (L::kTwo) {      // behind q, k and g, which are needed first
+    load_s();
+    __builtin_amdgcn_sched_barrier(0);
+  }
   // E by doubling: after r rounds the product over the last 2^r nodes of the path
   if (gate != KDA_GATE_NONE)
     for (int jump = parent; __ballot(jump >= 0);) {
@@ -563,28 +605,30 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
   for (int I = 0; I < kTB; ++I)
 #pragma unroll
     for (int c = 0; c < kNT; ++c) U[I][c] = W[I][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  typename Op::F8 sf[4][kNT];              // S as operands, in place of sreg
   auto times_s = [&](bool u, bool w) __attribute__((always_inline)) {
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
-      typename Op::F8 sf[kNT];
+      if (u) {
 #pragma unroll
-      for (int c = 0; c < kNT; ++c) {
-        float x[8];
+        for (int c = 0; c < kNT; ++c) {
+          float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = sreg[ks][j][c];
-        sf[c] = Op::make8(x);
+          for (int j = 0; j < 8; ++j) x[j] = sreg[ks][j][c];
+          sf[ks][c] = Op::make8(x);
+        }
       }
 #pragma unroll
       for (int I = 0; I < kTB; ++I) {
         if (u) {
           const typename Op::F8 a = Op::get8(s_ke + (16 * I + lr) * Op::kRowBytes, 32 * ks + 8 * lg);
 #pragma unroll
-          for (int c = 0; c < kNT; ++c) U[I][c] = Op::mma(a, sf[c], U[I][c]);
+          for (int c = 0; c < kNT; ++c) U[I][c] = Op::mma(a, sf[ks][c], U[I][c]);
         }
         if (w) {
           const typename Op::F8 a = Op::get8(s_qe + (16 * I + lr) * Op::kRowBytes, 32 * ks + 8 * lg);
 #pragma unroll
-          for (int c = 0; c < kNT; ++c) W[I][c] = Op::mma(a, sf[c], W[I][c]);
+          for (int c = 0; c < kNT; ++c) W[I][c] = Op::mma(a, sf[ks][c], W[I][c]);
         }
       }
     }
@@ -609,12 +653,13 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
     int I, J;
     if (tile_of(set, x, is_b, I, J)) {
       const int j = 16 * J + lr;
+      const uint32_t* anc32 = (const uint32_t*)s_anc + (J >> 1);
       f32x4 y;
       bool odd = false;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int i = 16 * I + 4 * lg + r;
-        const bool on = (s_anc[i] >> j & 1) && (is_b || i != j);
+        const bool on = (anc32[2 * i] >> (j & 31) & 1) && (is_b || i != j);
         y[r] = on ? (is_b ? mat[set][x][r] : -s_b[i] * mat[set][x][r]) : 0.f;
         odd |= !is_finite(y[r]);
       }
@@ -739,7 +784,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
             y[c] = scale * W[I][c][r];
             if (any && ((s_anc[i] & bad[c]) || (bad_o >> i & 1))) y[c] = __builtin_nanf("");
           }
-          Cols::store(o + row(i) * D + col0 + kNT * lr, y[0], y[kNT - 1]);
+          Cols::store((TIn*)((char*)(o + first + col0) + off(i) + cols), y[0], y[kNT - 1]);
         }
       }
     }
@@ -771,7 +816,7 @@ static hipError_t launch_tree_128(const TreeArgs& a) {
   // the deepest path whose decays span at most kMaxSpan; every tree if T does
   const float deepest = a.gate == KDA_GATE_NONE || a.g_min == 0.f ? (float)kMaxNodes : kMaxSpan / -a.g_min;
   const int reach = deepest >= (float)a.T ? 0 : (int)deepest;
-  if (reach == 0 && deepest < 1.f) return launch_paths<128, TIn>(a, 0);
+  if ((reach == 0 && deepest < 1.f) || (int64_t)a.H * 128 * 4 >= 1 << 24) return launch_paths<128, TIn>(a, 0);
   hipError_t e;
   switch ((a.T + 15) / 16) {
     case 1: e = launch_tiles<1, 4, TIn, Op>(a, reach); break;
