@@ -56,6 +56,23 @@ template <> struct Pair<float> {
   static __device__ __forceinline__ void store(float* p, float a, float b) { *(f32x2*)p = f32x2{a, b}; }
 };
 
+// kN consecutive elements (a multiple of 16 bytes) in 16-byte loads.
+template <typename T, int kN> struct Run {
+  u32x4 w[kN * sizeof(T) / 16];
+  __device__ __forceinline__ void load(const void* p) {
+#pragma unroll
+    for (int i = 0; i < (int)(kN * sizeof(T) / 16); ++i) w[i] = ((const u32x4*)p)[i];
+  }
+  __device__ __forceinline__ float get(int c) const {
+    if constexpr (sizeof(T) == 4) {
+      return __builtin_bit_cast(float, (uint32_t)w[c / 4][c % 4]);
+    } else {
+      const uint32_t d = w[c / 8][c / 2 % 4];
+      return __builtin_bit_cast(float, c % 2 ? d & 0xffff0000u : d << 16);
+    }
+  }
+};
+
 // One element, with the interface of Pair.
 template <typename T> struct One {
   T w;
@@ -294,12 +311,22 @@ struct SplitOp {                 // two bf16 terms
     split2(x[2], x[3], f.hi.y, f.lo.y);
     return f;
   }
-  // channels 2 lane, 2 lane + 1 of a row
-  static __device__ __forceinline__ void put2(char* row, int lane, float a, float b) {
-    uint32_t hi, lo;
-    split2(a, b, hi, lo);
-    ((uint32_t*)row)[lane] = hi;
-    ((uint32_t*)(row + 272))[lane] = lo;
+  // channels c .. c + kN - 1 of a row, kN and c multiples of 8
+  template <int kN>
+  static __device__ __forceinline__ void put(char* row, int c, const float (&x)[kN]) {
+#pragma unroll
+    for (int i = 0; i < kN / 8; ++i) {
+      u32x4 hi, lo;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t h, l;
+        split2(x[8 * i + 2 * j], x[8 * i + 2 * j + 1], h, l);
+        hi[j] = h;
+        lo[j] = l;
+      }
+      *(u32x4*)(row + 2 * (c + 8 * i)) = hi;
+      *(u32x4*)(row + 272 + 2 * (c + 8 * i)) = lo;
+    }
   }
   static __device__ __forceinline__ F8 get8(const char* row, int c) {
     return {*(const u32x4*)(row + 2 * c), *(const u32x4*)(row + 272 + 2 * c)};
@@ -343,8 +370,11 @@ struct FloatOp {
     return f;
   }
   static __device__ __forceinline__ F4 make4(f32x4 x) { return {x}; }
-  static __device__ __forceinline__ void put2(char* row, int lane, float a, float b) {
-    ((f32x2*)row)[lane] = f32x2{a, b};
+  template <int kN>
+  static __device__ __forceinline__ void put(char* row, int c, const float (&x)[kN]) {
+#pragma unroll
+    for (int i = 0; i < kN / 4; ++i)
+      *(f32x4*)(row + 4 * (c + 4 * i)) = f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
   }
   static __device__ __forceinline__ F8 get8(const char* row, int c) {
     F8 f;
@@ -387,10 +417,9 @@ struct TileLds {
   static constexpr int kStride = kT + 4;                 // row of A or B, elements
   static constexpr size_t kRows = (size_t)kT * Op::kRowBytes;
   static constexpr size_t kMat = (size_t)kT * kStride * 4;
-  static constexpr size_t kE = (size_t)kT * 128 * 4;
   static constexpr size_t kDiag = (size_t)kTB * 16 * 20 * 4;
-  static constexpr size_t kTail = 2 * kMat + 2 * kDiag > kE ? 2 * kMat + 2 * kDiag : kE;
-  static constexpr size_t kTailAt = kTwo ? 0 : 3 * kRows;   // E, then A, B, diagonal blocks and inverses
+  static constexpr size_t kTail = 2 * kMat + 2 * kDiag;
+  static constexpr size_t kTailAt = kTwo ? 0 : 3 * kRows;   // A, B, diagonal blocks and inverses
   static constexpr size_t kBytes = kTwo ? 2 * kRows : 3 * kRows + kTail;
   static_assert(!kTwo || kTail <= 2 * kRows, "matrices lie inside the planes");
 };
@@ -404,7 +433,6 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
   constexpr int D = 128;
   using L = TileLds<kTB, kWaves, Op>;
   constexpr int kT = L::kT, kNT = 8 / kWaves;            // n-tiles of a wave
-  constexpr int kRowsPerWave = kT / kWaves;
   const uint32_t n = blockIdx.x / (uint32_t)H, h = blockIdx.x % (uint32_t)H;
   const int nt = num_nodes ? min(max(num_nodes[n], 0), T) : T;
   if (nt == 0) return;
@@ -414,7 +442,6 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
   char* s_ke = lds;                                      // planes: k E, k / E, q E, [kT] rows each
   char* s_kq = s_ke + L::kRows;
   char* s_qe = L::kTwo ? s_ke : s_kq + L::kRows;
-  float* s_E = (float*)(lds + L::kTailAt);               // [kT][128]
   char* s_A = lds + L::kTailAt;                          // -beta A
   char* s_B = s_A + L::kMat;
   float* s_diag = (float*)(s_B + L::kMat);               // [kTB][16][20] diagonal blocks of -beta A
@@ -430,33 +457,28 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
 
   const int parent = lane < nt ? clean_parent(parents, (size_t)n * T, lane) : -1;
   const float braw = beta[((size_t)n * T + min(lane, nt - 1)) * H + h];
-  // this wave's nodes: wave + kWaves x, two channels per lane
-  Pair<TIn> lk[kRowsPerWave], lq[kRowsPerWave];
-  float te[kRowsPerWave][2];
+  // Lane (group, node) holds kC consecutive channels of its node; a wave all
+  // nodes of 128 / kWaves channels, so that decays multiply along the paths by
+  // exchanges inside the wave.
+  constexpr int kNodes = kTB <= 2 ? kT : 64, kC = D / kWaves / (kWave / kNodes);
+  const int node = lane % kNodes, chan = wave * (D / kWaves) + lane / kNodes * kC;
+  const bool live = node < nt;
+  Run<TIn, kC> lk, lq;
+  float te[kC];
+  {
+    const uint32_t at = off(min(node, nt - 1)) + chan * (uint32_t)sizeof(TIn);
+    lk.load((const char*)(k + first) + at);
+    lq.load((const char*)(q + first) + at);
+    if (gate == KDA_GATE_CHANNEL) {
+      Run<float, kC> lg4;
+      lg4.load((const char*)(g + first) + __umul24((uint32_t)min(node, nt - 1), (uint32_t)H * D * 4) + chan * 4u);
 #pragma unroll
-  for (int x = 0; x < kRowsPerWave; ++x) {
-    const size_t at = (size_t)min(wave + kWaves * x, nt - 1) * H * D;   // uniform
-    const uint32_t mine = 2 * lane * sizeof(TIn);
-    lk[x].load((const TIn*)((const char*)(k + first + at) + mine));
-    lq[x].load((const TIn*)((const char*)(q + first + at) + mine));
-  }
-  if (gate == KDA_GATE_CHANNEL) {
+      for (int c = 0; c < kC; ++c) te[c] = lg4.get(c);
+    } else {
+      const float one = gate == KDA_GATE_HEAD ? g[((size_t)n * T + min(node, nt - 1)) * H + h] : 0.f;
 #pragma unroll
-    for (int x = 0; x < kRowsPerWave; ++x) {
-      const size_t at = (size_t)min(wave + kWaves * x, nt - 1) * H * D;
-      const f32x2 e = *(const f32x2*)((const char*)(g + first + at) + 8u * lane);
-      te[x][0] = e[0];
-      te[x][1] = e[1];
+      for (int c = 0; c < kC; ++c) te[c] = one;
     }
-  } else if (gate == KDA_GATE_HEAD) {
-    const float mine = g[((size_t)n * T + min(lane, nt - 1)) * H + h];    // lane t: node t
-#pragma unroll
-    for (int x = 0; x < kRowsPerWave; ++x)
-      te[x][0] = te[x][1] =
-          __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine), wave + kWaves * x));
-  } else {
-#pragma unroll
-    for (int x = 0; x < kRowsPerWave; ++x) te[x][0] = te[x][1] = 0.f;
   }
   // S in operand layout: rows 32 ks + 8 lg + j, columns col0 + kNT lr + {0 ..}
   const int col0 = wave * 16 * kNT;
@@ -498,74 +520,72 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
   const float alpha_min = __builtin_amdgcn_exp2f(g_min * kLog2e);
   if (gate == KDA_GATE_NONE) {
 #pragma unroll
-    for (int x = 0; x < kRowsPerWave; ++x) te[x][0] = te[x][1] = 1.f;
+    for (int c = 0; c < kC; ++c) te[c] = 1.f;
   } else if (fe_flags & KDA_FE_GATE_LOGITS) {
 #pragma unroll
-    for (int x = 0; x < kRowsPerWave; ++x)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) te[x][c] = gate_alpha_logit(te[x][c], alpha_min);
+    for (int c = 0; c < kC; ++c) te[c] = gate_alpha_logit(te[c], alpha_min);
   } else {
 #pragma unroll
-    for (int x = 0; x < kRowsPerWave; ++x)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) te[x][c] = gate_alpha(te[x][c], g_min);
+    for (int c = 0; c < kC; ++c) te[c] = gate_alpha(te[c], g_min);
   }
-  // scales of k and q: 1, the inverse norms, or 0 for rows past the last node
-  float rk[kRowsPerWave], rq[kRowsPerWave];
-#pragma unroll
-  for (int x = 0; x < kRowsPerWave; ++x) rk[x] = rq[x] = 1.f;
+  // scales of k and q: 1 or the inverse norms (sums over the waves by LDS)
+  float rk = 1.f, rq = 1.f;
   if (fe_flags & KDA_FE_L2NORM_QK) {
+    float sk = 0.f, sq = 0.f;
 #pragma unroll
-    for (int x = 0; x < kRowsPerWave; ++x) {
-      rk[x] = wave_sum(lk[x].get(0) * lk[x].get(0) + lk[x].get(1) * lk[x].get(1));
-      rq[x] = wave_sum(lq[x].get(0) * lq[x].get(0) + lq[x].get(1) * lq[x].get(1));
+    for (int c = 0; c < kC; ++c) {
+      sk += lk.get(c) * lk.get(c);
+      sq += lq.get(c) * lq.get(c);
     }
 #pragma unroll
-    for (int x = 0; x < kRowsPerWave; ++x) { rk[x] = inv_norm(rk[x], fe_eps); rq[x] = inv_norm(rq[x], fe_eps); }
-  }
+    for (int m = kNodes; m < kWave; m *= 2) { sk += __shfl_xor(sk, m); sq += __shfl_xor(sq, m); }
+    f32x2* s_norm = (f32x2*)lds;                          // [kWaves][kNodes]
+    if (lane < kNodes) s_norm[wave * kNodes + node] = f32x2{sk, sq};
+    lds_barrier();
+    f32x2 sum = {0.f, 0.f};
 #pragma unroll
-  for (int x = 0; x < kRowsPerWave; ++x)
-    if (wave + kWaves * x >= nt) te[x][0] = te[x][1] = 1.f, rk[x] = rq[x] = 0.f;
+    for (int w = 0; w < kWaves; ++w) sum += s_norm[w * kNodes + node];
+    rk = inv_norm(sum[0], fe_eps);
+    rq = inv_norm(sum[1], fe_eps);
+    lds_barrier();                                        // the planes come over it
+  }
   if constexpr (L::kTwo) {      // behind q, k and g, which are needed first
     load_s();
     __builtin_amdgcn_sched_barrier(0);
   }
   // E by doubling: after r rounds the product over the last 2^r nodes of the path
-  if (gate != KDA_GATE_NONE)
-    for (int jump = parent; __ballot(jump >= 0);) {
+  if (gate != KDA_GATE_NONE) {
+    const int base = lane - node;
+    for (int jump = __shfl(parent, node); __ballot(jump >= 0);) {
+      const int from = base + max(jump, 0);
+      float e[kC];
 #pragma unroll
-      for (int x = 0; x < kRowsPerWave; ++x)
-        *(f32x2*)(s_E + (wave + kWaves * x) * D + 2 * lane) = f32x2{te[x][0], te[x][1]};
-      lds_barrier();
-      f32x2 e[kRowsPerWave];
-      int p[kRowsPerWave];
+      for (int c = 0; c < kC; ++c) e[c] = __shfl(te[c], from);
+      const int next = __shfl(jump, from);
 #pragma unroll
-      for (int x = 0; x < kRowsPerWave; ++x) {
-        p[x] = __builtin_amdgcn_readlane(jump, wave + kWaves * x);
-        e[x] = *(const f32x2*)(s_E + max(p[x], 0) * D + 2 * lane);
-      }
-      __builtin_amdgcn_sched_barrier(0);   // all reads in flight before the first is waited for
-#pragma unroll
-      for (int x = 0; x < kRowsPerWave; ++x) {
-        te[x][0] *= p[x] >= 0 ? e[x][0] : 1.f;
-        te[x][1] *= p[x] >= 0 ? e[x][1] : 1.f;
-      }
-      const int next = __shfl(jump, max(jump, 0));
+      for (int c = 0; c < kC; ++c) te[c] *= jump >= 0 ? e[c] : 1.f;
       jump = jump >= 0 ? next : -1;
-      lds_barrier();
     }
+  }
+  // rows past the last node are 0
   auto put_q = [&]() __attribute__((always_inline)) {
+    float x[kC];
 #pragma unroll
-    for (int x = 0; x < kRowsPerWave; ++x)
-      Op::put2(s_qe + (wave + kWaves * x) * Op::kRowBytes, lane, lq[x].get(0) * rq[x] * te[x][0],
-               lq[x].get(1) * rq[x] * te[x][1]);
+    for (int c = 0; c < kC; ++c) x[c] = live ? lq.get(c) * rq * te[c] : 0.f;
+    if (kNodes == kT || node < kT) Op::put(s_qe + node * Op::kRowBytes, chan, x);
   };
+  {
+    float x[kC], y[kC];
 #pragma unroll
-  for (int x = 0; x < kRowsPerWave; ++x) {
-    const int i = wave + kWaves * x;
-    const float e0 = te[x][0], e1 = te[x][1], k0 = lk[x].get(0) * rk[x], k1 = lk[x].get(1) * rk[x];
-    Op::put2(s_ke + i * Op::kRowBytes, lane, k0 * e0, k1 * e1);
-    Op::put2(s_kq + i * Op::kRowBytes, lane, k0 * __builtin_amdgcn_rcpf(e0), k1 * __builtin_amdgcn_rcpf(e1));
+    for (int c = 0; c < kC; ++c) {
+      const float kc = live ? lk.get(c) * rk : 0.f;
+      x[c] = kc * te[c];
+      y[c] = live ? kc * __builtin_amdgcn_rcpf(te[c]) : 0.f;
+    }
+    if (kNodes == kT || node < kT) {
+      Op::put(s_ke + node * Op::kRowBytes, chan, x);
+      Op::put(s_kq + node * Op::kRowBytes, chan, y);
+    }
   }
   if constexpr (!L::kTwo) put_q();
   lds_barrier();
