@@ -108,14 +108,59 @@ __device__ __forceinline__ uint64_t ancestors(int parent, int lane) {
   return anc;
 }
 
-// Whether a sequence takes the tile kernel: it forms decays between nodes as
-// quotients E_i / E_j, so the smallest E, at least exp(depth * g_min), must stay
-// far inside the range of fp32 and of a two-term bf16 split. `reach` is
-// kMaxSpan / -g_min, the deepest tree allowed.
-constexpr float kMaxSpan = 60.f;
-__device__ __forceinline__ bool shallow(uint64_t anc, bool live, int reach) {
-  return __ballot(live && __builtin_popcountll(anc) > reach) == 0;
+// Decays between nodes as quotients E_i / E_j of the decays from the state.
+// Where every E of any tree of T nodes is at least 2^-kMaxSpan, far inside the
+// range of fp32 and of a two-term bf16 split, they are formed as they stand.
+// Otherwise G = log2 E is kept in fp64 and referred, per block of 16 rows and
+// channel, to R half way between the block's largest and smallest G:
+//   E_i / E_j = 2^(G_i - R) 2^(R - G_j).
+// The first exponent is at most half the block's spread in size, and so is the
+// second from above whenever j is an ancestor of a node of the block (from
+// below it may underflow, as the quotient does). So only the spread inside a
+// block is limited, not the depth of the tree. What exceeds that too (a floor
+// below -5.2 with chains of 16, blocks that mix deep and shallow branches) is
+// left to the path kernel; both kernels decide it from the tree alone.
+constexpr float kMaxSpan = 87.f;      // log2 (2^-87 = e^-60)
+constexpr float kMaxSpread = 120.f;   // log2: factors reach 2^60
+
+// 2^x, x any finite fp64: the integer part goes to the exponent, so that a
+// large x costs no digits. Overflows to infinity, underflows to 0.
+__device__ __forceinline__ float exp2_wide(double x) {
+  const double i = rint(fmin(fmax(x, -400.0), 400.0));
+  return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f((float)(fmin(fmax(x, -400.0), 400.0) - i)), (int)i);
 }
+
+// log2 of the decay of one channel.
+__device__ __forceinline__ double log2_alpha(float g, bool logits, float g_min) {
+  const double l2e = 1.4426950408889634074;
+  if (!logits) return (double)fminf(fmaxf(g, g_min), 0.f) * l2e;
+  // -softplus(a) = min(-a, 0) - ln(1 + e^-|a|)
+  const float soft = fminf(-g, 0.f) - log1pf(__builtin_amdgcn_exp2f(-fabsf(g) * kLog2e));
+  return (double)fmaxf(soft, g_min) * l2e;
+}
+
+// Largest depth of a block's nodes below their deepest common ancestor, over
+// the blocks: the number of decays a block's spread consists of, at most.
+__device__ __forceinline__ int block_depth(uint64_t anc, bool live) {
+  uint64_t common = live ? anc : ~0ull;
+  int deep = live ? __builtin_popcountll(anc) : 0;
+#pragma unroll
+  for (int m = 1; m < 16; m *= 2) {
+    common &= __shfl_xor((unsigned long long)common, m);
+    deep = max(deep, __shfl_xor(deep, m));
+  }
+  int most = deep ? deep - __builtin_popcountll(common) : 0;
+  most = max(most, __shfl_xor(most, 16));
+  return max(most, __shfl_xor(most, 32));
+}
+// How many decays at the floor stay within `span` (log2), at most kMaxNodes.
+static int reach_of(float span, float g_min, int gate) {
+  if (gate == KDA_GATE_NONE || g_min == 0.f) return kMaxNodes;
+  const float r = span / (-g_min * kLog2e);
+  return r >= (float)kMaxNodes ? kMaxNodes : (int)r;
+}
+
+constexpr int kNoneTaken = -1;
 
 // ---- any decays, any head size -------------------------------------------------
 // One 256-thread workgroup per (sequence, head). A_ij and B_ij are summed pair
@@ -133,14 +178,14 @@ __global__ __launch_bounds__(256) void tree_path_kernel(
     const TIn* __restrict__ q, const TIn* __restrict__ k, const TIn* __restrict__ v,
     const float* __restrict__ g, const float* __restrict__ beta, const float* __restrict__ state,
     const int32_t* __restrict__ parents, const int32_t* __restrict__ num_nodes, TIn* __restrict__ o, int H,
-    int T, float scale, float g_min, uint32_t fe_flags, float fe_eps, int gate, int skip_reach) {
+    int T, float scale, float g_min, uint32_t fe_flags, float fe_eps, int gate, int taken) {
   const uint32_t n = blockIdx.x / (uint32_t)H, h = blockIdx.x % (uint32_t)H;
   const int nt = num_nodes ? min(max(num_nodes[n], 0), T) : T;
   if (nt == 0) return;
   const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
-  if (skip_reach > 0) {   // the tile kernel takes the shallow ones
+  if (taken != kNoneTaken) {   // sequences whose blocks are no deeper are another kernel's
     const int p = lane < nt ? clean_parent(parents, (size_t)n * T, lane) : -1;
-    if (shallow(ancestors(p, lane), lane < nt, skip_reach)) return;
+    if (block_depth(ancestors(p, lane), lane < nt) <= taken) return;
   }
   extern __shared__ float smem[];
   float* s_k = smem;
@@ -408,9 +453,9 @@ __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) < __builtin
 // operand planes would leave room for one workgroup per compute unit, which
 // then either loads or computes: q E takes the place of k E once A and U are
 // formed, and the matrices lie over the planes (two workgroups; 64 nodes on 64
-// x 32 heads: FIGURE). With one or two tiles all lie side by side and two
+// x 32 heads: 192 us with one, 113 with two). With one or two tiles all lie side by side and two
 // barriers are saved.
-template <int kTB, int kWaves, typename Op>
+template <int kTB, int kWaves, typename Op, bool kDeep>
 struct TileLds {
   static constexpr int kT = 16 * kTB;
   static constexpr bool kTwo = kTB >= 3;
@@ -419,19 +464,21 @@ struct TileLds {
   static constexpr size_t kMat = (size_t)kT * kStride * 4;
   static constexpr size_t kDiag = (size_t)kTB * 16 * 20 * 4;
   static constexpr size_t kTail = 2 * kMat + 2 * kDiag;
-  static constexpr size_t kTailAt = kTwo ? 0 : 3 * kRows;   // A, B, diagonal blocks and inverses
-  static constexpr size_t kBytes = kTwo ? 2 * kRows : 3 * kRows + kTail;
+  // A, B, diagonal blocks and inverses; kDeep: after two planes and the rows of one block
+  static constexpr size_t kTailAt = kDeep ? 2 * kRows + 32 * Op::kRowBytes : kTwo ? 0 : 3 * kRows;
+  static constexpr size_t kBytes = !kDeep && kTwo ? 2 * kRows : kTailAt + kTail;
   static_assert(!kTwo || kTail <= 2 * kRows, "matrices lie inside the planes");
 };
 
-template <int kTB, int kWaves, typename TIn, typename Op>
-__global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
+// kDeep: A and B with the decays of each block of rows referred to its own R.
+template <int kTB, int kWaves, typename TIn, typename Op, bool kDeep>
+__global__ __launch_bounds__(64 * kWaves, kDeep ? 2 : 4) void tree_tile_kernel(
     const TIn* __restrict__ q, const TIn* __restrict__ k, const TIn* __restrict__ v,
     const float* __restrict__ g, const float* __restrict__ beta, const float* __restrict__ state,
     const int32_t* __restrict__ parents, const int32_t* __restrict__ num_nodes, TIn* __restrict__ o, int H,
     int T, float scale, float g_min, uint32_t fe_flags, float fe_eps, int gate, int reach) {
   constexpr int D = 128;
-  using L = TileLds<kTB, kWaves, Op>;
+  using L = TileLds<kTB, kWaves, Op, kDeep>;
   constexpr int kT = L::kT, kNT = 8 / kWaves;            // n-tiles of a wave
   const uint32_t n = blockIdx.x / (uint32_t)H, h = blockIdx.x % (uint32_t)H;
   const int nt = num_nodes ? min(max(num_nodes[n], 0), T) : T;
@@ -441,7 +488,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char* s_ke = lds;                                      // planes: k E, k / E, q E, [kT] rows each
   char* s_kq = s_ke + L::kRows;
-  char* s_qe = L::kTwo ? s_ke : s_kq + L::kRows;
+  char* s_qe = L::kTwo || kDeep ? s_ke : s_kq + L::kRows;
   char* s_A = lds + L::kTailAt;                          // -beta A
   char* s_B = s_A + L::kMat;
   float* s_diag = (float*)(s_B + L::kMat);               // [kTB][16][20] diagonal blocks of -beta A
@@ -495,7 +542,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
         for (int c = 0; c < kNT; ++c) sreg[ks][j][c] = ((const float*)base)[j * D + c];
     }
   };
-  if constexpr (!L::kTwo) load_s();
+  if constexpr (!L::kTwo && !kDeep) load_s();
   const uint32_t cols = kNT * lr * sizeof(TIn);
   using Cols = std::conditional_t<kNT == 2, Pair<TIn>, One<TIn>>;
   Cols vreg[kTB][4];
@@ -506,11 +553,11 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
       for (int r = 0; r < 4; ++r)
         vreg[I][r].load((const TIn*)((const char*)(v + first + col0) + off(min(16 * I + 4 * lg + r, nt - 1)) + cols));
   };
-  if constexpr (!L::kTwo) load_v();
+  if constexpr (!L::kTwo && !kDeep) load_v();
 
   // the tree: ancestors, and whether this kernel takes it
   const uint64_t anc = ancestors(parent, lane);
-  if (reach > 0 && !shallow(anc, lane < nt, reach)) return;
+  if (kDeep && block_depth(anc, lane < nt) > reach) return;   // the path kernel takes it
   if (wave == 0) {
     s_anc[lane] = anc;
     s_b[lane] = lane >= nt ? 0.f : fe_flags & KDA_FE_BETA_LOGITS ? beta_logit(braw) : braw;
@@ -518,7 +565,11 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
   }
   // decays, normalised rows
   const float alpha_min = __builtin_amdgcn_exp2f(g_min * kLog2e);
-  if (gate == KDA_GATE_NONE) {
+  double G[kC];                                           // (kDeep)
+  if constexpr (kDeep) {
+#pragma unroll
+    for (int c = 0; c < kC; ++c) G[c] = log2_alpha(te[c], fe_flags & KDA_FE_GATE_LOGITS, g_min);
+  } else if (gate == KDA_GATE_NONE) {
 #pragma unroll
     for (int c = 0; c < kC; ++c) te[c] = 1.f;
   } else if (fe_flags & KDA_FE_GATE_LOGITS) {
@@ -549,7 +600,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
     rq = inv_norm(sum[1], fe_eps);
     lds_barrier();                                        // the planes come over it
   }
-  if constexpr (L::kTwo) {      // behind q, k and g, which are needed first
+  if constexpr (L::kTwo || kDeep) {      // behind q, k and g, which are needed first
     load_s();
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -558,14 +609,26 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
     const int base = lane - node;
     for (int jump = __shfl(parent, node); __ballot(jump >= 0);) {
       const int from = base + max(jump, 0);
-      float e[kC];
-#pragma unroll
-      for (int c = 0; c < kC; ++c) e[c] = __shfl(te[c], from);
       const int next = __shfl(jump, from);
+      if constexpr (kDeep) {
 #pragma unroll
-      for (int c = 0; c < kC; ++c) te[c] *= jump >= 0 ? e[c] : 1.f;
+        for (int c = 0; c < kC; ++c) {
+          const double e = __shfl(G[c], from);
+          G[c] += jump >= 0 ? e : 0.0;
+        }
+      } else {
+        float e[kC];
+#pragma unroll
+        for (int c = 0; c < kC; ++c) e[c] = __shfl(te[c], from);
+#pragma unroll
+        for (int c = 0; c < kC; ++c) te[c] *= jump >= 0 ? e[c] : 1.f;
+      }
       jump = jump >= 0 ? next : -1;
     }
+  }
+  if constexpr (kDeep) {
+#pragma unroll
+    for (int c = 0; c < kC; ++c) te[c] = exp2_wide(G[c]);
   }
   // rows past the last node are 0
   auto put_q = [&]() __attribute__((always_inline)) {
@@ -580,14 +643,14 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
     for (int c = 0; c < kC; ++c) {
       const float kc = live ? lk.get(c) * rk : 0.f;
       x[c] = kc * te[c];
-      y[c] = live ? kc * __builtin_amdgcn_rcpf(te[c]) : 0.f;
+      y[c] = live && !kDeep ? kc * __builtin_amdgcn_rcpf(te[c]) : 0.f;
     }
     if (kNodes == kT || node < kT) {
       Op::put(s_ke + node * Op::kRowBytes, chan, x);
-      Op::put(s_kq + node * Op::kRowBytes, chan, y);
+      if (!kDeep) Op::put(s_kq + node * Op::kRowBytes, chan, y);
     }
   }
-  if constexpr (!L::kTwo) put_q();
+  if constexpr (!L::kTwo && !kDeep) put_q();
   lds_barrier();
 
   // U = (k E) S and W = (q E) S; A and B by tiles (I, J <= I), shared out over
@@ -653,8 +716,83 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
       }
     }
   };
-  tiles(std::integral_constant<int, 0>{});
-  if constexpr (L::kTwo) {
+  // a tile of A or B, masked to ancestors, to LDS
+  auto put_tile = [&](bool is_b, int I, int J, f32x4 m) __attribute__((always_inline)) {
+    const int j = 16 * J + lr;
+    const uint32_t* anc32 = (const uint32_t*)s_anc + (J >> 1);
+    f32x4 y;
+    bool odd = false;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = 16 * I + 4 * lg + r;
+      const bool on = (anc32[2 * i] >> (j & 31) & 1) && (is_b || i != j);
+      y[r] = on ? (is_b ? m[r] : -s_b[i] * m[r]) : 0.f;
+      odd |= !is_finite(y[r]);
+    }
+    if (__ballot(odd)) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (!is_finite(y[r])) {
+          atomicOr(&s_bad[is_b], 1ull << (16 * I + 4 * lg + r));
+          y[r] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      Op::put1(is_b ? s_B : s_A, L::kStride, 16 * I + 4 * lg + r, j, y[r]);
+      if (!is_b && I == J) s_diag[(16 * I + 4 * lg + r) * 20 + lr] = y[r];
+    }
+  };
+  if constexpr (kDeep) {
+    times_s(true, false);
+    lds_barrier();
+    put_q();
+    lds_barrier();
+    times_s(false, true);
+    load_v();
+    static_for<0, kTB>([&](auto II) __attribute__((always_inline)) {
+      constexpr int I = decltype(II)::value;
+      if (16 * I < nt) {
+        char* s_rows = s_kq + L::kRows;                     // 16 rows of k, 16 of q
+        const bool mine = node / 16 == I;
+        float x[kC], y[kC], z[kC];
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+          float hi = live ? (float)G[c] : -__builtin_inff(), lo = live ? (float)G[c] : __builtin_inff();
+          hi = fmaxf(hi, row_ror<8>(hi)); hi = fmaxf(hi, row_ror<4>(hi));
+          hi = fmaxf(hi, row_ror<2>(hi)); hi = fmaxf(hi, row_ror<1>(hi));
+          lo = fminf(lo, row_ror<8>(lo)); lo = fminf(lo, row_ror<4>(lo));
+          lo = fminf(lo, row_ror<2>(lo)); lo = fminf(lo, row_ror<1>(lo));
+          const double R = (double)__shfl(0.5f * (hi + lo), lane - node + 16 * I);
+          const float kc = live ? lk.get(c) * rk : 0.f, e = exp2_wide(G[c] - R);
+          // (2^(R - G) may overflow for nodes that are nobody's ancestor here)
+          x[c] = live ? kc * e : 0.f;
+          y[c] = live ? lq.get(c) * rq * e : 0.f;
+          z[c] = live ? kc * exp2_wide(R - G[c]) : 0.f;
+        }
+        if (mine) {
+          Op::put(s_rows + (node % 16) * Op::kRowBytes, chan, x);
+          Op::put(s_rows + (16 + node % 16) * Op::kRowBytes, chan, y);
+        }
+        if (node < 16 * (I + 1)) Op::put(s_kq + node * Op::kRowBytes, chan, z);
+        lds_barrier();
+        static_for<0, (2 * (I + 1) + kWaves - 1) / kWaves>([&](auto X) __attribute__((always_inline)) {
+          const int unit = wave + kWaves * decltype(X)::value, J = unit >> 1;
+          if (J <= I) {
+            const bool is_b = unit & 1;
+            f32x4 m = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              m = Op::mma(Op::get8(s_rows + (16 * is_b + lr) * Op::kRowBytes, 32 * ks + 8 * lg),
+                          Op::get8(s_kq + (16 * J + lr) * Op::kRowBytes, 32 * ks + 8 * lg), m);
+            put_tile(is_b, I, J, m);
+          }
+        });
+        lds_barrier();
+      }
+    });
+  } else if constexpr (L::kTwo) {
+    tiles(std::integral_constant<int, 0>{});
     times_s(true, false);
     lds_barrier();
     put_q();
@@ -664,40 +802,16 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
     load_v();                              // (no registers to spare for it before)
     lds_barrier();
   } else {
+    tiles(std::integral_constant<int, 0>{});
     times_s(true, true);
   }
-  // masked A and B to LDS (over E, or over the planes)
-  static_for<0, kSets * kTurns>([&](auto X) __attribute__((always_inline)) {
-    constexpr int set = decltype(X)::value / kTurns, x = decltype(X)::value % kTurns;
-    bool is_b;
-    int I, J;
-    if (tile_of(set, x, is_b, I, J)) {
-      const int j = 16 * J + lr;
-      const uint32_t* anc32 = (const uint32_t*)s_anc + (J >> 1);
-      f32x4 y;
-      bool odd = false;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * I + 4 * lg + r;
-        const bool on = (anc32[2 * i] >> (j & 31) & 1) && (is_b || i != j);
-        y[r] = on ? (is_b ? mat[set][x][r] : -s_b[i] * mat[set][x][r]) : 0.f;
-        odd |= !is_finite(y[r]);
-      }
-      if (__ballot(odd)) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (!is_finite(y[r])) {
-            atomicOr(&s_bad[is_b], 1ull << (16 * I + 4 * lg + r));
-            y[r] = 0.f;
-          }
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        Op::put1(is_b ? s_B : s_A, L::kStride, 16 * I + 4 * lg + r, j, y[r]);
-        if (!is_b && I == J) s_diag[(16 * I + 4 * lg + r) * 20 + lr] = y[r];
-      }
-    }
-  });
+  if constexpr (!kDeep)
+    static_for<0, kSets * kTurns>([&](auto X) __attribute__((always_inline)) {
+      constexpr int set = decltype(X)::value / kTurns, x = decltype(X)::value % kTurns;
+      bool is_b;
+      int I, J;
+      if (tile_of(set, x, is_b, I, J)) put_tile(is_b, I, J, mat[set][x]);
+    });
   lds_barrier();
 
   // Inverses X of I + beta A = I - N on the diagonal blocks, row lr of block lg
@@ -811,46 +925,312 @@ __global__ __launch_bounds__(64 * kWaves, 4) void tree_tile_kernel(
   }
 }
 
+// ---- D = 16 --------------------------------------------------------------------------
+// The same blocks of 16 nodes, one wave per head and no LDS: lane (group lg, lr)
+// holds channels 4 lg .. + 3 of node 16 I + lr, which is the operand layout of
+// a 16 x 16 x 16 product, and A and B are formed transposed, which leaves them
+// in operand layout too. All products are fp32 (16 x 16 x 4).
+template <int kTB, typename TIn>
+__global__ __launch_bounds__(256, kTB >= 3 ? 2 : 4) void tree_small_kernel(
+    const TIn* __restrict__ q, const TIn* __restrict__ k, const TIn* __restrict__ v,
+    const float* __restrict__ g, const float* __restrict__ beta, const float* __restrict__ state,
+    const int32_t* __restrict__ parents, const int32_t* __restrict__ num_nodes, TIn* __restrict__ o,
+    uint32_t heads, int H, int T, float scale, float g_min, uint32_t fe_flags, float fe_eps, int gate, int reach) {
+  constexpr int D = 16;
+  using Op = FloatOp;
+  const uint32_t head = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  if (head >= heads) return;
+  const uint32_t n = head / (uint32_t)H, h = head % (uint32_t)H;
+  const int nt = num_nodes ? min(max(num_nodes[n], 0), T) : T;
+  if (nt == 0) return;
+  const int lane = threadIdx.x % kWave, lr = lane % 16, lg = lane / 16;
+  auto row = [&](int t) __attribute__((always_inline)) { return ((size_t)n * T + t) * H + h; };
+  const int parent = lane < nt ? clean_parent(parents, (size_t)n * T, lane) : -1;
+  const float braw = beta[row(min(lane, nt - 1))];
+  float kv[kTB][4], qv[kTB][4], gv[kTB][4];
+#pragma unroll
+  for (int I = 0; I < kTB; ++I) {
+    const size_t at = row(min(16 * I + lr, nt - 1));
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      kv[I][c] = Elem<TIn>::load(k + at * D + 4 * lg + c);
+      qv[I][c] = Elem<TIn>::load(q + at * D + 4 * lg + c);
+      gv[I][c] = gate == KDA_GATE_NONE ? 0.f : g[gate == KDA_GATE_CHANNEL ? at * D + 4 * lg + c : at];
+    }
+  }
+  Op::F4 sf;                                   // S[4 lg + j][lr]
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sf.x[j] = state[(size_t)head * D * D + (4 * lg + j) * D + lr];
+  float vv[kTB][4];
+#pragma unroll
+  for (int I = 0; I < kTB; ++I)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) vv[I][r] = Elem<TIn>::load(v + row(min(16 * I + 4 * lg + r, nt - 1)) * D + lr);
+
+  const uint64_t anc = ancestors(parent, lane);
+  if (block_depth(anc, lane < nt) > reach) return;          // the path kernel takes it
+  const float b = fe_flags & KDA_FE_BETA_LOGITS ? beta_logit(braw) : braw;
+  if (fe_flags & KDA_FE_L2NORM_QK) {
+#pragma unroll
+    for (int I = 0; I < kTB; ++I) {
+      float sk = 0.f, sq = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) { sk += kv[I][c] * kv[I][c]; sq += qv[I][c] * qv[I][c]; }
+      sk += __shfl_xor(sk, 16); sk += __shfl_xor(sk, 32);
+      sq += __shfl_xor(sq, 16); sq += __shfl_xor(sq, 32);
+      const float rk = inv_norm(sk, fe_eps), rq = inv_norm(sq, fe_eps);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) { kv[I][c] *= rk; qv[I][c] *= rq; }
+    }
+  }
+  // G by doubling inside each block, then on from the path's last node before it
+  double G[kTB][4];
+  static_for<0, kTB>([&](auto II) __attribute__((always_inline)) {
+    constexpr int I = decltype(II)::value;
+    const bool live = 16 * I + lr < nt;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (!live) kv[I][c] = qv[I][c] = 0.f;
+      G[I][c] = gate == KDA_GATE_NONE ? 0.0 : log2_alpha(gv[I][c], fe_flags & KDA_FE_GATE_LOGITS, g_min);
+    }
+    int up = __shfl(parent, 16 * I + lr);
+    while (__ballot(up >= 16 * I)) {
+      const int from = 16 * lg + (up & 15);
+      const bool on = up >= 16 * I;
+      const int next = __shfl(up, from);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const double x = __shfl(G[I][c], from);
+        G[I][c] += on ? x : 0.0;
+      }
+      up = on ? next : up;
+    }
+    static_for<0, I>([&](auto JJ) __attribute__((always_inline)) {
+      constexpr int J = decltype(JJ)::value;
+      const bool on = up >= 0 && up / 16 == J;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const double x = __shfl(G[J][c], 16 * lg + (up & 15));
+        G[I][c] += on ? x : 0.0;
+      }
+    });
+  });
+
+  // U, W, A and B (transposed products: acc[r] = element (row lr, column 4 lg + r))
+  f32x4 U[kTB], W[kTB], A[kTB][kTB], B[kTB][kTB];
+  uint64_t bad_d = 0, bad_o = 0;             // nodes with d, with o not finite in every column
+  auto note = [&](f32x4& x, int I, uint64_t& bits) __attribute__((always_inline)) {
+    const bool odd = !(is_finite(x[0]) && is_finite(x[1]) && is_finite(x[2]) && is_finite(x[3]));
+    uint64_t m = __ballot(odd);
+    if (m) {
+      m |= m >> 32;
+      m |= m >> 16;
+      bits |= (m & 0xffff) << (16 * I);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[r] = is_finite(x[r]) ? x[r] : 0.f;
+    }
+  };
+  static_for<0, kTB>([&](auto II) __attribute__((always_inline)) {
+    constexpr int I = decltype(II)::value;
+    U[I] = W[I] = f32x4{0.f, 0.f, 0.f, 0.f};
+    static_for<0, I + 1>([&](auto JJ) __attribute__((always_inline)) {
+      A[I][decltype(JJ)::value] = B[I][decltype(JJ)::value] = f32x4{0.f, 0.f, 0.f, 0.f};
+    });
+    if (16 * I < nt) {
+      const bool live = 16 * I + lr < nt;
+      Op::F4 ke, qe, kr, qr;
+      double R[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float hi = live ? (float)G[I][c] : -__builtin_inff(), lo = live ? (float)G[I][c] : __builtin_inff();
+        hi = fmaxf(hi, row_ror<8>(hi)); hi = fmaxf(hi, row_ror<4>(hi));
+        hi = fmaxf(hi, row_ror<2>(hi)); hi = fmaxf(hi, row_ror<1>(hi));
+        lo = fminf(lo, row_ror<8>(lo)); lo = fminf(lo, row_ror<4>(lo));
+        lo = fminf(lo, row_ror<2>(lo)); lo = fminf(lo, row_ror<1>(lo));
+        R[c] = 0.5 * ((double)hi + (double)lo);
+        const float e = exp2_wide(G[I][c]), er = live ? exp2_wide(G[I][c] - R[c]) : 0.f;
+        ke.x[c] = kv[I][c] * e;
+        qe.x[c] = qv[I][c] * e;
+        kr.x[c] = kv[I][c] * er;
+        qr.x[c] = qv[I][c] * er;
+      }
+      U[I] = Op::mma(ke, sf, U[I]);
+      W[I] = Op::mma(qe, sf, W[I]);
+      const uint64_t mine = __shfl((unsigned long long)anc, 16 * I + lr);
+      const float bi = -__shfl(b, 16 * I + lr);
+      static_for<0, I + 1>([&](auto JJ) __attribute__((always_inline)) {
+        constexpr int J = decltype(JJ)::value;
+        Op::F4 kq;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) kq.x[c] = kv[J][c] * exp2_wide(R[c] - G[J][c]);
+        f32x4 a = {0.f, 0.f, 0.f, 0.f}, bb = {0.f, 0.f, 0.f, 0.f};
+        a = Op::mma(kq, kr, a);
+        bb = Op::mma(kq, qr, bb);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int j = 16 * J + 4 * lg + r;
+          const bool on = live && (mine >> j & 1);
+          a[r] = on && j != 16 * I + lr ? bi * a[r] : 0.f;
+          bb[r] = on ? bb[r] : 0.f;
+        }
+        note(a, I, bad_d);
+        note(bb, I, bad_o);
+        A[I][J] = a;
+        B[I][J] = bb;
+      });
+    }
+  });
+
+  // d and o, block by block
+  Op::F4 d[kTB];
+  uint64_t bad = 0;                           // rows of the lane's column that are not finite
+  auto clean = [&](f32x4& x, int I) __attribute__((always_inline)) {
+    if (__ballot(!(is_finite(x[0]) && is_finite(x[1]) && is_finite(x[2]) && is_finite(x[3])))) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (!is_finite(x[r])) {
+          bad |= 1ull << (16 * I + 4 * lg + r);
+          x[r] = 0.f;
+        }
+    }
+  };
+  static_for<0, kTB>([&](auto II) __attribute__((always_inline)) {
+    constexpr int I = decltype(II)::value;
+    d[I].x = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (16 * I < nt) {
+      f32x4 x;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float bi = __shfl(b, 16 * I + 4 * lg + r);
+        x[r] = 16 * I + 4 * lg + r < nt ? bi * (vv[I][r] - U[I][r]) : 0.f;
+      }
+      static_for<0, I>([&](auto JJ) __attribute__((always_inline)) {
+        constexpr int J = decltype(JJ)::value;
+        x = Op::mma(Op::F4{A[I][J]}, d[J], x);
+      });
+      clean(x, I);
+      // (I - N)^-1 X by substitution: row lr of the inverse, last column first,
+      // N_ij from lane (j / 4, i)
+      float y[16];
+      static_for<0, 16>([&](auto C) __attribute__((always_inline)) {
+        constexpr int j = 15 - decltype(C)::value;
+        float s0 = j == lr ? 1.f : 0.f;
+        static_for<j + 1, 16>([&](auto K) __attribute__((always_inline)) {
+          constexpr int i = 16 + j - decltype(K)::value;
+          s0 += y[i] * __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, (float)A[I][I][j % 4]),
+                                                                          j / 4 * 16 + i));
+        });
+        y[j] = s0;
+        asm volatile("" : "+v"(y[j]));
+      });
+      f32x4 inv;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        inv[r] = lg < 2 ? (lg == 0 ? y[r] : y[4 + r]) : (lg == 2 ? y[8 + r] : y[12 + r]);
+      f32x4 z = {0.f, 0.f, 0.f, 0.f};
+      z = Op::mma(Op::F4{inv}, Op::make4(x), z);
+      clean(z, I);
+      d[I].x = z;
+    }
+  });
+  const bool any = __ballot(bad != 0) || bad_d || bad_o;
+  if (any) {
+    bad |= __shfl_xor((unsigned long long)bad, 16);
+    bad |= __shfl_xor((unsigned long long)bad, 32);
+    bad |= bad_d;
+  }
+  static_for<0, kTB>([&](auto II) __attribute__((always_inline)) {
+    constexpr int I = decltype(II)::value;
+    if (16 * I < nt) {
+      f32x4 y = W[I];
+      static_for<0, I + 1>([&](auto JJ) __attribute__((always_inline)) {
+        constexpr int J = decltype(JJ)::value;
+        y = Op::mma(Op::F4{B[I][J]}, d[J], y);
+      });
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * I + 4 * lg + r;
+        float out = scale * y[r];
+        if (any) {
+          const uint64_t mine = __shfl((unsigned long long)anc, i);
+          if ((mine & bad) || (bad_o >> i & 1)) out = __builtin_nanf("");
+        }
+        if (i < nt) Elem<TIn>::store(o + row(i) * D + lr, out);
+      }
+    }
+  });
+}
+
 template <int D, typename TIn>
-static hipError_t launch_paths(const TreeArgs& a, int skip_reach) {
+static hipError_t launch_paths(const TreeArgs& a, int taken) {
   const unsigned blocks = (unsigned)((int64_t)a.N * a.H);
   hipLaunchKernelGGL((tree_path_kernel<D, TIn>), dim3(blocks), dim3(256), path_lds_bytes<D>(a.T), a.stream,
                      (const TIn*)a.q, (const TIn*)a.k, (const TIn*)a.v, a.g, a.beta, a.state, a.parents,
                      a.num_nodes, (TIn*)a.o, a.H, a.T, a.scale, a.g_min, a.fe_flags, a.fe_eps, (int)a.gate,
-                     skip_reach);
+                     taken);
   return hipGetLastError();
 }
 
-template <int kTB, int kWaves, typename TIn, typename Op>
+template <int kTB, int kWaves, typename TIn, typename Op, bool kDeep>
 static hipError_t launch_tiles(const TreeArgs& a, int reach) {
   const unsigned blocks = (unsigned)((int64_t)a.N * a.H);
-  constexpr size_t lds = TileLds<kTB, kWaves, Op>::kBytes;
-  hipLaunchKernelGGL((tree_tile_kernel<kTB, kWaves, TIn, Op>), dim3(blocks), dim3(64 * kWaves), lds, a.stream,
+  constexpr size_t lds = TileLds<kTB, kWaves, Op, kDeep>::kBytes;
+  hipLaunchKernelGGL((tree_tile_kernel<kTB, kWaves, TIn, Op, kDeep>), dim3(blocks), dim3(64 * kWaves), lds, a.stream,
                      (const TIn*)a.q, (const TIn*)a.k, (const TIn*)a.v, a.g, a.beta, a.state, a.parents, a.num_nodes, (TIn*)a.o, a.H, a.T, a.scale, a.g_min, a.fe_flags,
                      a.fe_eps, (int)a.gate, reach);
   return hipGetLastError();
 }
 
+template <typename TIn, typename Op, bool kDeep>
+static hipError_t launch_blocks(const TreeArgs& a, int reach) {
+  switch ((a.T + 15) / 16) {
+    case 1: return launch_tiles<1, 4, TIn, Op, kDeep>(a, reach);
+    case 2: return launch_tiles<2, 8, TIn, Op, kDeep>(a, reach);
+    case 3: return launch_tiles<3, 8, TIn, Op, kDeep>(a, reach);
+    default: return launch_tiles<4, 8, TIn, Op, kDeep>(a, reach);
+  }
+}
+
 template <typename TIn, typename Op>
 static hipError_t launch_tree_128(const TreeArgs& a) {
-  // the deepest path whose decays span at most kMaxSpan; every tree if T does
-  const float deepest = a.gate == KDA_GATE_NONE || a.g_min == 0.f ? (float)kMaxNodes : kMaxSpan / -a.g_min;
-  const int reach = deepest >= (float)a.T ? 0 : (int)deepest;
-  if ((reach == 0 && deepest < 1.f) || (int64_t)a.H * 128 * 4 >= 1 << 24) return launch_paths<128, TIn>(a, 0);
+  const int reach = reach_of(kMaxSpread, a.g_min, a.gate);
+  // (the tile kernels' 24-bit row offsets: H D < 2^22)
+  if (reach < 1 || (int64_t)a.H * 128 * 4 >= 1 << 24) return launch_paths<128, TIn>(a, kNoneTaken);
+  if (reach_of(kMaxSpan, a.g_min, a.gate) >= a.T) return launch_blocks<TIn, Op, false>(a, 0);
+  const hipError_t e = launch_blocks<TIn, Op, true>(a, reach);
+  // (a block is at most T decays deep)
+  if (e != hipSuccess || reach >= a.T) return e;
+  return launch_paths<128, TIn>(a, reach);
+}
+
+template <int kTB, typename TIn>
+static hipError_t launch_small(const TreeArgs& a, int reach) {
+  const unsigned heads = (unsigned)((int64_t)a.N * a.H);
+  hipLaunchKernelGGL((tree_small_kernel<kTB, TIn>), dim3(heads / 4 + (heads % 4 != 0)), dim3(256), 0, a.stream,
+                     (const TIn*)a.q, (const TIn*)a.k, (const TIn*)a.v, a.g, a.beta, a.state, a.parents, a.num_nodes,
+                     (TIn*)a.o, heads, a.H, a.T, a.scale, a.g_min, a.fe_flags, a.fe_eps, (int)a.gate, reach);
+  return hipGetLastError();
+}
+
+template <typename TIn>
+static hipError_t launch_tree_16(const TreeArgs& a) {
+  const int reach = reach_of(kMaxSpread, a.g_min, a.gate);
+  if (reach < 1) return launch_paths<16, TIn>(a, kNoneTaken);
   hipError_t e;
   switch ((a.T + 15) / 16) {
-    case 1: e = launch_tiles<1, 4, TIn, Op>(a, reach); break;
-    case 2: e = launch_tiles<2, 8, TIn, Op>(a, reach); break;
-    case 3: e = launch_tiles<3, 8, TIn, Op>(a, reach); break;
-    default: e = launch_tiles<4, 8, TIn, Op>(a, reach);
+    case 1: e = launch_small<1, TIn>(a, reach); break;
+    case 2: e = launch_small<2, TIn>(a, reach); break;
+    case 3: e = launch_small<3, TIn>(a, reach); break;
+    default: e = launch_small<4, TIn>(a, reach);
   }
-  if (e != hipSuccess || reach == 0) return e;
-  return launch_paths<128, TIn>(a, reach);
+  // (a block is at most T decays deep)
+  if (e != hipSuccess || reach >= a.T) return e;
+  return launch_paths<16, TIn>(a, reach);
 }
 
 hipError_t launch_tree(const TreeArgs& a) {
   if (a.D == 128) return a.bf16 ? launch_tree_128<bf16_bits, SplitOp>(a) : launch_tree_128<float, FloatOp>(a);
-  return a.bf16 ? launch_paths<16, bf16_bits>(a, 0) : launch_paths<16, float>(a, 0);
+  return a.bf16 ? launch_tree_16<bf16_bits>(a) : launch_tree_16<float>(a);
 }
 
 // ---- commit of a path -------------------------------------------------------------

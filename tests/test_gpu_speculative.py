@@ -178,6 +178,49 @@ def test_a_nodes_nan_reaches_its_descendants_only(T, D, dtype, what):
         assert torch.equal(o[hit][:, rest], clean[hit][:, rest])
 
 
+@pytest.mark.parametrize("D,dtype", [(128, BF16), (128, F32), (16, BF16), (16, F32)])
+@pytest.mark.parametrize("T,g_min,flags,gate", [(64, -5.0, 0, 0), (40, -5.0, kda.FE_ALL, 0), (33, -2.5, 0, 1), (16, -5.0, 0, 0),
+                                                (48, -12.0, 0, 0), (64, -80.0, 0, 0)])
+def test_deep_trees(T, D, dtype, g_min, flags, gate):
+    """Decays that span more than fp32: chains, bushy trees, and branches that
+    mix deep and shallow nodes in one block (which no block's reference fits),
+    as sequences of one call."""
+    N, H = 5, 1
+    s = Step(N, T, H, D, dtype, 31 + T, gate, flags, g_min)
+    par = random_parents(N, T, "bushy", T)
+    par[0] = np.arange(T) - 1
+    par[1] = np.maximum(np.arange(T) - 2, -1)                # two chains, in turn
+    par[2] = np.arange(T) - 1
+    par[2, T // 2::3] = 0                                    # branches off the root beside the deep chain
+    nodes = np.array([T, T, T, T, T - 3], np.int32)
+    o = kda.decode_tree(*s.args, s.state, dev(par, torch.int32), dev(nodes, torch.int32), g_min=g_min, options=s.options)
+    s.check_tree(o, par, nodes)
+    assert torch.equal(o, kda.decode_tree(*s.args, s.state, dev(par, torch.int32), dev(nodes, torch.int32), g_min=g_min,
+                                          options=s.options))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_tree_of_very_many_heads(dtype):
+    """A row of all heads past 2^24 bytes (another kernel) against the same
+    memory as two sequences of half the heads."""
+    H, D = 32768, 128
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    q, k, v = (torch.randn(1, 1, H, D, device=DEV, generator=gen) for _ in range(3))
+    q, k = (x / x.norm(dim=-1, keepdim=True) for x in (q, k))
+    q, k, v = (x.to(dtype) for x in (q, k, v))
+    g = -torch.rand(1, 1, H, D, device=DEV, generator=gen)
+    b = torch.rand(1, 1, H, device=DEV, generator=gen)
+    st = 0.1 * torch.randn(1, H, D, D, device=DEV, generator=gen)
+    two = lambda x: x.reshape(2, -1, H // 2, *x.shape[3:])  # noqa: E731
+    o = kda.decode_tree(q, k, v, g, b, st).reshape(2, 1, H // 2, D)
+    ref = kda.decode_tree(*(two(x) for x in (q, k, v, g)), two(b), st.reshape(2, H // 2, D, D))
+    # one node: o = (E q) S + (q . k) d, terms below |q||S| + |d| < 8; both sides
+    # within (D + 22) 2^-24 (plus the operand splits) of it and a rounding of o
+    tol = 2 * 8 * (150 * 2.0 ** -24 + PRODUCT[dtype])
+    err = (o.float() - ref.float()).abs()
+    assert (err <= tol + (2.0 ** -7 if dtype is BF16 else 0.0) * ref.float().abs()).all()
+
+
 def test_tree_of_a_chain_is_the_token_decode():
     """The tree's outputs of a chain against kda_decode_tokens, which runs the
     recurrence: both within their bounds of the exact value, so within twice."""
