@@ -182,37 +182,52 @@ __device__ __forceinline__ void load_group(const T* row, int first, int a, int b
   }
 }
 
+// 16 bytes; kOnce: of a row that is read once, past the caches (the sums over
+// 256 x 2 rows of 131072: 57 us through them, 50 us past them, 5.3 TB/s).
+template <bool kOnce, typename T>
+__device__ __forceinline__ u32x4 load16(const T* p) {
+  if constexpr (kOnce) return __builtin_nontemporal_load((const u32x4*)p);
+  else return *(const u32x4*)p;
+}
+
 // f(element, p, q) for the elements of [a, b) that fall to thread tid of
-// `threads` (kQ = false: q is 0). Aligned groups run kUnroll at a time with
-// all their loads in flight; a group past the end is loaded again from the last one with
-// its values dropped, so there is no branch between the loads.
-template <bool kQ, int kUnroll = 4, typename T, typename F>
+// `threads` (kQ = false: q is 0). Aligned groups run eight at a time with all
+// their loads in flight, the rest four at a time: a group past the end is
+// loaded again from the last one with its values dropped, so there is no
+// branch between the loads, and f is called by all lanes together.
+template <bool kQ, bool kOnce, typename T, typename F>
 __device__ __forceinline__ void for_range(const T* p, const T* q, int a, int b, int tid, int threads, F&& f) {
   const int head = min((kPer<T> - skew(p + a)) % kPer<T>, b - a);
   const int groups = (b - a - head) / kPer<T>;
   const T *pg = p + a + head, *qg = kQ ? q + a + head : nullptr;
-  for (int base = 0; base < groups; base += threads * kUnroll) {
-    const int i = base + tid;
+  auto some = [&](int base, auto Unroll, auto Whole) __attribute__((always_inline)) {
+    constexpr int kUnroll = decltype(Unroll)::value;
+    constexpr bool kWhole = decltype(Whole)::value;
     u32x4 x[kUnroll], y[kUnroll];
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      const int at = min(i + k * threads, groups - 1);
-      x[k] = *(const u32x4*)(pg + at * kPer<T>);
-      if (kQ) y[k] = *(const u32x4*)(qg + at * kPer<T>);
+      const int i = base + tid + k * threads, at = kWhole ? i : min(i, groups - 1);
+      x[k] = load16<kOnce>(pg + at * kPer<T>);
+      if (kQ) y[k] = load16<kOnce>(qg + at * kPer<T>);
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      const bool on = i + k * threads < groups;
-      if (!on) x[k] = u32x4{0, 0, 0, 0};
+      const int i = base + tid + k * threads;
+      if (!kWhole && i >= groups) x[k] = u32x4{0, 0, 0, 0};
       T u[kPer<T>], w[kPer<T>];
       *(u32x4*)u = x[k];
       if (kQ) *(u32x4*)w = y[k];
 #pragma unroll
       for (int j = 0; j < kPer<T>; ++j)
-        f(a + head + (i + k * threads) * kPer<T> + j, weight<T>(u[j]), kQ ? weight<T>(w[j]) : 0.0);
+        f(a + head + i * kPer<T> + j, weight<T>(u[j]), kQ ? weight<T>(w[j]) : 0.0);
     }
-  }
+  };
+  int base = 0;
+  if constexpr (kOnce)                // (the walk's registers hold four)
+    for (; base + 8 * threads <= groups; base += 8 * threads)
+      some(base, std::integral_constant<int, 8>{}, std::true_type{});
+  for (; base < groups; base += 4 * threads) some(base, std::integral_constant<int, 4>{}, std::false_type{});
   const int tail = a + head + groups * kPer<T>;
   const int x = tid < head ? a + tid : tail + (tid - head);     // fewer than 2 kPer, all in one turn
   double wp = 0.0, wq = 0.0;
@@ -269,7 +284,7 @@ __global__ __launch_bounds__(kWalkThreads) void walk_kernel(
   walk<T>(d, true, nt, lane, cur, count, spent, accepted, [&](int at, double C) {
     const size_t row = ((size_t)n * T_ + at) * (size_t)V;
     double sum = 0.0;
-    for_range<true, 8>(target + row, draft + row, 0, V, tid, kWalkThreads,
+    for_range<true, false>(target + row, draft + row, 0, V, tid, kWalkThreads,
                        [&](int, double p, double q) { sum += residual(p, q, C); });
     sum = wave_sum(sum);
     // two buffers in turn: a wave may start the next sum while another still
@@ -320,25 +335,25 @@ __global__ __launch_bounds__(256) void sums_kernel(
   if constexpr (kDraft) {
     // the row of q matters only after a rejection
     if (spent > 0.0)
-      for_range<true>(target + row, draft + row, a, b, lane, kWave, [&](int, double p, double q) {
+      for_range<true, true>(target + row, draft + row, a, b, lane, kWave, [&](int, double p, double q) {
         rs += residual(p, q, spent);
         ps += p;
       });
     else
-      for_range<false>(target + row, (const T*)nullptr, a, b, lane, kWave, [&](int, double p, double) { ps += p; });
+      for_range<false, true>(target + row, (const T*)nullptr, a, b, lane, kWave, [&](int, double p, double) { ps += p; });
     if (!(spent > 0.0)) rs = ps;
   } else {
     const int gone = gone_token(tokens, parents, n, T_, nt, cur, lane);
     const uint64_t here = __ballot(gone >= a && gone < b);
     if (here)
-      for_range<false>(target + row, (const T*)nullptr, a, b, lane, kWave, [&](int x, double p, double) {
+      for_range<false, true>(target + row, (const T*)nullptr, a, b, lane, kWave, [&](int x, double p, double) {
         bool out = false;
         for (uint64_t m = here; m; m &= m - 1) out |= x == __builtin_amdgcn_readlane(gone, __builtin_ctzll(m));
         rs += out ? 0.0 : p;
         ps += p;
       });
     else
-      for_range<false>(target + row, (const T*)nullptr, a, b, lane, kWave, [&](int, double p, double) { ps += p; });
+      for_range<false, true>(target + row, (const T*)nullptr, a, b, lane, kWave, [&](int, double p, double) { ps += p; });
     if (!here) rs = ps;
   }
   rs = wave_sum(rs);
