@@ -80,6 +80,13 @@ bool aligned16(std::initializer_list<const void*> ps) {
   return true;
 }
 
+// Arrays read one 4-byte element at a time need their natural alignment only.
+bool aligned4(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if ((uintptr_t)p & 3) return false;
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -312,6 +319,13 @@ kda_status kda_decode_tokens(const void* q, const void* k, const void* v, kda_dt
   return from_hip(kda::launch_decode(a));
 }
 
+// A launch takes fewer than 2^32 threads: one workgroup of 256 per head, or of
+// 1024 per sequence (and up to 16 of 256) of a verification.
+constexpr int64_t kMaxHeads = KDA_MAX_LAUNCH_HEADS;
+static_assert(kMaxHeads * 256 < 1ll << 32, "workgroups of the tree, commit and cache kernels");
+static_assert(KDA_VERIFY_MAX_SEQS * 1024ll < 1ll << 32 && KDA_VERIFY_MAX_SEQS * 16ll * 256 < 1ll << 32,
+              "workgroups of the verification kernels");
+
 // Tree step: the checks kda_decode_tree and kda_commit_path share, in the order
 // of kda_decode_tokens.
 namespace {
@@ -322,9 +336,14 @@ kda_status tree_args_ok(int dt, const kda_options* opt, int32_t N, int32_t T, in
   if (!supported_dims(Dk, Dv)) return KDA_ERR_UNSUPPORTED;
   if (T < 1 || T > KDA_TREE_MAX_NODES) return KDA_ERR_INVALID_ARG;
   if (!decode_floor_ok(g_min)) return KDA_ERR_INVALID_ARG;
-  if (N < 0 || H <= 0 || (int64_t)N * T > INT32_MAX || (int64_t)N * T * H > INT32_MAX)
+  if (N < 0 || H <= 0 || (int64_t)N * H > kMaxHeads || (int64_t)N * T * H > INT32_MAX)
     return KDA_ERR_INVALID_ARG;
   return KDA_OK;
+}
+
+bool verify_sizes_ok(int32_t N, int32_t T, int32_t V) {
+  return N >= 0 && N <= KDA_VERIFY_MAX_SEQS && T >= 1 && T <= KDA_TREE_MAX_NODES && V >= 1 &&
+         V <= KDA_VERIFY_MAX_VOCAB;
 }
 }  // namespace
 
@@ -338,7 +357,7 @@ kda_status kda_decode_tree(const void* q, const void* k, const void* v, kda_dtyp
   if (st != KDA_OK || N == 0) return st;
   const bool need_g = gate_of(opt) != KDA_GATE_NONE;
   if (!q || !k || !v || (need_g && !g) || !beta || !state || !o) return KDA_ERR_INVALID_ARG;
-  if (!aligned16({q, k, v, g, beta, state, o, parents, num_nodes})) return KDA_ERR_INVALID_ARG;
+  if (!aligned16({q, k, v, g, beta, state, o}) || !aligned4({parents, num_nodes})) return KDA_ERR_INVALID_ARG;
   kda::TreeArgs a;
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.state = const_cast<float*>(state); a.o = o;
   a.parents = parents; a.num_nodes = num_nodes;
@@ -361,7 +380,7 @@ kda_status kda_commit_path(const void* k, const void* v, kda_dtype dtype, const 
   if (st != KDA_OK || N == 0) return st;
   const bool need_g = gate_of(opt) != KDA_GATE_NONE;
   if (!k || !v || (need_g && !g) || !beta || !state || !path || !accept) return KDA_ERR_INVALID_ARG;
-  if (!aligned16({k, v, g, beta, state, path, accept})) return KDA_ERR_INVALID_ARG;
+  if (!aligned16({k, v, g, beta, state}) || !aligned4({path, accept})) return KDA_ERR_INVALID_ARG;
   kda::TreeArgs a;
   a.q = nullptr; a.k = k; a.v = v; a.g = g; a.beta = beta; a.state = state; a.o = nullptr;
   a.parents = nullptr; a.num_nodes = nullptr;
@@ -376,8 +395,7 @@ kda_status kda_commit_path(const void* k, const void* v, kda_dtype dtype, const 
 }
 
 size_t kda_verify_workspace_size(int32_t N, int32_t T, int32_t V) {
-  if (N < 0 || T < 1 || T > KDA_TREE_MAX_NODES || V < 1 ||
-      V > KDA_VERIFY_MAX_VOCAB || (int64_t)N * T > INT32_MAX) return 0;
+  if (!verify_sizes_ok(N, T, V)) return 0;
   return kda::verify_workspace(N, T, V);
 }
 
@@ -388,12 +406,11 @@ kda_status kda_verify_drafts(const void* target, const void* draft, kda_dtype dt
                              void* workspace, size_t workspace_bytes, hipStream_t stream) {
   const int dt = enum_code(dtype);
   if (dt != KDA_BF16 && dt != KDA_F32) return KDA_ERR_UNSUPPORTED;
-  if (N < 0 || T < 1 || T > KDA_TREE_MAX_NODES || V < 1 ||
-      V > KDA_VERIFY_MAX_VOCAB || (int64_t)N * T > INT32_MAX)
-    return KDA_ERR_INVALID_ARG;
+  if (!verify_sizes_ok(N, T, V)) return KDA_ERR_INVALID_ARG;
   if (N == 0) return KDA_OK;
   if (!target || !tokens || !uniforms || !accept || !path || !next_token) return KDA_ERR_INVALID_ARG;
-  if (!aligned16({target, draft, tokens, parents, num_nodes, uniforms, accept, path, next_token}))
+  if (!aligned16({target, draft}) ||
+      !aligned4({tokens, parents, num_nodes, uniforms, accept, path, next_token}))
     return KDA_ERR_INVALID_ARG;
   if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < kda::verify_workspace(N, T, V))
     return KDA_ERR_WORKSPACE;
@@ -416,10 +433,10 @@ kda_status cache_args(const void* states, const int32_t* slots, const void* valu
                       hipStream_t stream, kda::CacheArgs* a) {
   if (format != KDA_CACHE_INT8 && format != KDA_CACHE_E4M3) return KDA_ERR_UNSUPPORTED;
   if (!supported_dims(Dk, Dv)) return KDA_ERR_UNSUPPORTED;
-  if (N < 0 || num_slots < 0 || H <= 0 || (int64_t)N * H > INT32_MAX) return KDA_ERR_INVALID_ARG;
+  if (N < 0 || num_slots < 0 || H <= 0 || (int64_t)N * H > kMaxHeads) return KDA_ERR_INVALID_ARG;
   if (!slots && N > num_slots) return KDA_ERR_INVALID_ARG;
   if (N > 0 && (!states || (num_slots > 0 && (!values || !scales)))) return KDA_ERR_INVALID_ARG;
-  if (!aligned16({states, slots, values, scales})) return KDA_ERR_INVALID_ARG;
+  if (!aligned16({states, values, scales}) || !aligned4({slots})) return KDA_ERR_INVALID_ARG;
   a->states = (float*)states; a->slots = slots;
   a->values = (void*)values; a->scales = (uint8_t*)scales;
   a->N = N; a->num_slots = num_slots; a->H = H; a->D = Dk;

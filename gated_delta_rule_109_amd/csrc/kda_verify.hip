@@ -221,13 +221,15 @@ __device__ __forceinline__ void for_range(const T* p, const T* q, int a, int b, 
 #pragma unroll
       for (int j = 0; j < kPer<T>; ++j)
         f(a + head + i * kPer<T> + j, weight<T>(u[j]), kQ ? weight<T>(w[j]) : 0.0);
+      if (!kOnce) __builtin_amdgcn_sched_barrier(0);   // one group's fp64 values at a time
     }
   };
   int base = 0;
-  if constexpr (kOnce)                // (the walk's registers hold four)
-    for (; base + 8 * threads <= groups; base += 8 * threads)
-      some(base, std::integral_constant<int, 8>{}, std::true_type{});
-  for (; base < groups; base += 4 * threads) some(base, std::integral_constant<int, 4>{}, std::false_type{});
+  for (; base + 8 * threads <= groups; base += 8 * threads)
+    some(base, std::integral_constant<int, 8>{}, std::true_type{});
+  constexpr int kRest = kOnce ? 4 : 8;   // a walk's sum is one round trip to memory
+#pragma unroll 1
+  for (; base < groups; base += kRest * threads) some(base, std::integral_constant<int, kRest>{}, std::false_type{});
   const int tail = a + head + groups * kPer<T>;
   const int x = tid < head ? a + tid : tail + (tid - head);     // fewer than 2 kPer, all in one turn
   double wp = 0.0, wq = 0.0;
@@ -285,7 +287,7 @@ __global__ __launch_bounds__(kWalkThreads) void walk_kernel(
     const size_t row = ((size_t)n * T_ + at) * (size_t)V;
     double sum = 0.0;
     for_range<true, false>(target + row, draft + row, 0, V, tid, kWalkThreads,
-                       [&](int, double p, double q) { sum += residual(p, q, C); });
+                           [&](int, double p, double q) { sum += residual(p, q, C); });
     sum = wave_sum(sum);
     // two buffers in turn: a wave may start the next sum while another still
     // reads this one, but not the one after it

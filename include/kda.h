@@ -348,8 +348,13 @@ kda_status kda_decode_tokens(const void* q, const void* k, const void* v, kda_dt
  *     NULL means chains: node i follows node i - 1.
  *   - num_nodes [N] int32 (device), or NULL for T nodes each: sequence n uses
  *     its first num_nodes[n] nodes (clamped to [0, T]). Nothing of the others
- *     is read, and their rows of o are left as they were. */
+ *     is read, and their rows of o are left as they were.
+ *   - int32 arrays and uniforms need 4-byte alignment only (a slice of them
+ *     will do); every other tensor 16, as everywhere. */
 #define KDA_TREE_MAX_NODES 64
+/* Most heads of all sequences together (N * H) that one call of the tree step
+ * or of the state cache takes. */
+#define KDA_MAX_LAUNCH_HEADS 16777215
 
 /* Attention of a tree of T drafted tokens per sequence over its recurrent
  * state. Every node's output is the recurrence's output after the tokens on
@@ -364,8 +369,13 @@ kda_status kda_decode_tokens(const void* q, const void* k, const void* v, kda_dt
  *   o       [N, T, H, Dv] dtype; must not overlap the inputs
  * A node whose inputs are not finite, or overflow, makes outputs of itself and
  * its descendants non-finite, and no others.
- * T outside [1, KDA_TREE_MAX_NODES] is KDA_ERR_INVALID_ARG; the other errors
- * are those of kda_decode_tokens. */
+ * T outside [1, KDA_TREE_MAX_NODES] and N * H above KDA_MAX_LAUNCH_HEADS are
+ * KDA_ERR_INVALID_ARG; the other errors are those of kda_decode_tokens.
+ * Cost: one pass over the state and the tokens while the decays of a tree span
+ * at most 2^87 (T * -g_min <= 60); with lower floors A and B are formed with
+ * a reference per 16 nodes (about three times the time at 64 nodes), and trees
+ * that mix deep and shallow branches within 16 consecutive nodes, or floors
+ * below -83, run pair by pair. */
 kda_status kda_decode_tree(const void* q, const void* k, const void* v, kda_dtype dtype,
                            const float* g, const float* beta, const float* state,
                            const int32_t* parents, const int32_t* num_nodes, void* o, int32_t N,
@@ -385,8 +395,9 @@ kda_status kda_commit_path(const void* k, const void* v, kda_dtype dtype, const 
                            const int32_t* accept, int32_t N, int32_t T, int32_t H, int32_t Dk,
                            int32_t Dv, float g_min, const kda_options* opt, hipStream_t stream);
 
-/* Largest vocabulary kda_verify_drafts takes. */
+/* Largest vocabulary and most sequences kda_verify_drafts takes. */
 #define KDA_VERIFY_MAX_VOCAB (1 << 24)
+#define KDA_VERIFY_MAX_SEQS ((1 << 20) - 1)
 
 /* Bytes of device workspace kda_verify_drafts needs (0 for sizes it refuses).
  * It needs no initialisation; calls that may overlap need one each. */
@@ -424,10 +435,10 @@ size_t kda_verify_workspace_size(int32_t N, int32_t T, int32_t V);
  * For chains, accept is the accept of kda_decode_tokens.
  *   workspace   256-byte aligned device scratch of
  *               kda_verify_workspace_size(N, T, V) bytes
- * target and draft must be 16-byte aligned, as every tensor; V may be odd.
- * Errors: KDA_ERR_INVALID_ARG (null required pointer, N < 0, T outside
- * [1, KDA_TREE_MAX_NODES], V outside [1, KDA_VERIFY_MAX_VOCAB], N * T above
- * INT32_MAX), KDA_ERR_UNSUPPORTED
+ * V may be odd.
+ * Errors: KDA_ERR_INVALID_ARG (null required pointer, N outside
+ * [0, KDA_VERIFY_MAX_SEQS], T outside [1, KDA_TREE_MAX_NODES], V outside
+ * [1, KDA_VERIFY_MAX_VOCAB]), KDA_ERR_UNSUPPORTED
  * (dtype), KDA_ERR_WORKSPACE, KDA_ERR_HIP. */
 kda_status kda_verify_drafts(const void* target, const void* draft, kda_dtype dtype,
                              const int32_t* tokens, const int32_t* parents,
@@ -456,13 +467,14 @@ typedef enum { KDA_CACHE_INT8 = 0, KDA_CACHE_E4M3 = 1 } kda_cache_format;
 
 /* Writes N states into the cache.
  *   states  [N, H, Dk, Dv] fp32
- *   slots   [N] int32 (device): the slot of each state, or NULL for slot n. A
+ *   slots   [N] int32 (device, 4-byte aligned): the slot of each state, or NULL
+ *           for slot n. A
  *           state whose slot is outside [0, num_slots) is not written. Where
  *           two states name one slot, the later one is written.
  *   values  [num_slots, H, Dk, Dv] 8-bit;  scales [num_slots, H, Dk * Dv / 32]
  *           uint8, e + 127. Slots that are not named are left as they were.
  * Errors: KDA_ERR_INVALID_ARG (null required pointer, N or num_slots < 0,
- * H <= 0, N * H above INT32_MAX, without slots N > num_slots),
+ * H <= 0, N * H above KDA_MAX_LAUNCH_HEADS, without slots N > num_slots),
  * KDA_ERR_UNSUPPORTED (head size or format), KDA_ERR_HIP. */
 kda_status kda_state_store(const float* states, const int32_t* slots, void* values,
                            uint8_t* scales, kda_cache_format format, int32_t N,

@@ -148,20 +148,22 @@ def test_tree_of_each_sequences_own_size(T, D, dtype):
     assert (o[~live] == 42.0).all()
 
 
-@pytest.mark.parametrize("T,D,dtype", [(16, 128, BF16), (50, 128, BF16), (21, 128, F32), (16, 16, F32)])
+@pytest.mark.parametrize("T,D,dtype,g_min", [(16, 128, BF16, LN_HALF), (50, 128, BF16, LN_HALF), (21, 128, F32, LN_HALF),
+                                             (16, 16, F32, LN_HALF), (50, 128, BF16, -5.0), (20, 128, F32, -5.0),
+                                             (50, 16, BF16, -5.0), (9, 128, F32, -100.0)])
 @pytest.mark.parametrize("what", ["v", "k", "q", "beta"])
-def test_a_nodes_nan_reaches_its_descendants_only(T, D, dtype, what):
-    s = Step(1, T, 2, D, dtype, 21)
+def test_a_nodes_nan_reaches_its_descendants_only(T, D, dtype, g_min, what):
+    s = Step(1, T, 2, D, dtype, 21, g_min=g_min)
     par = random_parents(1, T, "bushy", 8)
     p = dev(par, torch.int32)
-    clean = kda.decode_tree(*s.args, s.state, p)
+    clean = kda.decode_tree(*s.args, s.state, p, g_min=g_min)
     i = 3
     x = s.args[["q", "k", "v", "g", "beta"].index(what)]
     if what == "beta":
         x[0, i, 1] = float("inf")
     else:
         x[0, i, 1, 5] = float("nan")
-    o = kda.decode_tree(*s.args, s.state, p)
+    o = kda.decode_tree(*s.args, s.state, p, g_min=g_min)
     below = {i}
     for t in range(i + 1, T):
         if int(par[0, t]) in below:
@@ -361,6 +363,20 @@ def test_verify_edges():
             check_verify(x, None, np.array([[0, t, t, t]], np.int32), u, star)
 
 
+def test_verify_of_a_chain_given_as_a_tree():
+    """parents that spell chains out give what no parents give (other kernels)."""
+    rng = np.random.default_rng(3)
+    N, T, V = 9, 6, 3003
+    target, draft = probabilities(rng, N, T, V, BF16)
+    tokens = rng.integers(0, V, (N, T)).astype(np.int32)
+    tokens[:, 1:] = draft[:, :-1].float().argmax(-1).numpy()
+    u = rng.random((N, T)).astype(np.float32)
+    for d in (draft, None):
+        a = check_verify(target, d, tokens, u, None)
+        b = check_verify(target, d, tokens, u, random_parents(N, T, "chain", 0))
+        assert [x.tolist() for x in a] == [x.tolist() for x in b]
+
+
 def test_verify_rejects_a_near_certain_token_exactly():
     """One token holds all but 2^-60 of a row: without it the residual is the
     rest, which no subtraction of sums may lose."""
@@ -461,6 +477,47 @@ def test_cache_reads_every_code():
         with np.errstate(over="ignore", invalid="ignore"):
             want = speculative.dequantise(vals, cache.scales.cpu().numpy()).astype(np.float32).reshape(got.shape)
         np.testing.assert_array_equal(got, want)
+
+
+def test_offsets_past_32_bits():
+    """States of 4.4 G values, a cache of 2.2 G and rows of 2.2 G probabilities:
+    the last sequence gives what it gives alone."""
+    N, T, H, D = 4200, 2, 64, 128
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    one = Step(1, T, H, D, BF16, 6)
+    args = [x.expand(N, *x.shape[1:]).contiguous() for x in one.args]
+    state = torch.zeros(N, H, D, D, device=DEV)
+    state[-1] = one.state[0]
+    assert state.numel() > 2 ** 32
+    o = kda.decode_tree(*args, state)
+    assert torch.equal(o[-1], kda.decode_tree(*one.args, one.state)[0])
+    assert torch.equal(o[7], kda.decode_tree(*one.args, torch.zeros_like(one.state))[0])
+    path = torch.zeros(N, T, device=DEV, dtype=torch.int32)
+    path[:, 1] = 1
+    accept = torch.zeros(N, device=DEV, dtype=torch.int32)
+    accept[-1] = 2
+    kda.commit_path(*args[1:], state, path, accept)
+    kda.commit_path(*one.args[1:], one.state, path[-1:], torch.full((1,), 2, device=DEV, dtype=torch.int32))
+    assert torch.equal(state[-1], one.state[0])
+    cache = kda.make_state_cache(2100, H, D, DEV)
+    assert cache.values.numel() > 2 ** 31
+    slots = torch.full((1,), 2099, device=DEV, dtype=torch.int32)
+    kda.state_store(one.state, cache, slots)
+    small = kda.make_state_cache(1, H, D, DEV)
+    kda.state_store(one.state, small)
+    assert torch.equal(kda.state_load(cache, slots), kda.state_load(small))
+    del state, args, o, cache
+    N, T, V = 17, 64, 2000003
+    target = torch.zeros(N, T, V, device=DEV, dtype=BF16)
+    assert target.numel() > 2 ** 31
+    target[-1, :, -9:] = torch.rand(T, 9, device=DEV, generator=gen).to(BF16)
+    tokens = torch.full((N, T), V - 1, device=DEV, dtype=torch.int32)
+    u = torch.rand(N, T, device=DEV, generator=gen)
+    u[-1, 1:60] = 0.0
+    many = kda.verify_drafts(target, None, tokens, u)
+    alone = kda.verify_drafts(target[-1:].contiguous(), None, tokens[-1:], u[-1:].contiguous())
+    assert [x[-1].tolist() for x in many] == [x[0].tolist() for x in alone]
+    assert int(many[0][-1]) >= 60 and V - 9 <= int(many[2][-1]) < V and many[2][0] == -1
 
 
 def full_step(s, par, target, draft, tokens, u, nodes, cache, slots, ws):
