@@ -12,9 +12,8 @@
 // passes a threshold, and in fp32 the sum's rounding would be as wide as many
 // tokens. Bound by the bytes of the rows p and q of the last node.
 //
-// Three steps: the walk down the tree (alone in its kernel only when masses
-// are summed), the partial sums of the last node's r over chunks of the
-// vocabulary, and the choice of the token inside one chunk.
+// Three steps: the walk down the tree, the partial sums of the last node's r
+// over chunks of the vocabulary, and the choice of the token inside one chunk.
 #include "kda_device.h"
 #include "kda_internal.h"
 
@@ -51,6 +50,26 @@ VerifyPlan verify_plan(int32_t N, int32_t V) {
   p.sums = up(sizeof(Walk) * (size_t)N);
   p.total = p.sums + up(2 * sizeof(double) * (size_t)N * p.chunks);
   return p;
+}
+
+// Whether one workgroup per sequence does all of it (whole_kernel), or the
+// rows are spread over the GPU (walk, sums, choose). The first saves one or two
+// launches and a second read of the nodes; the second is faster where few
+// compute units would read long rows, or where the sequences are a little more
+// than the 256 compute units that each hold one such workgroup. Measured, T = 4
+// to 8, fp32, whole / spread in us:
+//   chains with draft rows        N 48        256        320
+//     V  8192                     13 / 15     12 / 15
+//     V 40000                     15 / 19     17 / 21    32 / 27
+//     V 131072                    28 / 19     51 / 60    71 / 58
+//   trees with draft rows         N 8         48         256        768
+//     V 65536                     25 / 25     32 / 36    48 / 63    83 / 91
+//     V 131072                    44 / 39     49 / 56    88 / 103   156 / 165
+// (in trees the walk itself takes one workgroup per sequence).
+bool whole(int32_t N, int32_t V, bool sampled_tree) {
+  if (sampled_tree) return V <= 65536 || N >= 32;
+  if (V <= 16384) return N <= 1024;
+  return N <= 256 && (V <= 49152 || N >= 160);
 }
 
 // A stored probability; whatever is no finite positive number counts as 0.
@@ -270,6 +289,30 @@ __device__ __forceinline__ bool is_gone(const Gone& gone, int x) {
 // fixed order, so all waves take the same turns.
 constexpr int kWalkThreads = 1024;
 template <typename T>
+struct Mass {
+  const T *target, *draft;
+  uint32_t n;
+  int T_, V, tid, turn = 0;
+  __device__ __forceinline__ double operator()(int at, double C) {
+    __shared__ double s_sum[2][kWalkThreads / kWave];
+    const size_t row = ((size_t)n * T_ + at) * (size_t)V;
+    double sum = 0.0;
+    for_range<true, false>(target + row, draft + row, 0, V, tid, kWalkThreads,
+                           [&](int, double p, double q) { sum += residual(p, q, C); });
+    sum = wave_sum(sum);
+    // two buffers in turn: a wave may start the next sum while another still
+    // reads this one, but not the one after it
+    if (tid % kWave == 0) s_sum[turn][tid / kWave] = sum;
+    __syncthreads();
+    double total = 0.0;
+#pragma unroll
+    for (int w = 0; w < kWalkThreads / kWave; ++w) total += s_sum[turn][w];
+    turn ^= 1;
+    return total;
+  }
+};
+
+template <typename T>
 __global__ __launch_bounds__(kWalkThreads) void walk_kernel(
     const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
     const int32_t* __restrict__ parents, const int32_t* __restrict__ num_nodes,
@@ -278,28 +321,39 @@ __global__ __launch_bounds__(kWalkThreads) void walk_kernel(
   const uint32_t n = blockIdx.x;
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int nt = node_count(num_nodes, n, T_);
-  __shared__ double s_sum[2][kWalkThreads / kWave];
   const Nodes<T> d = load_nodes<T>(target, draft, tokens, parents, uniforms, n, T_, nt, V, lane);
-  int cur, count, turn = 0;
+  int cur, count;
   double spent;
   uint64_t accepted;
-  walk<T>(d, true, nt, lane, cur, count, spent, accepted, [&](int at, double C) {
-    const size_t row = ((size_t)n * T_ + at) * (size_t)V;
-    double sum = 0.0;
-    for_range<true, false>(target + row, draft + row, 0, V, tid, kWalkThreads,
-                           [&](int, double p, double q) { sum += residual(p, q, C); });
-    sum = wave_sum(sum);
-    // two buffers in turn: a wave may start the next sum while another still
-    // reads this one, but not the one after it
-    if (lane == 0) s_sum[turn][wave] = sum;
-    __syncthreads();
-    double total = 0.0;
-#pragma unroll
-    for (int w = 0; w < kWalkThreads / kWave; ++w) total += s_sum[turn][w];
-    turn ^= 1;
-    return total;
-  });
+  Mass<T> mass{target, draft, n, T_, V, tid};
+  walk<T>(d, true, nt, lane, cur, count, spent, accepted, [&](int at, double C) { return mass(at, C); });
   if (wave == 0) write_walk(lane, n, T_, nt, cur, count, spent, accepted, accept, path, next_token, walks);
+}
+
+// Sums of r and p over elements [a, b) of the last node's row, by one wave.
+// gone: lane t's rejected token (without draft rows), or -1.
+template <typename T, bool kDraft>
+__device__ __forceinline__ void wave_sums(const T* p, const T* q, double spent, int gone, int a, int b, int lane,
+                                          double& rs, double& ps) {
+  rs = ps = 0.0;
+  const uint64_t here = kDraft ? 0 : __ballot(gone >= a && gone < b);
+  if (kDraft && spent > 0.0)            // (the row of q matters only after a rejection)
+    for_range<true, true>(p, q, a, b, lane, kWave, [&](int, double x, double y) {
+      rs += residual(x, y, spent);
+      ps += x;
+    });
+  else if (here)
+    for_range<false, true>(p, (const T*)nullptr, a, b, lane, kWave, [&](int at, double x, double) {
+      bool out = false;
+      for (uint64_t m = here; m; m &= m - 1) out |= at == __builtin_amdgcn_readlane(gone, __builtin_ctzll(m));
+      rs += out ? 0.0 : x;
+      ps += x;
+    });
+  else
+    for_range<false, true>(p, (const T*)nullptr, a, b, lane, kWave, [&](int, double x, double) { ps += x; });
+  if (!(kDraft && spent > 0.0) && !here) rs = ps;
+  rs = wave_sum(rs);
+  ps = wave_sum(ps);
 }
 
 // Partial sums of the last node's r (and of p, for the case that r is 0
@@ -333,33 +387,9 @@ __global__ __launch_bounds__(256) void sums_kernel(
   if (nt == 0) return;
   const size_t row = ((size_t)n * T_ + cur) * (size_t)V;
   const int a = part * chunk, b = min(V - a, chunk) + a;
-  double rs = 0.0, ps = 0.0;
-  if constexpr (kDraft) {
-    // the row of q matters only after a rejection
-    if (spent > 0.0)
-      for_range<true, true>(target + row, draft + row, a, b, lane, kWave, [&](int, double p, double q) {
-        rs += residual(p, q, spent);
-        ps += p;
-      });
-    else
-      for_range<false, true>(target + row, (const T*)nullptr, a, b, lane, kWave, [&](int, double p, double) { ps += p; });
-    if (!(spent > 0.0)) rs = ps;
-  } else {
-    const int gone = gone_token(tokens, parents, n, T_, nt, cur, lane);
-    const uint64_t here = __ballot(gone >= a && gone < b);
-    if (here)
-      for_range<false, true>(target + row, (const T*)nullptr, a, b, lane, kWave, [&](int x, double p, double) {
-        bool out = false;
-        for (uint64_t m = here; m; m &= m - 1) out |= x == __builtin_amdgcn_readlane(gone, __builtin_ctzll(m));
-        rs += out ? 0.0 : p;
-        ps += p;
-      });
-    else
-      for_range<false, true>(target + row, (const T*)nullptr, a, b, lane, kWave, [&](int, double p, double) { ps += p; });
-    if (!here) rs = ps;
-  }
-  rs = wave_sum(rs);
-  ps = wave_sum(ps);
+  const int gone = kDraft ? -1 : gone_token(tokens, parents, n, T_, nt, cur, lane);
+  double rs, ps;
+  wave_sums<T, kDraft>(target + row, draft + row, spent, gone, a, b, lane, rs, ps);
   if (lane < 2) sums[((size_t)n * chunks + part) * 2 + lane] = lane ? ps : rs;
 }
 
@@ -374,58 +404,36 @@ __device__ __forceinline__ double wave_scan(double x, int lane) {
 }
 
 // The next token: the chunk where the running sum of r passes u * sum(r), then
-// the token inside it. One workgroup per sequence; a tile of the chunk is kRun
-// consecutive elements per thread. Where rounding leaves the threshold past
-// the last sum, the last token with r > 0 is taken.
-template <typename T, bool kDraft>
-__global__ __launch_bounds__(256) void choose_kernel(
-    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
-    const int32_t* __restrict__ parents, const int32_t* __restrict__ num_nodes,
-    const float* __restrict__ uniforms, int32_t* __restrict__ next_token, int T_, int V, int chunk, int chunks,
-    const Walk* __restrict__ walks, const double* __restrict__ sums) {
-  constexpr int kRun = 16;
-  const uint32_t n = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  const int nt = node_count(num_nodes, n, T_);
-  if (nt == 0) return;
-  __shared__ double s_sum[4];
-  __shared__ int s_last[4];
+// the token inside it. r, p: the sums of chunk `lane`. A tile of the chunk is
+// kRun consecutive elements per thread. Where rounding leaves the threshold
+// past the last sum, the last token with r > 0 is taken. Returns the token, in
+// every thread; -1 if p is 0 everywhere.
+template <typename T, bool kDraft, int kThreads, int kRun>
+__device__ __forceinline__ int choose(const T* tp, const T* tq, double spent, double u, double r, double p, int gone,
+                                      int V, int chunk, int tid) {
+  constexpr int kWaves = kThreads / kWave;
+  const int lane = tid % kWave, wave = tid / kWave;
+  __shared__ double s_sum[kWaves];
+  __shared__ int s_last[kWaves];
   __shared__ int s_token;
   __shared__ Gone s_gone;
-  const int cur = walks[n].node;
-  double spent = walks[n].spent;
-  // every wave: the chunk sums, their total and the chunk of the threshold
-  double r = 0.0, p = 0.0;
-  if (lane < chunks) {
-    r = sums[((size_t)n * chunks + lane) * 2];
-    p = sums[((size_t)n * chunks + lane) * 2 + 1];
-  }
   const bool plain = !(wave_sum(r) > 0.0);     // r is 0 everywhere: draw from p
   if (plain) { r = p; spent = 0.0; }
   const double upto = wave_scan(r, lane);
   const uint64_t some = __ballot(r > 0.0);
-  if (!some) {
-    if (tid == 0) next_token[n] = -1;
-    return;
-  }
-  const double goal = fmax((double)uniforms[(size_t)n * T_], 0.0) * __shfl(upto, kWave - 1);
+  if (!some) return -1;
+  const double goal = fmax(u, 0.0) * __shfl(upto, kWave - 1);
   const uint64_t past = __ballot(upto > goal) & some;
   const int part = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);
   double left = goal - __shfl(upto - r, part);
 
-  if constexpr (!kDraft) {
-    if (wave == 0) {
-      list_gone(s_gone, plain ? -1 : gone_token(tokens, parents, n, T_, nt, cur, lane), lane);
-    }
-  }
+  if (!kDraft && wave == 0) list_gone(s_gone, plain ? -1 : gone, lane);
   if (tid == 0) s_token = -1;
   __syncthreads();
-  const size_t row = ((size_t)n * T_ + cur) * (size_t)V;
-  const T* tp = target + row;
-  const T* tq = kDraft && spent > 0.0 ? draft + row : nullptr;
+  if (!(kDraft && spent > 0.0)) tq = nullptr;
   const int a = part * chunk, b = min(V - a, chunk) + a;
   int last = -1;                                // last token with r > 0 so far
-  for (int tile = a - skew(tp + a); tile < b; tile += 256 * kRun) {
+  for (int tile = a - skew(tp + a); tile < b; tile += kThreads * kRun) {
     const int first = tile + tid * kRun;
     double w[kRun], sum = 0.0;
     int mine = -1;
@@ -454,8 +462,9 @@ __global__ __launch_bounds__(256) void choose_kernel(
     __syncthreads();
     double before = 0.0;
     for (int x = 0; x < wave; ++x) before += s_sum[x];
-    const double total = ((s_sum[0] + s_sum[1]) + s_sum[2]) + s_sum[3];
-    for (int x = 0; x < 4; ++x) last = max(last, s_last[x]);
+    double total = before;
+    for (int x = wave; x < kWaves; ++x) total += s_sum[x];
+    for (int x = 0; x < kWaves; ++x) last = max(last, s_last[x]);
     // the first thread whose running sum passes the threshold finds the token
     double run = before + (incl - sum);
     const bool here = before + incl > left;
@@ -477,8 +486,67 @@ __global__ __launch_bounds__(256) void choose_kernel(
     left -= total;
     __syncthreads();
   }
-  if (tid == 0) next_token[n] = s_token != -1 ? s_token : last;
+  return s_token != -1 ? s_token : last;
 }
+
+template <typename T, bool kDraft>
+__global__ __launch_bounds__(256) void choose_kernel(
+    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
+    const int32_t* __restrict__ parents, const int32_t* __restrict__ num_nodes,
+    const float* __restrict__ uniforms, int32_t* __restrict__ next_token, int T_, int V, int chunk, int chunks,
+    const Walk* __restrict__ walks, const double* __restrict__ sums) {
+  const uint32_t n = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int nt = node_count(num_nodes, n, T_);
+  if (nt == 0) return;
+  const int cur = walks[n].node;
+  double r = 0.0, p = 0.0;
+  if (lane < chunks) {
+    r = sums[((size_t)n * chunks + lane) * 2];
+    p = sums[((size_t)n * chunks + lane) * 2 + 1];
+  }
+  const size_t row = ((size_t)n * T_ + cur) * (size_t)V;
+  const int gone = kDraft ? -1 : gone_token(tokens, parents, n, T_, nt, cur, lane);
+  const int token = choose<T, kDraft, 256, 16>(target + row, draft + row, walks[n].spent,
+                                               (double)uniforms[(size_t)n * T_], r, p, gone, V, chunk, tid);
+  if (tid == 0) next_token[n] = token;
+}
+
+// All three steps by one workgroup per sequence: one launch, but a row passes
+// through one compute unit.
+template <typename T, bool kDraft>
+__global__ __launch_bounds__(kWalkThreads) void whole_kernel(
+    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
+    const int32_t* __restrict__ parents, const int32_t* __restrict__ num_nodes,
+    const float* __restrict__ uniforms, int32_t* __restrict__ accept, int32_t* __restrict__ path,
+    int32_t* __restrict__ next_token, int T_, int V, int chunk, Walk* __restrict__ walks) {
+  constexpr int kWaves = kWalkThreads / kWave;
+  const uint32_t n = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int nt = node_count(num_nodes, n, T_);
+  __shared__ double s_part[2][kWaves];
+  const Nodes<T> d = load_nodes<T>(target, draft, tokens, parents, uniforms, n, T_, nt, V, lane);
+  int cur, count;
+  double spent;
+  uint64_t accepted;
+  Mass<T> mass{target, draft, n, T_, V, tid};
+  walk<T>(d, kDraft, nt, lane, cur, count, spent, accepted, [&](int at, double C) { return mass(at, C); });
+  if (wave == 0) write_walk(lane, n, T_, nt, cur, count, spent, accepted, accept, path, next_token, walks);
+  if (nt == 0) return;
+  const size_t row = ((size_t)n * T_ + cur) * (size_t)V;
+  const int gone = kDraft ? -1 : gone_token(tokens, parents, n, T_, nt, cur, lane);
+  const int a = min(wave * chunk, V), b = min(V - a, chunk) + a;
+  double rs, ps;
+  wave_sums<T, kDraft>(target + row, draft + row, spent, gone, a, b, lane, rs, ps);
+  if (lane == 0) { s_part[0][wave] = rs; s_part[1][wave] = ps; }
+  __syncthreads();
+  double r = 0.0, p = 0.0;
+  if (lane < kWaves) { r = s_part[0][lane]; p = s_part[1][lane]; }
+  const int token = choose<T, kDraft, kWalkThreads, 8>(target + row, draft + row, spent,
+                                                       (double)uniforms[(size_t)n * T_], r, p, gone, V, chunk, tid);
+  if (tid == 0) next_token[n] = token;
+}
+
 
 template <typename T>
 hipError_t launch_verify_t(const VerifyArgs& a) {
@@ -495,7 +563,17 @@ hipError_t launch_verify_t(const VerifyArgs& a) {
   hipLaunchKernelGGL((choose_kernel<T, DRAFT>), dim3((unsigned)a.N), dim3(256), 0, a.stream, target, draft,         \
                      a.tokens, a.parents, a.num_nodes, a.uniforms, a.next_token, a.T, a.V, p.chunk, p.chunks,       \
                      walks, sums)
-  if (draft && a.parents) {
+  if (whole(a.N, a.V, draft && a.parents)) {
+    const int chunk = ((a.V + 15) / 16 + 7) / 8 * 8;
+    if (draft)
+      hipLaunchKernelGGL((whole_kernel<T, true>), dim3((unsigned)a.N), dim3(kWalkThreads), 0, a.stream, target, draft,
+                         a.tokens, a.parents, a.num_nodes, a.uniforms, a.accept, a.path, a.next_token, a.T, a.V,
+                         chunk, walks);
+    else
+      hipLaunchKernelGGL((whole_kernel<T, false>), dim3((unsigned)a.N), dim3(kWalkThreads), 0, a.stream, target,
+                         draft, a.tokens, a.parents, a.num_nodes, a.uniforms, a.accept, a.path, a.next_token, a.T,
+                         a.V, chunk, walks);
+  } else if (draft && a.parents) {
     hipLaunchKernelGGL((walk_kernel<T>), dim3((unsigned)a.N), dim3(kWalkThreads), 0, a.stream, target, draft,
                        a.tokens, a.parents, a.num_nodes, a.uniforms, a.accept, a.path, a.next_token, a.T, a.V, walks);
     KDA_SUMS(true, false);

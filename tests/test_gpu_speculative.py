@@ -296,6 +296,10 @@ VERIFY = [
     (2, 33, 5003, F32, "bushy", False), (70, 5, 4097, F32, "chain", True), (66, 7, 8209, BF16, "bushy", True),
     (65, 3, 65537, F32, "chain", True), (2, 3, 300001, BF16, "star", True), (4, 12, 777, F32, "forest", True),
     (4, 12, 777, F32, "bad", False),
+    # either side of the sizes at which the library spreads the rows over the GPU
+    (2, 3, 49152, F32, "chain", True), (2, 3, 49153, F32, "chain", True), (3, 4, 49155, BF16, "bushy", False),
+    (2, 4, 65537, F32, "bushy", True), (33, 3, 65539, BF16, "star", True), (257, 2, 16385, F32, "chain", True),
+    (160, 2, 49157, BF16, "chain", False), (1025, 2, 40, F32, "chain", True), (1025, 2, 40, BF16, "chain", False),
 ]
 
 
