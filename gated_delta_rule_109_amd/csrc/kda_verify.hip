@@ -10,7 +10,8 @@
 //
 // All sums are fp64: a token is chosen where a running sum of up to V values
 // passes a threshold, and in fp32 the sum's rounding would be as wide as many
-// tokens. Bound by the bytes of the rows p and q of the last node.
+// tokens. Bound by the bytes of the rows p and q of the last node: 256 sequences
+// and 131072 tokens of fp32 50 us, 5.4 TB/s.
 //
 // Three steps: the walk down the tree, the partial sums of the last node's r
 // over chunks of the vocabulary, and the choice of the token inside one chunk.
