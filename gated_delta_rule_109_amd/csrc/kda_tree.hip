@@ -1248,13 +1248,15 @@ hipError_t launch_tree(const TreeArgs& a) {
 // ---- commit of a path -------------------------------------------------------------
 // The recurrence over the accepted nodes, the state in registers from its one
 // read to its one write (8 D^2 bytes per head, which is what the call costs:
-// 256 x 32 heads with paths of 0 to 16 nodes 206 us, 5.2 TB/s; paths of at most
-// a few nodes take what a decode step does, 0.18 ms).
+// 256 x 32 heads with paths of 0 to 16 nodes 206 to 222 us, 4.9 to 5.2 TB/s; up
+// to eight nodes each take what a decode step does in the same loop over three
+// sets of states, 219 to 231 us against 218, and 16 nodes 269).
 // Thread layout as the decode kernel's: D = 128, a 256-thread workgroup per
 // head, lane l of wave w owns columns 32w + 4(l % 8) .. +3 of rows
 // (l / 8) + 8i; D = 16, one wave per head.
 // The nodes' vectors are staged kBatch nodes at a time; the first batch is
-// loaded ahead of the state so that both are in flight together.
+// loaded ahead of the state so that both are in flight together (behind it
+// measured the same).
 constexpr int kBatch = 8;
 
 template <int D, typename TIn>
@@ -1270,16 +1272,18 @@ __global__ __launch_bounds__(D == 128 ? 256 : 64) void commit_kernel(
   constexpr int kIters = kBatch * D / kThreads;
   const uint32_t head = blockIdx.x, n = head / (uint32_t)H, h = head % (uint32_t)H;
   const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
-  // the path's length: accept, cut before the first index outside [0, T)
-  const int node_of_lane = path[(size_t)n * T + min(lane, T - 1)];
-  const uint64_t bad = __ballot(!(lane < T && node_of_lane >= 0 && node_of_lane < T));
-  int len = min(max(accept[n], 0), T);
-  if (bad) len = min(len, __builtin_ctzll(bad));
-  if (len == 0) return;
   const int cg = lane % kColGroups, rg = lane / kColGroups;
   const int col = wave * 4 * kColGroups + 4 * cg;
+  int len = min(max(accept[n], 0), T);
+  if (len == 0) return;
+  const int node_of_lane = path[(size_t)n * T + min(lane, T - 1)];
+  // the path's length: accept, cut before the first index outside [0, T)
+  const uint64_t bad = __ballot(!(lane < T && node_of_lane >= 0 && node_of_lane < T));
+  if (bad) len = min(len, __builtin_ctzll(bad));
+  if (len == 0) return;
+  // row of the path's node i; called by all lanes together (it reads lane i)
   auto row = [&](int i) __attribute__((always_inline)) {
-    return ((size_t)n * T + path[(size_t)n * T + i]) * H + h;
+    return ((size_t)n * T + __builtin_amdgcn_ds_bpermute(4 * i, node_of_lane)) * H + h;
   };
   const float alpha_min = __builtin_amdgcn_exp2f(g_min * kLog2e);
   const bool norm = fe_flags & KDA_FE_L2NORM_QK;
@@ -1296,7 +1300,7 @@ __global__ __launch_bounds__(D == 128 ? 256 : 64) void commit_kernel(
       tv[x] = Elem<TIn>::load(v + r * D + c);
       ta[x] = gate == KDA_GATE_NONE ? 0.f : g[gate == KDA_GATE_CHANNEL ? r * D + c : r];
     }
-    if (tid < kBatch) tb = beta[row(min(first + tid, len - 1))];
+    tb = beta[row(min(first + tid % kBatch, len - 1))];
   };
   auto stage = [&]() __attribute__((always_inline)) {
 #pragma unroll
