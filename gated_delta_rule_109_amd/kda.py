@@ -330,10 +330,11 @@ def decode_tokens(q, k, v, g, beta, state, accept=None, scale=1.0, g_min=LN_HALF
 # ---- one speculative step over trees of drafted tokens ---------------------------
 
 def _check_step(*specs):
-    """Every given tensor (name, tensor or None, shape, dtype) has its shape and
-    dtype, is contiguous, and all are on one device, whose index is returned.
-    One pass over what is right; the first thing wrong is looked up after it."""
-    dev = next(t for _, t, _, _ in specs if t is not None).get_device()
+    """Every given tensor (name, tensor or None, shape, dtype; the first one not
+    None) has its shape and dtype, is contiguous, and all are on one device,
+    whose index is returned. One pass over what is right; the first thing wrong
+    is looked up after it."""
+    dev = specs[0][1].get_device()
     for _, t, shape, dtype in specs:
         if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()
                               or t.get_device() != dev):
@@ -368,9 +369,9 @@ def _addr(t: Optional[torch.Tensor]):
 
 def _call(dev, where, fn, *args):
     """fn(*args, stream) on device dev's current stream, with dev current. These
-    calls take microseconds, so the stream's handle is read without building
-    a torch.cuda.Stream around it (2.2 us of a call's 13)."""
-    if torch.cuda.current_device() != dev:
+    calls take microseconds, so device and stream are read as the numbers they
+    are (a torch.cuda.Stream around the handle costs 2.2 us of a call's 13)."""
+    if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _call(dev, where, fn, *args)
     st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
@@ -393,9 +394,9 @@ def decode_tree(q, k, v, g, beta, state, parents=None, num_nodes=None, scale=1.0
                       ("o", o, (N, T, H, D), q.dtype))
     if o is None:
         o = torch.empty_like(v) if num_nodes is None else torch.zeros_like(v)
-    _call(dev, "kda_decode_tree", lib().kda_decode_tree, _addr(q), _addr(k), _addr(v), _dtype_code(q), _addr(g),
-          _addr(beta), _addr(state), _addr(parents), _addr(num_nodes), _addr(o), N, T, H, D, v.shape[3], float(scale),
-          float(g_min), _opt_ptr(options))
+    _call(dev, "kda_decode_tree", lib().kda_decode_tree, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q),
+          _addr(g), _addr(beta), _addr(state), _addr(parents), _addr(num_nodes), o.data_ptr(), N, T, H, D, D,
+          float(scale), float(g_min), _opt_ptr(options))
     return o
 
 
@@ -409,8 +410,9 @@ def commit_path(k, v, g, beta, state, path, accept, g_min=LN_HALF, options: Opti
     specs, g = _step_inputs(k, k, v, g, beta, (N, T), H, D, options)
     dev = _check_step(*specs[1:], ("state", state, (N, H, D, D), torch.float32), ("path", path, (N, T), torch.int32),
                       ("accept", accept, (N,), torch.int32))
-    _call(dev, "kda_commit_path", lib().kda_commit_path, _addr(k), _addr(v), _dtype_code(k), _addr(g), _addr(beta),
-          _addr(state), _addr(path), _addr(accept), N, T, H, D, v.shape[3], float(g_min), _opt_ptr(options))
+    _call(dev, "kda_commit_path", lib().kda_commit_path, k.data_ptr(), v.data_ptr(), _dtype_code(k), _addr(g),
+          _addr(beta), _addr(state), path.data_ptr(), accept.data_ptr(), N, T, H, D, D, float(g_min),
+          _opt_ptr(options))
     return state
 
 
@@ -450,9 +452,9 @@ def verify_drafts(target, draft, tokens, uniforms, parents=None, num_nodes=None,
         path = torch.empty_like(tokens)
     if next_token is None:
         next_token = tokens.new_empty(N)
-    _call(dev, "kda_verify_drafts", lib().kda_verify_drafts, _addr(target), _addr(draft), code, _addr(tokens),
-          _addr(parents), _addr(num_nodes), _addr(uniforms), _addr(accept), _addr(path), _addr(next_token), N, T, V,
-          _addr(workspace), workspace.numel())
+    _call(dev, "kda_verify_drafts", lib().kda_verify_drafts, target.data_ptr(), _addr(draft), code, tokens.data_ptr(),
+          _addr(parents), _addr(num_nodes), uniforms.data_ptr(), accept.data_ptr(), path.data_ptr(),
+          next_token.data_ptr(), N, T, V, workspace.data_ptr(), workspace.numel())
     return accept, path, next_token
 
 
@@ -493,9 +495,9 @@ def _cache_call(where, fn, first, cache: StateCache, slots, states):
     if S >= 2 ** 31:
         raise ValueError(f"num_slots: {S} is above INT32_MAX")
     if first == "states":
-        args = (_addr(states), _addr(slots), _addr(cache.values), _addr(cache.scales))
+        args = (states.data_ptr(), _addr(slots), cache.values.data_ptr(), cache.scales.data_ptr())
     else:
-        args = (_addr(cache.values), _addr(cache.scales), _addr(slots), _addr(states))
+        args = (cache.values.data_ptr(), cache.scales.data_ptr(), _addr(slots), states.data_ptr())
     _call(dev, where, fn, *args, cache.format, N, S, H, D, D)
 
 

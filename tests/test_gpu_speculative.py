@@ -623,6 +623,29 @@ def test_on_another_stream_and_twice_the_same():
             assert torch.equal(x, y)
 
 
+def test_two_steps_at_once():
+    """Two steps with their own caches and workspaces on two streams, over and
+    over: each gives what it gives alone."""
+    steps, wants, firsts = [step_setup()[0], step_setup(N=4, T=9)[0]], [], []
+    for a in steps:
+        cache = a[7]
+        firsts.append([cache.values.clone(), cache.scales.clone()])
+        wants.append([x.clone() for x in full_step(*a)])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for a, first, stream in zip(steps, firsts, streams):
+            with torch.cuda.stream(stream):
+                a[7].values.copy_(first[0])
+                a[7].scales.copy_(first[1])
+                got.append(full_step(*a))
+        torch.cuda.synchronize()
+        for want, out in zip(wants, got):
+            for x, y in zip(want, out):
+                assert torch.equal(x, y)
+
+
 def test_empty_calls():
     x = torch.empty(0, 4, 2, 128, device=DEV, dtype=BF16)
     g, b, st = torch.empty(0, 4, 2, 128, device=DEV), torch.empty(0, 4, 2, device=DEV), torch.empty(0, 2, 128, 128, device=DEV)
