@@ -454,6 +454,8 @@ kda_status kda_state_store(const float* states, const int32_t* slots, void* valu
   const kda_status st =
       cache_args(states, slots, values, scales, enum_code(format), N, num_slots, H, Dk, Dv, stream, &a);
   if (st != KDA_OK || N == 0 || num_slots == 0) return st;
+  // (every head reads the slots behind its own)
+  if (slots && N > KDA_STORE_MAX_LISTED) return KDA_ERR_INVALID_ARG;
   return from_hip(kda::launch_cache_store(a));
 }
 

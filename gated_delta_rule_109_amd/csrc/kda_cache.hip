@@ -91,9 +91,19 @@ __global__ __launch_bounds__(D == 128 ? 256 : 64) void cache_store_kernel(
   f32x4 x[kIters];
 #pragma unroll
   for (int i = 0; i < kIters; ++i) x[i] = __builtin_nontemporal_load(src + tid + i * kThreads);
-  if (slots) {   // a later state of the same slot is the one that is written
+  if (slots && n + 1 < (uint32_t)N) {   // a later state of the same slot is the one that is written
+    // kScan loads in flight, those past the end of the last entry (a later
+    // state's too): 16384 states of 128 x 128 in 252 us, 311 with one at a time,
+    // 222 without a list
+    constexpr int kScan = 8;
     int later = 0;
-    for (int64_t m = (int64_t)n + 1 + tid; m < N; m += kThreads) later |= slots[m] == slot;
+    for (int m = (int)n + 1 + tid; m < N; m += kScan * kThreads) {
+      int other[kScan];
+#pragma unroll
+      for (int j = 0; j < kScan; ++j) other[j] = slots[min(m + j * kThreads, N - 1)];
+#pragma unroll
+      for (int j = 0; j < kScan; ++j) later |= other[j] == slot;
+    }
     if (__syncthreads_or(later)) return;
   }
   const size_t dst = (size_t)slot * H + h;

@@ -120,9 +120,10 @@ __device__ __forceinline__ Nodes<T> load_nodes(const T* target, const T* draft, 
   return d;
 }
 
-// One element's residual weight. Mode without draft: the rejected tokens are
+// One element's residual weight, rounded the same wherever it is formed (a sum
+// above 0 has an element above 0). Mode without draft: the rejected tokens are
 // taken out by the callers.
-__device__ __forceinline__ double residual(double p, double q, double spent) { return fmax(p - spent * q, 0.0); }
+__device__ __forceinline__ double residual(double p, double q, double spent) { return fmax(fma(-spent, q, p), 0.0); }
 
 // Walks one sequence's tree; every lane of the calling wave returns the same.
 // mass(cur, spent): sum of the residual row of node cur, for a node with

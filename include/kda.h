@@ -463,6 +463,7 @@ kda_status kda_verify_drafts(const void* target, const void* draft, kda_dtype dt
  * NaN (e4m3). A stored value whose product with the step passes FLT_MAX reads
  * as FLT_MAX of its sign. */
 #define KDA_CACHE_BLOCK 32
+#define KDA_STORE_MAX_LISTED (1 << 20)   /* most states of a store with a list of slots */
 typedef enum { KDA_CACHE_INT8 = 0, KDA_CACHE_E4M3 = 1 } kda_cache_format;
 
 /* Writes N states into the cache.
@@ -470,11 +471,14 @@ typedef enum { KDA_CACHE_INT8 = 0, KDA_CACHE_E4M3 = 1 } kda_cache_format;
  *   slots   [N] int32 (device, 4-byte aligned): the slot of each state, or NULL
  *           for slot n. A
  *           state whose slot is outside [0, num_slots) is not written. Where
- *           two states name one slot, the later one is written.
+ *           two states name one slot, the later one is written. (Each
+ *           head looks through the entries behind its own: 14 % of the time at
+ *           16384 states of one head of 128 x 128, more with more or smaller ones.)
  *   values  [num_slots, H, Dk, Dv] 8-bit;  scales [num_slots, H, Dk * Dv / 32]
  *           uint8, e + 127. Slots that are not named are left as they were.
  * Errors: KDA_ERR_INVALID_ARG (null required pointer, N or num_slots < 0,
- * H <= 0, N * H above KDA_MAX_LAUNCH_HEADS, without slots N > num_slots),
+ * H <= 0, N * H above KDA_MAX_LAUNCH_HEADS, without slots N > num_slots, a
+ * store with slots of N > KDA_STORE_MAX_LISTED),
  * KDA_ERR_UNSUPPORTED (head size or format), KDA_ERR_HIP. */
 kda_status kda_state_store(const float* states, const int32_t* slots, void* values,
                            uint8_t* scales, kda_cache_format format, int32_t N,

@@ -458,6 +458,19 @@ def test_cache_slots_outside_twice_and_without_a_list(fmt):
     check_cache(cache, x[:3], [0, 1, 2])
 
 
+@pytest.mark.parametrize("N,H,D,num_slots", [
+    (600, 1, 16, 7), (5000, 1, 16, 700), (5000, 2, 16, 6000), (2300, 1, 128, 40), (513, 1, 16, 512), (2049, 1, 128, 1)])
+def test_cache_of_long_lists_that_name_slots_again(N, H, D, num_slots):
+    x = torch.randn(N, H, D, D, device=DEV, generator=torch.Generator(DEV).manual_seed(N))
+    slots = np.random.default_rng(num_slots).integers(0, num_slots, N).astype(np.int32)
+    slots[0] = slots[-1]                                      # the first and the last state
+    cache, want = (kda.make_state_cache(num_slots, H, D, DEV) for _ in range(2))
+    kda.state_store(x, cache, dev(slots, torch.int32))
+    last = {int(s): n for n, s in enumerate(slots)}           # each slot's latest state, stored without repeats
+    kda.state_store(x[torch.tensor(list(last.values()), device=DEV)], want, dev(np.array(list(last), np.int32), torch.int32))
+    assert torch.equal(cache.values, want.values) and torch.equal(cache.scales, want.scales)
+
+
 @pytest.mark.parametrize("fmt", [torch.int8, torch.float8_e4m3fn])
 def test_cache_of_values_that_are_not_finite(fmt):
     x = states(1, 1, 16, 8)

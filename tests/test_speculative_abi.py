@@ -127,6 +127,11 @@ def test_cache_refuses(call, bad, status):
     assert call(**bad) == status
 
 
+def test_store_refuses_longer_lists():
+    assert store(N=(1 << 20) + 1, H=1) == BAD
+    assert store(N=(1 << 20) + 1, H=1, num_slots=0) == OK      # nothing to store into
+
+
 def test_nothing_to_store_into():
     assert store(num_slots=0, values=None, scales=None) == OK
 
