@@ -133,6 +133,7 @@ def _counter_csv(d):
 
 def kernel_key(name):
     """A kernel's name with its template arguments, without the parameter list."""
+    name = name.replace("(anonymous namespace)::", "")
     return re.sub(r"\(.*", "", name).replace("void ", "").strip()
 
 

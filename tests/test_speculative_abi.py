@@ -10,7 +10,7 @@ import sys
 import pytest
 import torch
 
-from gated_delta_rule_109_amd import kda
+from gated_delta_rule_109_amd import kda, profiling
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P = ctypes.c_void_p(4096)             # a 16- and 256-byte aligned address that is never read
@@ -213,3 +213,8 @@ def test_c_abi_refusals_under_asan_and_ubsan():
                         "tests/test_speculative_abi.py"], env=env, cwd=ROOT, capture_output=True, text=True,
                        timeout=900)
     assert r.returncode == 0, (r.stdout[-3000:], r.stderr[-3000:])
+
+
+def test_profiles_name_the_verification_kernels():
+    assert profiling.kernel_key("void kda::(anonymous namespace)::whole_kernel<float, true>(float const*, int)") == \
+        "kda::whole_kernel<float, true>"
