@@ -110,7 +110,7 @@ __device__ __forceinline__ uint64_t ancestors(int parent, int lane) {
 
 // Decays between nodes as quotients E_i / E_j of the decays from the state.
 // Where every E of any tree of T nodes is at least 2^-kMaxSpan, far inside the
-// range of fp32 and of a two-term bf16 split, they are formed as they stand.
+// range of fp32, they are formed as they stand.
 // Otherwise G = log2 E is kept in fp64 and referred, per block of 16 rows and
 // channel, to R half way between the block's largest and smallest G:
 //   E_i / E_j = 2^(G_i - R) 2^(R - G_j).
@@ -312,12 +312,15 @@ __global__ __launch_bounds__(256) void tree_path_kernel(
 //   3. (I + beta A)^-1 of the 16 x 16 diagonal blocks, one row per lane;
 //   4. d by blocks of 16 nodes, then o = W + B d. The accumulator layout of a
 //      16 x 16 tile is the K = 16 operand layout, so d feeds the products as it is.
-// Operands of bf16 tensors are split in two bf16 terms (16 bits of mantissa,
-// 2^-17 relative, far below the bf16 rounding of o), three products each; fp32
-// tensors use the fp32 matrix instructions, at an eighth of the rate.
-// Measured: 256 x 32 heads, 16 nodes, bf16 133 us (739 MB, 5.6 TB/s: bound by
-// the reads); 64 x 32 heads, 64 nodes 97 us (336 MB; bound by the phases of its
-// two workgroups per compute unit); one sequence of 32 heads and 8 nodes 7 us.
+// All products use the fp32 matrix instructions, for bf16 tensors too: S, the
+// decayed rows, A, B and d have 24 bits whatever the tensors have. Operands of
+// two bf16 terms (16 bits, an eighth of the matrix time) took 142 us against
+// 167 to 184 for 256 x 32 heads of 16 nodes and 114 against 173 for 64 x 32
+// heads of 64, but rounded 0.5 % of the outputs the other way (now 0.02 %);
+// three terms (24 bits) took 160 and 180 us.
+// Measured in those two cases: 4.0 to 4.4 TB/s and 1.9 TB/s, bound by loads and
+// matrix products that overlap only in part (a workgroup does first the ones,
+// then the others).
 //
 // Values that are not finite: a product over nodes would carry one node's NaN
 // to nodes that do not descend from it (0 * NaN). So they are replaced by 0
@@ -325,92 +328,9 @@ __global__ __launch_bounds__(256) void tree_path_kernel(
 // column (A, B) and per node and column (d); the outputs of their nodes and
 // descendants are then set to NaN.
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
-// Two floats to packed bf16, round to nearest even, as the dword they are
-// stored in (bf16 vector types would be taken apart and packed again).
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
-}
-// x = hi + lo, both packed
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16(a, b);
-  asm("" : "+v"(hi));
-  lo = pack_bf16(a - __builtin_bit_cast(float, hi << 16), b - __builtin_bit_cast(float, hi & 0xffff0000u));
-}
-
-struct SplitOp {                 // two bf16 terms
-  static constexpr int kRowBytes = 2 * 272;      // a row of 128: hi, lo, each padded by 16 bytes
-  struct F8 { u32x4 hi, lo; };
-  struct F4 { uint2 hi, lo; };
-  static __device__ __forceinline__ F8 make8(const float (&x)[8]) {
-    F8 f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t h, l;
-      split2(x[2 * j], x[2 * j + 1], h, l);
-      f.hi[j] = h;
-      f.lo[j] = l;
-    }
-    return f;
-  }
-  static __device__ __forceinline__ F4 make4(f32x4 x) {
-    F4 f;
-    split2(x[0], x[1], f.hi.x, f.lo.x);
-    split2(x[2], x[3], f.hi.y, f.lo.y);
-    return f;
-  }
-  // channels c .. c + kN - 1 of a row, kN and c multiples of 8
-  template <int kN>
-  static __device__ __forceinline__ void put(char* row, int c, const float (&x)[kN]) {
-#pragma unroll
-    for (int i = 0; i < kN / 8; ++i) {
-      u32x4 hi, lo;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t h, l;
-        split2(x[8 * i + 2 * j], x[8 * i + 2 * j + 1], h, l);
-        hi[j] = h;
-        lo[j] = l;
-      }
-      *(u32x4*)(row + 2 * (c + 8 * i)) = hi;
-      *(u32x4*)(row + 272 + 2 * (c + 8 * i)) = lo;
-    }
-  }
-  static __device__ __forceinline__ F8 get8(const char* row, int c) {
-    return {*(const u32x4*)(row + 2 * c), *(const u32x4*)(row + 272 + 2 * c)};
-  }
-  // element (i, j) of a matrix with rows of `stride` elements
-  static __device__ __forceinline__ void put1(char* m, int stride, int i, int j, float x) {
-    const __bf16 hi = f32_to_bf16(x);
-    ((__bf16*)m)[2 * i * stride + j] = hi;
-    ((__bf16*)m)[(2 * i + 1) * stride + j] = f32_to_bf16(x - bf16v_to_f32(hi));
-  }
-  static __device__ __forceinline__ F4 get4(const char* m, int stride, int i, int j) {
-    return {*(const uint2*)(m + 2 * (2 * i * stride + j)), *(const uint2*)(m + 2 * ((2 * i + 1) * stride + j))};
-  }
-  static __device__ __forceinline__ f32x4 mma32(u32x4 a, u32x4 b, f32x4 c) {
-    return mfma32(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c);
-  }
-  static __device__ __forceinline__ f32x4 mma(const F8& a, const F8& b, f32x4 c) {
-    c = mma32(a.lo, b.hi, c);
-    c = mma32(a.hi, b.lo, c);
-    return mma32(a.hi, b.hi, c);
-  }
-  static __device__ __forceinline__ f32x4 mma16(uint2 a, uint2 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, a), __builtin_bit_cast(s16x4, b), c, 0,
-                                                     0, 0);
-  }
-  static __device__ __forceinline__ f32x4 mma(const F4& a, const F4& b, f32x4 c) {
-    c = mma16(a.lo, b.hi, c);
-    c = mma16(a.hi, b.lo, c);
-    return mma16(a.hi, b.hi, c);
-  }
-};
-
+// Operands of products on the fp32 matrix instructions (16 x 16 x 4).
 struct FloatOp {
-  static constexpr int kRowBytes = 528;
+  static constexpr int kRowBytes = 528;               // a row of 128, padded by 16 bytes
   struct F8 { float x[8]; };
   struct F4 { f32x4 x; };
   static __device__ __forceinline__ F8 make8(const float (&x)[8]) {
@@ -458,10 +378,11 @@ __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) < __builtin
 // operand planes would leave room for one workgroup per compute unit, which
 // then either loads or computes: q E takes the place of k E once A and U are
 // formed, and the matrices lie over the planes (two workgroups; 64 nodes on 64
-// x 32 heads: 192 us with one, 113 with two). With one or two tiles all lie side by side and two
-// barriers are saved.
-template <int kTB, int kWaves, typename Op, bool kDeep>
+// x 32 heads: 210 us with one, 173 with two). With one or two tiles all lie side
+// by side and two barriers are saved.
+template <int kTB, bool kDeep>
 struct TileLds {
+  using Op = FloatOp;
   static constexpr int kT = 16 * kTB;
   static constexpr bool kTwo = kTB >= 3;
   static constexpr int kStride = kT + 4;                 // row of A or B, elements
@@ -476,15 +397,16 @@ struct TileLds {
 };
 
 // kDeep: A and B with the decays of each block of rows referred to its own R
-// (64-node chains, floor -5, 64 x 32 heads: 335 to 341 us; pair by pair 3037).
-template <int kTB, int kWaves, typename TIn, typename Op, bool kDeep>
+// (64-node chains, floor -5, 64 x 32 heads: 384 us; pair by pair 3037).
+template <int kTB, int kWaves, typename TIn, bool kDeep>
 __global__ __launch_bounds__(64 * kWaves, kDeep ? 2 : 4) void tree_tile_kernel(
     const TIn* __restrict__ q, const TIn* __restrict__ k, const TIn* __restrict__ v,
     const float* __restrict__ g, const float* __restrict__ beta, const float* __restrict__ state,
     const int32_t* __restrict__ parents, const int32_t* __restrict__ num_nodes, TIn* __restrict__ o, int H,
     int T, float scale, float g_min, uint32_t fe_flags, float fe_eps, int gate, int reach) {
   constexpr int D = 128;
-  using L = TileLds<kTB, kWaves, Op, kDeep>;
+  using Op = FloatOp;
+  using L = TileLds<kTB, kDeep>;
   constexpr int kT = L::kT, kNT = 8 / kWaves;            // n-tiles of a wave
   const uint32_t n = blockIdx.x / (uint32_t)H, h = blockIdx.x % (uint32_t)H;
   const int nt = num_nodes ? min(max(num_nodes[n], 0), T) : T;
@@ -537,7 +459,7 @@ __global__ __launch_bounds__(64 * kWaves, kDeep ? 2 : 4) void tree_tile_kernel(
   const int col0 = wave * 16 * kNT;
   // (a uniform base and one 32-bit lane offset: no 64-bit address per load).
   // With two n-tiles a wave reads whole 128-byte lines, once, past the caches
-  // (256x32 heads, 16 nodes: 138 -> 133 us); with one, two waves share them.
+  // (256x32 heads, 16 nodes: 184 us, 185 through them); with one, two waves share them.
   const uint32_t lane_off = (uint32_t)(8 * lg * D + kNT * lr) * 4;
   float sreg[4][8][kNT];
   auto load_s = [&]() __attribute__((always_inline)) {
@@ -1183,33 +1105,33 @@ static hipError_t launch_paths(const TreeArgs& a, int taken) {
   return hipGetLastError();
 }
 
-template <int kTB, int kWaves, typename TIn, typename Op, bool kDeep>
+template <int kTB, int kWaves, typename TIn, bool kDeep>
 static hipError_t launch_tiles(const TreeArgs& a, int reach) {
   const unsigned blocks = (unsigned)((int64_t)a.N * a.H);
-  constexpr size_t lds = TileLds<kTB, kWaves, Op, kDeep>::kBytes;
-  hipLaunchKernelGGL((tree_tile_kernel<kTB, kWaves, TIn, Op, kDeep>), dim3(blocks), dim3(64 * kWaves), lds, a.stream,
+  constexpr size_t lds = TileLds<kTB, kDeep>::kBytes;
+  hipLaunchKernelGGL((tree_tile_kernel<kTB, kWaves, TIn, kDeep>), dim3(blocks), dim3(64 * kWaves), lds, a.stream,
                      (const TIn*)a.q, (const TIn*)a.k, (const TIn*)a.v, a.g, a.beta, a.state, a.parents, a.num_nodes, (TIn*)a.o, a.H, a.T, a.scale, a.g_min, a.fe_flags,
                      a.fe_eps, (int)a.gate, reach);
   return hipGetLastError();
 }
 
-template <typename TIn, typename Op, bool kDeep>
+template <typename TIn, bool kDeep>
 static hipError_t launch_blocks(const TreeArgs& a, int reach) {
   switch ((a.T + 15) / 16) {
-    case 1: return launch_tiles<1, 4, TIn, Op, kDeep>(a, reach);
-    case 2: return launch_tiles<2, 8, TIn, Op, kDeep>(a, reach);
-    case 3: return launch_tiles<3, 8, TIn, Op, kDeep>(a, reach);
-    default: return launch_tiles<4, 8, TIn, Op, kDeep>(a, reach);
+    case 1: return launch_tiles<1, 4, TIn, kDeep>(a, reach);
+    case 2: return launch_tiles<2, 8, TIn, kDeep>(a, reach);
+    case 3: return launch_tiles<3, 8, TIn, kDeep>(a, reach);
+    default: return launch_tiles<4, 8, TIn, kDeep>(a, reach);
   }
 }
 
-template <typename TIn, typename Op>
+template <typename TIn>
 static hipError_t launch_tree_128(const TreeArgs& a) {
   const int reach = reach_of(kMaxSpread, a.g_min, a.gate);
   // (the tile kernels' 24-bit row offsets: H D < 2^22)
   if (reach < 1 || (int64_t)a.H * 128 * 4 >= 1 << 24) return launch_paths<128, TIn>(a, kNoneTaken);
-  if (reach_of(kMaxSpan, a.g_min, a.gate) >= a.T) return launch_blocks<TIn, Op, false>(a, 0);
-  const hipError_t e = launch_blocks<TIn, Op, true>(a, reach);
+  if (reach_of(kMaxSpan, a.g_min, a.gate) >= a.T) return launch_blocks<TIn, false>(a, 0);
+  const hipError_t e = launch_blocks<TIn, true>(a, reach);
   // (a block is at most T decays deep)
   if (e != hipSuccess || reach >= a.T) return e;
   return launch_paths<128, TIn>(a, reach);
@@ -1241,7 +1163,7 @@ static hipError_t launch_tree_16(const TreeArgs& a) {
 }
 
 hipError_t launch_tree(const TreeArgs& a) {
-  if (a.D == 128) return a.bf16 ? launch_tree_128<bf16_bits, SplitOp>(a) : launch_tree_128<float, FloatOp>(a);
+  if (a.D == 128) return a.bf16 ? launch_tree_128<bf16_bits>(a) : launch_tree_128<float>(a);
   return a.bf16 ? launch_tree_16<bf16_bits>(a) : launch_tree_16<float>(a);
 }
 

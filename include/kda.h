@@ -367,6 +367,7 @@ kda_status kda_decode_tokens(const void* q, const void* k, const void* v, kda_dt
  *   q, k, v [N, T, H, D] dtype, g, beta and opt as in kda_decode_tokens
  *   state   [N, H, Dk, Dv] fp32, read only
  *   o       [N, T, H, Dv] dtype; must not overlap the inputs
+ * Products and sums are fp32, whatever dtype is; o is rounded once.
  * A node whose inputs are not finite, or overflow, makes outputs of itself and
  * its descendants non-finite, and no others.
  * T outside [1, KDA_TREE_MAX_NODES] and N * H above KDA_MAX_LAUNCH_HEADS are

@@ -223,6 +223,34 @@ def test_tree_of_very_many_heads(dtype):
     assert (err <= tol + (2.0 ** -7 if dtype is BF16 else 0.0) * ref.float().abs()).all()
 
 
+@pytest.mark.parametrize("D,dtype", [(128, BF16), (128, F32), (16, BF16)])
+@pytest.mark.parametrize("T,g_min", [(1, LN_HALF), (16, LN_HALF), (30, LN_HALF), (45, LN_HALF), (64, LN_HALF),
+                                     (64, -5.0), (20, -5.0), (7, -100.0)])
+def test_operands_keep_fp32s_digits(T, D, dtype, g_min):
+    """Sums that cancel down to digits 2^-20 below their terms. Every product and
+    every sum here is exact in fp32, in any order (multiples of 2^-20 below 4), so
+    the outputs are too; operands of fewer than 21 bits would lose them."""
+    m = torch.arange(1, D + 1, device=DEV).float() * 2.0 ** -20     # (at most 8 bits: exact in bf16)
+    state = torch.zeros(2, 1, D, D, device=DEV)
+    state[:, 0, 2] = 1.0 + 2.0 ** -9 + m
+    state[:, 0, 5] = 1.0 + 2.0 ** -9
+    q = torch.zeros(2, T, 1, D, device=DEV, dtype=dtype)
+    k, v = torch.zeros_like(q), torch.zeros_like(q)
+    g = torch.zeros(2, T, 1, D, device=DEV)
+    beta = torch.zeros(2, T, 1, device=DEV)
+    # sequence 0 reads q = e_2 - e_5 from the state: m
+    q[0, :, 0, 2], q[0, :, 0, 5] = 1.0, -1.0
+    # sequence 1: the last node writes d = v - S^T k with k = e_2 - e_5 and reads what it wrote: -m + v
+    k[1, T - 1, 0, 2], k[1, T - 1, 0, 5] = 1.0, -1.0
+    beta[1, T - 1] = 1.0
+    q[1, T - 1, 0, 5] = -1.0                                        # S^T q - d (k . e_5) = -S_5 + d
+    v[1, T - 1] = 1.0
+    o = kda.decode_tree(q, k, v, g, beta, state, g_min=g_min).double()
+    assert torch.equal(o[0, :, 0], m.double().expand(T, D))
+    # -S_5 + (1 - m) = -2^-9 - m: at most 12 bits, rounded to the outputs' type
+    assert torch.equal(o[1, T - 1, 0], (-(2.0 ** -9) - m).to(dtype).double())
+
+
 def test_tree_of_a_chain_is_the_token_decode():
     """The tree's outputs of a chain against kda_decode_tokens, which runs the
     recurrence: both within their bounds of the exact value, so within twice."""
