@@ -180,6 +180,37 @@ def test_a_nodes_nan_reaches_its_descendants_only(T, D, dtype, g_min, what):
         assert torch.equal(o[hit][:, rest], clean[hit][:, rest])
 
 
+@pytest.mark.parametrize("T,D,dtype,g_min", [(16, 128, BF16, LN_HALF), (30, 128, BF16, LN_HALF), (50, 128, BF16, LN_HALF),
+                                             (50, 128, BF16, -5.0), (50, 128, F32, LN_HALF), (20, 16, BF16, LN_HALF),
+                                             (9, 128, BF16, -100.0)])
+def test_a_nodes_finite_values_near_the_largest_stay_its_own(T, D, dtype, g_min):
+    """A delta row of 3.4014e38, which is finite in fp32 (the largest: 3.4028e38)
+    but rounds to infinity in bf16, belongs to its node and descendants only."""
+    s = Step(1, T, 1, D, dtype, 77, g_min=g_min)
+    par = random_parents(1, T, "bushy", 8)
+    p = dev(par, torch.int32)
+    i = 3
+    k, v, g, b = s.args[1:]
+    s.state[0, 0, 2] = -1.2e36
+    k[0, i] = 0.0
+    k[0, i, 0, 2] = 1.0
+    g[0, :, 0, 2] = 0.0                                       # S^T (E k) = -1.2e36 at node i
+    b[0, i] = 1.0
+    # the other nodes neither read nor write that channel
+    for x in s.args[:2]:
+        x[0, [t for t in range(T) if t != i], 0, 2] = 0.0
+    clean = kda.decode_tree(*s.args, s.state, p, g_min=g_min)
+    v[0, i] = torch.finfo(BF16).max                           # 3.3895e38, and 1.2e36 from the state
+    o = kda.decode_tree(*s.args, s.state, p, g_min=g_min)
+    below = {i}
+    for t in range(i + 1, T):
+        if int(par[0, t]) in below:
+            below.add(t)
+    rest = [t for t in range(T) if t not in below]
+    assert len(rest) > 4 and torch.isfinite(clean[0, rest]).all()
+    assert torch.equal(o[0, rest], clean[0, rest])
+
+
 @pytest.mark.parametrize("D,dtype", [(128, BF16), (128, F32), (16, BF16), (16, F32)])
 @pytest.mark.parametrize("T,g_min,flags,gate", [(64, -5.0, 0, 0), (40, -5.0, kda.FE_ALL, 0), (33, -2.5, 0, 1), (16, -5.0, 0, 0),
                                                 (48, -12.0, 0, 0), (64, -80.0, 0, 0)])
