@@ -81,11 +81,13 @@ template <typename T> struct One {
   static __device__ __forceinline__ void store(T* p, float a, float) { Elem<T>::store(p, a); }
 };
 
-// Decay of one channel of token row `row` (a row of the [N, T, H] grid).
+// Decay of one channel of token row `row` (a row of the [N, T, H] grid). The
+// clamps of gate_alpha drop a NaN, which is kept here.
 __device__ __forceinline__ float load_alpha(const float* g, int gate, size_t row, int D, int c, uint32_t fe_flags,
                                             float g_min, float alpha_min) {
   if (gate == KDA_GATE_NONE) return 1.f;
   const float x = g[gate == KDA_GATE_CHANNEL ? row * D + c : row];
+  if (x != x) return x;
   return fe_flags & KDA_FE_GATE_LOGITS ? gate_alpha_logit(x, alpha_min) : gate_alpha(x, g_min);
 }
 
@@ -325,8 +327,8 @@ __global__ __launch_bounds__(256) void tree_path_kernel(
 // Values that are not finite: a product over nodes would carry one node's NaN
 // to nodes that do not descend from it (0 * NaN). So they are replaced by 0
 // before such a product and remembered as bits, per node where they reach every
-// column (A, B) and per node and column (d); the outputs of their nodes and
-// descendants are then set to NaN.
+// column (A, B, NaN decays) and per node and column (d); the outputs of their
+// nodes and descendants are then set to NaN.
 
 // Operands of products on the fp32 matrix instructions (16 x 16 x 4).
 struct FloatOp {
@@ -424,6 +426,7 @@ __global__ __launch_bounds__(64 * kWaves, kDeep ? 2 : 4) void tree_tile_kernel(
   __shared__ uint64_t s_anc[kMaxNodes];
   __shared__ __attribute__((aligned(16))) float s_b[kMaxNodes];
   __shared__ unsigned long long s_bad[2];                // nodes with d, with o not finite in every column
+  __shared__ uint64_t s_gate[kWaves];                    // nodes with NaN decays in a wave's channels
   // Rows of this head inside the sequence by 32-bit byte offsets from uniform
   // bases (the launcher sees to 4 H D < 2^24): one instruction an address.
   const uint32_t row_bytes = (uint32_t)H * D * sizeof(TIn);
@@ -495,7 +498,15 @@ __global__ __launch_bounds__(64 * kWaves, kDeep ? 2 : 4) void tree_tile_kernel(
     s_b[lane] = lane >= nt ? 0.f : fe_flags & KDA_FE_BETA_LOGITS ? beta_logit(braw) : braw;
     if (lane < 2) s_bad[lane] = 0;
   }
-  // decays, normalised rows
+  // decays, normalised rows; a node with a NaN decay is remembered as bad, the
+  // decay itself is the floor's from here on (the clamps drop NaN)
+  bool nan_gate = false;
+#pragma unroll
+  for (int c = 0; c < kC; ++c) nan_gate |= te[c] != te[c];
+  uint64_t nan_nodes = __ballot(nan_gate && live);
+  if (kNodes <= 32) nan_nodes |= nan_nodes >> 32;
+  if (kNodes == 16) nan_nodes |= nan_nodes >> 16;
+  if (lane == 0) s_gate[wave] = nan_nodes & (~0ull >> (64 - kNodes));
   const float alpha_min = __builtin_amdgcn_exp2f(g_min * kLog2e);
   double G[kC];                                           // (kDeep)
   if constexpr (kDeep) {
@@ -819,7 +830,9 @@ __global__ __launch_bounds__(64 * kWaves, kDeep ? 2 : 4) void tree_tile_kernel(
       }
     }
   }
-  const uint64_t bad_d = s_bad[0], bad_o = s_bad[1];
+  uint64_t bad_d = s_bad[0], bad_o = s_bad[1];
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) bad_d |= s_gate[w];
   bool any = bad_d | bad_o;
 #pragma unroll
   for (int c = 0; c < kNT; ++c) any |= bad[c] != 0;
@@ -918,10 +931,18 @@ __global__ __launch_bounds__(256, kTB >= 3 ? 2 : 4) void tree_small_kernel(
     }
   }
   // G by doubling inside each block, then on from the path's last node before it
+  uint64_t bad_d = 0, bad_o = 0;             // nodes with d, with o not finite in every column
   double G[kTB][4];
   static_for<0, kTB>([&](auto II) __attribute__((always_inline)) {
     constexpr int I = decltype(II)::value;
     const bool live = 16 * I + lr < nt;
+    bool odd = false;                        // a NaN decay, which log2_alpha's clamps drop
+#pragma unroll
+    for (int c = 0; c < 4; ++c) odd |= gv[I][c] != gv[I][c];
+    uint64_t m = __ballot(odd && live);
+    m |= m >> 32;
+    m |= m >> 16;
+    bad_d |= (m & 0xffff) << (16 * I);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       if (!live) kv[I][c] = qv[I][c] = 0.f;
@@ -952,7 +973,6 @@ __global__ __launch_bounds__(256, kTB >= 3 ? 2 : 4) void tree_small_kernel(
 
   // U, W, A and B (transposed products: acc[r] = element (row lr, column 4 lg + r))
   f32x4 U[kTB], W[kTB], A[kTB][kTB], B[kTB][kTB];
-  uint64_t bad_d = 0, bad_o = 0;             // nodes with d, with o not finite in every column
   auto note = [&](f32x4& x, int I, uint64_t& bits) __attribute__((always_inline)) {
     const bool odd = !(is_finite(x[0]) && is_finite(x[1]) && is_finite(x[2]) && is_finite(x[3]));
     uint64_t m = __ballot(odd);
@@ -1230,7 +1250,8 @@ __global__ __launch_bounds__(D == 128 ? 256 : 64) void commit_kernel(
       const int e = tid + x * kThreads, t = e / D, c = e % D;
       s_k[t][c] = tk[x];
       s_v[t][c] = tv[x];
-      s_a[t][c] = gate == KDA_GATE_NONE              ? 1.f
+      s_a[t][c] = gate == KDA_GATE_NONE            ? 1.f
+                  : ta[x] != ta[x]                ? ta[x]        // (the clamps would drop a NaN)
                   : fe_flags & KDA_FE_GATE_LOGITS ? gate_alpha_logit(ta[x], alpha_min)
                                                   : gate_alpha(ta[x], g_min);
     }

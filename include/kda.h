@@ -368,8 +368,11 @@ kda_status kda_decode_tokens(const void* q, const void* k, const void* v, kda_dt
  *   state   [N, H, Dk, Dv] fp32, read only
  *   o       [N, T, H, Dv] dtype; must not overlap the inputs
  * Products and sums are fp32, whatever dtype is; o is rounded once.
- * A node whose inputs are not finite, or overflow, makes outputs of itself and
- * its descendants non-finite, and no others.
+ * A node whose k, v or beta is not finite or whose g is NaN, and a node whose
+ * products overflow, makes outputs of itself and its descendants non-finite (of
+ * a value in v: in its column), and no others; a q that is not finite, those of
+ * its own node. Infinite g are clamped like any other. (A NaN in g reads as
+ * g_min in kda_decode_step and kda_decode_tokens.)
  * T outside [1, KDA_TREE_MAX_NODES] and N * H above KDA_MAX_LAUNCH_HEADS are
  * KDA_ERR_INVALID_ARG; the other errors are those of kda_decode_tokens.
  * Cost: one pass over the state and the tokens while the decays of a tree span
@@ -390,7 +393,8 @@ kda_status kda_decode_tree(const void* q, const void* k, const void* v, kda_dtyp
  *   path    [N, T] int32 (device), as kda_verify_drafts writes it; a value
  *           outside [0, T) ends the path
  *   accept  [N] int32 (device), clamped to [0, T]; 0 leaves the state untouched
- * Only the listed nodes are read. Errors as kda_decode_tree. */
+ * Only the listed nodes are read. What is not finite in them (NaN in g
+ * included) makes the state so. Errors as kda_decode_tree. */
 kda_status kda_commit_path(const void* k, const void* v, kda_dtype dtype, const float* g,
                            const float* beta, float* state, const int32_t* path,
                            const int32_t* accept, int32_t N, int32_t T, int32_t H, int32_t Dk,

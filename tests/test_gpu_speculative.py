@@ -180,6 +180,59 @@ def test_a_nodes_nan_reaches_its_descendants_only(T, D, dtype, g_min, what):
         assert torch.equal(o[hit][:, rest], clean[hit][:, rest])
 
 
+@pytest.mark.parametrize("gate,flags", [(kda.GATE_CHANNEL, 0), (kda.GATE_HEAD, 0), (kda.GATE_CHANNEL, kda.FE_ALL)])
+@pytest.mark.parametrize("T,D,dtype,g_min", [(16, 128, BF16, LN_HALF), (50, 128, BF16, LN_HALF), (21, 128, F32, LN_HALF),
+                                             (16, 16, F32, LN_HALF), (50, 128, BF16, -5.0), (20, 128, F32, -5.0),
+                                             (50, 16, BF16, -5.0), (9, 128, F32, -100.0)])
+def test_a_nan_decay_reaches_its_nodes_descendants_only(T, D, dtype, g_min, gate, flags):
+    """A NaN log-decay (or logit) makes every column of its node and the nodes
+    below it NaN, the state of a path through it too; infinite ones are clamped."""
+    s = Step(2, T, 2, D, dtype, 22, gate, flags, g_min)
+    par = random_parents(2, T, "bushy", 8)
+    p, opts = dev(par, torch.int32), dict(g_min=g_min, options=s.options)
+    g = s.args[3]
+    i, h = 3, 1
+    g[1, i, h].reshape(-1)[-1] = float("nan")
+    # behind a sequence's last node nothing is read, a NaN decay neither
+    nodes = np.array([T - 2, T], np.int32)
+    g[0, T - 2:] = float("nan")
+    o = kda.decode_tree(*s.args, s.state, p, dev(nodes, torch.int32), **opts)
+    hit = torch.zeros(2, T, 2, dtype=torch.bool, device=DEV)
+    below = {i}
+    for t in range(i + 1, T):
+        if int(par[1, t]) in below:
+            below.add(t)
+    hit[1, sorted(below), h] = True
+    live = torch.arange(T, device=DEV) < dev(nodes, torch.int32)[:, None]
+    assert torch.isnan(o[hit]).all()
+    # the other nodes against the oracle, which has the inputs without NaN (not bit
+    # for bit against a run without: the decays' reference in a block of nodes, and
+    # so the rounding, goes by the decays of all its live nodes)
+    ref = speculative.decode_tree(s.q, s.k, s.v, s.g, s.b, s.s0, par, nodes, 1.0, g_min)
+    for n in range(2):
+        rows = (~hit & live[..., None])[n, :nodes[n]].cpu().numpy()
+        tol = speculative.tree_bound(s.q[n], s.k[n], s.v[n], s.g[n], s.b[n], s.s0[n],
+                                     speculative.parents_of(par[n], T), nodes[n], 1.0, g_min, s.product)
+        if dtype is BF16:
+            tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref[n, :nodes[n]])
+        assert (np.abs(host(o[n, :nodes[n]]) - ref[n, :nodes[n]]) <= tol)[rows].all()
+    # the commit of a path through the node, and of one beside it
+    path = torch.full((2, T), -1, device=DEV, dtype=torch.int32)
+    path[0, :2], path[1, :2] = torch.tensor([0, 1]), torch.tensor([0, i])
+    state = s.state.clone()
+    kda.commit_path(*s.args[1:], state, path, torch.full((2,), 2, device=DEV, dtype=torch.int32), **opts)
+    assert torch.isfinite(state[0]).all() and torch.isfinite(state[1, 0]).all() and torch.isnan(state[1, 1]).all()
+    # infinities: the floor and no decay (as logits the other way round)
+    ends = [s.args[3].clone() for _ in range(2)]
+    low, none = (float("-inf"), float("inf")) if not flags else (float("inf"), float("-inf"))
+    for x, inf, stand_in in ((ends[0], low, 1e30 if flags else -1e30), (ends[1], none, -1e30 if flags else 1e30)):
+        x.nan_to_num_(nan=0.25)
+        y = x.clone()
+        x[1, i], y[1, i] = inf, stand_in
+        both = [kda.decode_tree(*s.args[:3], z, s.args[4], s.state, p, **opts) for z in (x, y)]
+        assert torch.equal(*both) and torch.isfinite(both[0]).all()
+
+
 @pytest.mark.parametrize("T,D,dtype,g_min", [(16, 128, BF16, LN_HALF), (30, 128, BF16, LN_HALF), (50, 128, BF16, LN_HALF),
                                              (50, 128, BF16, -5.0), (50, 128, F32, LN_HALF), (20, 16, BF16, LN_HALF),
                                              (9, 128, BF16, -100.0)])
