@@ -23,6 +23,7 @@ namespace kda {
 namespace {
 
 constexpr int kMaxChunks = 64;
+constexpr int kManySeqs = 64;
 
 // Per-sequence workspace record.
 struct Walk {
@@ -42,7 +43,7 @@ struct VerifyPlan {
 // sequences to fill the GPU otherwise.
 VerifyPlan verify_plan(int32_t N, int32_t V) {
   VerifyPlan p;
-  const int least = N >= 64 ? 4096 : 1024;
+  const int least = N >= kManySeqs ? 4096 : 1024;
   const int chunk = ((V + kMaxChunks - 1) / kMaxChunks + 7) / 8 * 8;
   p.chunk = chunk < least ? least : chunk;
   p.chunks = (V + p.chunk - 1) / p.chunk;
@@ -594,7 +595,13 @@ hipError_t launch_verify_t(const VerifyArgs& a) {
 
 }  // namespace
 
-size_t verify_workspace(int32_t N, int32_t T, int32_t V) { return verify_plan(N, V).total; }
+// Grows with N and V, so that a workspace serves every smaller call too: a plan
+// for fewer than 64 sequences has up to four times the chunks for each, so it may
+// need more than one for a few more sequences.
+size_t verify_workspace(int32_t N, int32_t T, int32_t V) {
+  const size_t few = verify_plan(N < kManySeqs ? N : kManySeqs - 1, V).total, all = verify_plan(N, V).total;
+  return few > all ? few : all;
+}
 
 hipError_t launch_verify(const VerifyArgs& a) {
   return a.bf16 ? launch_verify_t<bf16_bits>(a) : launch_verify_t<float>(a);

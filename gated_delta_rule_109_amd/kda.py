@@ -417,7 +417,8 @@ def commit_path(k, v, g, beta, state, path, accept, g_min=LN_HALF, options: Opti
 
 
 def verify_workspace(N: int, T: int, V: int, device) -> torch.Tensor:
-    """A workspace for verify_drafts calls of these sizes, one after another."""
+    """A workspace for verify_drafts calls of these sizes and smaller ones, one
+    after another."""
     size = int(lib().kda_verify_workspace_size(int(N), int(T), int(V)))
     if size == 0 and N != 0:
         raise KdaError(KDA_ERR_INVALID_ARG, "kda_verify_workspace_size")

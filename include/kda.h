@@ -405,7 +405,9 @@ kda_status kda_commit_path(const void* k, const void* v, kda_dtype dtype, const 
 #define KDA_VERIFY_MAX_SEQS ((1 << 20) - 1)
 
 /* Bytes of device workspace kda_verify_drafts needs (0 for sizes it refuses).
- * It needs no initialisation; calls that may overlap need one each. */
+ * They do not shrink as N, T or V grow: a workspace of the largest sizes serves
+ * every smaller call. It needs no initialisation; calls that may overlap need
+ * one each. */
 size_t kda_verify_workspace_size(int32_t N, int32_t T, int32_t V);
 
 /* Verification of drafted tokens against the target model's probabilities, by

@@ -493,6 +493,18 @@ def test_verify_of_a_chain_given_as_a_tree():
         assert [x.tolist() for x in a] == [x.tolist() for x in b]
 
 
+def test_verify_in_a_workspace_of_a_larger_batch():
+    """A batch that shrinks keeps its workspace (the rows are spread over the GPU
+    at these sizes, so the workspace holds partial sums)."""
+    rng = np.random.default_rng(12)
+    T, V = 2, 65536
+    ws = kda.verify_workspace(64, 4, V, DEV)
+    for N in (63, 17, 1):
+        target, draft = probabilities(rng, N, T, V, BF16)
+        tokens = draft[:, :1].float().argmax(-1).expand(N, T).numpy().astype(np.int32)
+        check_verify(target, draft, tokens, rng.random((N, T)).astype(np.float32), None, workspace=ws)
+
+
 def test_verify_rejects_a_near_certain_token_exactly():
     """One token holds all but 2^-60 of a row: without it the residual is the
     rest, which no subtraction of sums may lose."""

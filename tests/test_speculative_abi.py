@@ -115,6 +115,27 @@ def test_verify_workspace_size():
         assert verify(N=N, V=V, workspace_bytes=s - 1) == WS
 
 
+def test_verify_workspace_serves_smaller_calls():
+    """A server allocates once for its largest sizes: no smaller batch, tree or
+    vocabulary needs more."""
+    size = kda.lib().kda_verify_workspace_size
+    some_n = [1, 2, 16, 17, 31, 48, 62, 63, 64, 65, 66, 96, 128, 200, 255, 256, 257, 300, 512, 1000, 4096, 1 << 16, (1 << 20) - 1]
+    some_v = [1, 7, 1000, 1024, 1025, 4096, 4097, 32768, 50001, 65535, 65536, 65537, 66048, 66049, 131072, 262144, 262145,
+              300001, 1 << 20, 2000003, (1 << 24) - 1, 1 << 24]
+    for V in some_v:
+        sizes = [size(N, 5, V) for N in some_n]
+        assert sizes == sorted(sizes), V
+        assert size(64, 1, V) == size(64, 64, V)
+    for N in some_n:
+        sizes = [size(N, 5, V) for V in some_v]
+        assert sizes == sorted(sizes), N
+        sizes = [size(N, 5, V) for V in range(60000, 70000, 7)]
+        assert sizes == sorted(sizes), N
+    for V in (32768, 50001, 65536, 131072):
+        sizes = [size(N, 5, V) for N in range(0, 300)]
+        assert sizes == sorted(sizes), V
+
+
 @pytest.mark.parametrize("call", [store, load])
 @pytest.mark.parametrize("bad,status", [
     (dict(format=2), UNSUP), (dict(format=-1), UNSUP), (dict(Dk=64, Dv=64), UNSUP), (dict(Dv=16), UNSUP),
