@@ -87,6 +87,25 @@ bool aligned4(std::initializer_list<const void*> ps) {
   return true;
 }
 
+// An array as a call uses it (p NULL: not used).
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  return a.p && b.p && (uintptr_t)a.p < (uintptr_t)b.p + b.bytes && (uintptr_t)b.p < (uintptr_t)a.p + a.bytes;
+}
+// Whether no array that is written shares a byte with another one of the call.
+bool apart(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  for (const Span* w = written.begin(); w != written.end(); ++w) {
+    for (const Span* x = w + 1; x != written.end(); ++x)
+      if (overlap(*w, *x)) return false;
+    for (const Span& r : read)
+      if (overlap(*w, r)) return false;
+  }
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -414,6 +433,12 @@ kda_status kda_verify_drafts(const void* target, const void* draft, kda_dtype dt
     return KDA_ERR_INVALID_ARG;
   if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < kda::verify_workspace(N, T, V))
     return KDA_ERR_WORKSPACE;
+  // several workgroups read a sequence's nodes while one writes its results
+  const size_t nodes = (size_t)N * T, row = (size_t)V * (dt == KDA_BF16 ? 2 : 4);
+  if (!apart({{accept, 4ull * N}, {path, 4 * nodes}, {next_token, 4ull * N}, {workspace, kda::verify_workspace(N, T, V)}},
+             {{target, nodes * row}, {draft, nodes * row}, {tokens, 4 * nodes}, {parents, 4 * nodes},
+              {num_nodes, 4ull * N}, {uniforms, 4 * nodes}}))
+    return KDA_ERR_INVALID_ARG;
   kda::VerifyArgs a;
   a.target = target; a.draft = draft;
   a.tokens = tokens; a.parents = parents; a.num_nodes = num_nodes; a.uniforms = uniforms;

@@ -432,7 +432,8 @@ def verify_drafts(target, draft, tokens, uniforms, parents=None, num_nodes=None,
     draft [N,T,V] those that a node's children were drawn from (None: chosen
     without sampling); tokens int32 [N,T]; uniforms float32 [N,T], entry i >= 1
     for node i's test and entry 0 for the next token; parents and num_nodes as
-    in decode_tree. workspace (verify_workspace) is allocated when None.
+    in decode_tree. workspace (verify_workspace) is allocated when None, and so
+    are the outputs, which must not overlap each other or an input.
     Returns (accept [N], path [N,T], next_token [N]), int32: accept is that of
     decode_tokens (chains) and, with path, of commit_path."""
     N, T, V = target.shape

@@ -442,7 +442,8 @@ size_t kda_verify_workspace_size(int32_t N, int32_t T, int32_t V);
  * For chains, accept is the accept of kda_decode_tokens.
  *   workspace   256-byte aligned device scratch of
  *               kda_verify_workspace_size(N, T, V) bytes
- * V may be odd.
+ * accept, path, next_token and the workspace overlap neither each other nor an
+ * input (KDA_ERR_INVALID_ARG). V may be odd.
  * Errors: KDA_ERR_INVALID_ARG (null required pointer, N outside
  * [0, KDA_VERIFY_MAX_SEQS], T outside [1, KDA_TREE_MAX_NODES], V outside
  * [1, KDA_VERIFY_MAX_VOCAB]), KDA_ERR_UNSUPPORTED

@@ -505,6 +505,30 @@ def test_verify_in_a_workspace_of_a_larger_batch():
         check_verify(target, draft, tokens, rng.random((N, T)).astype(np.float32), None, workspace=ws)
 
 
+def test_verify_of_arrays_side_by_side():
+    """Inputs and outputs that touch without overlapping, in one buffer."""
+    rng = np.random.default_rng(13)
+    N, T, V = 5, 7, 900
+    target, draft = probabilities(rng, N, T, V, F32)
+    tokens, u = rng.integers(0, V, (N, T)).astype(np.int32), rng.random((N, T)).astype(np.float32)
+    par, nodes = random_parents(N, T, "bushy", 1), np.full(N, T, np.int32)
+    buf = torch.full((3 * N + 3 * N * T,), 7, device=DEV, dtype=torch.int32)
+    at = 0
+    parts = []
+    for shape in ((N,), (N, T), (N, T), (N,), (N, T), (N,)):
+        size = int(np.prod(shape))
+        parts.append(buf[at:at + size].view(shape))
+        at += size
+    accept, tok, path, next_token, p, nn = parts
+    tok.copy_(dev(tokens, torch.int32)); p.copy_(dev(par, torch.int32)); nn.copy_(dev(nodes, torch.int32))
+    got = kda.verify_drafts(target.to(DEV), draft.to(DEV), tok, dev(u), p, nn, accept=accept, path=path, next_token=next_token)
+    want = speculative.verify(target.numpy(), draft.numpy(), tokens, u, par, nodes)
+    assert all(a.tolist() == b.tolist() for a, b in zip(got, want))
+    assert torch.equal(tok, dev(tokens, torch.int32)) and torch.equal(p, dev(par, torch.int32))
+    with pytest.raises(kda.KdaError):
+        kda.verify_drafts(target.to(DEV), draft.to(DEV), tok, dev(u), p, nn, accept=accept, path=tok, next_token=next_token)
+
+
 def test_verify_rejects_a_near_certain_token_exactly():
     """One token holds all but 2^-60 of a row: without it the residual is the
     rest, which no subtraction of sums may lose."""

@@ -105,6 +105,28 @@ def test_verify_refuses(bad, status):
     assert verify(**bad) == status
 
 
+# every array of a verification 1 MiB from the next, so that none overlaps
+APART = {name: (1 << 20) * (i + 1) for i, name in enumerate(
+    ("target", "draft", "tokens", "parents", "num_nodes", "uniforms", "accept", "path", "next_token", "workspace"))}
+
+
+@pytest.mark.parametrize("out", ["accept", "path", "next_token", "workspace"])
+@pytest.mark.parametrize("other", list(APART))
+def test_verify_refuses_outputs_that_overlap(out, other):
+    """An output on top of another array, or with its first or last bytes in it:
+    workgroups read a sequence's nodes while one of them writes."""
+    if out == other:
+        return
+    N, T, V = 2, 5, 1000
+    bytes_of = dict(target=4 * N * T * V, draft=4 * N * T * V, tokens=4 * N * T, parents=4 * N * T, num_nodes=4 * N,
+                    uniforms=4 * N * T, accept=4 * N, path=4 * N * T, next_token=4 * N,
+                    workspace=kda.lib().kda_verify_workspace_size(N, T, V))
+    step = 256 if out == "workspace" else 4
+    for at in (0, bytes_of[other] - 1 & -step, -(bytes_of[out] - 1 & -step)):
+        a = {**APART, out: APART[other] + at}
+        assert verify(**{k: ctypes.c_void_p(x) for k, x in a.items()}, N=N, T=T, V=V) == BAD
+
+
 def test_verify_workspace_size():
     size = kda.lib().kda_verify_workspace_size
     assert size(0, 5, 100) == 0 and size(-1, 5, 100) == 0 and size(1, 0, 100) == 0 and size(1, 65, 100) == 0
