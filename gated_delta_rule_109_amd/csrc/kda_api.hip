@@ -338,10 +338,12 @@ kda_status kda_decode_tokens(const void* q, const void* k, const void* v, kda_dt
   return from_hip(kda::launch_decode(a));
 }
 
-// A launch takes fewer than 2^32 threads: one workgroup of 256 per head, or of
-// 1024 per sequence (and up to 16 of 256) of a verification.
-constexpr int64_t kMaxHeads = KDA_MAX_LAUNCH_HEADS;
-static_assert(kMaxHeads * 256 < 1ll << 32, "workgroups of the tree, commit and cache kernels");
+// A launch takes fewer than 2^32 threads: one workgroup of 256 per head (of 512
+// for larger trees of larger heads), or of 1024 per sequence (and up to 16 of
+// 256) of a verification.
+constexpr int64_t kMaxHeads = KDA_MAX_LAUNCH_HEADS, kMaxTreeHeads = KDA_MAX_LARGE_TREE_HEADS;
+static_assert(kMaxHeads * kda::kHeadThreads < 1ll << 32, "workgroups of the tree, commit and cache kernels");
+static_assert(kMaxTreeHeads * kda::kLargeTreeThreads < 1ll << 32, "workgroups of the tree kernels of 512 threads");
 static_assert(KDA_VERIFY_MAX_SEQS * 1024ll < 1ll << 32 && KDA_VERIFY_MAX_SEQS * 16ll * 256 < 1ll << 32,
               "workgroups of the verification kernels");
 
@@ -374,6 +376,7 @@ kda_status kda_decode_tree(const void* q, const void* k, const void* v, kda_dtyp
   const int dt = enum_code(dtype);
   const kda_status st = tree_args_ok(dt, opt, N, T, H, Dk, Dv, g_min);
   if (st != KDA_OK || N == 0) return st;
+  if (Dk == 128 && T > 16 && (int64_t)N * H > kMaxTreeHeads) return KDA_ERR_INVALID_ARG;
   const bool need_g = gate_of(opt) != KDA_GATE_NONE;
   if (!q || !k || !v || (need_g && !g) || !beta || !state || !o) return KDA_ERR_INVALID_ARG;
   if (!aligned16({q, k, v, g, beta, state, o}) || !aligned4({parents, num_nodes})) return KDA_ERR_INVALID_ARG;

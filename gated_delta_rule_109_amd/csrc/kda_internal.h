@@ -50,6 +50,10 @@ struct TreeArgs {
   hipStream_t stream;
 };
 
+// Most threads per head of the tree, commit and cache kernels, and of trees of
+// more than 16 nodes with heads of 128.
+constexpr int kHeadThreads = 256, kLargeTreeThreads = 512;
+
 struct VerifyArgs {
   const void *target, *draft;
   const int32_t *tokens, *parents, *num_nodes;

@@ -1129,6 +1129,7 @@ template <int kTB, int kWaves, typename TIn, bool kDeep>
 static hipError_t launch_tiles(const TreeArgs& a, int reach) {
   const unsigned blocks = (unsigned)((int64_t)a.N * a.H);
   constexpr size_t lds = TileLds<kTB, kDeep>::kBytes;
+  static_assert(64 * kWaves <= (kTB == 1 ? kHeadThreads : kLargeTreeThreads), "threads that the launch limits count");
   hipLaunchKernelGGL((tree_tile_kernel<kTB, kWaves, TIn, kDeep>), dim3(blocks), dim3(64 * kWaves), lds, a.stream,
                      (const TIn*)a.q, (const TIn*)a.k, (const TIn*)a.v, a.g, a.beta, a.state, a.parents, a.num_nodes, (TIn*)a.o, a.H, a.T, a.scale, a.g_min, a.fe_flags,
                      a.fe_eps, (int)a.gate, reach);

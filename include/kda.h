@@ -355,6 +355,8 @@ kda_status kda_decode_tokens(const void* q, const void* k, const void* v, kda_dt
 /* Most heads of all sequences together (N * H) that one call of the tree step
  * or of the state cache takes. */
 #define KDA_MAX_LAUNCH_HEADS 16777215
+/* The same for kda_decode_tree with D = 128 and T > 16. */
+#define KDA_MAX_LARGE_TREE_HEADS 8388607
 
 /* Attention of a tree of T drafted tokens per sequence over its recurrent
  * state. Every node's output is the recurrence's output after the tokens on
@@ -373,8 +375,8 @@ kda_status kda_decode_tokens(const void* q, const void* k, const void* v, kda_dt
  * a value in v: in its column), and no others; a q that is not finite, those of
  * its own node. Infinite g are clamped like any other. (A NaN in g reads as
  * g_min in kda_decode_step and kda_decode_tokens.)
- * T outside [1, KDA_TREE_MAX_NODES] and N * H above KDA_MAX_LAUNCH_HEADS are
- * KDA_ERR_INVALID_ARG; the other errors are those of kda_decode_tokens.
+ * T outside [1, KDA_TREE_MAX_NODES] and N * H above KDA_MAX_LAUNCH_HEADS (or
+ * KDA_MAX_LARGE_TREE_HEADS where that holds) are KDA_ERR_INVALID_ARG; the other errors are those of kda_decode_tokens.
  * Cost: one pass over the state and the tokens while the decays of a tree span
  * at most 2^87 (T * -g_min <= 60); with lower floors A and B are formed with
  * a reference per 16 nodes (about three times the time at 64 nodes), and trees

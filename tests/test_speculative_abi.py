@@ -85,6 +85,13 @@ def test_tree_and_commit_options(call):
     assert call(N=0, k=None, v=None) == OK
 
 
+def test_tree_launch_limits():
+    """Trees of more than 16 nodes with heads of 128 launch 512 threads a head:
+    a launch of 2^32 threads or more is refused before it is tried."""
+    assert tree(N=1 << 18, H=32, T=17) == BAD                 # 2^23 heads: 2^32 threads
+    assert tree(N=1 << 18, H=32, T=64) == BAD
+
+
 def test_tree_and_commit_own_pointers():
     for name in ("q", "o"):
         assert tree(**{name: None}) == BAD and tree(**{name: ODD}) == BAD
