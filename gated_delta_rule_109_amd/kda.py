@@ -416,9 +416,16 @@ def commit_path(k, v, g, beta, state, path, accept, g_min=LN_HALF, options: Opti
     return state
 
 
+def _check_int32(*sizes):
+    """Sizes that the C ABI's int32 cannot carry (ctypes would drop the high bits)."""
+    if max(sizes) >= 2 ** 31:
+        raise ValueError(f"sizes {sizes} are outside int32")
+
+
 def verify_workspace(N: int, T: int, V: int, device) -> torch.Tensor:
     """A workspace for verify_drafts calls of these sizes and smaller ones, one
     after another."""
+    _check_int32(N, T, V)
     size = int(lib().kda_verify_workspace_size(int(N), int(T), int(V)))
     if size == 0 and N != 0:
         raise KdaError(KDA_ERR_INVALID_ARG, "kda_verify_workspace_size")
@@ -437,6 +444,7 @@ def verify_drafts(target, draft, tokens, uniforms, parents=None, num_nodes=None,
     Returns (accept [N], path [N,T], next_token [N]), int32: accept is that of
     decode_tokens (chains) and, with path, of commit_path."""
     N, T, V = target.shape
+    _check_int32(N, T, V)
     code = _dtype_code(target)
     if tokens is None or uniforms is None:
         raise ValueError("tokens and uniforms are required")
@@ -494,8 +502,7 @@ def _cache_call(where, fn, first, cache: StateCache, slots, states):
     dev = _check_step(("values", cache.values, (S, H, D, D), cache.values.dtype),
                       ("scales", cache.scales, (S, H, D * D // CACHE_BLOCK), torch.uint8),
                       ("slots", slots, (N,), torch.int32), ("states", states, (N, H, D, D), torch.float32))
-    if S >= 2 ** 31:
-        raise ValueError(f"num_slots: {S} is above INT32_MAX")
+    _check_int32(S, N)
     if first == "states":
         args = (states.data_ptr(), _addr(slots), cache.values.data_ptr(), cache.scales.data_ptr())
     else:

@@ -236,6 +236,16 @@ def test_binding_checks_verify():
         kda.verify_workspace(1, 65, 100, "cpu")
 
 
+@pytest.mark.parametrize("N,T,V", [(1, 2, 2 ** 32 + 5), (2 ** 32 + 1, 2, 5), (1, 2 ** 32 + 2, 5), (1, 2, 2 ** 31)])
+def test_binding_refuses_sizes_past_int32(N, T, V):
+    """A vocabulary of 2^32 + 5 must not run as one of 5."""
+    big = lambda *s, dtype=torch.float32: torch.empty(*s, dtype=dtype, device="meta")  # noqa: E731
+    with pytest.raises(ValueError, match="int32"):
+        kda.verify_workspace(N, T, V, "cpu")
+    with pytest.raises(ValueError, match="int32"):
+        kda.verify_drafts(big(N, T, V), None, big(N, T, dtype=I32), big(N, T))
+
+
 def test_binding_checks_cache():
     with pytest.raises(TypeError, match="values: expected"):
         kda.make_state_cache(2, 2, 16, "cpu", dtype=torch.uint8)
