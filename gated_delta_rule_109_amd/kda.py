@@ -348,11 +348,18 @@ def _check_step(*specs):
     raise ValueError("tensors on more than one device: one call takes one device")
 
 
+def _check_int32(*sizes):
+    """Sizes that the C ABI's int32 cannot carry (ctypes would drop the high bits)."""
+    if max(sizes) >= 2 ** 31:
+        raise ValueError(f"sizes {sizes} are outside int32")
+
+
 def _step_inputs(q, k, v, g, beta, lead, H, D, options):
     """Specifications of a step's q, k, v, g and beta."""
     dt = q.dtype
     if dt is not torch.bfloat16 and dt is not torch.float32:
         raise TypeError(f"q/k/v must be bfloat16 or float32, got {dt}")
+    _check_int32(*lead, H)
     shape = (*lead, H, D)
     gshape = _gate_shape(lead, H, D, options)
     if gshape is None:
@@ -414,12 +421,6 @@ def commit_path(k, v, g, beta, state, path, accept, g_min=LN_HALF, options: Opti
           _addr(beta), _addr(state), path.data_ptr(), accept.data_ptr(), N, T, H, D, D, float(g_min),
           _opt_ptr(options))
     return state
-
-
-def _check_int32(*sizes):
-    """Sizes that the C ABI's int32 cannot carry (ctypes would drop the high bits)."""
-    if max(sizes) >= 2 ** 31:
-        raise ValueError(f"sizes {sizes} are outside int32")
 
 
 def verify_workspace(N: int, T: int, V: int, device) -> torch.Tensor:

@@ -246,6 +246,16 @@ def test_binding_refuses_sizes_past_int32(N, T, V):
         kda.verify_drafts(big(N, T, V), None, big(N, T, dtype=I32), big(N, T))
 
 
+def test_step_refuses_sizes_past_int32():
+    big = lambda *s, dtype=torch.float32: torch.empty(*s, dtype=dtype, device="meta")  # noqa: E731
+    for N, T, H in ((1, 2 ** 32 + 5, 1), (2 ** 32 + 1, 2, 1), (1, 2, 2 ** 32 + 3)):
+        x, g, b, state = big(N, T, H, 16, dtype=BF16), big(N, T, H, 16), big(N, T, H), big(N, H, 16, 16)
+        with pytest.raises(ValueError, match="int32"):
+            kda.decode_tree(x, x, x, g, b, state)
+        with pytest.raises(ValueError, match="int32"):
+            kda.commit_path(x, x, g, b, state, big(N, T, dtype=I32), big(N, dtype=I32))
+
+
 def test_binding_checks_cache():
     with pytest.raises(TypeError, match="values: expected"):
         kda.make_state_cache(2, 2, 16, "cpu", dtype=torch.uint8)
