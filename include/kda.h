@@ -423,7 +423,7 @@ size_t kda_verify_workspace_size(int32_t N, int32_t T, int32_t V);
  *   tokens    [N, T] int32: the token of each node (tokens[n][0] is not read)
  *   parents, num_nodes   as above (NULL parents: chains)
  *   uniforms  [N, T] fp32 in [0, 1): entry i >= 1 tests node i, entry 0 draws
- *             the next token
+ *             the next token (NaN: node i is not accepted; the draw is that of 0)
  * From the root, with p and q the rows of the current node, r = p, c = 1 and
  * C = 0, its children are tried in the order of their indices. A child with
  * token x is accepted, and becomes the current node, iff

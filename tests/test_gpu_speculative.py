@@ -529,6 +529,30 @@ def test_verify_of_arrays_side_by_side():
         kda.verify_drafts(target.to(DEV), draft.to(DEV), tok, dev(u), p, nn, accept=accept, path=tok, next_token=next_token)
 
 
+@pytest.mark.parametrize("N,V,tree", [(3, 700, "chain"), (3, 700, "star"), (2, 66001, "chain"), (2, 66001, "star")])
+@pytest.mark.parametrize("with_draft", [True, False])
+def test_verify_of_uniforms_that_are_nan(N, V, tree, with_draft):
+    """The kernel reads the NaN itself: a test of NaN accepts nothing, and a draw
+    of NaN is one of 0 (the first token of the residual, one of many here)."""
+    rng = np.random.default_rng(V)
+    T = 4
+    target, draft = probabilities(rng, N, T, V, F32)
+    target[:, :, :3] = 0.0                                    # the draw of 0 is token 3 or the next one left
+    par = random_parents(N, T, tree, 0)
+    tokens = rng.integers(4, V, (N, T)).astype(np.int32)
+    u = rng.random((N, T)).astype(np.float32) * 0.5
+    u[:, 0], u[0, 1:], u[1, 2] = np.nan, np.nan, np.nan
+    stand_in = np.where(np.isnan(u), np.float32(1e30), u)     # rejects: every token has weight in both rows
+    stand_in[:, 0] = 0.0
+    d = draft if with_draft else None
+    got = kda.verify_drafts(target.to(DEV), None if d is None else d.to(DEV), dev(tokens, torch.int32), dev(u),
+                            None if tree == "chain" else dev(par, torch.int32))
+    want = speculative.verify(target.numpy(), None if d is None else d.numpy(), tokens, stand_in, par)
+    for a, b in zip(got, want):
+        assert a.tolist() == b.tolist()
+    assert got[0][0] == 1 and (got[2] >= 3).all() and (got[2] < 3 + 64).all()
+
+
 def test_verify_rejects_a_near_certain_token_exactly():
     """One token holds all but 2^-60 of a row: without it the residual is the
     rest, which no subtraction of sums may lose."""
