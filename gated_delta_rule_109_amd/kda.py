@@ -435,8 +435,9 @@ def verify_workspace(N: int, T: int, V: int, device) -> torch.Tensor:
 
 def verify_drafts(target, draft, tokens, uniforms, parents=None, num_nodes=None,
                   workspace: Optional[torch.Tensor] = None, accept=None, path=None, next_token=None):
-    """kda_verify_drafts: rejection sampling of drafted tokens. target [N,T,V]
-    (bfloat16 or float32) holds the target's probabilities after each node,
+    """kda_verify_drafts: rejection sampling of drafted tokens, without loss for
+    rows that sum to 1 (rows are never normalised; what bfloat16 rows shift is
+    in kda.h). target [N,T,V] (bfloat16 or float32) holds the target's probabilities after each node,
     draft [N,T,V] those that a node's children were drawn from (None: chosen
     without sampling); tokens int32 [N,T]; uniforms float32 [N,T], entry i >= 1
     for node i's test and entry 0 for the next token; parents and num_nodes as

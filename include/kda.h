@@ -413,8 +413,15 @@ kda_status kda_commit_path(const void* k, const void* v, kda_dtype dtype, const 
 size_t kda_verify_workspace_size(int32_t N, int32_t T, int32_t V);
 
 /* Verification of drafted tokens against the target model's probabilities, by
- * rejection sampling from given random numbers: the tokens it returns are
- * distributed as the target's own samples.
+ * rejection sampling from given random numbers. Where the rows of target and
+ * draft sum to 1, the tokens it returns are distributed as the target's own
+ * samples. The rows are used as they are, never normalised: each node is tested
+ * as if its rows summed to 1. A row whose sum is off by d leaves the
+ * distribution off by about d (fp32 rows: their rounding; bf16 rows: up to
+ * 2^-8). Among the tokens that remain after a rejection the shift is larger:
+ * without draft their weight counts as 1 - r(x) where it is sum(r) - r(x), so
+ * a row of 0.9975, 0.00125, 0.00125 (bf16: 0.9961, 0.00125, 0.00125) accepts
+ * its second token 32 % of the times that the first was rejected, not 50 %.
  *   target    [N, T, V] dtype: row i is the target's distribution after node i
  *   draft     [N, T, V] dtype: row i is the distribution that the children of
  *             node i were drawn from (independently); or NULL when the drafts

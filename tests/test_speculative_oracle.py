@@ -3,6 +3,7 @@ the C oracle along every path, the verification's distribution in closed form,
 the cache's rounding against definitions that do not share its code."""
 import numpy as np
 import pytest
+import torch
 
 from gated_delta_rule_109_amd.workloads import make_inputs
 from oracle import reference, speculative
@@ -68,6 +69,44 @@ def test_verification_returns_the_targets_distribution():
                         cum = np.cumsum(r2 / r2.sum())
                         assert tok[0] == np.searchsorted(cum, u0, side="right")
     assert np.abs(got - p).max() < 2 / M
+
+
+@pytest.mark.parametrize("drafts", [(1, 2), (2, 0), (1, 1), (3, 2), (0, 0)])
+def test_drafts_that_were_not_sampled_leave_the_targets_distribution(drafts):
+    """A root with two children whose tokens were chosen without sampling (one
+    may repeat or have no probability): over all uniforms the first token has
+    the target's distribution. The tests' uniforms are integrated exactly over
+    their thresholds, the draw's over a grid of 1 / 64."""
+    p = np.array([0.5, 0.2, 0.3, 0.0])
+    x1, x2 = drafts
+    M = 64
+    got = np.zeros(4)
+    t1 = p[x1]                                               # accepted below these
+    left = 1.0 - p[x1]
+    r2 = p.copy(); r2[x1] = 0.0
+    t2 = min(1.0, r2[x2] / left)
+    for w1, u1 in ((t1, t1 / 2), (1 - t1, (1 + t1) / 2)):
+        for w2, u2 in ((t2, t2 / 2), (1 - t2, (1 + t2) / 2)):
+            if w1 * w2 == 0:
+                continue
+            for u0 in (np.arange(M) + 0.5) / M:
+                acc, path, tok = speculative.verify(np.stack([p] * 3)[None], None, np.array([[0, x1, x2]]),
+                                                    np.array([[u0, u1, u2]]), parents=np.array([[-1, 0, 0]]))
+                first = (x1, x2)[path[0, 1] - 1] if acc[0] == 2 else tok[0]
+                got[first] += w1 * w2 / M
+    assert np.abs(got - p).max() < 2 / M
+
+
+def test_rows_are_used_as_if_they_summed_to_one():
+    """The header's example: given that the first token is rejected, the second
+    is accepted below u = 0.5 of exact rows and below 0.32 of their bf16 values."""
+    p = torch.tensor([0.9975, 0.00125, 0.00125])
+    for row, below in ((p.double(), 0.5), (p.bfloat16().double(), 0.32)):
+        row = row.numpy()
+        for u2, accepted in ((below - 0.01, 2), (below + 0.01, 1)):
+            acc, _, _ = speculative.verify(np.stack([row] * 3)[None], None, np.array([[0, 0, 1]]),
+                                           np.array([[0.5, 0.999, u2]]), parents=np.array([[-1, 0, 0]]))
+            assert acc[0] == accepted
 
 
 def test_verification_by_hand():
