@@ -57,20 +57,41 @@ VerifyPlan verify_plan(int32_t N, int32_t V) {
 // Whether one workgroup per sequence does all of it (whole_kernel), or the
 // rows are spread over the GPU (walk, sums, choose). The first saves one or two
 // launches and a second read of the nodes; the second is faster where few
-// compute units would read long rows, or where the sequences are a little more
-// than the 256 compute units that each hold one such workgroup. Measured, T = 4
-// to 8, fp32, whole / spread in us:
-//   chains with draft rows        N 48        256        320
-//     V  8192                     13 / 15     12 / 15
-//     V 40000                     15 / 19     17 / 21    32 / 27
-//     V 131072                    28 / 19     51 / 60    71 / 58
-//   trees with draft rows         N 8         48         256        768
-//     V 65536                     25 / 25     32 / 36    48 / 63    83 / 91
-//     V 131072                    44 / 39     49 / 56    88 / 103   156 / 165
-// (in trees the walk itself takes one workgroup per sequence).
+// compute units would read long rows, or where the sequences are more than the
+// 256 compute units that each hold one such workgroup. In trees with draft rows
+// the walk itself takes one workgroup per sequence, so there is less to spread.
+// Measured, T = 6, whole / spread in us, * where the rule takes the slower one by
+// more than 2 us:
+//   fp32                 N 8      48       160      256      320      1024
+//   chains, draft rows
+//     V  16384           15/18    15/18    15/18    15/17    21/19    46/38
+//     V  49152           23/27    17/17    19/20    23/26    36/31    83/77
+//     V 131072           26/17    29/17    36/37    48/51    76/62    174/172
+//   chains or trees without draft rows
+//     V  16384           15/18    15/18    15/17    15/18    19/19    38/29
+//     V  49152           22/27    15/16    17/19    18/22    29/25    61/48
+//     V 131072           22/17    25/16    28/26    34/34    53/41    116/98
+//   trees, draft rows
+//     V  16384           18/21    21/24    23/29    24/30    28/34    61/59
+//     V  49152           26/25    35/37    35/44    42/52    46/56    107/117
+//     V 131072           57/52    48/54    67/81    78/93    94/104   229/243
+//   bf16
+//   chains, draft rows
+//     V  16384           14/17    14/17    15/17    14/17    22/17    44/24
+//     V  49152           16/17    17/17    18/17    19/20    31/22    67/45
+//     V 131072           21/17    22/17    25/25    29/32    48/37    107/91
+//   chains or trees without draft rows
+//     V  16384           14/16    14/16    14/16    14/17    22/18    42/24
+//     V  49152           16/16    16/17    17/18    18/19    28/21    58/38
+//     V 131072           21/17    21/17    24/22    26/27    41/31    88/66
+//   trees, draft rows
+//     V  16384           24/25    31/32    35/37    35/37    38/39    79/66*
+//     V  49152           28/25*   38/37    35/37    39/43    45/47    97/85*
+//     V 131072           60/52    48/45*   61/64    65/70    76/75    149/140*
+// The borders at long rows: chains with draft rows, V 65536, fp32: N 128 22/21,
+// 160 23/24; trees, V 65536: N 8 26/25, V 131072: N 32 52/52.
 bool whole(int32_t N, int32_t V, bool sampled_tree) {
   if (sampled_tree) return V <= 65536 || N >= 32;
-  if (V <= 16384) return N <= 1024;
   return N <= 256 && (V <= 49152 || N >= 160);
 }
 
