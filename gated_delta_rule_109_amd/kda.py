@@ -515,7 +515,8 @@ def _cache_call(where, fn, first, cache: StateCache, slots, states):
 def state_store(states, cache: StateCache, slots=None):
     """kda_state_store: states [N,H,D,D] into the cache's slots (device int32
     [N]; None: slot n), quantised to 8 bits. A state whose slot is outside the
-    cache is not written; of two states for one slot the later one is."""
+    cache is not written; of two states for one slot the later one is. With
+    slots the time grows with H N^2 (see kda.h)."""
     _cache_call("kda_state_store", lib().kda_state_store, "states", cache, slots, states)
 
 
