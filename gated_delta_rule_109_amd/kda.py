@@ -30,6 +30,7 @@ EXPORTED = ("kda_status_string", "kda_prefill_num_checkpoints", "kda_prefill_wor
 DECODE_MAX_TOKENS = 16
 TREE_MAX_NODES = 64
 CACHE_INT8, CACHE_E4M3 = 0, 1
+INT32_MAX = 2 ** 31 - 1
 CACHE_BLOCK = 32                                 # values that share a scale
 FE_L2NORM_QK, FE_GATE_LOGITS, FE_BETA_LOGITS = 1, 2, 4
 FE_ALL = FE_L2NORM_QK | FE_GATE_LOGITS | FE_BETA_LOGITS
@@ -348,10 +349,10 @@ def _check_step(*specs):
     raise ValueError("tensors on more than one device: one call takes one device")
 
 
-def _check_int32(*sizes):
+def _check_int32(a, b, c):
     """Sizes that the C ABI's int32 cannot carry (ctypes would drop the high bits)."""
-    if max(sizes) >= 2 ** 31:
-        raise ValueError(f"sizes {sizes} are outside int32")
+    if a > INT32_MAX or b > INT32_MAX or c > INT32_MAX:
+        raise ValueError(f"sizes {a}, {b}, {c}: one is outside int32")
 
 
 def _step_inputs(q, k, v, g, beta, lead, H, D, options):
@@ -359,7 +360,7 @@ def _step_inputs(q, k, v, g, beta, lead, H, D, options):
     dt = q.dtype
     if dt is not torch.bfloat16 and dt is not torch.float32:
         raise TypeError(f"q/k/v must be bfloat16 or float32, got {dt}")
-    _check_int32(*lead, H)
+    _check_int32(lead[0], lead[1], H)
     shape = (*lead, H, D)
     gshape = _gate_shape(lead, H, D, options)
     if gshape is None:
@@ -504,7 +505,7 @@ def _cache_call(where, fn, first, cache: StateCache, slots, states):
     dev = _check_step(("values", cache.values, (S, H, D, D), cache.values.dtype),
                       ("scales", cache.scales, (S, H, D * D // CACHE_BLOCK), torch.uint8),
                       ("slots", slots, (N,), torch.int32), ("states", states, (N, H, D, D), torch.float32))
-    _check_int32(S, N)
+    _check_int32(S, N, H)
     if first == "states":
         args = (states.data_ptr(), _addr(slots), cache.values.data_ptr(), cache.scales.data_ptr())
     else:

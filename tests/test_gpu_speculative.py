@@ -132,6 +132,17 @@ def test_tree(N, T, H, D, dtype, tree, gate, flags, g_min):
         assert torch.equal(o, kda.decode_tree(*s.args, s.state, None, scale=0.7, g_min=g_min, options=s.options))
 
 
+@pytest.mark.parametrize("N,T,H,D,dtype,tree,gate,flags,g_min", [x for x in TREES if x[4] is BF16])
+def test_tree_of_bf16_within_the_bound_of_fp32_products(N, T, H, D, dtype, tree, gate, flags, g_min):
+    """bf16 tensors against the bound of fp32 arithmetic, without the allowance
+    for operands of two bf16 terms, and the one rounding of the outputs."""
+    s = Step(N, T, H, D, dtype, 900 + T, gate, flags, g_min)
+    s.product = FRONT_END if flags else 0.0
+    par = random_parents(N, T, tree, T + 1)
+    o = kda.decode_tree(*s.args, s.state, dev(par, torch.int32), scale=1.3, g_min=g_min, options=s.options)
+    s.check_tree(o, par, scale=1.3)
+
+
 @pytest.mark.parametrize("T,D,dtype", [(16, 128, BF16), (40, 128, F32), (16, 128, F32), (64, 128, BF16), (19, 16, BF16)])
 def test_tree_of_each_sequences_own_size(T, D, dtype):
     nodes = np.array([0, 1, T, T + 9, -3, T // 2], np.int32)
