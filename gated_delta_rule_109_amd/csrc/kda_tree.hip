@@ -316,13 +316,16 @@ __global__ __launch_bounds__(256) void tree_path_kernel(
 //      16 x 16 tile is the K = 16 operand layout, so d feeds the products as it is.
 // All products use the fp32 matrix instructions, for bf16 tensors too: S, the
 // decayed rows, A, B and d have 24 bits whatever the tensors have. Operands of
-// two bf16 terms (16 bits, an eighth of the matrix time) took 142 us against
-// 167 to 184 for 256 x 32 heads of 16 nodes and 114 against 173 for 64 x 32
-// heads of 64, but rounded 0.5 % of the outputs the other way (now 0.02 %);
-// three terms (24 bits) took 160 and 180 us.
-// Measured in those two cases: 4.0 to 4.4 TB/s and 1.9 TB/s, bound by loads and
-// matrix products that overlap only in part (a workgroup does first the ones,
-// then the others).
+// two bf16 terms (16 bits, less than a fifth of the matrix time) took 133 to 142
+// us for 256 x 32 heads of 16 nodes and 97 to 114 for 64 x 32 heads of 64, but
+// rounded 0.5 % of the outputs the other way (now 0.02 %); three terms (24 bits)
+// 160 and 180, with the fp32 instructions 167 and 175 on the same card.
+// Measured: 256 x 32 heads, 16 nodes, bf16 154 to 187 us (739 MB, 4.0 to 4.8
+// TB/s), 128 x 32 heads, 32 nodes 158 to 179 us, 64 x 32 heads, 64 nodes 160 to
+// 175 us (336 MB); the products alone would take 70, 77 and 90 us at the rate of
+// a large fp32 matrix product (154 TFLOP/s). Bound by loads and products that
+// overlap only in part, since a workgroup does first the ones and then the
+// others. One sequence of 32 heads and 8 nodes 9 us.
 //
 // Values that are not finite: a product over nodes would carry one node's NaN
 // to nodes that do not descend from it (0 * NaN). So they are replaced by 0
@@ -399,7 +402,7 @@ struct TileLds {
 };
 
 // kDeep: A and B with the decays of each block of rows referred to its own R
-// (64-node chains, floor -5, 64 x 32 heads: 384 us; pair by pair 3037).
+// (64-node chains, floor -5, 64 x 32 heads: 379 to 389 us; pair by pair 3037).
 template <int kTB, int kWaves, typename TIn, bool kDeep>
 __global__ __launch_bounds__(64 * kWaves, kDeep ? 2 : 4) void tree_tile_kernel(
     const TIn* __restrict__ q, const TIn* __restrict__ k, const TIn* __restrict__ v,

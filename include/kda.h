@@ -379,7 +379,7 @@ kda_status kda_decode_tokens(const void* q, const void* k, const void* v, kda_dt
  * KDA_MAX_LARGE_TREE_HEADS where that holds) are KDA_ERR_INVALID_ARG; the other errors are those of kda_decode_tokens.
  * Cost: one pass over the state and the tokens while the decays of a tree span
  * at most 2^87 (T * -g_min <= 60); with lower floors A and B are formed with
- * a reference per 16 nodes (about three times the time at 64 nodes), and trees
+ * a reference per 16 nodes (2.3 times the time at 64 nodes), and trees
  * that mix deep and shallow branches within 16 consecutive nodes, or floors
  * below -83, run pair by pair. */
 kda_status kda_decode_tree(const void* q, const void* k, const void* v, kda_dtype dtype,
