@@ -497,4 +497,237 @@ kda_status kda_state_load(const void* values, const uint8_t* scales, const int32
   return from_hip(kda::launch_cache_load(a));
 }
 
+namespace {
+
+// ---- the layer around a recurrence ----
+
+bool packed_ok(const int32_t* cu, int32_t num_seqs, int32_t T) {
+  return T >= 0 && T <= KDA_MAX_PACKED_TOKENS && num_seqs >= 0 && (cu || num_seqs == 1) && aligned4({cu});
+}
+kda::Packed packed(const int32_t* cu, int32_t num_seqs, int32_t T) { return kda::Packed{cu, num_seqs, T}; }
+
+size_t elem(int dt) { return dt == KDA_BF16 ? 2 : 4; }
+// rows of `width` elements, `stride` apart
+Span rows(const void* p, int64_t n, int64_t stride, int64_t width, size_t e) {
+  return Span{p, n > 0 ? ((size_t)(n - 1) * stride + width) * e : 0};
+}
+Span flat(const void* p, size_t n, size_t e) { return Span{p, n * e}; }
+// A stride holds a row, and the whole array's bytes fit 63 bits.
+bool stride_ok(int64_t stride, int64_t width, int64_t n) {
+  return stride >= width && stride <= (INT64_MAX / 8 - width) / (n > 0 ? n : 1);
+}
+bool ssm_size_ok(int32_t N, int32_t P) {
+  return (N == 16 || N == 32 || N == 64 || N == 128 || N == 256) && P >= 16 && P <= 256 && P % 16 == 0;
+}
+
+kda_status ssm_args(const void* x, int64_t x_stride, const float* dt, const float* a, const void* b,
+                    int64_t b_stride, const void* c, int64_t c_stride, const float* skip, const float* dt_bias,
+                    int32_t softplus, int dtype, int32_t num_seqs, int32_t T, int32_t H, int32_t G, int32_t N,
+                    int32_t P, const float* initial_state, float* final_state, void* y, hipStream_t stream,
+                    kda::SsmArgs* out) {
+  if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_UNSUPPORTED;
+  if (!ssm_size_ok(N, P)) return KDA_ERR_UNSUPPORTED;
+  if (H <= 0 || G <= 0 || H % G || (softplus != 0 && softplus != 1)) return KDA_ERR_INVALID_ARG;
+  if ((int64_t)num_seqs * H > INT32_MAX || (int64_t)T * H > INT32_MAX) return KDA_ERR_INVALID_ARG;
+  const size_t e = elem(dtype);
+  const int64_t xw = (int64_t)H * P, bw = (int64_t)G * N, step = 16 / (int64_t)e;
+  if (!stride_ok(x_stride, xw, T) || !stride_ok(b_stride, bw, T) || !stride_ok(c_stride, bw, T) ||
+      x_stride % step || b_stride % step || c_stride % step)
+    return KDA_ERR_INVALID_ARG;
+  if (!a || (T > 0 && (!x || !dt || !b || !c || !y))) return KDA_ERR_INVALID_ARG;
+  if (!aligned16({x, dt, a, b, c, skip, dt_bias, initial_state, final_state, y})) return KDA_ERR_INVALID_ARG;
+  out->x = x; out->b = b; out->c = c;
+  out->x_stride = x_stride; out->b_stride = b_stride; out->c_stride = c_stride;
+  out->dt = dt; out->a = a; out->skip = skip; out->dt_bias = dt_bias;
+  out->softplus = softplus != 0;
+  out->H = H; out->G = G; out->N = N; out->P = P;
+  out->initial_state = initial_state; out->final_state = final_state;
+  out->y = y;
+  out->workspace = nullptr;
+  out->bf16 = dtype == KDA_BF16;
+  out->stream = stream;
+  return KDA_OK;
+}
+
+// Whether what a scan writes (y, the state, the workspace) overlaps nothing else.
+bool ssm_apart(const kda::SsmArgs& a, int64_t T, int64_t num_seqs, const int32_t* cu, const Span& workspace) {
+  const size_t e = a.bf16 ? 2 : 4;
+  const Span state = flat(a.final_state, (size_t)num_seqs * a.H * a.N * a.P, 4);
+  const Span initial = a.initial_state == a.final_state ? Span{nullptr, 0} : flat(a.initial_state, (size_t)num_seqs * a.H * a.N * a.P, 4);
+  return apart({rows(a.y, T, (int64_t)a.H * a.P, (int64_t)a.H * a.P, e), state, workspace},
+               {rows(a.x, T, a.x_stride, (int64_t)a.H * a.P, e), rows(a.b, T, a.b_stride, (int64_t)a.G * a.N, e),
+                rows(a.c, T, a.c_stride, (int64_t)a.G * a.N, e), flat(a.dt, (size_t)T * a.H, 4), flat(a.a, a.H, 4),
+                flat(a.skip, a.H, 4), flat(a.dt_bias, a.H, 4), initial, flat(cu, cu ? (size_t)num_seqs + 1 : 0, 4)});
+}
+
+kda_status conv_args(const void* x, int64_t x_stride, const float* weight, const float* bias, int dtype, int64_t rows_,
+                     int32_t C, int32_t width, int32_t activation, void* y, hipStream_t stream, kda::ConvArgs* out) {
+  if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_UNSUPPORTED;
+  if (C < 1 || C > KDA_CONV_MAX_CHANNELS || width < 2 || width > KDA_CONV_MAX_WIDTH) return KDA_ERR_INVALID_ARG;
+  if (activation != KDA_ACT_NONE && activation != KDA_ACT_SILU) return KDA_ERR_INVALID_ARG;
+  if (!stride_ok(x_stride, C, rows_)) return KDA_ERR_INVALID_ARG;
+  if (!weight || (rows_ > 0 && (!x || !y))) return KDA_ERR_INVALID_ARG;
+  if (!aligned16({x, weight, bias, y})) return KDA_ERR_INVALID_ARG;
+  out->x = x; out->x_stride = x_stride;
+  out->weight = weight; out->bias = bias;
+  out->C = C; out->width = width;
+  out->silu = activation == KDA_ACT_SILU;
+  out->y = y;
+  out->bf16 = dtype == KDA_BF16;
+  out->stream = stream;
+  return KDA_OK;
+}
+
+// Checks both norms share.
+kda_status norm_args_ok(int dtype, int32_t T, int32_t D, int32_t activation, float eps) {
+  if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_UNSUPPORTED;
+  if (T < 0 || D < 1 || D > KDA_NORM_MAX || activation < KDA_ACT_NONE || activation > KDA_ACT_SIGMOID)
+    return KDA_ERR_INVALID_ARG;
+  return eps >= 0.f && eps <= FLT_MAX ? KDA_OK : KDA_ERR_INVALID_ARG;
+}
+
+}  // namespace
+
+kda_status kda_conv_prefill(const void* x, int64_t x_stride, const float* weight, const float* bias, kda_dtype dtype,
+                            const int32_t* cu_seqlens, int32_t num_seqs, int32_t T, int32_t C, int32_t width,
+                            int32_t activation, const void* initial_state, void* final_state, void* y,
+                            hipStream_t stream) {
+  const int dt = enum_code(dtype);
+  kda::ConvArgs a;
+  const kda_status st = conv_args(x, x_stride, weight, bias, dt, T, C, width, activation, y, stream, &a);
+  if (st != KDA_OK) return st;
+  if (!packed_ok(cu_seqlens, num_seqs, T) || !aligned16({initial_state, final_state})) return KDA_ERR_INVALID_ARG;
+  a.seqs = packed(cu_seqlens, num_seqs, T);
+  a.N = 0;
+  a.initial_state = initial_state; a.final_state = final_state;
+  if (kda::conv_groups(a, false) > kda::kMaxGroups) return KDA_ERR_INVALID_ARG;
+  const size_t e = elem(dt), state = (size_t)num_seqs * (width - 1) * C;
+  const Span initial = initial_state == final_state ? Span{nullptr, 0} : flat(initial_state, state, e);
+  if (!apart({rows(y, T, C, C, e), flat(final_state, state, e)},
+             {rows(x, T, x_stride, C, e), flat(weight, (size_t)C * width, 4), flat(bias, C, 4), initial,
+              flat(cu_seqlens, cu_seqlens ? (size_t)num_seqs + 1 : 0, 4)}))
+    return KDA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return KDA_OK;
+  return from_hip(kda::launch_conv(a));
+}
+
+kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, const float* bias, kda_dtype dtype,
+                         void* state, int32_t N, int32_t C, int32_t width, int32_t activation, void* y,
+                         hipStream_t stream) {
+  const int dt = enum_code(dtype);
+  kda::ConvArgs a;
+  const kda_status st = conv_args(x, x_stride, weight, bias, dt, N, C, width, activation, y, stream, &a);
+  if (st != KDA_OK) return st;
+  if (N < 0 || (N > 0 && !state) || !aligned16({state})) return KDA_ERR_INVALID_ARG;
+  a.seqs = packed(nullptr, 1, 0);
+  a.N = N;
+  a.initial_state = state; a.final_state = state;
+  if (kda::conv_groups(a, true) > kda::kMaxGroups) return KDA_ERR_INVALID_ARG;
+  const size_t e = elem(dt);
+  if (!apart({rows(y, N, C, C, e), flat(state, (size_t)N * (width - 1) * C, e)},
+             {rows(x, N, x_stride, C, e), flat(weight, (size_t)C * width, 4), flat(bias, C, 4)}))
+    return KDA_ERR_INVALID_ARG;
+  if (N == 0) return KDA_OK;
+  return from_hip(kda::launch_conv_step(a));
+}
+
+size_t kda_ssm_workspace_size(int32_t num_seqs, int32_t T, int32_t H, int32_t N, int32_t P) {
+  if (num_seqs < 0 || T < 0 || T > KDA_MAX_PACKED_TOKENS || H <= 0 || (int64_t)T * H > INT32_MAX || !ssm_size_ok(N, P))
+    return 0;
+  return kda::ssm_workspace(num_seqs, T, H, N, P);
+}
+
+kda_status kda_ssm_prefill(const void* x, int64_t x_stride, const float* dt, const float* a, const void* b,
+                           int64_t b_stride, const void* c, int64_t c_stride, const float* skip, const float* dt_bias,
+                           int32_t dt_softplus, kda_dtype dtype, const int32_t* cu_seqlens, int32_t num_seqs, int32_t T,
+                           int32_t H, int32_t G, int32_t N, int32_t P, const float* initial_state, float* final_state,
+                           void* y, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  kda::SsmArgs s;
+  if (!packed_ok(cu_seqlens, num_seqs, T)) return KDA_ERR_INVALID_ARG;
+  const kda_status st = ssm_args(x, x_stride, dt, a, b, b_stride, c, c_stride, skip, dt_bias, dt_softplus,
+                                 enum_code(dtype), num_seqs, T, H, G, N, P, initial_state, final_state, y, stream, &s);
+  if (st != KDA_OK) return st;
+  s.seqs = packed(cu_seqlens, num_seqs, T);
+  if (kda::ssm_groups(s) > kda::kMaxGroups) return KDA_ERR_INVALID_ARG;
+  const size_t need = kda::ssm_workspace(num_seqs, T, H, N, P);
+  if (need && (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+  s.workspace = workspace;
+  if (!ssm_apart(s, T, num_seqs, cu_seqlens, Span{need ? workspace : nullptr, need})) return KDA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return KDA_OK;
+  return from_hip(kda::launch_ssm(s));
+}
+
+kda_status kda_ssm_step(const void* x, int64_t x_stride, const float* dt, const float* a, const void* b,
+                        int64_t b_stride, const void* c, int64_t c_stride, const float* skip, const float* dt_bias,
+                        int32_t dt_softplus, kda_dtype dtype, float* state, int32_t num_seqs, int32_t H, int32_t G,
+                        int32_t N, int32_t P, void* y, hipStream_t stream) {
+  kda::SsmArgs s;
+  if (num_seqs < 0 || (num_seqs > 0 && !state)) return KDA_ERR_INVALID_ARG;
+  const kda_status st = ssm_args(x, x_stride, dt, a, b, b_stride, c, c_stride, skip, dt_bias, dt_softplus,
+                                 enum_code(dtype), num_seqs, num_seqs, H, G, N, P, state, state, y, stream, &s);
+  if (st != KDA_OK) return st;
+  s.seqs = packed(nullptr, num_seqs, num_seqs);
+  if ((int64_t)num_seqs * H > kda::kMaxGroups) return KDA_ERR_INVALID_ARG;
+  if (!ssm_apart(s, num_seqs, num_seqs, nullptr, Span{nullptr, 0})) return KDA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return KDA_OK;
+  return from_hip(kda::launch_ssm_step(s));
+}
+
+kda_status kda_gated_norm(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride, const float* weight,
+                          int32_t weight_per_head, kda_dtype dtype, int32_t T, int32_t H, int32_t D,
+                          int32_t activation, int32_t gate_first, float eps, void* y, hipStream_t stream) {
+  const int dt = enum_code(dtype);
+  const kda_status st = norm_args_ok(dt, T, D, activation, eps);
+  if (st != KDA_OK) return st;
+  if (H < 1 || (int64_t)T * H > INT32_MAX || (weight_per_head != 0 && weight_per_head != 1) ||
+      (gate_first != 0 && gate_first != 1))
+    return KDA_ERR_INVALID_ARG;
+  const int64_t w = (int64_t)H * D;
+  if (!stride_ok(x_stride, w, T) || (gate && !stride_ok(gate_stride, w, T))) return KDA_ERR_INVALID_ARG;
+  if (T == 0) return KDA_OK;
+  if (!x || !weight || !y || !aligned16({x, gate, weight, y})) return KDA_ERR_INVALID_ARG;
+  const size_t e = elem(dt);
+  if (!apart({rows(y, T, w, w, e)}, {rows(x, T, x_stride, w, e), rows(gate, T, gate ? gate_stride : w, w, e),
+                                     flat(weight, (weight_per_head ? (size_t)H : 1) * D, 4)}))
+    return KDA_ERR_INVALID_ARG;
+  kda::GatedNormArgs a;
+  a.x = x; a.gate = gate;
+  a.x_stride = x_stride; a.gate_stride = gate ? gate_stride : 0;
+  a.weight = weight;
+  a.T = T; a.H = H; a.D = D; a.act = activation;
+  a.weight_per_head = weight_per_head != 0; a.gate_first = gate_first != 0;
+  a.eps = eps;
+  a.y = y;
+  a.bf16 = dt == KDA_BF16;
+  a.stream = stream;
+  return from_hip(kda::launch_gated_norm(a));
+}
+
+kda_status kda_residual_norm(const void* x, const void* residual, const void* gate, const float* weight,
+                             const float* post_weight, const float* scale, kda_dtype dtype, int32_t T, int32_t C,
+                             int32_t activation, float alpha, float eps, void* residual_out, void* y,
+                             hipStream_t stream) {
+  const int dt = enum_code(dtype);
+  const kda_status st = norm_args_ok(dt, T, C, activation, eps);
+  if (st != KDA_OK) return st;
+  if (!(alpha >= -FLT_MAX && alpha <= FLT_MAX)) return KDA_ERR_INVALID_ARG;
+  if (T == 0) return KDA_OK;
+  if (!x || !weight || !y || !aligned16({x, residual, gate, weight, post_weight, scale, residual_out, y}))
+    return KDA_ERR_INVALID_ARG;
+  const size_t e = elem(dt), n = (size_t)T * C;
+  const Span before = residual == residual_out ? Span{nullptr, 0} : flat(residual, n, e);
+  if (!apart({flat(y, n, e), flat(residual_out, n, e)},
+             {flat(x, n, e), before, flat(gate, n, e), flat(weight, C, 4), flat(post_weight, C, 4), flat(scale, C, 4)}))
+    return KDA_ERR_INVALID_ARG;
+  kda::ResidualNormArgs a;
+  a.x = x; a.residual = residual; a.gate = gate;
+  a.weight = weight; a.post_weight = post_weight; a.scale = scale;
+  a.T = T; a.C = C; a.act = activation;
+  a.alpha = alpha; a.eps = eps;
+  a.residual_out = residual_out; a.y = y;
+  a.bf16 = dt == KDA_BF16;
+  a.stream = stream;
+  return from_hip(kda::launch_residual_norm(a));
+}
+
 }  // extern "C"

@@ -75,6 +75,64 @@ struct CacheArgs {
   hipStream_t stream;
 };
 
+// Packed sequences, as the calls around the recurrence take them (kda.h): the
+// offsets are known on the device only.
+struct Packed {
+  const int32_t* cu;          // device [num_seqs + 1], or NULL (one sequence of T tokens)
+  int32_t num_seqs, T;
+};
+
+struct ConvArgs {
+  const void* x;
+  int64_t x_stride;
+  const float *weight, *bias;
+  Packed seqs;                // (unused by a step)
+  int32_t N, C, width;        // N: sequences of a step
+  bool silu;
+  const void* initial_state;  // a step: the state, updated in place
+  void* final_state;
+  void* y;
+  bool bf16;
+  hipStream_t stream;
+};
+
+struct SsmArgs {
+  const void *x, *b, *c;
+  int64_t x_stride, b_stride, c_stride;
+  const float *dt, *a, *skip, *dt_bias;
+  bool softplus;
+  Packed seqs;                // a step: T = num_seqs, one token each
+  int32_t H, G, N, P;
+  const float* initial_state; // a step: the state, updated in place
+  float* final_state;
+  void* y;
+  void* workspace;
+  bool bf16;
+  hipStream_t stream;
+};
+
+struct GatedNormArgs {
+  const void *x, *gate;
+  int64_t x_stride, gate_stride;
+  const float* weight;
+  int32_t T, H, D, act;
+  bool weight_per_head, gate_first;
+  float eps;
+  void* y;
+  bool bf16;
+  hipStream_t stream;
+};
+
+struct ResidualNormArgs {
+  const void *x, *residual, *gate;
+  const float *weight, *post_weight, *scale;
+  int32_t T, C, act;
+  float alpha, eps;
+  void *residual_out, *y;
+  bool bf16;
+  hipStream_t stream;
+};
+
 struct PrefillArgs {
   const void *q, *k, *v;
   const float *g, *beta;
@@ -142,6 +200,23 @@ hipError_t launch_commit(const TreeArgs& a);
 hipError_t launch_verify(const VerifyArgs& a);
 hipError_t launch_cache_store(const CacheArgs& a);
 hipError_t launch_cache_load(const CacheArgs& a);
+
+hipError_t launch_conv(const ConvArgs& a);
+hipError_t launch_conv_step(const ConvArgs& a);
+hipError_t launch_ssm(const SsmArgs& a);
+hipError_t launch_ssm_step(const SsmArgs& a);
+hipError_t launch_gated_norm(const GatedNormArgs& a);
+hipError_t launch_residual_norm(const ResidualNormArgs& a);
+
+// Most workgroups one launch of these kernels takes: 256 threads each, fewer
+// than 2^32 together.
+constexpr int64_t kMaxGroups = (1 << 24) - 1;
+// Workgroups the largest launch of a call needs.
+int64_t conv_groups(const ConvArgs& a, bool step);
+int64_t ssm_groups(const SsmArgs& a);
+
+// Workspace of a scan (bytes; sizes validated).
+size_t ssm_workspace(int32_t num_seqs, int32_t T, int32_t H, int32_t N, int32_t P);
 
 // Workspace of a verification (bytes; N, T, V validated).
 size_t verify_workspace(int32_t N, int32_t T, int32_t V);

@@ -26,7 +26,9 @@ LN_HALF = math.log(0.5)
 EXPORTED = ("kda_status_string", "kda_prefill_num_checkpoints", "kda_prefill_workspace_size",
             "kda_prefill_workspace_size_window", "kda_prefill_chunked", "kda_prefill_chunked_ex", "kda_prefill_chunked_noalloc",
             "kda_decode_step", "kda_decode_tokens", "kda_decode_tree", "kda_commit_path",
-            "kda_verify_workspace_size", "kda_verify_drafts", "kda_state_store", "kda_state_load")
+            "kda_verify_workspace_size", "kda_verify_drafts", "kda_state_store", "kda_state_load",
+            "kda_conv_prefill", "kda_conv_step", "kda_ssm_workspace_size", "kda_ssm_prefill", "kda_ssm_step",
+            "kda_gated_norm", "kda_residual_norm")
 DECODE_MAX_TOKENS = 16
 TREE_MAX_NODES = 64
 CACHE_INT8, CACHE_E4M3 = 0, 1
@@ -35,6 +37,10 @@ CACHE_BLOCK = 32                                 # values that share a scale
 FE_L2NORM_QK, FE_GATE_LOGITS, FE_BETA_LOGITS = 1, 2, 4
 FE_ALL = FE_L2NORM_QK | FE_GATE_LOGITS | FE_BETA_LOGITS
 GATE_CHANNEL, GATE_HEAD, GATE_NONE = 0, 1, 2     # KDA, Gated DeltaNet, DeltaNet
+ACT_NONE, ACT_SILU, ACT_SIGMOID = 0, 1, 2
+CONV_MAX_WIDTH = 4
+SSM_STATES = (16, 32, 64, 128, 256)              # rows of a scan's state
+NORM_MAX = 16384
 
 
 MAX_SEGMENTS = 16
@@ -112,6 +118,23 @@ def lib():
         L.kda_state_store.argtypes = [_vp, _vp, _vp, _vp, ctypes.c_int, _i32, _i32, _i32, _i32, _i32, _vp]
         L.kda_state_load.restype = ctypes.c_int
         L.kda_state_load.argtypes = [_vp, _vp, _vp, _vp, ctypes.c_int, _i32, _i32, _i32, _i32, _i32, _vp]
+        i64, f32, code = ctypes.c_int64, ctypes.c_float, ctypes.c_int
+        L.kda_conv_prefill.restype = ctypes.c_int
+        L.kda_conv_prefill.argtypes = [_vp, i64, _vp, _vp, code, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp]
+        L.kda_conv_step.restype = ctypes.c_int
+        L.kda_conv_step.argtypes = [_vp, i64, _vp, _vp, code, _vp, _i32, _i32, _i32, _i32, _vp, _vp]
+        L.kda_ssm_workspace_size.restype = ctypes.c_size_t
+        L.kda_ssm_workspace_size.argtypes = [_i32, _i32, _i32, _i32, _i32]
+        L.kda_ssm_prefill.restype = ctypes.c_int
+        L.kda_ssm_prefill.argtypes = [_vp, i64, _vp, _vp, _vp, i64, _vp, i64, _vp, _vp, _i32, code, _vp, _i32, _i32, _i32,
+                                      _i32, _i32, _i32, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+        L.kda_ssm_step.restype = ctypes.c_int
+        L.kda_ssm_step.argtypes = [_vp, i64, _vp, _vp, _vp, i64, _vp, i64, _vp, _vp, _i32, code, _vp, _i32, _i32, _i32,
+                                   _i32, _i32, _vp, _vp]
+        L.kda_gated_norm.restype = ctypes.c_int
+        L.kda_gated_norm.argtypes = [_vp, i64, _vp, i64, _vp, _i32, code, _i32, _i32, _i32, _i32, _i32, f32, _vp, _vp]
+        L.kda_residual_norm.restype = ctypes.c_int
+        L.kda_residual_norm.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, code, _i32, _i32, _i32, f32, f32, _vp, _vp, _vp]
         _lib = L
     return _lib
 
@@ -529,3 +552,224 @@ def state_load(cache: StateCache, slots=None, states=None):
         states = torch.empty(N, *cache.values.shape[1:], dtype=torch.float32, device=cache.values.device)
     _cache_call("kda_state_load", lib().kda_state_load, "cache", cache, slots, states)
     return states
+
+
+# ---- the layer around a recurrence: short convolution, state-space scan, norms ---------
+
+def _row_stride(t, name, lead_shape):
+    """Elements from one row of t [lead, ..] to the next; a row itself is
+    contiguous. (One row has no next one: its own length.)"""
+    if t.shape != lead_shape:
+        raise ValueError(f"{name}: expected shape {tuple(lead_shape)}, got {tuple(t.shape)}")
+    width = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != width:
+            raise ValueError(f"{name}: rows must be contiguous")
+        width *= size
+    if t.shape[0] <= 1:
+        return width
+    if t.stride(0) < width:
+        raise ValueError(f"{name}: rows overlap")
+    return t.stride(0)
+
+
+def _storage_code(t, name):
+    if t.dtype is torch.bfloat16:
+        return KDA_BF16
+    if t.dtype is torch.float32:
+        return KDA_F32
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _check_rest(x, *specs):
+    """The given tensors (name, tensor or None, shape, dtype, whether its rows
+    may be strided) are right and on x's device, whose index is returned."""
+    dev = x.get_device()
+    for name, t, shape, dtype, strided in specs:
+        if t is None:
+            continue
+        if t.shape != shape or t.dtype is not dtype:
+            _expect(t, name, shape, dtype)
+        if not strided and not t.is_contiguous():
+            raise ValueError(f"{name}: tensors must be contiguous device tensors")
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: tensors must be contiguous device tensors, all on one device")
+    if dev < 0:
+        raise ValueError("tensors must be contiguous device tensors")
+    return dev
+
+
+def _num_seqs(cu_seqlens):
+    if cu_seqlens is None:
+        return 1
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens: expected a device int32 tensor [num_seqs + 1]")
+    return cu_seqlens.shape[0] - 1
+
+
+def conv_prefill(x, weight, bias=None, cu_seqlens=None, initial_state=None, activation=ACT_SILU,
+                 out_final_state=True, y=None, final_state=None):
+    """kda_conv_prefill: causal convolution of x [T,C] (rows may be strided: a
+    part of a wider row) with weight [C,K] (float32, K 2 .. 4) and its
+    activation (ACT_NONE, ACT_SILU). cu_seqlens: device int32 [num_seqs+1]
+    offsets of the packed sequences (None: one sequence). initial_state
+    [num_seqs,K-1,C] holds the inputs before each sequence (None: zeros) and
+    may be final_state. Rows of no sequence are left as they were (of a y made
+    here: not initialised). Returns (y [T,C], final_state or None)."""
+    T, C = x.shape
+    K = weight.shape[-1]
+    N = _num_seqs(cu_seqlens)
+    _check_int32(T, C, N)
+    code = _storage_code(x, "x")
+    stride = _row_stride(x, "x", (T, C))
+    sshape = (N, K - 1, C)
+    dev = _check_rest(x, ("weight", weight, (C, K), torch.float32, False), ("bias", bias, (C,), torch.float32, False),
+                      ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, False),
+                      ("initial_state", initial_state, sshape, x.dtype, False),
+                      ("final_state", final_state, sshape, x.dtype, False), ("y", y, (T, C), x.dtype, False))
+    if y is None:
+        y = x.new_empty(T, C)
+    if final_state is None and out_final_state:
+        final_state = x.new_empty(sshape)
+    _call(dev, "kda_conv_prefill", lib().kda_conv_prefill, x.data_ptr(), stride, weight.data_ptr(), _addr(bias), code,
+          _addr(cu_seqlens), N, T, C, K, int(activation), _addr(initial_state), _addr(final_state), y.data_ptr())
+    return y, final_state
+
+
+def conv_step(x, weight, state, bias=None, activation=ACT_SILU, y=None):
+    """kda_conv_step: one token of each of N sequences, x [N,C] (rows may be
+    strided), state [N,K-1,C] updated in place. Returns y [N,C]."""
+    N, C = x.shape
+    K = weight.shape[-1]
+    _check_int32(N, C, K)
+    code = _storage_code(x, "x")
+    stride = _row_stride(x, "x", (N, C))
+    if state is None:
+        raise ValueError("state is required")
+    dev = _check_rest(x, ("weight", weight, (C, K), torch.float32, False), ("bias", bias, (C,), torch.float32, False),
+                      ("state", state, (N, K - 1, C), x.dtype, False), ("y", y, (N, C), x.dtype, False))
+    if y is None:
+        y = x.new_empty(N, C)
+    _call(dev, "kda_conv_step", lib().kda_conv_step, x.data_ptr(), stride, weight.data_ptr(), _addr(bias), code,
+          state.data_ptr(), N, C, K, int(activation), y.data_ptr())
+    return y
+
+
+def ssm_workspace(num_seqs: int, T: int, H: int, N: int, P: int, device) -> torch.Tensor:
+    """A workspace for ssm_prefill calls of these sizes and smaller ones (state
+    size N), one after another."""
+    _check_int32(num_seqs, T, H)
+    size = int(lib().kda_ssm_workspace_size(int(num_seqs), int(T), int(H), int(N), int(P)))
+    return torch.empty(max(size, 256), dtype=torch.uint8, device=device)
+
+
+def _ssm_inputs(x, dt, a, b, c, skip, dt_bias, T):
+    """Sizes, strides and specifications of what a scan reads."""
+    H, P = x.shape[1:]
+    if b.dim() != 3:
+        raise ValueError(f"b: expected shape [T, G, N], got {tuple(b.shape)}")
+    G, N = b.shape[1:]
+    code = _storage_code(x, "x")
+    if b.dtype is not x.dtype or c.dtype is not x.dtype:
+        raise TypeError(f"b, c: expected {x.dtype}, got {b.dtype}, {c.dtype}")
+    strides = (_row_stride(x, "x", (T, H, P)), _row_stride(b, "b", (T, G, N)), _row_stride(c, "c", (T, G, N)))
+    specs = (("b", b, (T, G, N), x.dtype, True), ("c", c, (T, G, N), x.dtype, True),
+             ("dt", dt, (T, H), torch.float32, False), ("a", a, (H,), torch.float32, False),
+             ("skip", skip, (H,), torch.float32, False), ("dt_bias", dt_bias, (H,), torch.float32, False))
+    return (H, P, G, N), code, strides, specs
+
+
+def ssm_prefill(x, dt, a, b, c, skip=None, dt_bias=None, dt_softplus=False, cu_seqlens=None, initial_state=None,
+                out_final_state=True, y=None, final_state=None, workspace: Optional[torch.Tensor] = None):
+    """kda_ssm_prefill: selective state-space scan of x [T,H,P] with b, c
+    [T,G,N] (bfloat16 or float32; rows may be strided, parts of one wider row),
+    step sizes dt [T,H] (float32; logits with dt_softplus, dt_bias [H] added
+    first) and decay rates a [H] (negative); skip [H] adds skip * x.
+    cu_seqlens as in conv_prefill; initial_state [num_seqs,H,N,P] float32 may
+    be final_state. workspace (ssm_workspace) is allocated when None. Rows of
+    no sequence are left as they were (of a y made here: not initialised).
+    Returns (y [T,H,P], final_state or None)."""
+    T = x.shape[0]
+    (H, P, G, N), code, (xs, bs, cs), specs = _ssm_inputs(x, dt, a, b, c, skip, dt_bias, T)
+    S = _num_seqs(cu_seqlens)
+    _check_int32(T, H, S)
+    sshape = (S, H, N, P)
+    dev = _check_rest(x, *specs, ("cu_seqlens", cu_seqlens, (S + 1,), torch.int32, False),
+                      ("initial_state", initial_state, sshape, torch.float32, False),
+                      ("final_state", final_state, sshape, torch.float32, False),
+                      ("y", y, (T, H, P), x.dtype, False),
+                      ("workspace", workspace, None if workspace is None else (workspace.numel(),), torch.uint8, False))
+    if y is None:
+        y = x.new_empty(T, H, P)
+    if final_state is None and out_final_state:
+        final_state = dt.new_empty(sshape)
+    if workspace is None:
+        workspace = ssm_workspace(S, T, H, N, P, x.device)
+    _call(dev, "kda_ssm_prefill", lib().kda_ssm_prefill, x.data_ptr(), xs, dt.data_ptr(), a.data_ptr(), b.data_ptr(), bs,
+          c.data_ptr(), cs, _addr(skip), _addr(dt_bias), int(dt_softplus), code, _addr(cu_seqlens), S, T, H, G, N, P,
+          _addr(initial_state), _addr(final_state), y.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return y, final_state
+
+
+def ssm_step(x, dt, a, b, c, state, skip=None, dt_bias=None, dt_softplus=False, y=None):
+    """kda_ssm_step: one token of each of S sequences: x [S,H,P], dt [S,H], b, c
+    [S,G,N]; state [S,H,N,P] float32 updated in place. Otherwise as
+    ssm_prefill. Returns y [S,H,P]."""
+    S = x.shape[0]
+    (H, P, G, N), code, (xs, bs, cs), specs = _ssm_inputs(x, dt, a, b, c, skip, dt_bias, S)
+    _check_int32(S, H, G)
+    if state is None:
+        raise ValueError("state is required")
+    dev = _check_rest(x, *specs, ("state", state, (S, H, N, P), torch.float32, False),
+                      ("y", y, (S, H, P), x.dtype, False))
+    if y is None:
+        y = x.new_empty(S, H, P)
+    _call(dev, "kda_ssm_step", lib().kda_ssm_step, x.data_ptr(), xs, dt.data_ptr(), a.data_ptr(), b.data_ptr(), bs,
+          c.data_ptr(), cs, _addr(skip), _addr(dt_bias), int(dt_softplus), code, state.data_ptr(), S, H, G, N, P,
+          y.data_ptr())
+    return y
+
+
+def gated_norm(x, gate, weight, activation=ACT_SIGMOID, gate_first=False, eps=1e-6, y=None):
+    """kda_gated_norm: norm of each head's row of x [T,H,D], times weight
+    (float32 [D], or [H,D]) and the activation of gate [T,H,D] (None: no gate),
+    which with gate_first multiplies x before the norm. Rows of x and gate
+    [T,..] may be strided. Returns y [T,H,D]."""
+    T, H, D = x.shape
+    _check_int32(T, H, D)
+    code = _storage_code(x, "x")
+    xs = _row_stride(x, "x", (T, H, D))
+    gs = 0 if gate is None else _row_stride(gate, "gate", (T, H, D))
+    per_head = weight.dim() == 2
+    dev = _check_rest(x, ("gate", gate, (T, H, D), x.dtype, True),
+                      ("weight", weight, (H, D) if per_head else (D,), torch.float32, False),
+                      ("y", y, (T, H, D), x.dtype, False))
+    if y is None:
+        y = x.new_empty(T, H, D)
+    _call(dev, "kda_gated_norm", lib().kda_gated_norm, x.data_ptr(), xs, _addr(gate), gs, weight.data_ptr(),
+          int(per_head), code, T, H, D, int(activation), int(gate_first), float(eps), y.data_ptr())
+    return y
+
+
+def residual_norm(x, residual, weight, post_weight=None, gate=None, activation=ACT_SIGMOID, scale=None, alpha=1.0,
+                  eps=1e-6, residual_out=None, y=None):
+    """kda_residual_norm: residual' = residual + alpha * scale * act(gate) * v
+    and y = norm(residual') * weight, over rows [T,C]; v is x, or norm(x) *
+    post_weight. residual, gate [T,C] and scale [C] may be None; residual_out
+    may be residual. Returns (residual', y)."""
+    T, C = x.shape
+    _check_int32(T, C, C)
+    code = _storage_code(x, "x")
+    dt, f32 = x.dtype, torch.float32
+    dev = _check_rest(x, ("x", x, (T, C), dt, False), ("residual", residual, (T, C), dt, False),
+                      ("weight", weight, (C,), f32, False), ("post_weight", post_weight, (C,), f32, False),
+                      ("gate", gate, (T, C), dt, False), ("scale", scale, (C,), f32, False),
+                      ("residual_out", residual_out, (T, C), dt, False), ("y", y, (T, C), dt, False))
+    if residual_out is None:
+        residual_out = torch.empty_like(x)
+    if y is None:
+        y = torch.empty_like(x)
+    _call(dev, "kda_residual_norm", lib().kda_residual_norm, x.data_ptr(), _addr(residual), _addr(gate),
+          weight.data_ptr(), _addr(post_weight), _addr(scale), code, T, C, int(activation), float(alpha), float(eps),
+          residual_out.data_ptr(), y.data_ptr())
+    return residual_out, y

@@ -514,6 +514,143 @@ kda_status kda_state_load(const void* values, const uint8_t* scales, const int32
                           float* states, kda_cache_format format, int32_t N, int32_t num_slots,
                           int32_t H, int32_t Dk, int32_t Dv, hipStream_t stream);
 
+/* ---- the layer around a recurrence: short convolution, state-space scan, norms -------
+ *
+ * What a layer with a recurrent state does right before and after it, and the
+ * member of the family without the delta rule. The calls of this section share
+ * these conventions:
+ *   - Sequences are packed: T tokens, sequence n holds tokens cu_seqlens[n] ..
+ *     cu_seqlens[n + 1] - 1. cu_seqlens is [num_seqs + 1] int32 DEVICE memory
+ *     (4-byte aligned), read by the kernels only, so a captured graph replays
+ *     with new offsets; NULL means one sequence of all T tokens (num_seqs 1).
+ *     A sequence may be empty: its final state is its initial state. Tokens
+ *     before cu_seqlens[0] and from cu_seqlens[num_seqs] on belong to no
+ *     sequence: nothing of them is read, and their outputs are left as they
+ *     were. Offsets are clamped to [0, T]; decreasing ones give wrong outputs
+ *     but no access outside the arrays.
+ *   - *_stride: elements from one token's row to the next, at least the row's
+ *     own (so that parts of a wider row, a projection's output, are used in
+ *     place). Arrays without a stride are contiguous.
+ *   - Outputs overlap neither each other nor an input (KDA_ERR_INVALID_ARG),
+ *     except where noted.
+ *   - Sums and states are fp32 or wider; outputs are rounded once. */
+#define KDA_MAX_PACKED_TOKENS (1 << 30)   /* largest T of these calls */
+typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1, KDA_ACT_SIGMOID = 2 } kda_act;
+
+/* Causal convolution over the last `width` tokens, channel by channel, with
+ * the activation behind it: what q, k and v (or x, B and C) pass before the
+ * recurrence.
+ *     y[t][c] = act(bias[c] + sum_{j < width} weight[c][j] x[t - width + 1 + j][c])
+ * Rows before a sequence's first come from its state: the last width - 1
+ * inputs before it, oldest first.
+ *   x       [T, C] dtype, x_stride;  y [T, C] dtype
+ *   weight  [C, width] fp32;  bias [C] fp32 or NULL (0)
+ *   width   2 .. KDA_CONV_MAX_WIDTH;  activation KDA_ACT_NONE or KDA_ACT_SILU
+ *   initial_state  [num_seqs, width - 1, C] dtype, or NULL (zeros)
+ *   final_state    the same, or NULL to skip; may be initial_state itself. The
+ *                  state holds input rows, so it has their type and is exact.
+ * Errors: KDA_ERR_INVALID_ARG (null required pointer, misaligned or overlapping
+ * arrays, T or num_seqs < 0, num_seqs != 1 without cu_seqlens, C outside
+ * [1, KDA_CONV_MAX_CHANNELS], x_stride < C, width, activation; more than 2^24
+ * workgroups), KDA_ERR_UNSUPPORTED (dtype), KDA_ERR_HIP. */
+#define KDA_CONV_MAX_WIDTH 4
+#define KDA_CONV_MAX_CHANNELS (1 << 20)
+kda_status kda_conv_prefill(const void* x, int64_t x_stride, const float* weight,
+                            const float* bias, kda_dtype dtype, const int32_t* cu_seqlens,
+                            int32_t num_seqs, int32_t T, int32_t C, int32_t width,
+                            int32_t activation, const void* initial_state, void* final_state,
+                            void* y, hipStream_t stream);
+
+/* One token of each of N sequences: x [N, C] (x_stride), y [N, C], state
+ * [N, width - 1, C] dtype, read and updated in place. Otherwise as
+ * kda_conv_prefill. */
+kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, const float* bias,
+                         kda_dtype dtype, void* state, int32_t N, int32_t C, int32_t width,
+                         int32_t activation, void* y, hipStream_t stream);
+
+/* Selective state-space scan (one decay per head and token, no delta rule).
+ * Per sequence and head h of group j = h / (H / G), token by token:
+ *     d_t = dt[t][h] + dt_bias[h], with dt_softplus ln(1 + e^d) of it
+ *     S_t = exp(d_t a[h]) S_{t-1} + d_t b[t][j] x[t][h]^T          (N x P, fp32)
+ *     y_t = S_t^T c[t][j] + skip[h] x[t][h]
+ *   x   [T, H, P] dtype, x_stride;  y [T, H, P] dtype
+ *   b, c  [T, G, N] dtype, b_stride, c_stride; H % G == 0
+ *   dt  [T, H] fp32;  a [H] fp32 (negative for a decay; any value is taken)
+ *   skip, dt_bias  [H] fp32, or NULL (0)
+ *   initial_state  [num_seqs, H, N, P] fp32 (row = state channel, P contiguous,
+ *                  as the states of the delta rule), or NULL (zeros)
+ *   final_state    the same, or NULL to skip; may be initial_state itself
+ *   N  16, 32, 64, 128 or 256;  P a multiple of 16 up to 256; the strides of x,
+ *      b and c are multiples of 16 bytes
+ * bf16 tensors run in chunks of KDA_SSM_CHUNK tokens on the matrix cores: b, c
+ * and x are exact there, every fp32 factor is carried in two bf16 terms for
+ * outputs (2^-16 of each product) and three for states (2^-24); the decays
+ * between two tokens come from sums in fp64. fp32 tensors run token by token
+ * in fp32. Values that are not finite in x, b or dt make outputs non-finite from
+ * their token on (of a value in x: in its column), as the recurrence does, and
+ * no outputs before; a c that is not finite, those of its token.
+ *   workspace  256-byte aligned device scratch of kda_ssm_workspace_size(num_seqs,
+ *              T, H, N, P) bytes (0: may be NULL): the states of segments of long sequences, which
+ *              run side by side. It needs no initialisation; sizes do not shrink
+ *              as num_seqs, T, H or P grow, so that of the largest call serves
+ *              smaller ones; calls that may overlap need one each.
+ * Errors: KDA_ERR_INVALID_ARG (as kda_conv_prefill; G < 1 or H % G), KDA_ERR_UNSUPPORTED
+ * (dtype, N or P), KDA_ERR_WORKSPACE, KDA_ERR_HIP. */
+#define KDA_SSM_CHUNK 64
+size_t kda_ssm_workspace_size(int32_t num_seqs, int32_t T, int32_t H, int32_t N, int32_t P);
+kda_status kda_ssm_prefill(const void* x, int64_t x_stride, const float* dt, const float* a,
+                           const void* b, int64_t b_stride, const void* c, int64_t c_stride,
+                           const float* skip, const float* dt_bias, int32_t dt_softplus,
+                           kda_dtype dtype, const int32_t* cu_seqlens, int32_t num_seqs, int32_t T,
+                           int32_t H, int32_t G, int32_t N, int32_t P, const float* initial_state,
+                           float* final_state, void* y, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
+/* One token of each of num_seqs sequences: x [num_seqs, H, P], dt, b, c and y
+ * likewise, state [num_seqs, H, N, P] fp32, read and updated in place (fp32
+ * arithmetic for both types). Otherwise as kda_ssm_prefill. */
+kda_status kda_ssm_step(const void* x, int64_t x_stride, const float* dt, const float* a,
+                        const void* b, int64_t b_stride, const void* c, int64_t c_stride,
+                        const float* skip, const float* dt_bias, int32_t dt_softplus,
+                        kda_dtype dtype, float* state, int32_t num_seqs, int32_t H, int32_t G,
+                        int32_t N, int32_t P, void* y, hipStream_t stream);
+
+/* Longest rows of the two norms. */
+#define KDA_NORM_MAX 16384
+
+/* Norm of each head's outputs with the output gate, between a recurrence and
+ * the projection behind it. With norm(v) = v / sqrt(mean(v^2) + eps) over the D
+ * values of a (token, head) row:
+ *     y = norm(x) * weight * act(gate)       (gate_first = 0)
+ *     y = norm(x * act(gate)) * weight       (gate_first = 1)
+ *   x, gate  [T, H, D] dtype, x_stride, gate_stride; gate may be NULL (1)
+ *   weight   fp32 [D] (weight_per_head = 0) or [H, D] (1)
+ *   y        [T, H, D] dtype
+ * Squares are summed in fp32: rows with |v| near 2^64 overflow to norm 0.
+ * Errors: KDA_ERR_INVALID_ARG (null required pointer, misaligned or overlapping
+ * arrays, T < 0, H < 1, D outside [1, KDA_NORM_MAX], T * H above INT32_MAX,
+ * stride < H * D, activation, eps negative or not finite, flags other than 0
+ * and 1), KDA_ERR_UNSUPPORTED (dtype), KDA_ERR_HIP. */
+kda_status kda_gated_norm(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride,
+                          const float* weight, int32_t weight_per_head, kda_dtype dtype, int32_t T,
+                          int32_t H, int32_t D, int32_t activation, int32_t gate_first, float eps,
+                          void* y, hipStream_t stream);
+
+/* Between two blocks: the norm after the first with its gate and residual
+ * scale, the residual sum, and the norm before the second, over rows of C:
+ *     v  = x, with post_weight norm(x) * post_weight
+ *     r' = residual + alpha * scale * act(gate) * v      (scale, gate: 1 if NULL)
+ *     y  = norm(r') * weight                             (r' before it is rounded)
+ *   x, residual, gate  [T, C] dtype;  residual NULL: 0
+ *   weight, post_weight, scale  [C] fp32; post_weight and scale may be NULL
+ *   residual_out  [T, C] dtype, or NULL to skip; may be residual itself
+ *   y             [T, C] dtype
+ * Errors as kda_gated_norm (C for D; alpha not finite). */
+kda_status kda_residual_norm(const void* x, const void* residual, const void* gate,
+                             const float* weight, const float* post_weight, const float* scale,
+                             kda_dtype dtype, int32_t T, int32_t C, int32_t activation, float alpha,
+                             float eps, void* residual_out, void* y, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,6 +11,7 @@ Modules:
   oracle.chunk_spec -- fp64 chunked (matmul) form, used to pin chunk algebra
   oracle.frontend   -- fp64 front end: q/k L2 normalisation, gate and beta
                        from raw logits
+  oracle.layer      -- fp64 short convolution, state-space scan and norms
   oracle.variants   -- GDN (one decay per head) and DeltaNet (no decay) gates
                        as per-channel KDA gates
 """
