@@ -532,6 +532,7 @@ kda_status ssm_args(const void* x, int64_t x_stride, const float* dt, const floa
   const size_t e = elem(dtype);
   const int64_t xw = (int64_t)H * P, bw = (int64_t)G * N, step = 16 / (int64_t)e;
   if (!stride_ok(x_stride, xw, T) || !stride_ok(b_stride, bw, T) || !stride_ok(c_stride, bw, T) ||
+      x_stride > KDA_SSM_MAX_STRIDE || b_stride > KDA_SSM_MAX_STRIDE || c_stride > KDA_SSM_MAX_STRIDE ||
       x_stride % step || b_stride % step || c_stride % step)
     return KDA_ERR_INVALID_ARG;
   if (!a || (T > 0 && (!x || !dt || !b || !c || !y))) return KDA_ERR_INVALID_ARG;
@@ -600,7 +601,7 @@ kda_status kda_conv_prefill(const void* x, int64_t x_stride, const float* weight
   a.seqs = packed(cu_seqlens, num_seqs, T);
   a.N = 0;
   a.initial_state = initial_state; a.final_state = final_state;
-  if (kda::conv_groups(a, false) > kda::kMaxGroups) return KDA_ERR_INVALID_ARG;
+  if (kda::conv_threads(a, false) > kda::kMaxThreads) return KDA_ERR_INVALID_ARG;
   const size_t e = elem(dt), state = (size_t)num_seqs * (width - 1) * C;
   const Span initial = initial_state == final_state ? Span{nullptr, 0} : flat(initial_state, state, e);
   if (!apart({rows(y, T, C, C, e), flat(final_state, state, e)},
@@ -622,7 +623,7 @@ kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, c
   a.seqs = packed(nullptr, 1, 0);
   a.N = N;
   a.initial_state = state; a.final_state = state;
-  if (kda::conv_groups(a, true) > kda::kMaxGroups) return KDA_ERR_INVALID_ARG;
+  if (kda::conv_threads(a, true) > kda::kMaxThreads) return KDA_ERR_INVALID_ARG;
   const size_t e = elem(dt);
   if (!apart({rows(y, N, C, C, e), flat(state, (size_t)N * (width - 1) * C, e)},
              {rows(x, N, x_stride, C, e), flat(weight, (size_t)C * width, 4), flat(bias, C, 4)}))
@@ -648,7 +649,7 @@ kda_status kda_ssm_prefill(const void* x, int64_t x_stride, const float* dt, con
                                  enum_code(dtype), num_seqs, T, H, G, N, P, initial_state, final_state, y, stream, &s);
   if (st != KDA_OK) return st;
   s.seqs = packed(cu_seqlens, num_seqs, T);
-  if (kda::ssm_groups(s) > kda::kMaxGroups) return KDA_ERR_INVALID_ARG;
+  if (kda::ssm_threads(s) > kda::kMaxThreads) return KDA_ERR_INVALID_ARG;
   const size_t need = kda::ssm_workspace(num_seqs, T, H, N, P);
   if (need && (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
   s.workspace = workspace;
@@ -667,7 +668,7 @@ kda_status kda_ssm_step(const void* x, int64_t x_stride, const float* dt, const 
                                  enum_code(dtype), num_seqs, num_seqs, H, G, N, P, state, state, y, stream, &s);
   if (st != KDA_OK) return st;
   s.seqs = packed(nullptr, num_seqs, num_seqs);
-  if ((int64_t)num_seqs * H > kda::kMaxGroups) return KDA_ERR_INVALID_ARG;
+  if ((int64_t)num_seqs * H * 256 > kda::kMaxThreads) return KDA_ERR_INVALID_ARG;
   if (!ssm_apart(s, num_seqs, num_seqs, nullptr, Span{nullptr, 0})) return KDA_ERR_INVALID_ARG;
   if (num_seqs == 0) return KDA_OK;
   return from_hip(kda::launch_ssm_step(s));
@@ -700,6 +701,7 @@ kda_status kda_gated_norm(const void* x, int64_t x_stride, const void* gate, int
   a.y = y;
   a.bf16 = dt == KDA_BF16;
   a.stream = stream;
+  if (kda::gated_threads(a) > kda::kMaxThreads) return KDA_ERR_INVALID_ARG;
   return from_hip(kda::launch_gated_norm(a));
 }
 
@@ -727,6 +729,7 @@ kda_status kda_residual_norm(const void* x, const void* residual, const void* ga
   a.residual_out = residual_out; a.y = y;
   a.bf16 = dt == KDA_BF16;
   a.stream = stream;
+  if (kda::residual_threads(a) > kda::kMaxThreads) return KDA_ERR_INVALID_ARG;
   return from_hip(kda::launch_residual_norm(a));
 }
 

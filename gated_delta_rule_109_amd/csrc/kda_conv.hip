@@ -161,11 +161,11 @@ hipError_t by_type(const ConvArgs& a, bool step) {
 
 }  // namespace
 
-int64_t conv_groups(const ConvArgs& a, bool step) {
+int64_t conv_threads(const ConvArgs& a, bool step) {
   const int v = a.bf16 ? (vectors<bf16_bits, 8>(a) ? 8 : 1) : (vectors<float, 4>(a) ? 4 : 1);
-  if (step) return ((int64_t)a.N * (a.C / v) + kThreads - 1) / kThreads;
+  if (step) return (int64_t)a.N * (a.C / v) + kThreads;
   const int ct = channel_threads(a.C / v);
-  return part_slots(a.seqs, kThreads / ct * kTokens) * ((a.C / v + ct - 1) / ct);
+  return part_slots(a.seqs, kThreads / ct * kTokens) * ((a.C / v + ct - 1) / ct) * kThreads;
 }
 
 hipError_t launch_conv(const ConvArgs& a) { return by_type(a, false); }

@@ -208,12 +208,12 @@ hipError_t launch_ssm_step(const SsmArgs& a);
 hipError_t launch_gated_norm(const GatedNormArgs& a);
 hipError_t launch_residual_norm(const ResidualNormArgs& a);
 
-// Most workgroups one launch of these kernels takes: 256 threads each, fewer
-// than 2^32 together.
-constexpr int64_t kMaxGroups = (1 << 24) - 1;
-// Workgroups the largest launch of a call needs.
-int64_t conv_groups(const ConvArgs& a, bool step);
-int64_t ssm_groups(const SsmArgs& a);
+// Threads of a call's largest launch: fewer than 2^32.
+constexpr int64_t kMaxThreads = (1ll << 32) - 1;
+int64_t conv_threads(const ConvArgs& a, bool step);
+int64_t ssm_threads(const SsmArgs& a);
+int64_t gated_threads(const GatedNormArgs& a);
+int64_t residual_threads(const ResidualNormArgs& a);
 
 // Workspace of a scan (bytes; sizes validated).
 size_t ssm_workspace(int32_t num_seqs, int32_t T, int32_t H, int32_t N, int32_t P);

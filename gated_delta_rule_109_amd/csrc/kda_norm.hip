@@ -190,19 +190,45 @@ void residual_t(const ResidualNormArgs& a) {
   });
 }
 
+int64_t row_threads(int64_t rows, int n, int v) {
+  int64_t t = 0;
+  auto f = [&](auto L, auto) { t = (rows + 255) * decltype(L)::value; };
+  if (v == 8) by_length<8>(n, f);
+  else if (v == 4) by_length<4>(n, f);
+  else by_length<1>(n, f);
+  return t;
+}
+int width_of(const GatedNormArgs& a) {
+  const int v = a.bf16 ? 8 : 4;
+  return a.D % v == 0 && a.x_stride % v == 0 && (!a.gate || a.gate_stride % v == 0) ? v : 1;
+}
+int width_of(const ResidualNormArgs& a) {
+  const int v = a.bf16 ? 8 : 4;
+  return a.C % v == 0 ? v : 1;
+}
+
 }  // namespace
 
+int64_t gated_threads(const GatedNormArgs& a) {
+  const int v = width_of(a);
+  return row_threads((int64_t)a.T * a.H, (a.D + v - 1) / v, v);
+}
+int64_t residual_threads(const ResidualNormArgs& a) {
+  const int v = width_of(a);
+  return row_threads(a.T, (a.C + v - 1) / v, v);
+}
+
 hipError_t launch_gated_norm(const GatedNormArgs& a) {
-  const int v = a.bf16 ? 8 : 4;
-  const bool vec = a.D % v == 0 && a.x_stride % v == 0 && (!a.gate || a.gate_stride % v == 0);
+  const bool vec = width_of(a) > 1;
   if (a.bf16) vec ? gated_t<bf16_bits, 8>(a) : gated_t<bf16_bits, 1>(a);
   else vec ? gated_t<float, 4>(a) : gated_t<float, 1>(a);
   return hipGetLastError();
 }
 
 hipError_t launch_residual_norm(const ResidualNormArgs& a) {
-  if (a.bf16) a.C % 8 == 0 ? residual_t<bf16_bits, 8>(a) : residual_t<bf16_bits, 1>(a);
-  else a.C % 4 == 0 ? residual_t<float, 4>(a) : residual_t<float, 1>(a);
+  const bool vec = width_of(a) > 1;
+  if (a.bf16) vec ? residual_t<bf16_bits, 8>(a) : residual_t<bf16_bits, 1>(a);
+  else vec ? residual_t<float, 4>(a) : residual_t<float, 1>(a);
   return hipGetLastError();
 }
 

@@ -3,34 +3,44 @@
 //
 //   S_t = exp(d_t a) S_{t-1} + d_t b_t x_t^T,   y_t = S_t^T c_t + skip x_t
 //
-// One decay per head and token; S is N x P in fp32.
+// One decay per head and token; S is N x P in fp32. fp32 tensors run token by
+// token, bf16 tensors in chunks on the matrix cores.
 #include "kda_pack.h"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kColumns = 64;         // columns of a head one workgroup owns
-constexpr int kGroupTarget = 1024;   // workgroups that segments of one sequence make up
-constexpr int kMinSegment = 128;     // tokens
+constexpr int kColumns = 64;   // columns of a head one workgroup of the token kernel owns
 
 // Segments. A call with few sequences, heads and columns cuts its sequences
-// every segment_len tokens, and the segments run side by side in two launches:
-//   1: every segment but the last of its sequence, from a zero state, for its
-//      last state alone; the first segment from the initial state and with its
-//      outputs.
-//   2: the segments behind the first, from the state in front of them,
-//      S(j) = end_0 carried over segments 1 .. j - 1: S <- e^{sum d a} S + end_i.
-// Nothing in the second launch reads initial states, so they may be the final
-// ones. (segment j of a sequence that starts at token s stores its last state
-// at entry s / len + j: sequences have fewer entries than segments, so no two
-// meet.)
-int segment_len(const Packed& s, int H, int P) {
-  const int64_t groups = (int64_t)H * ((P + kColumns - 1) / kColumns);
-  const int64_t parts = kGroupTarget / groups;          // segments all sequences have together
-  if (parts < 2 || s.T < 2 * kMinSegment) return s.T > 0 ? s.T : 1;
+// every segment_len tokens, and the segments run side by side in three launches:
+//   1: every segment but the last of its sequence, for its last state alone: the
+//      first from the initial state, the others from 0.
+//   2: the states in front of the segments, in order:
+//      front(j + 1) = e^{sum of d a over segment j} front(j) + last state of segment j.
+//   3: every segment from the state in front of it, with its outputs.
+// Final states may replace the initial ones: where they do, the first launch keeps
+// a copy for the first segment of the third. The state in front of segment j of a
+// sequence that starts at token s is entry 2 (s / len) + j: a sequence of two or
+// more segments reaches over at least one multiple of len, and has at most one
+// segment more than it reaches over, so no two meet and there are 2 T / len.
+struct Split {
+  int columns;     // columns of a head one workgroup owns
+  int target;      // workgroups that the segments of a call make up
+  int shortest;    // tokens of the shortest segment
+};
+constexpr Split kTokenSplit = {kColumns, 1024, 128};
+// (the chunks' workgroups have 8 waves where a head has more than 64 columns, else 4)
+constexpr Split kChunkSplit = {64, 512, 256}, kWideSplit = {128, 512, 256};
+const Split& split_of(bool bf16, int P) { return !bf16 ? kTokenSplit : P <= 64 ? kChunkSplit : kWideSplit; }
+int column_blocks(const Split& s, int P) { return (P + s.columns - 1) / s.columns; }
+
+int segment_len(const Packed& s, int H, int P, const Split& sp) {
+  const int64_t parts = sp.target / ((int64_t)H * column_blocks(sp, P));   // segments of all sequences together
+  if (parts < 2 || s.T < 2 * sp.shortest) return s.T > 0 ? s.T : 1;
   const int64_t len = ((s.T + parts - 1) / parts + KDA_SSM_CHUNK - 1) / KDA_SSM_CHUNK * KDA_SSM_CHUNK;
-  return (int)(len > kMinSegment ? len : kMinSegment);
+  return (int)(len > sp.shortest ? len : sp.shortest);
 }
 
 // d_t of one token and head.
@@ -50,24 +60,34 @@ struct SsmParams {
   const float* initial_state;
   float* final_state;
   void* y;
-  float* ends;      // last states of segments [entry][H][P blocks][..]
-  double* sums;     // sum of d a over them [entry][H]
+  bool keep;        // final states replace the initial ones
+  float* ends;      // states in front of segments [entry][H][P blocks][..]
+  double* sums;     // sum of d a over a segment, at the entry in front of it [entry][H]
 };
+__device__ __forceinline__ size_t entry_of(const SsmParams& a, const Part& p, int h, int j) {
+  return (size_t)(2 * (p.start / a.len) + j) * a.H + h;
+}
+// State in front of segment j, `vecs` vectors for each column block.
+__device__ __forceinline__ f32x4* front_of(const SsmParams& a, const Part& p, int h, int j, int pblocks, int pb,
+                                           int vecs) {
+  return (f32x4*)a.ends + (entry_of(a, p, h, j) * pblocks + pb) * (size_t)vecs;
+}
 
-// Token by token in fp32. A workgroup owns kColumns columns of one head: wave w
+// ---- fp32: token by token ---------------------------------------------------------------
+//
+// A workgroup owns kColumns columns of one head: wave w
 // the 16 columns 16 w .., lane l column l % 16 and the N / 4 rows
 // 16 i + 4 (l / 16) + 0..3. Tokens are staged kStage at a time.
 constexpr int kStage = 16;
 
-template <typename T, int N>
-__global__ __launch_bounds__(kThreads) void ssm_token_kernel(SsmParams a, int pass) {
+template <int N, bool outputs>
+__global__ __launch_bounds__(kThreads) void ssm_token_kernel(SsmParams a) {
   const int pblocks = (a.P + kColumns - 1) / kColumns;
   const int pb = blockIdx.x % pblocks, h = blockIdx.x / pblocks % a.H;
   Part p;
   if (!find_part(a.seqs, a.len, blockIdx.x / pblocks / a.H, p)) return;
   const bool last = p.j == p.parts - 1;
-  if (pass == 1 ? last && p.j > 0 : p.j == 0) return;
-  const bool outputs = pass == 2 || p.j == 0;
+  if (!outputs && last) return;
   const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave, q = lane / 16;
   const int col = pb * kColumns + wave * 16 + lane % 16;
   const bool live = pb * kColumns + wave * 16 < a.P;    // (P is a multiple of 16)
@@ -77,22 +97,17 @@ __global__ __launch_bounds__(kThreads) void ssm_token_kernel(SsmParams a, int pa
 #pragma unroll
   for (int i = 0; i < R; ++i) s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   const size_t state = ((size_t)p.n * a.H + h) * N * a.P + col;
-  auto entry = [&](int j) { return ((size_t)(p.start / a.len + j) * a.H + h); };
-  auto end_of = [&](int j) { return (f32x4*)a.ends + (entry(j) * pblocks + pb) * (R * kThreads) + tid; };
+  auto front = [&](int j) { return front_of(a, p, h, j, pblocks, pb, R * kThreads) + tid; };
   if (live) {
-    if (p.j == 0) {
-      if (a.initial_state)
+    if (outputs && (p.j > 0 || (p.parts > 1 && a.keep))) {
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+      for (int i = 0; i < R; ++i) s[i] = front(p.j)[i * kThreads];
+    } else if (p.j == 0 && a.initial_state) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][e] = a.initial_state[state + (size_t)(16 * i + 4 * q + e) * a.P];
-    } else if (pass == 2) {
+      for (int i = 0; i < R; ++i) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) s[i] = end_of(0)[i * kThreads];
-      for (int j = 1; j < p.j; ++j) {
-        const float f = __builtin_amdgcn_exp2f((float)(a.sums[entry(j)] * 1.4426950408889634));
-#pragma unroll
-        for (int i = 0; i < R; ++i) s[i] = f * s[i] + end_of(j)[i * kThreads];
+        for (int e = 0; e < 4; ++e) s[i][e] = a.initial_state[state + (size_t)(16 * i + 4 * q + e) * a.P];
+        if (!outputs && a.keep) front(0)[i * kThreads] = s[i];
       }
     }
   }
@@ -105,12 +120,12 @@ __global__ __launch_bounds__(kThreads) void ssm_token_kernel(SsmParams a, int pa
     __syncthreads();
     for (int e = tid; e < m * N; e += kThreads) {
       const int t = e / N, i = e % N;
-      sb[t][i] = Elem<T>::load((const T*)a.b + (tok + t) * a.b_stride + grp * N + i);
-      sc[t][i] = Elem<T>::load((const T*)a.c + (tok + t) * a.c_stride + grp * N + i);
+      sb[t][i] = Elem<float>::load((const float*)a.b + (tok + t) * a.b_stride + grp * N + i);
+      sc[t][i] = Elem<float>::load((const float*)a.c + (tok + t) * a.c_stride + grp * N + i);
     }
     for (int e = tid; e < m * kColumns; e += kThreads) {
       const int t = e / kColumns, i = pb * kColumns + e % kColumns;
-      if (i < a.P) sx[t][e % kColumns] = Elem<T>::load((const T*)a.x + (tok + t) * a.x_stride + (int64_t)h * a.P + i);
+      if (i < a.P) sx[t][e % kColumns] = Elem<float>::load((const float*)a.x + (tok + t) * a.x_stride + (int64_t)h * a.P + i);
     }
     if (tid < m) {
       const float d = step_size(a.dt[(tok + tid) * a.H + h], bias, a.softplus);
@@ -133,24 +148,521 @@ __global__ __launch_bounds__(kThreads) void ssm_token_kernel(SsmParams a, int pa
         if (outputs) {
           o += lane_xor<16>(o);
           o += lane_xor<32>(o);
-          if (q == 0) Elem<T>::store((T*)a.y + ((size_t)(tok + t) * a.H + h) * a.P + col, a.skip ? o + skip * xv : o);
+          if (q == 0) Elem<float>::store((float*)a.y + ((size_t)(tok + t) * a.H + h) * a.P + col, a.skip ? o + skip * xv : o);
         }
       }
     }
   }
-  if (!last) {
+  if (!outputs) {
     if (live)
 #pragma unroll
-      for (int i = 0; i < R; ++i) end_of(p.j)[i * kThreads] = s[i];
-    if (p.j > 0 && pb == 0 && wave == 0) {
+      for (int i = 0; i < R; ++i) front(p.j + 1)[i * kThreads] = s[i];
+    if (pb == 0 && wave == 0) {
       for (int m = 1; m < kStage; m *= 2) sum += __shfl_xor(sum, m);
-      if (tid == 0) a.sums[entry(p.j)] = sum;
+      if (tid == 0) a.sums[entry_of(a, p, h, p.j)] = sum;
     }
-  } else if (a.final_state && live) {
+  } else if (last && a.final_state && live) {
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) a.final_state[state + (size_t)(16 * i + 4 * q + e) * a.P] = s[i][e];
+  }
+}
+
+// ---- bf16: chunks of 64 tokens on the matrix cores --------------------------------------
+//
+// With c_t = sum of d a up to token t of the chunk and S the state in front of it:
+//     y_t = e^{c_t} C_t^T S + sum_{s <= t} M[t][s] x_s,  M[t][s] = e^{c_t - c_s} d_s (C_t . B_s), M[t][t] += skip
+//     S  <- e^{c_L} S + sum_s B_s (w_s x_s)^T,           w_s = e^{c_L - c_s} d_s
+// B, C and x are bf16 and enter the products as they are. The fp32 factor of
+// each product is split into bf16 terms, two for outputs (S and M) and three for
+// the state (w x): 2^-17 and 2^-26 of it are left out. Sums of d a are taken in
+// fp64 and handed on as two floats, so that their differences are exact to fp32.
+//
+// A workgroup owns 16 W columns of a head, wave w the 16 columns from 16 w on,
+// with their whole state in accumulators: tile k holds rows 16 k + 4 g
+// + i of column l % 16 (l the lane, g = l / 16). As operand of the next product a
+// lane holds 8 values along the sum: taking rows 16 (2v) + 4g + i and
+// 16 (2v + 1) + 4g + i for them makes the accumulators of two tiles that operand
+// without a move. The other operands are read in the same order:
+//   sC, sB  [token][N], natural order (C's part of it as two 8-byte reads)
+//   sBT, sXT  [row of B or column of x][token], sMh, sMl  [token t][token s]: token
+//        32 v + 16 u + 4 g + i at 32 v + 8 g + 4 u + i, one 16-byte read each
+// No padding: blocks of 16 bytes are XORed with bits of their row, so that the 16
+// lanes an LDS instruction serves at a time (16 bytes a lane: lanes 0-3, 12-15,
+// 20-23, 24-27 and so on) meet all 64 banks, and the rows of [row][token] arrays
+// change places in pairs in every other tile of 16, for the same in the stores.
+constexpr int kL = KDA_SSM_CHUNK, kDies = 8;
+
+// In an array [..][64 tokens], block b (8 tokens) of row 16 k + l is b ^ (l >> 1),
+// and where rows change places (k odd) the row is 16 k + (l ^ 1); in an array [64
+// tokens][NP channels], block b (8 channels) of token 16 u + l is b ^ channel_mask(l).
+// A lane keeps one place in each array; others are that one XOR a constant (other
+// blocks) plus a constant (other tiles).
+template <int NP>
+__device__ __forceinline__ constexpr int channel_mask(int l) {
+  return NP >= 128 ? l : NP == 64 ? l >> 1 : -(l >> 2) & 3;
+}
+// v, and the compiler does not know it: what is made of it is made where it is
+// used, not once and kept in registers (which spill).
+template <typename T>
+__device__ __forceinline__ T fresh(T v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// The value of lane `l` (its low 6 bits).
+__device__ __forceinline__ double lane_value(double x, int l) {
+  const uint2 v = __builtin_bit_cast(uint2, x);
+  return __builtin_bit_cast(double, make_uint2(__builtin_amdgcn_ds_bpermute(4 * l, v.x),
+                                               __builtin_amdgcn_ds_bpermute(4 * l, v.y)));
+}
+// Nothing moves across it: keeps the reads of later products, which would take
+// registers that are not there, behind the products before them.
+__device__ __forceinline__ void stay() { __builtin_amdgcn_sched_barrier(0); }
+
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+
+struct Rows4 {  // 8 columns of 4 tokens
+  u32x4 r[4];
+};
+// Place of columns 8 cv .. 8 cv + 7 (the first of them), tokens 4 sr .. 4 sr + 3.
+__device__ __forceinline__ int transposed_place(int cv, int sr) {
+  const int block = 4 * (sr / 8) + (sr & 3), half = (sr / 4) & 1;
+  return (8 * cv + (cv / 2 & 1)) * kL + (block ^ 4 * (cv & 1)) * 8 + 4 * half;
+}
+__device__ __forceinline__ void store_transposed(bf16_bits* dst, int place, const Rows4& q) {
+  const u32x4 a = q.r[0], b = q.r[1], c = q.r[2], d = q.r[3];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint2 even, odd;   // columns 2 j, 2 j + 1 of the 8
+    even.x = __builtin_amdgcn_perm(b[j], a[j], 0x05040100u);
+    even.y = __builtin_amdgcn_perm(d[j], c[j], 0x05040100u);
+    odd.x = __builtin_amdgcn_perm(b[j], a[j], 0x07060302u);
+    odd.y = __builtin_amdgcn_perm(d[j], c[j], 0x07060302u);
+    *(uint2*)(dst + (place ^ 8 * j) + 2 * j * kL) = even;
+    *(uint2*)(dst + (place ^ (8 * j + kL)) + 2 * j * kL) = odd;
+  }
+}
+
+// x = h + m + l in bf16, each the rest of the one before rounded to nearest.
+__device__ __forceinline__ void split3(f32x4 x, bf16x4& h, bf16x4& m, bf16x4& l) {
+  h = to_bf16x4(x);
+  const f32x4 r = x - from_bf16x4(h);
+  m = to_bf16x4(r);
+  l = to_bf16x4(r - from_bf16x4(m));
+}
+
+// What the tokens of a chunk need of d and a.
+struct Decays {
+  float hi[kL], lo[kL];   // c_t log2 e
+  float d[kL];            // d_t
+  float e[kL];            // e^{c_t}
+  float w[kL];            // e^{c_L - c_t} d_t
+  float total;            // e^{c_L}
+};
+
+template <int N, int W, bool outputs>
+__global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_kernel(SsmParams a) {
+  constexpr int kThreads = 64 * W, kCols = 16 * W, NP = N < 32 ? 32 : N, KS = NP / 32, NT = N / 16, NV = N / 8;
+  const int pblocks = (a.P + kCols - 1) / kCols;
+  // Workgroups go to the 8 dies in turn: numbered so that those that share B and C
+  // (a group's heads in a segment) are on one die and meet in its L2.
+  const int share = a.H / a.G * pblocks;
+  const int id = (blockIdx.x / (kDies * share) * kDies + blockIdx.x % kDies) * share + blockIdx.x / kDies % share;
+  const int pb = id % pblocks, h = id / pblocks % a.H;
+  Part p;
+  if (!find_part(a.seqs, a.len, id / pblocks / a.H, p)) return;
+  const bool last = p.j == p.parts - 1;
+  if (!outputs && last) return;
+  const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave, g = lane / 16, l16 = lane % 16;
+  const int wcol = wave * 16;                       // first column of the wave in the workgroup's
+  const int col0 = pb * kCols;                           // and of the workgroup in the head
+  const int grp = h / (a.H / a.G);
+  const float av = a.a[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, skip = a.skip ? a.skip[h] : 0.f;
+
+  constexpr int kB = kL * NP, kM = 2 * kL * kL;
+  __shared__ __attribute__((aligned(16))) bf16_bits sC[kL * NP], sBM[kB > kM ? kB : kM], sBT[N * kL], sXT[kCols * kL];
+  __shared__ Decays dec[4];
+  bf16_bits *sB = sBM, *sMh = sBM, *sMl = sBM + kL * kL;  // (M overwrites B once it is used)
+
+  // ---- state in front of the segment
+  f32x4 s[NT];
+  auto front = [&](int j) { return front_of(a, p, h, j, pblocks, pb, NT * kThreads) + tid; };
+  const size_t state = ((size_t)p.n * a.H + h) * N * a.P + col0 + wcol + l16;
+  const bool from_front = outputs && (p.j > 0 || (p.parts > 1 && a.keep));
+  const bool live = col0 + wcol < a.P;                   // (P is a multiple of 16)
+  if (from_front) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k) s[k] = front(p.j)[k * kThreads];
+  } else if (p.j == 0 && a.initial_state && live) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[k][i] = a.initial_state[state + (size_t)(16 * k + 4 * g + i) * a.P];
+  } else {
+#pragma unroll
+    for (int k = 0; k < NT; ++k) s[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  if (!outputs && p.j == 0 && a.keep)
+#pragma unroll
+    for (int k = 0; k < NT; ++k) front(0)[k * kThreads] = s[k];
+
+  // ---- loads of a chunk into registers, and from there into LDS. Runs of 4 tokens
+  // by 8 columns of x and then of B are shared out over the threads (run i: tokens
+  // 4 (i / 4 % 16), columns 8 (4 (i / 64) + i % 4): 64 bytes of a row together), and
+  // the rows of C after them.
+  constexpr int kXRuns = 2 * W * 16, kRuns = kXRuns + NV * 16, UR = (kRuns + kThreads - 1) / kThreads;
+  constexpr int kCUnits = kL * NV, UC = (kCUnits + kThreads - 1) / kThreads;
+  static_assert(kXRuns % kWave == 0 && kThreads % kWave == 0, "a wave's runs are of one array");
+  static_assert(kThreads % NV == 0, "units of C");
+  Rows4 rr[UR];
+  u32x4 rc[UC];
+  const u32x4 zero = {0u, 0u, 0u, 0u};
+  // Byte offsets of a thread's rows from a chunk's first token (64 rows of at most
+  // KDA_SSM_MAX_STRIDE elements: below 2^31). What is the same for a wave is kept
+  // in scalars.
+  const char* gx = (const char*)((const bf16_bits*)a.x + p.first * a.x_stride + (int64_t)h * a.P + col0);
+  const char* gb = (const char*)((const bf16_bits*)a.b + p.first * a.b_stride + grp * N);
+  const char* gc = (const char*)((const bf16_bits*)a.c + p.first * a.c_stride + grp * N);
+  const int64_t xs = 2 * a.x_stride, bs = 2 * a.b_stride, cs = 2 * a.c_stride;
+  constexpr int kBRun = NV < 4 ? NV : 4;                 // (columns of B in a wave's runs)
+  const int uwave = __builtin_amdgcn_readfirstlane(wave);
+  // Run k of the thread: of x, or of B; its columns / 8 and tokens / 4; whether there
+  // is one. (A thread without one, or with columns behind the head's, reads the
+  // first columns: nothing is made of them.)
+  auto of_x = [&](int k) { return uwave * kWave + k * kThreads < kXRuns; };
+  auto run_col = [&](int k, uint32_t t) -> int {
+    const uint32_t id = t + k * kThreads, b = id - kXRuns;
+    return of_x(k) ? 4 * (id / 64) + id % 4 : kBRun * (b / (16 * kBRun)) + b % kBRun;
+  };
+  auto run_tok = [&](int k, uint32_t t) -> int { return (of_x(k) ? t / 4 : t / kBRun) % 16; };
+  uint32_t first[UR], off[UR];   // bytes from a chunk's first token to a run's columns, and to its first row of them
+  int place[UR];                 // of its columns in sXT or sBT
+#pragma unroll
+  for (int k = 0; k < UR; ++k) {
+    const int cv = run_col(k, tid), sr = run_tok(k, tid);
+    first[k] = (of_x(k) ? col0 + 8 * cv < a.P : tid + k * kThreads < kRuns) ? 16 * cv : 0;
+    off[k] = 4 * sr * (uint32_t)(of_x(k) ? xs : bs) + first[k];
+    place[k] = transposed_place(cv, sr);
+  }
+  // Of the last chunk of a segment, rows behind the end are read as its last row
+  // (offsets grow with the row, so the smaller of two is the earlier row): their
+  // step sizes are 0, so nothing is added by them, and no output is theirs.
+  auto load = [&](int t0) __attribute__((always_inline)) {
+    const uint32_t rows = min(p.count - t0, kL) - 1;
+#pragma unroll
+    for (int k = 0; k < UR; ++k) {
+      const char* base = of_x(k) ? gx : gb;
+      const uint32_t step = (uint32_t)(of_x(k) ? xs : bs), at = fresh(off[k]), most = fresh(first[k]) + rows * step;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) rr[k].r[r] = *(const u32x4*)(base + min(at + r * step, most));
+    }
+    gx += kL * xs;
+    gb += kL * bs;
+  };
+  const uint32_t coff = tid / NV * (uint32_t)cs + tid % NV * 16;
+  auto load_c = [&](int t0) __attribute__((always_inline)) {
+    const uint32_t rows = min(p.count - t0, kL) - 1, at = fresh(coff), most = fresh(threadIdx.x) % NV * 16 + rows * (uint32_t)cs;
+#pragma unroll
+    for (int k = 0; k < UC; ++k) rc[k] = *(const u32x4*)(gc + min(at + k * (kThreads / NV) * (uint32_t)cs, most));
+    gc += kL * cs;
+  };
+  auto store = [&]() __attribute__((always_inline)) {
+    const uint32_t t = fresh(threadIdx.x);
+#pragma unroll
+    for (int k = 0; k < UR; ++k) {
+      const int at = fresh(place[k]);
+      if (of_x(k)) {
+        store_transposed(sXT, at, rr[k]);
+      } else if (kRuns % kThreads == 0 || t + k * kThreads < kRuns) {
+        store_transposed(sBT, at, rr[k]);
+        if (outputs) {
+          const int cv = run_col(k, t), sr = run_tok(k, t);
+          const int row = 4 * sr * NP + (cv ^ channel_mask<NP>(4 * (sr & 3))) * 8;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) *(u32x4*)(sB + (row ^ channel_mask<NP>(r) * 8) + r * NP) = rr[k].r[r];
+        }
+      }
+    }
+    if (outputs) {
+      constexpr int kRows = kThreads / NV;
+      static_assert(kRows % 16 == 0 || NP >= 128, "the mask is linear in the row");
+      const int cplace = t / NV * NP + (t % NV ^ channel_mask<NP>(t / NV % 16)) * 8;
+#pragma unroll
+      for (int k = 0; k < UC; ++k)
+        if (kCUnits % kThreads == 0 || t + k * kThreads < kCUnits)
+          *(u32x4*)(sC + (cplace ^ k * kRows % 16 * 8) + k * kRows * NP) = rc[k];
+    }
+    if (N < NP && outputs && tid < kL)                   // the half of a block of 32 channels that N = 16 leaves
+#pragma unroll
+      for (int b = NV; b < NP / 8; ++b) {
+        const int at = tid * NP + (b ^ channel_mask<NP>(tid % 16)) * 8;
+        *(u32x4*)(sB + at) = zero, *(u32x4*)(sC + at) = zero;
+      }
+  };
+  // A lane's places as it reads: its row and block g of a tile of a [row][token]
+  // array (1: the row it changes places with), of a [token][channel] array, and the
+  // 4 channels 4 g of the latter.
+  const int token_read[2] = {l16 * kL + (g ^ l16 >> 1) * 8, (l16 ^ 1) * kL + (g ^ l16 >> 1) * 8};
+  const int channel_read = l16 * NP + (g ^ channel_mask<NP>(l16)) * 8;
+  const int half_read = l16 * NP + (g / 2 ^ channel_mask<NP>(l16)) * 8 + 4 * (g & 1);
+  // Wave w, lane t: what becomes of dt in the w-th of the next four chunks.
+  float rdt = 0.f;
+  double sum = 0.0;                                      // of the segment's d a, in the four waves' parts
+  auto load_dt = [&](int t0) __attribute__((always_inline)) {
+    const int t = t0 + fresh(threadIdx.x);                       // (kL * wave + lane)
+    rdt = uwave < 4 && t < p.count ? a.dt[(size_t)(p.first + t) * a.H + h] : 0.f;
+  };
+  auto decays = [&](int t0) __attribute__((always_inline)) {
+    if (uwave >= 4 || t0 + kL * uwave >= p.count) return;
+    Decays& q = dec[uwave];
+    const int t = fresh(threadIdx.x), at = t & (kWave - 1);
+    const float d = t0 + t < p.count ? step_size(rdt, bias, a.softplus) : 0.f;
+    double c = (double)d * av;
+#pragma unroll
+    for (int m = 1; m < kL; m *= 2) {
+      const double o = lane_value(c, at - m);
+      if (at >= m) c += o;
+    }
+    const double end = lane_value(c, kL - 1);
+    if (!outputs) sum += end;
+    constexpr double kL2 = 1.4426950408889634;
+    const float hi = (float)(c * kL2);
+    q.hi[at] = hi;
+    q.lo[at] = (float)(c * kL2 - hi);
+    q.d[at] = d;
+    q.e[at] = __builtin_amdgcn_exp2f(hi);
+    q.w[at] = __builtin_amdgcn_exp2f((float)((end - c) * kL2)) * d;
+    if (at == 0) q.total = __builtin_amdgcn_exp2f((float)(end * kL2));
+  };
+
+  // (as the loads: a scalar base, and a row of H P <= KDA_SSM_MAX_STRIDE elements a lane)
+  const int64_t yrow = 2 * (int64_t)a.H * a.P;
+  char* gy = (char*)((bf16_bits*)a.y + ((size_t)p.first * a.H + h) * a.P + col0);
+  load_dt(0);
+  if (p.count > 0) {
+    load(0);
+    if (outputs) load_c(0);
+  }
+#pragma unroll 1
+  for (int t0 = 0; t0 < p.count; t0 += kL) {
+    const Decays& q = dec[t0 / kL & 3];
+    if ((t0 / kL & 3) == 0) {
+      decays(t0);
+      load_dt(t0 + 4 * kL);
+    }
+    store();
+    lds_barrier();
+    if (t0 + kL < p.count) load(t0 + kL);
+    if (outputs) {
+      // ---- M, transposed (a lane: one t, 4 s each), in tiles of 16 t by 16 s: the
+      // ten up to the diagonal and two of zeros, shared out over the waves
+      constexpr int kTiles = 12, kPer = (kTiles + W - 1) / W;
+      bf16x4 mh[kPer], ml[kPer];
+      const int cr = fresh(channel_read), mr = fresh(token_read[0]);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int id = uwave + k * W;
+        // tiles (tt, u) by id: 0 .. 3 (3, u), 4 .. 6 (2, u), 7 (1, 0), 8 (1, 1), 9 (0, 0), 10 (0, 1), 11 (2, 3)
+        const int tt = id < 4 ? 3 : id < 7 ? 2 : id < 9 ? 1 : id < 11 ? 0 : 2;
+        const int u = id < 4 ? id : id < 7 ? id - 4 : id < 9 ? id - 7 : id < 11 ? id - 9 : 3;
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+        if (id < 10) {
+          const int t = 16 * tt + l16;
+          bf16x8 b[KS], c[KS];
+#pragma unroll
+          for (int v = 0; v < KS; ++v) {
+            b[v] = *(const bf16x8*)(sB + (cr ^ 32 * v) + 16 * u * NP);
+            c[v] = *(const bf16x8*)(sC + (cr ^ 32 * v) + 16 * tt * NP);
+          }
+#pragma unroll
+          for (int v = 0; v < KS; ++v) x = mfma32(b[v], c[v], x);
+          const float thi = q.hi[t], tlo = q.lo[t];
+          const f32x4 shi = *(const f32x4*)&q.hi[16 * u + 4 * g], slo = *(const f32x4*)&q.lo[16 * u + 4 * g],
+                      sd = *(const f32x4*)&q.d[16 * u + 4 * g];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] *= __builtin_amdgcn_exp2f((thi - shi[i]) + (tlo - slo[i])) * sd[i];
+          if (u == tt) {
+            const int at = fresh(l16) - 4 * g;                // the diagonal's place among the lane's 4
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float v = i == at ? x[i] + skip : x[i];
+              x[i] = i <= at ? v : 0.f;
+            }
+          }
+        }
+        split_bf16(x, mh[k], ml[k]);
+        stay();
+      }
+      lds_barrier();                                     // B is used
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int id = uwave + k * W;
+        const int tt = id < 4 ? 3 : id < 7 ? 2 : id < 9 ? 1 : id < 11 ? 0 : 2;
+        const int u = id < 4 ? id : id < 7 ? id - 4 : id < 9 ? id - 7 : id < 11 ? id - 9 : 3;
+        const int at = (mr ^ 32 * (u / 2)) + 16 * tt * kL + 4 * (u & 1);
+        if (id < kTiles) {
+          *(bf16x4*)(sMh + at) = mh[k];
+          *(bf16x4*)(sMl + at) = ml[k];
+        }
+      }
+      lds_barrier();
+    }
+    // ---- x of the wave's columns: operands of both products
+    auto x_operand = [&](int v) __attribute__((always_inline)) {
+      return *(const bf16x8*)(sXT + (fresh(token_read[uwave & 1]) ^ 32 * v) + uwave * 16 * kL);
+    };
+    bf16x8 xo[2] = {x_operand(0), x_operand(1)};
+    if (outputs) {
+      // ---- y, transposed (a lane: one t, 4 columns): the state's part first
+      f32x4 y[4];
+      const int hr = fresh(half_read), mr = fresh(token_read[0]);
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) y[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int v = 0; v < KS; ++v) {
+        bf16x4 h0, l0, h1 = {}, l1 = {};
+        split_bf16(s[2 * v], h0, l0);
+        if constexpr (NT > 1) split_bf16(s[2 * v + 1], h1, l1);
+        const bf16x8 sh = cat(h0, h1), sl = cat(l0, l1);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+          const bf16x8 c = cat(*(const bf16x4*)(sC + (hr ^ 32 * v) + 16 * tt * NP),
+                               *(const bf16x4*)(sC + (hr ^ (32 * v + 16)) + 16 * tt * NP));
+          y[tt] = mfma32(sl, c, y[tt]);
+          y[tt] = mfma32(sh, c, y[tt]);
+        }
+        stay();
+      }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) y[tt] *= q.e[16 * tt + l16];
+      // A value that is not finite would reach earlier tokens through M's zeros:
+      // it is taken out here, and its column made NaN from its token on.
+      const u16x8 most = __builtin_elementwise_max(__builtin_bit_cast(u16x8, xo[0]) & (uint16_t)0x7fff,
+                                                   __builtin_bit_cast(u16x8, xo[1]) & (uint16_t)0x7fff);
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) bad |= most[i] >= 0x7f80;
+      const bool any_bad = __any(bad);
+      int from = kL;
+      if (any_bad) {
+        const int fg = fresh(threadIdx.x) / 16 % 4;
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (!((float)xo[v][i] * 0.f == 0.f)) {
+              xo[v][i] = (__bf16)0.f;
+              from = min(from, 32 * v + 16 * (i / 4) + 4 * fg + i % 4);
+            }
+        from = min(from, __builtin_amdgcn_ds_bpermute(4 * (fresh(threadIdx.x) ^ 16), from));
+        from = min(from, __builtin_amdgcn_ds_bpermute(4 * (fresh(threadIdx.x) ^ 32), from));
+      }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int v = 0; v <= tt / 2; ++v) {
+          const int at = (mr ^ 32 * v) + 16 * tt * kL;
+          y[tt] = mfma32(xo[v], *(const bf16x8*)(sMl + at), y[tt]);
+          y[tt] = mfma32(xo[v], *(const bf16x8*)(sMh + at), y[tt]);
+        }
+      stay();
+      if (any_bad) {
+        const uint32_t ft = fresh(threadIdx.x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int first = __builtin_amdgcn_ds_bpermute(4 * (ft / 16 % 4 * 4 + i), from);
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt)
+            if (16 * tt + (int)(ft % 16) >= first) y[tt][i] = __builtin_nanf("");
+        }
+#pragma unroll
+        for (int v = 0; v < 2; ++v) xo[v] = x_operand(v);
+      }
+      if (live) {
+        const int left = p.count - t0 - l16;
+        const uint32_t yoff = l16 * (uint32_t)yrow + 2 * (16 * uwave + 4 * g);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+          if (16 * tt < left) *(bf16x4*)(gy + 16 * tt * yrow + yoff) = to_bf16x4(y[tt]);
+      }
+      gy += kL * yrow;
+      if (t0 + kL < p.count) load_c(t0 + kL);            // (late: the registers are needed until here)
+    }
+    // ---- the state behind the chunk
+    const float total = q.total;
+    const int br[2] = {fresh(token_read[0]), fresh(token_read[1])};
+#pragma unroll
+    for (int k = 0; k < NT; ++k) s[k] *= total;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      bf16x4 h0, m0, l0, h1, m1, l1;
+      split3(from_bf16x4(lo_half(xo[v])) * *(const f32x4*)&q.w[32 * v + 4 * g], h0, m0, l0);
+      split3(from_bf16x4(hi_half(xo[v])) * *(const f32x4*)&q.w[32 * v + 16 + 4 * g], h1, m1, l1);
+      const bf16x8 xh = cat(h0, h1), xm = cat(m0, m1), xl = cat(l0, l1);
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        const bf16x8 b = *(const bf16x8*)(sBT + (br[k & 1] ^ 32 * v) + 16 * k * kL);
+        s[k] = mfma32(b, xl, s[k]);
+        s[k] = mfma32(b, xm, s[k]);
+        s[k] = mfma32(b, xh, s[k]);
+        if (k % 4 == 3) stay();
+      }
+    }
+    lds_barrier();                                       // the chunk is used
+  }
+
+  if (!outputs) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k) front(p.j + 1)[k * kThreads] = s[k];
+    if (pb == 0) {
+      __shared__ double part[4];
+      if (lane == 0 && wave < 4) part[wave] = sum;
+      __syncthreads();
+      if (tid == 0) a.sums[entry_of(a, p, h, p.j)] = part[0] + part[1] + part[2] + part[3];
+    }
+  } else if (last && a.final_state && live) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a.final_state[state + (size_t)(16 * k + 4 * g + i) * a.P] = s[k][i];
+  }
+}
+
+// The states in front of the segments of one sequence (a block per 256 vectors of
+// them and per multiple of len, where at most one sequence of several segments
+// starts). vecs: vectors of a head's state.
+__global__ __launch_bounds__(kThreads) void ssm_front_kernel(SsmParams a, int blocks, int vecs) {
+  const int b = blockIdx.x % blocks, h = blockIdx.x / blocks % a.H, at = blockIdx.x / blocks / a.H;
+  int lo = 0, hi = a.seqs.num_seqs;   // the last sequence that starts before (at + 1) len
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if (token_offset(a.seqs, mid) / a.len <= at) lo = mid;
+    else hi = mid;
+  }
+  Part p;
+  p.start = token_offset(a.seqs, lo);
+  p.length = token_offset(a.seqs, lo + 1) - p.start;
+  const int i = b * kThreads + threadIdx.x;
+  if (p.start / a.len != at || p.length <= 2 * a.len || i >= vecs) return;
+  const int parts = (p.length - 1) / a.len + 1;
+  const size_t step = (size_t)a.H * vecs;
+  f32x4* v = (f32x4*)a.ends + entry_of(a, p, h, 1) * vecs + i;
+  f32x4 s = *v;
+  constexpr int U = 4;                // segments whose states are on their way at once
+  for (int j = 1; j < parts - 1; j += U) {
+    const int m = min(U, parts - 1 - j);
+    f32x4 e[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) e[u] = v[(size_t)(min(u, m - 1) + 1) * step];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (u < m) {
+        s = __builtin_amdgcn_exp2f((float)(a.sums[entry_of(a, p, h, j + u)] * 1.4426950408889634)) * s + e[u];
+        v[(size_t)(u + 1) * step] = s;
+      }
+    v += (size_t)m * step;
   }
 }
 
@@ -214,52 +726,82 @@ SsmParams params_of(const SsmArgs& a, int len) {
   p.H = a.H; p.G = a.G; p.P = a.P; p.len = len;
   p.initial_state = a.initial_state; p.final_state = a.final_state;
   p.y = a.y;
+  p.keep = a.initial_state && a.initial_state == a.final_state;
   p.ends = nullptr; p.sums = nullptr;
   return p;
 }
 
-int64_t entries(const Packed& s, int len) { return len < s.T ? s.T / len : 0; }
-size_t end_bytes(int H, int N, int P) { return (size_t)H * ((P + kColumns - 1) / kColumns) * kColumns * N * 4; }
+int64_t entries(const Packed& s, int len) { return len < s.T ? 2 * (int64_t)(s.T / len) : 0; }
+size_t end_bytes(int H, int N, int P, const Split& sp) { return (size_t)H * column_blocks(sp, P) * sp.columns * N * 4; }
 
-template <typename T, int N>
-hipError_t launch_n(const SsmArgs& a) {
-  const int len = segment_len(a.seqs, a.H, a.P);
+// Workgroups: whole rounds of the dies (the last ones have no segment).
+int64_t launch_groups(const SsmArgs& a, const Split& sp) {
+  const int64_t blocks = column_blocks(sp, a.P), round = kDies * (a.H / a.G * blocks);
+  const int64_t groups = part_slots(a.seqs, segment_len(a.seqs, a.H, a.P, sp)) * a.H * blocks;
+  return (groups + round - 1) / round * round;
+}
+
+// All launches of a scan by a kernel (for states alone, and with outputs).
+template <typename K>
+hipError_t launch_passes(K states, K outputs, const SsmArgs& a, const Split& sp, int threads) {
+  const int len = segment_len(a.seqs, a.H, a.P, sp);
   SsmParams p = params_of(a, len);
   const int64_t e = entries(a.seqs, len);
   p.ends = (float*)a.workspace;
-  p.sums = (double*)((char*)a.workspace + e * end_bytes(a.H, N, a.P));
-  const unsigned groups = (unsigned)ssm_groups(a);
-  for (int pass = 1; pass <= (e > 0 ? 2 : 1); ++pass)
-    hipLaunchKernelGGL((ssm_token_kernel<T, N>), dim3(groups), dim3(kThreads), 0, a.stream, p, pass);
+  p.sums = (double*)((char*)a.workspace + e * end_bytes(a.H, a.N, a.P, sp));
+  const unsigned groups = (unsigned)launch_groups(a, sp);
+  if (e > 0) {
+    hipLaunchKernelGGL(states, dim3(groups), dim3(threads), 0, a.stream, p);
+    const int vecs = column_blocks(sp, a.P) * sp.columns * a.N / 4, blocks = (vecs + kThreads - 1) / kThreads;
+    hipLaunchKernelGGL(ssm_front_kernel, dim3((unsigned)(e / 2 * a.H * blocks)), dim3(kThreads), 0, a.stream, p, blocks,
+                       vecs);
+  }
+  hipLaunchKernelGGL(outputs, dim3(groups), dim3(threads), 0, a.stream, p);
   return hipGetLastError();
 }
-template <typename T>
-hipError_t launch_t(const SsmArgs& a) {
-  switch (a.N) {
-    case 16: return launch_n<T, 16>(a);
-    case 32: return launch_n<T, 32>(a);
-    case 64: return launch_n<T, 64>(a);
-    case 128: return launch_n<T, 128>(a);
-    default: return launch_n<T, 256>(a);
-  }
+template <int N>
+hipError_t launch_n(const SsmArgs& a) {
+  const Split& sp = split_of(a.bf16, a.P);
+  if (!a.bf16) return launch_passes(ssm_token_kernel<N, false>, ssm_token_kernel<N, true>, a, sp, kThreads);
+  return a.P <= 64 ? launch_passes(ssm_chunk_kernel<N, 4, false>, ssm_chunk_kernel<N, 4, true>, a, sp, 4 * sp.columns) : launch_passes(ssm_chunk_kernel<N, 8, false>, ssm_chunk_kernel<N, 8, true>, a, sp, 4 * sp.columns);
+}
+
+size_t workspace_of(int32_t T, int32_t H, int32_t N, int32_t P, const Split& sp) {
+  const size_t by_target = (size_t)sp.target * ((size_t)sp.columns * N * 4 + 8);
+  const size_t by_length = (size_t)(T / sp.shortest) * (end_bytes(H, N, P, sp) + (size_t)H * 8);
+  return 2 * (by_target < by_length ? by_target : by_length);
 }
 
 }  // namespace
 
-int64_t ssm_groups(const SsmArgs& a) {
-  return part_slots(a.seqs, segment_len(a.seqs, a.H, a.P)) * a.H * ((a.P + kColumns - 1) / kColumns);
+int64_t ssm_threads(const SsmArgs& a) {
+  const Split& sp = split_of(a.bf16, a.P);
+  return launch_groups(a, sp) * (a.bf16 ? 4 * sp.columns : kThreads);
 }
 
-// At most kGroupTarget / groups segments of one sequence's worth, and at most
-// one per kMinSegment tokens: both grow with the sizes.
+// At most 2 target / (H column blocks) entries, and at most two per `shortest`
+// tokens: both grow with the sizes. Any type, and heads narrow or wide: the
+// largest.
 size_t ssm_workspace(int32_t num_seqs, int32_t T, int32_t H, int32_t N, int32_t P) {
   (void)num_seqs;
-  const size_t by_target = (size_t)kGroupTarget * kColumns * N * 4 + (size_t)kGroupTarget * 8;
-  const size_t by_length = (size_t)(T / kMinSegment) * (end_bytes(H, N, P) + (size_t)H * 8);
-  return by_target < by_length ? by_target : by_length;
+  size_t most = 0;
+  for (const Split* sp : {&kTokenSplit, &kChunkSplit, &kWideSplit}) {
+    if (sp == &kWideSplit && P <= 64) continue;
+    const size_t w = workspace_of(T, H, N, P, *sp);
+    most = w > most ? w : most;
+  }
+  return most;
 }
 
-hipError_t launch_ssm(const SsmArgs& a) { return a.bf16 ? launch_t<bf16_bits>(a) : launch_t<float>(a); }
+hipError_t launch_ssm(const SsmArgs& a) {
+  switch (a.N) {
+    case 16: return launch_n<16>(a);
+    case 32: return launch_n<32>(a);
+    case 64: return launch_n<64>(a);
+    case 128: return launch_n<128>(a);
+    default: return launch_n<256>(a);
+  }
+}
 
 hipError_t launch_ssm_step(const SsmArgs& a) {
   SsmParams p = params_of(a, 1);

@@ -551,8 +551,8 @@ typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1, KDA_ACT_SIGMOID = 2 } kda_act
  *                  state holds input rows, so it has their type and is exact.
  * Errors: KDA_ERR_INVALID_ARG (null required pointer, misaligned or overlapping
  * arrays, T or num_seqs < 0, num_seqs != 1 without cu_seqlens, C outside
- * [1, KDA_CONV_MAX_CHANNELS], x_stride < C, width, activation; more than 2^24
- * workgroups), KDA_ERR_UNSUPPORTED (dtype), KDA_ERR_HIP. */
+ * [1, KDA_CONV_MAX_CHANNELS], x_stride < C, width, activation; sizes whose
+ * launch would take 2^32 threads), KDA_ERR_UNSUPPORTED (dtype), KDA_ERR_HIP. */
 #define KDA_CONV_MAX_WIDTH 4
 #define KDA_CONV_MAX_CHANNELS (1 << 20)
 kda_status kda_conv_prefill(const void* x, int64_t x_stride, const float* weight,
@@ -581,7 +581,7 @@ kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, c
  *                  as the states of the delta rule), or NULL (zeros)
  *   final_state    the same, or NULL to skip; may be initial_state itself
  *   N  16, 32, 64, 128 or 256;  P a multiple of 16 up to 256; the strides of x,
- *      b and c are multiples of 16 bytes
+ *      b and c are multiples of 16 bytes, at most KDA_SSM_MAX_STRIDE elements
  * bf16 tensors run in chunks of KDA_SSM_CHUNK tokens on the matrix cores: b, c
  * and x are exact there, every fp32 factor is carried in two bf16 terms for
  * outputs (2^-16 of each product) and three for states (2^-24); the decays
@@ -597,6 +597,7 @@ kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, c
  * Errors: KDA_ERR_INVALID_ARG (as kda_conv_prefill; G < 1 or H % G), KDA_ERR_UNSUPPORTED
  * (dtype, N or P), KDA_ERR_WORKSPACE, KDA_ERR_HIP. */
 #define KDA_SSM_CHUNK 64
+#define KDA_SSM_MAX_STRIDE (1 << 23)
 size_t kda_ssm_workspace_size(int32_t num_seqs, int32_t T, int32_t H, int32_t N, int32_t P);
 kda_status kda_ssm_prefill(const void* x, int64_t x_stride, const float* dt, const float* a,
                            const void* b, int64_t b_stride, const void* c, int64_t c_stride,
@@ -628,9 +629,9 @@ kda_status kda_ssm_step(const void* x, int64_t x_stride, const float* dt, const 
  *   y        [T, H, D] dtype
  * Squares are summed in fp32: rows with |v| near 2^64 overflow to norm 0.
  * Errors: KDA_ERR_INVALID_ARG (null required pointer, misaligned or overlapping
- * arrays, T < 0, H < 1, D outside [1, KDA_NORM_MAX], T * H above INT32_MAX,
- * stride < H * D, activation, eps negative or not finite, flags other than 0
- * and 1), KDA_ERR_UNSUPPORTED (dtype), KDA_ERR_HIP. */
+ * arrays, T < 0, H < 1, D outside [1, KDA_NORM_MAX], T * H above INT32_MAX or
+ * a launch of 2^32 threads, stride < H * D, activation, eps negative or not
+ * finite, flags other than 0 and 1), KDA_ERR_UNSUPPORTED (dtype), KDA_ERR_HIP. */
 kda_status kda_gated_norm(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride,
                           const float* weight, int32_t weight_per_head, kda_dtype dtype, int32_t T,
                           int32_t H, int32_t D, int32_t activation, int32_t gate_first, float eps,

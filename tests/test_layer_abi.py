@@ -102,7 +102,7 @@ def test_conv_step_refuses(bad, status):
     (dict(dtype=-1), UNSUP), (dict(N=48), UNSUP), (dict(N=512, b_stride=1024, c_stride=1024), UNSUP), (dict(P=8), UNSUP),
     (dict(P=24), UNSUP), (dict(P=272), UNSUP), (dict(H=0), BAD), (dict(G=0), BAD), (dict(G=3), BAD),
     (dict(softplus=2), BAD), (dict(x_stride=255), BAD), (dict(x_stride=260), BAD), (dict(b_stride=56), BAD),
-    (dict(c_stride=68), BAD), (dict(b_stride=-64), BAD), (dict(x=None), BAD), (dict(dt=None), BAD), (dict(a=None), BAD),
+    (dict(x_stride=(1 << 23) + 8), BAD), (dict(c_stride=68), BAD), (dict(b_stride=-64), BAD), (dict(x=None), BAD), (dict(dt=None), BAD), (dict(a=None), BAD),
     (dict(b=None), BAD), (dict(c=None), BAD), (dict(y=None), BAD), (dict(x=at(1, 8)), BAD), (dict(dt=at(2, 4)), BAD),
     (dict(b=at(4, 2)), BAD), (dict(skip=at(6, 4)), BAD), (dict(y=at(1)), BAD), (dict(y=at(2)), BAD), (dict(y=at(9)), BAD),
     (dict(y=at(4, 64)), BAD), (dict(H=1 << 20, x_stride=1 << 26, G=1, b_stride=32, c_stride=32, num_seqs=1 << 12), BAD),
@@ -153,6 +153,8 @@ def test_ssm_workspace_covers_smaller_calls():
     (dict(eps=NAN), BAD), (dict(eps=INF), BAD), (dict(x_stride=255), BAD), (dict(gate_stride=0), BAD), (dict(x=None), BAD),
     (dict(weight=None), BAD), (dict(y=None), BAD), (dict(x=at(1, 2)), BAD), (dict(gate=at(2, 8)), BAD),
     (dict(weight=at(3, 4)), BAD), (dict(y=at(1)), BAD), (dict(y=at(2, 32)), BAD), (dict(y=at(3)), BAD),
+    (dict(T=1 << 22, H=1, D=16384, x_stride=16384, gate_stride=16384, per_head=1, weight=at(1 << 8), gate=at(1 << 9),
+          y=at(1 << 10)), BAD),                            # 2^32 threads
     (dict(T=0, x=None, y=None), OK),
 ])
 def test_gated_norm_refuses(bad, status):
@@ -166,6 +168,7 @@ def test_gated_norm_refuses(bad, status):
     (dict(gate=at(3, 4)), BAD), (dict(post=at(5, 4)), BAD), (dict(scale=at(6, 4)), BAD), (dict(out=at(7, 4)), BAD),
     (dict(y=at(1)), BAD), (dict(y=at(2)), BAD), (dict(out=at(8)), BAD), (dict(out=at(2, 16)), BAD), (dict(out=at(1)), BAD),
     (dict(out=at(5)), BAD), (dict(T=0, x=None, y=None), OK),
+    (dict(T=1 << 22, C=16384, x=at(1 << 8), residual=at(1 << 9), gate=None, out=at(1 << 10), y=at(1 << 11)), BAD),
 ])
 def test_residual_norm_refuses(bad, status):
     assert residual(**bad) == status
