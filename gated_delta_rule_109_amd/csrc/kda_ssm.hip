@@ -3,15 +3,14 @@
 //
 //   S_t = exp(d_t a) S_{t-1} + d_t b_t x_t^T,   y_t = S_t^T c_t + skip x_t
 //
-// One decay per head and token; S is N x P in fp32. fp32 tensors run token by
-// token, bf16 tensors in chunks on the matrix cores.
+// One decay per head and token; S is N x P in fp32. Prompts run in chunks on the
+// matrix cores.
 #include "kda_pack.h"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kColumns = 64;   // columns of a head one workgroup of the token kernel owns
 
 // Segments. A call with few sequences, heads and columns cuts its sequences
 // every segment_len tokens, and the segments run side by side in three launches:
@@ -30,10 +29,10 @@ struct Split {
   int target;      // workgroups that the segments of a call make up
   int shortest;    // tokens of the shortest segment
 };
-constexpr Split kTokenSplit = {kColumns, 1024, 128};
+constexpr Split kFullSplit = {64, 512, 128};         // fp32
 // (the chunks' workgroups have 8 waves where a head has more than 64 columns, else 4)
 constexpr Split kChunkSplit = {64, 512, 256}, kWideSplit = {128, 512, 256};
-const Split& split_of(bool bf16, int P) { return !bf16 ? kTokenSplit : P <= 64 ? kChunkSplit : kWideSplit; }
+const Split& split_of(bool bf16, int P) { return !bf16 ? kFullSplit : P <= 64 ? kChunkSplit : kWideSplit; }
 int column_blocks(const Split& s, int P) { return (P + s.columns - 1) / s.columns; }
 
 int segment_len(const Packed& s, int H, int P, const Split& sp) {
@@ -71,102 +70,6 @@ __device__ __forceinline__ size_t entry_of(const SsmParams& a, const Part& p, in
 __device__ __forceinline__ f32x4* front_of(const SsmParams& a, const Part& p, int h, int j, int pblocks, int pb,
                                            int vecs) {
   return (f32x4*)a.ends + (entry_of(a, p, h, j) * pblocks + pb) * (size_t)vecs;
-}
-
-// ---- fp32: token by token ---------------------------------------------------------------
-//
-// A workgroup owns kColumns columns of one head: wave w
-// the 16 columns 16 w .., lane l column l % 16 and the N / 4 rows
-// 16 i + 4 (l / 16) + 0..3. Tokens are staged kStage at a time.
-constexpr int kStage = 16;
-
-template <int N, bool outputs>
-__global__ __launch_bounds__(kThreads) void ssm_token_kernel(SsmParams a) {
-  const int pblocks = (a.P + kColumns - 1) / kColumns;
-  const int pb = blockIdx.x % pblocks, h = blockIdx.x / pblocks % a.H;
-  Part p;
-  if (!find_part(a.seqs, a.len, blockIdx.x / pblocks / a.H, p)) return;
-  const bool last = p.j == p.parts - 1;
-  if (!outputs && last) return;
-  const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave, q = lane / 16;
-  const int col = pb * kColumns + wave * 16 + lane % 16;
-  const bool live = pb * kColumns + wave * 16 < a.P;    // (P is a multiple of 16)
-  const int grp = h / (a.H / a.G);
-  constexpr int R = N / 16;
-  f32x4 s[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i) s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const size_t state = ((size_t)p.n * a.H + h) * N * a.P + col;
-  auto front = [&](int j) { return front_of(a, p, h, j, pblocks, pb, R * kThreads) + tid; };
-  if (live) {
-    if (outputs && (p.j > 0 || (p.parts > 1 && a.keep))) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) s[i] = front(p.j)[i * kThreads];
-    } else if (p.j == 0 && a.initial_state) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][e] = a.initial_state[state + (size_t)(16 * i + 4 * q + e) * a.P];
-        if (!outputs && a.keep) front(0)[i * kThreads] = s[i];
-      }
-    }
-  }
-  __shared__ float sb[kStage][N], sc[kStage][N], sx[kStage][kColumns], sf[kStage], sd[kStage];
-  const float av = a.a[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, skip = a.skip ? a.skip[h] : 0.f;
-  double sum = 0.0;
-  for (int t0 = 0; t0 < p.count; t0 += kStage) {
-    const int m = min(kStage, p.count - t0);
-    const int64_t tok = p.first + t0;
-    __syncthreads();
-    for (int e = tid; e < m * N; e += kThreads) {
-      const int t = e / N, i = e % N;
-      sb[t][i] = Elem<float>::load((const float*)a.b + (tok + t) * a.b_stride + grp * N + i);
-      sc[t][i] = Elem<float>::load((const float*)a.c + (tok + t) * a.c_stride + grp * N + i);
-    }
-    for (int e = tid; e < m * kColumns; e += kThreads) {
-      const int t = e / kColumns, i = pb * kColumns + e % kColumns;
-      if (i < a.P) sx[t][e % kColumns] = Elem<float>::load((const float*)a.x + (tok + t) * a.x_stride + (int64_t)h * a.P + i);
-    }
-    if (tid < m) {
-      const float d = step_size(a.dt[(tok + tid) * a.H + h], bias, a.softplus);
-      sd[tid] = d;
-      sf[tid] = expf(d * av);
-      sum += (double)d * av;
-    }
-    __syncthreads();
-    if (live) {
-      for (int t = 0; t < m; ++t) {
-        const float xv = sx[t][wave * 16 + lane % 16], f = sf[t], dx = sd[t] * xv;
-        float o = 0.f;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const f32x4 b = *(const f32x4*)&sb[t][16 * i + 4 * q], c = *(const f32x4*)&sc[t][16 * i + 4 * q];
-          s[i] = f * s[i] + b * dx;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o += s[i][e] * c[e];
-        }
-        if (outputs) {
-          o += lane_xor<16>(o);
-          o += lane_xor<32>(o);
-          if (q == 0) Elem<float>::store((float*)a.y + ((size_t)(tok + t) * a.H + h) * a.P + col, a.skip ? o + skip * xv : o);
-        }
-      }
-    }
-  }
-  if (!outputs) {
-    if (live)
-#pragma unroll
-      for (int i = 0; i < R; ++i) front(p.j + 1)[i * kThreads] = s[i];
-    if (pb == 0 && wave == 0) {
-      for (int m = 1; m < kStage; m *= 2) sum += __shfl_xor(sum, m);
-      if (tid == 0) a.sums[entry_of(a, p, h, p.j)] = sum;
-    }
-  } else if (last && a.final_state && live) {
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) a.final_state[state + (size_t)(16 * i + 4 * q + e) * a.P] = s[i][e];
-  }
 }
 
 // ---- bf16: chunks of 64 tokens on the matrix cores --------------------------------------
@@ -254,13 +157,37 @@ __device__ __forceinline__ void split3(f32x4 x, bf16x4& h, bf16x4& m, bf16x4& l)
 }
 
 // What the tokens of a chunk need of d and a.
+template <int L>
 struct Decays {
-  float hi[kL], lo[kL];   // c_t log2 e
-  float d[kL];            // d_t
-  float e[kL];            // e^{c_t}
-  float w[kL];            // e^{c_L - c_t} d_t
-  float total;            // e^{c_L}
+  float hi[L], lo[L];   // c_t log2 e
+  float d[L];           // d_t
+  float e[L];           // e^{c_t}
+  float w[L];           // e^{c_L - c_t} d_t
+  float total;          // e^{c_L}
 };
+// A wave's 64 tokens, one a lane (at: the lane): the decays of 64 / L chunks, with
+// the sums of the logarithms c = d a in fp64. Returns the last chunk's c_L in every
+// lane of it.
+template <int L>
+__device__ __forceinline__ double make_decays(float d, float a, int at, Decays<L>* dec) {
+  double c = (double)d * a;
+#pragma unroll
+  for (int m = 1; m < L; m *= 2) {
+    const double o = lane_value(c, at - m);
+    if (at % L >= m) c += o;
+  }
+  const double end = lane_value(c, at | (L - 1));
+  constexpr double kL2 = 1.4426950408889634;
+  const float hi = (float)(c * kL2);
+  Decays<L>& q = dec[at / L];
+  q.hi[at % L] = hi;
+  q.lo[at % L] = (float)(c * kL2 - hi);
+  q.d[at % L] = d;
+  q.e[at % L] = __builtin_amdgcn_exp2f(hi);
+  q.w[at % L] = __builtin_amdgcn_exp2f((float)((end - c) * kL2)) * d;
+  if (at % L == 0) q.total = __builtin_amdgcn_exp2f((float)(end * kL2));
+  return end;
+}
 
 template <int N, int W, bool outputs>
 __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_kernel(SsmParams a) {
@@ -283,7 +210,7 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
 
   constexpr int kB = kL * NP, kM = 2 * kL * kL;
   __shared__ __attribute__((aligned(16))) bf16_bits sC[kL * NP], sBM[kB > kM ? kB : kM], sBT[N * kL], sXT[kCols * kL];
-  __shared__ Decays dec[4];
+  __shared__ Decays<kL> dec[4];
   bf16_bits *sB = sBM, *sMh = sBM, *sMl = sBM + kL * kL;  // (M overwrites B once it is used)
 
   // ---- state in front of the segment
@@ -416,25 +343,10 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
   };
   auto decays = [&](int t0) __attribute__((always_inline)) {
     if (uwave >= 4 || t0 + kL * uwave >= p.count) return;
-    Decays& q = dec[uwave];
-    const int t = fresh(threadIdx.x), at = t & (kWave - 1);
-    const float d = t0 + t < p.count ? step_size(rdt, bias, a.softplus) : 0.f;
-    double c = (double)d * av;
-#pragma unroll
-    for (int m = 1; m < kL; m *= 2) {
-      const double o = lane_value(c, at - m);
-      if (at >= m) c += o;
-    }
-    const double end = lane_value(c, kL - 1);
+    const uint32_t t = fresh(threadIdx.x);
+    const float d = t0 + (int)t < p.count ? step_size(rdt, bias, a.softplus) : 0.f;
+    const double end = make_decays<kL>(d, av, t % kWave, dec + uwave);
     if (!outputs) sum += end;
-    constexpr double kL2 = 1.4426950408889634;
-    const float hi = (float)(c * kL2);
-    q.hi[at] = hi;
-    q.lo[at] = (float)(c * kL2 - hi);
-    q.d[at] = d;
-    q.e[at] = __builtin_amdgcn_exp2f(hi);
-    q.w[at] = __builtin_amdgcn_exp2f((float)((end - c) * kL2)) * d;
-    if (at == 0) q.total = __builtin_amdgcn_exp2f((float)(end * kL2));
   };
 
   // (as the loads: a scalar base, and a row of H P <= KDA_SSM_MAX_STRIDE elements a lane)
@@ -447,7 +359,7 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
   }
 #pragma unroll 1
   for (int t0 = 0; t0 < p.count; t0 += kL) {
-    const Decays& q = dec[t0 / kL & 3];
+    const Decays<kL>& q = dec[t0 / kL & 3];
     if ((t0 / kL & 3) == 0) {
       decays(t0);
       load_dt(t0 + 4 * kL);
@@ -630,6 +542,282 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
   }
 }
 
+// ---- fp32: chunks of 32 tokens on the matrix cores --------------------------------------
+//
+// The same, with products of fp32 (16 x 16 x 4): no factor is split. 64 columns a
+// workgroup, 16 a wave. As operand a lane holds 4 values along the sum, each for
+// one of four products: the accumulators of a tile are that operand as they are
+// (rows 16 k + 4 g + i, i the product), and 4 channels or tokens are one read.
+// Layouts as above, with blocks of 4 fp32.
+constexpr int kL32 = 32;
+
+__device__ __forceinline__ f32x4 mfma4(f32x4 a, f32x4 b, f32x4 c) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+  return c;
+}
+
+template <int N, bool outputs>
+__global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk32_kernel(SsmParams a) {
+  constexpr int kThreads = 256, kCols = 64, L = kL32, NT = N / 16, NV = N / 4;
+  const int pblocks = (a.P + kCols - 1) / kCols;
+  const int share = a.H / a.G * pblocks;
+  const int id = (blockIdx.x / (kDies * share) * kDies + blockIdx.x % kDies) * share + blockIdx.x / kDies % share;
+  const int pb = id % pblocks, h = id / pblocks % a.H;
+  Part p;
+  if (!find_part(a.seqs, a.len, id / pblocks / a.H, p)) return;
+  const bool last = p.j == p.parts - 1;
+  if (!outputs && last) return;
+  const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave, g = lane / 16, l16 = lane % 16;
+  const int wcol = wave * 16, col0 = pb * kCols, grp = h / (a.H / a.G);
+  const int uwave = __builtin_amdgcn_readfirstlane(wave);
+  const float av = a.a[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, skip = a.skip ? a.skip[h] : 0.f;
+
+  constexpr int kB = L * N, kM = L * L;
+  __shared__ __attribute__((aligned(16))) float sC[L * N], sBM[kB > kM ? kB : kM], sBT[N * L], sXT[kCols * L];
+  __shared__ Decays<L> dec[8];
+  float *sB = sBM, *sM = sBM;                            // (M overwrites B once it is used)
+
+  f32x4 s[NT];
+  auto front = [&](int j) { return front_of(a, p, h, j, pblocks, pb, NT * kThreads) + tid; };
+  const size_t state = ((size_t)p.n * a.H + h) * N * a.P + col0 + wcol + l16;
+  const bool live = col0 + wcol < a.P;                   // (P is a multiple of 16)
+  if (outputs && (p.j > 0 || (p.parts > 1 && a.keep))) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k) s[k] = front(p.j)[k * kThreads];
+  } else if (p.j == 0 && a.initial_state && live) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[k][i] = a.initial_state[state + (size_t)(16 * k + 4 * g + i) * a.P];
+  } else {
+#pragma unroll
+    for (int k = 0; k < NT; ++k) s[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  if (!outputs && p.j == 0 && a.keep)
+#pragma unroll
+    for (int k = 0; k < NT; ++k) front(0)[k * kThreads] = s[k];
+
+  // Runs of 4 tokens by 4 columns of x (128) and B (8 N / 4), rows of C.
+  constexpr int kXRuns = 16 * 8, kRuns = kXRuns + NV * 8, UR = (kRuns + kThreads - 1) / kThreads;
+  constexpr int kCUnits = L * NV, UC = (kCUnits + kThreads - 1) / kThreads;
+  f32x4 rr[UR][4], rc[UC];
+  const char* gx = (const char*)((const float*)a.x + p.first * a.x_stride + (int64_t)h * a.P + col0);
+  const char* gb = (const char*)((const float*)a.b + p.first * a.b_stride + grp * N);
+  const char* gc = (const char*)((const float*)a.c + p.first * a.c_stride + grp * N);
+  const int64_t xs = 4 * a.x_stride, bs = 4 * a.b_stride, cs = 4 * a.c_stride;
+  auto of_x = [&](int k) { return uwave * kWave + k * kThreads < kXRuns; };
+  // (run i: columns 4 (i % 4 + 4 (i / 32)), tokens 4 (i / 4 % 8))
+  auto run_col = [&](int k, uint32_t t) -> int {
+    const uint32_t i = t + k * kThreads - (of_x(k) ? 0 : kXRuns);
+    return i % 4 + 4 * (i / 32);
+  };
+  auto run_tok = [&](uint32_t t) -> int { return t / 4 % 8; };
+  uint32_t first[UR], off[UR];
+#pragma unroll
+  for (int k = 0; k < UR; ++k) {
+    const int cv = run_col(k, tid);
+    first[k] = (of_x(k) ? col0 + 4 * cv < a.P : tid + k * kThreads < kRuns) ? 16 * cv : 0;
+    off[k] = 4 * run_tok(tid) * (uint32_t)(of_x(k) ? xs : bs) + first[k];
+  }
+  const uint32_t coff = tid / NV * (uint32_t)cs + tid % NV * 16;
+  auto load = [&](int t0) __attribute__((always_inline)) {
+    const uint32_t rows = min(p.count - t0, L) - 1;
+#pragma unroll
+    for (int k = 0; k < UR; ++k) {
+      const char* base = of_x(k) ? gx : gb;
+      const uint32_t step = (uint32_t)(of_x(k) ? xs : bs), most = first[k] + rows * step;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) rr[k][r] = *(const f32x4*)(base + min(off[k] + r * step, most));
+    }
+    if (outputs) {
+      const uint32_t most = tid % NV * 16 + rows * (uint32_t)cs;
+#pragma unroll
+      for (int k = 0; k < UC; ++k)
+        rc[k] = *(const f32x4*)(gc + min(coff + k * (kThreads / NV) * (uint32_t)cs, most));
+    }
+    gx += L * xs;
+    gb += L * bs;
+    gc += L * cs;
+  };
+  // (masks of rows by their bytes: a row of 2 N bf16 is one of N fp32)
+  auto store = [&]() __attribute__((always_inline)) {
+    const uint32_t t = fresh(threadIdx.x);
+#pragma unroll
+    for (int k = 0; k < UR; ++k) {
+      if (kRuns % kThreads != 0 && t + k * kThreads >= kRuns) continue;
+      const int cv = run_col(k, t), sr = run_tok(t);
+      float* dst = of_x(k) ? sXT : sBT;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {                      // column 4 cv + c: row 4 (cv & 3) + c of its tile
+        const int l = 4 * (cv & 3) + c;
+        *(f32x4*)(dst + (16 * (cv / 4) + (l ^ (cv / 4 & 1))) * L + (sr ^ l >> 1) * 4) =
+            f32x4{rr[k][0][c], rr[k][1][c], rr[k][2][c], rr[k][3][c]};
+      }
+      if (outputs && !of_x(k))
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *(f32x4*)(sB + (4 * sr + r) * N + (cv ^ channel_mask<2 * N>(4 * (sr & 3) + r)) * 4) = rr[k][r];
+    }
+    if (outputs)
+#pragma unroll
+      for (int k = 0; k < UC; ++k) {
+        const int row = t / NV + k * (kThreads / NV);
+        if (kCUnits % kThreads == 0 || t + k * kThreads < kCUnits)
+          *(f32x4*)(sC + row * N + (t % NV ^ channel_mask<2 * N>(row % 16)) * 4) = rc[k];
+      }
+  };
+  const int token_read[2] = {l16 * L + (g ^ l16 >> 1) * 4, (l16 ^ 1) * L + (g ^ l16 >> 1) * 4};
+  const int channel_read = l16 * N + (g ^ channel_mask<2 * N>(l16)) * 4;
+
+  // Wave w, lane t: what becomes of dt in the 2 w-th and next of the next eight chunks.
+  float rdt = 0.f;
+  double sum = 0.0;
+  auto load_dt = [&](int t0) __attribute__((always_inline)) {
+    const int t = t0 + tid;
+    rdt = t < p.count ? a.dt[(size_t)(p.first + t) * a.H + h] : 0.f;
+  };
+  auto decays = [&](int t0) __attribute__((always_inline)) {
+    if (t0 + 2 * L * uwave >= p.count) return;
+    const uint32_t t = fresh(threadIdx.x);
+    const float d = t0 + (int)t < p.count ? step_size(rdt, bias, a.softplus) : 0.f;
+    const double end = make_decays<L>(d, av, t % kWave, dec + 2 * uwave);
+    if (!outputs) sum += end;                            // (a lane: of its half of the wave)
+  };
+
+  const int64_t yrow = 4 * (int64_t)a.H * a.P;
+  char* gy = (char*)((float*)a.y + ((size_t)p.first * a.H + h) * a.P + col0);
+  load_dt(0);
+  if (p.count > 0) load(0);
+#pragma unroll 1
+  for (int t0 = 0; t0 < p.count; t0 += L) {
+    const Decays<L>& q = dec[t0 / L & 7];
+    if ((t0 / L & 7) == 0) {
+      decays(t0);
+      load_dt(t0 + 8 * L);
+    }
+    store();
+    lds_barrier();
+    if (t0 + L < p.count) load(t0 + L);
+    if (outputs) {
+      // ---- M: tiles (tt, u) = (0, 0), (1, 0), (1, 1), a wave each
+      const int tt = uwave > 0, u = uwave == 2;
+      f32x4 m = {0.f, 0.f, 0.f, 0.f};
+      const int cr = fresh(channel_read);
+      if (uwave < 3) {
+        const int t = 16 * tt + l16;
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+          m = mfma4(*(const f32x4*)(sB + (cr ^ 16 * k) + 16 * u * N), *(const f32x4*)(sC + (cr ^ 16 * k) + 16 * tt * N), m);
+        const float thi = q.hi[t], tlo = q.lo[t];
+        const f32x4 shi = *(const f32x4*)&q.hi[16 * u + 4 * g], slo = *(const f32x4*)&q.lo[16 * u + 4 * g],
+                    sd = *(const f32x4*)&q.d[16 * u + 4 * g];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] *= __builtin_amdgcn_exp2f((thi - shi[i]) + (tlo - slo[i])) * sd[i];
+        if (u == tt) {
+          const int at = fresh(l16) - 4 * g;             // the diagonal's place among the lane's 4
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float v = i == at ? m[i] + skip : m[i];
+            m[i] = i <= at ? v : 0.f;
+          }
+        }
+      }
+      lds_barrier();                                     // B is used
+      if (uwave < 3) *(f32x4*)(sM + 16 * tt * L + (token_read[0] ^ 16 * u)) = m;
+      lds_barrier();
+    }
+    auto x_operand = [&](int u) __attribute__((always_inline)) {
+      return *(const f32x4*)(sXT + (fresh(token_read[uwave & 1]) ^ 16 * u) + uwave * 16 * L);
+    };
+    f32x4 xo[2] = {x_operand(0), x_operand(1)};
+    if (outputs) {
+      f32x4 y[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      const int cr = fresh(channel_read);
+#pragma unroll
+      for (int k = 0; k < NT; ++k)
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) y[tt] = mfma4(s[k], *(const f32x4*)(sC + (cr ^ 16 * k) + 16 * tt * N), y[tt]);
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) y[tt] *= q.e[16 * tt + l16];
+      // (values that are not finite: as above)
+      bool bad = false;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bad |= !(fabsf(xo[u][i]) < __builtin_inff());
+      const bool any_bad = __any(bad);
+      int from = L;
+      if (any_bad) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(fabsf(xo[u][i]) < __builtin_inff())) {
+              xo[u][i] = 0.f;
+              from = min(from, 16 * u + 4 * g + i);
+            }
+        from = min(from, __shfl_xor(from, 16));
+        from = min(from, __shfl_xor(from, 32));
+      }
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int u = 0; u <= tt; ++u)
+          y[tt] = mfma4(xo[u], *(const f32x4*)(sM + 16 * tt * L + (token_read[0] ^ 16 * u)), y[tt]);
+      if (any_bad) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int first_bad = __shfl(from, 4 * g + i);
+#pragma unroll
+          for (int tt = 0; tt < 2; ++tt)
+            if (16 * tt + l16 >= first_bad) y[tt][i] = __builtin_nanf("");
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) xo[u] = x_operand(u);
+      }
+      if (live) {
+        const int left = p.count - t0 - l16;
+        const uint32_t yoff = l16 * (uint32_t)yrow + 4 * (16 * uwave + 4 * g);
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+          if (16 * tt < left) *(f32x4*)(gy + 16 * tt * yrow + yoff) = y[tt];
+      }
+      gy += L * yrow;
+    }
+    const float total = q.total;
+#pragma unroll
+    for (int k = 0; k < NT; ++k) s[k] *= total;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const f32x4 xw = xo[u] * *(const f32x4*)&q.w[16 * u + 4 * g];
+#pragma unroll
+      for (int k = 0; k < NT; ++k)
+        s[k] = mfma4(*(const f32x4*)(sBT + (token_read[k & 1] ^ 16 * u) + 16 * k * L), xw, s[k]);
+    }
+    lds_barrier();                                       // the chunk is used
+  }
+
+  if (!outputs) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k) front(p.j + 1)[k * kThreads] = s[k];
+    if (pb == 0) {
+      __shared__ double part[8];
+      if (lane % L == 0) part[tid / L] = sum;
+      __syncthreads();
+      if (tid == 0) {
+        for (int i = 1; i < 8; ++i) sum += part[i];
+        a.sums[entry_of(a, p, h, p.j)] = sum;
+      }
+    }
+  } else if (last && a.final_state && live) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a.final_state[state + (size_t)(16 * k + 4 * g + i) * a.P] = s[k][i];
+  }
+}
+
 // The states in front of the segments of one sequence (a block per 256 vectors of
 // them and per multiple of len, where at most one sequence of several segments
 // starts). vecs: vectors of a head's state.
@@ -762,7 +950,7 @@ hipError_t launch_passes(K states, K outputs, const SsmArgs& a, const Split& sp,
 template <int N>
 hipError_t launch_n(const SsmArgs& a) {
   const Split& sp = split_of(a.bf16, a.P);
-  if (!a.bf16) return launch_passes(ssm_token_kernel<N, false>, ssm_token_kernel<N, true>, a, sp, kThreads);
+  if (!a.bf16) return launch_passes(ssm_chunk32_kernel<N, false>, ssm_chunk32_kernel<N, true>, a, sp, 4 * sp.columns);
   return a.P <= 64 ? launch_passes(ssm_chunk_kernel<N, 4, false>, ssm_chunk_kernel<N, 4, true>, a, sp, 4 * sp.columns) : launch_passes(ssm_chunk_kernel<N, 8, false>, ssm_chunk_kernel<N, 8, true>, a, sp, 4 * sp.columns);
 }
 
@@ -776,7 +964,7 @@ size_t workspace_of(int32_t T, int32_t H, int32_t N, int32_t P, const Split& sp)
 
 int64_t ssm_threads(const SsmArgs& a) {
   const Split& sp = split_of(a.bf16, a.P);
-  return launch_groups(a, sp) * (a.bf16 ? 4 * sp.columns : kThreads);
+  return launch_groups(a, sp) * 4 * sp.columns;
 }
 
 // At most 2 target / (H column blocks) entries, and at most two per `shortest`
@@ -785,7 +973,7 @@ int64_t ssm_threads(const SsmArgs& a) {
 size_t ssm_workspace(int32_t num_seqs, int32_t T, int32_t H, int32_t N, int32_t P) {
   (void)num_seqs;
   size_t most = 0;
-  for (const Split* sp : {&kTokenSplit, &kChunkSplit, &kWideSplit}) {
+  for (const Split* sp : {&kFullSplit, &kChunkSplit, &kWideSplit}) {
     if (sp == &kWideSplit && P <= 64) continue;
     const size_t w = workspace_of(T, H, N, P, *sp);
     most = w > most ? w : most;

@@ -584,9 +584,9 @@ kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, c
  *      b and c are multiples of 16 bytes, at most KDA_SSM_MAX_STRIDE elements
  * bf16 tensors run in chunks of KDA_SSM_CHUNK tokens on the matrix cores: b, c
  * and x are exact there, every fp32 factor is carried in two bf16 terms for
- * outputs (2^-16 of each product) and three for states (2^-24); the decays
- * between two tokens come from sums in fp64. fp32 tensors run token by token
- * in fp32. Values that are not finite in x, b or dt make outputs non-finite from
+ * outputs (2^-16 of each product) and three for states (2^-24). fp32 tensors run
+ * in chunks of half that length with products of fp32. The decays between two
+ * tokens come from sums in fp64. Values that are not finite in x, b or dt make outputs non-finite from
  * their token on (of a value in x: in its column), as the recurrence does, and
  * no outputs before; a c that is not finite, those of its token.
  *   workspace  256-byte aligned device scratch of kda_ssm_workspace_size(num_seqs,
