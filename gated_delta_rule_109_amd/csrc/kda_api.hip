@@ -601,7 +601,7 @@ kda_status kda_conv_prefill(const void* x, int64_t x_stride, const float* weight
   a.seqs = packed(cu_seqlens, num_seqs, T);
   a.N = 0;
   a.initial_state = initial_state; a.final_state = final_state;
-  if (kda::conv_threads(a, false) > kda::kMaxThreads) return KDA_ERR_INVALID_ARG;
+  if (kda::conv_threads(a) > kda::kMaxThreads) return KDA_ERR_INVALID_ARG;
   const size_t e = elem(dt), state = (size_t)num_seqs * (width - 1) * C;
   const Span initial = initial_state == final_state ? Span{nullptr, 0} : flat(initial_state, state, e);
   if (!apart({rows(y, T, C, C, e), flat(final_state, state, e)},
@@ -623,7 +623,6 @@ kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, c
   a.seqs = packed(nullptr, 1, 0);
   a.N = N;
   a.initial_state = state; a.final_state = state;
-  if (kda::conv_threads(a, true) > kda::kMaxThreads) return KDA_ERR_INVALID_ARG;
   const size_t e = elem(dt);
   if (!apart({rows(y, N, C, C, e), flat(state, (size_t)N * (width - 1) * C, e)},
              {rows(x, N, x_stride, C, e), flat(weight, (size_t)C * width, 4), flat(bias, C, 4)}))
@@ -729,7 +728,6 @@ kda_status kda_residual_norm(const void* x, const void* residual, const void* ga
   a.residual_out = residual_out; a.y = y;
   a.bf16 = dt == KDA_BF16;
   a.stream = stream;
-  if (kda::residual_threads(a) > kda::kMaxThreads) return KDA_ERR_INVALID_ARG;
   return from_hip(kda::launch_residual_norm(a));
 }
 

@@ -210,10 +210,9 @@ hipError_t launch_residual_norm(const ResidualNormArgs& a);
 
 // Threads of a call's largest launch: fewer than 2^32.
 constexpr int64_t kMaxThreads = (1ll << 32) - 1;
-int64_t conv_threads(const ConvArgs& a, bool step);
+int64_t conv_threads(const ConvArgs& a);   // (a step takes a bounded number)
 int64_t ssm_threads(const SsmArgs& a);
 int64_t gated_threads(const GatedNormArgs& a);
-int64_t residual_threads(const ResidualNormArgs& a);
 
 // Workspace of a scan (bytes; sizes validated).
 size_t ssm_workspace(int32_t num_seqs, int32_t T, int32_t H, int32_t N, int32_t P);

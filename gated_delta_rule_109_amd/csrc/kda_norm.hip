@@ -9,36 +9,44 @@
 namespace kda {
 namespace {
 
-// Sum over the L threads of a row (every one of them gets it).
+// Sum over the L threads of a row (every one of them gets it). Rows of more than a
+// wave: by way of LDS, in one of two places by turns (`turn`, the same for all), so
+// that one barrier a sum is enough: a place is written again after the barrier of
+// the sum between, which all of its readers have passed.
 template <int L>
-__device__ __forceinline__ float row_sum(float x) {
+__device__ __forceinline__ float row_sum(float x, int& turn) {
   static_for<0, 6>([&](auto B) __attribute__((always_inline)) {
     constexpr int m = 1 << decltype(B)::value;
     if constexpr (m < L) x += lane_xor<m>(x);
   });
   if constexpr (L > kWave) {
-    __shared__ float part[L / kWave];
-    __syncthreads();   // (an earlier sum's readers are done)
-    if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = x;
-    __syncthreads();
+    __shared__ float part[2][L / kWave];
+    float* p = part[turn];
+    turn ^= 1;
+    if (threadIdx.x % kWave == 0) p[threadIdx.x / kWave] = x;
+    lds_barrier();
     x = 0.f;
 #pragma unroll
-    for (int i = 0; i < L / kWave; ++i) x += part[i];
+    for (int i = 0; i < L / kWave; ++i) x += p[i];
   }
   return x;
 }
 
-template <int L> constexpr int threads_of() { return L > 256 ? L : 256; }
+// Most threads of a residual norm: four waves a SIMD.
+constexpr int64_t kResidualThreads = 256 * 4 * 4 * 64;
+
+// (a row of more than a wave has a workgroup to itself)
+template <int L> constexpr int threads_of() { return L > kWave ? L : 256; }
 
 // 1 / sqrt(mean of squares + eps) of a row whose threads hold v.
 template <int L, int I, int V>
-__device__ __forceinline__ float inv_rms(const float (&v)[I][V], int D, float eps) {
+__device__ __forceinline__ float inv_rms(const float (&v)[I][V], int D, float eps, int& turn) {
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < I; ++i)
 #pragma unroll
     for (int e = 0; e < V; ++e) s += v[i][e] * v[i][e];
-  return 1.0f / sqrtf(row_sum<L>(s) / (float)D + eps);
+  return rsqrtf(row_sum<L>(s, turn) * (1.0f / (float)D) + eps);
 }
 
 template <typename T, int V, int L, int I>
@@ -61,9 +69,9 @@ __global__ __launch_bounds__(threads_of<L>()) void gated_norm_kernel(const T* x,
 #pragma unroll
     for (int e = 0; e < V; ++e) v[i][e] = 0.f, g[i][e] = 1.f;
     if (live && d < D) {
-      load_vec<T, V>(px + d, v[i]);
+      from_bits<T, V>(load_first<T, V>(px + d, D - d), v[i]);
       if (pg) {
-        load_vec<T, V>(pg + d, g[i]);
+        from_bits<T, V>(load_first<T, V>(pg + d, D - d), g[i]);
 #pragma unroll
         for (int e = 0; e < V; ++e) g[i][e] = activate<T>(g[i][e], act);
       }
@@ -73,7 +81,8 @@ __global__ __launch_bounds__(threads_of<L>()) void gated_norm_kernel(const T* x,
       for (int e = 0; e < V; ++e) v[i][e] *= g[i][e], g[i][e] = 1.f;
     }
   }
-  const float s = inv_rms<L, I, V>(v, D, eps);
+  int turn = 0;
+  const float s = inv_rms<L, I, V>(v, D, eps, turn);
   if (!live) return;
   const float* w = weight + (per_head ? (int64_t)h * D : 0);
   T* py = y + r * D;
@@ -82,69 +91,91 @@ __global__ __launch_bounds__(threads_of<L>()) void gated_norm_kernel(const T* x,
     const int d = (lane + i * L) * V;
     if (d < D) {
       float o[V];
+      load_params<V>(w + d, D - d, 0.f, o);
 #pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = v[i][e] * s * w[d + e] * g[i][e];
-      store_vec<T, V>(py + d, o);
+      for (int e = 0; e < V; ++e) o[e] *= v[i][e] * s * g[i][e];
+      store_first<T, V>(py + d, to_bits<T, V>(o), D - d);
     }
   }
 }
 
+// A workgroup takes rows `step` apart, with its columns' weights in registers for
+// all of them (they are fp32: a row's weights are more bytes than the row) and the
+// next row's loads on their way while it works on one.
 template <typename T, int V, int L, int I>
 __global__ __launch_bounds__(threads_of<L>()) void residual_norm_kernel(const T* x, const T* residual, const T* gate,
                                                                         const float* weight, const float* post,
-                                                                        const float* scale, int64_t rows, int C,
-                                                                        int act, float alpha, float eps,
+                                                                        const float* scale, int64_t rows, int64_t step,
+                                                                        int C, int act, float alpha, float eps,
                                                                         T* residual_out, T* y) {
   const int lane = threadIdx.x % L;
-  const int64_t r = (int64_t)blockIdx.x * (threads_of<L>() / L) + threadIdx.x / L;
-  const bool live = r < rows;
-  const int64_t base = live ? r * C : 0;
-  float v[I][V], res[I][V];
+  const int64_t r0 = (int64_t)blockIdx.x * (threads_of<L>() / L);
+  float w[I][V], pw[I][V], k[I][V];
+  bits_t<T, V> nx[I] = {}, nr[I] = {}, ng[I] = {};
+  auto left = [&](int i) { return C - (lane + i * L) * V; };   // columns from a vector's first one on
+  // (threads without a row stay for the sums of their wave)
+  auto load = [&](int64_t r) __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < I; ++i) {
-    const int c = (lane + i * L) * V;
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[i][e] = 0.f, res[i][e] = 0.f;
-    if (live && c < C) {
-      load_vec<T, V>(x + base + c, v[i]);
-      if (residual) load_vec<T, V>(residual + base + c, res[i]);
-    }
-  }
-  const float s = post ? inv_rms<L, I, V>(v, C, eps) : 1.f;
-#pragma unroll
-  for (int i = 0; i < I; ++i) {
-    const int c = (lane + i * L) * V;
-    if (live && c < C) {
-      float g[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) g[e] = 1.f;
-      if (gate) {
-        load_vec<T, V>(gate + base + c, g);
-#pragma unroll
-        for (int e = 0; e < V; ++e) g[e] = activate<T>(g[e], act);
+    for (int i = 0; i < I; ++i)
+      if (r < rows && left(i) > 0) {
+        const int64_t at = r * C + (lane + i * L) * V;
+        nx[i] = load_first<T, V>(x + at, left(i));
+        if (residual) nr[i] = load_first<T, V>(residual + at, left(i));
+        if (gate) ng[i] = load_first<T, V>(gate + at, left(i));
       }
+  };
+  load(r0 + threadIdx.x / L);
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    const int c = (lane + i * L) * V;
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[i][e] = 0.f, pw[i][e] = k[i][e] = 1.f;
+    if (left(i) > 0) {
+      load_params<V>(weight + c, left(i), 0.f, w[i]);
+      if (post) load_params<V>(post + c, left(i), 0.f, pw[i]);
+      if (scale) load_params<V>(scale + c, left(i), 0.f, k[i]);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) k[i][e] *= alpha;
+  }
+  const int64_t mine = threadIdx.x / L;
+  int turn = 0;
+  for (int64_t rb = r0; rb < rows; rb += step) {
+    const int64_t r = rb + mine;
+    float v[I][V], res[I][V], g[I][V];
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      from_bits<T, V>(nx[i], v[i]);
+      from_bits<T, V>(nr[i], res[i]);
+      from_bits<T, V>(ng[i], g[i]);
+    }
+    load(r + step);
+    const float s = post ? inv_rms<L, I, V>(v, C, eps, turn) : 1.f;
+#pragma unroll
+    for (int i = 0; i < I; ++i)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         float u = v[i][e];
-        if (post) u = u * s * post[c + e];
-        u *= g[e];
-        if (scale) u *= scale[c + e];
-        v[i][e] = res[i][e] + alpha * u;
+        if (post) u = u * s * pw[i][e];
+        if (gate) u *= activate<T>(g[i][e], act);
+        // (columns behind the row's last: residual and v are 0 there, and s may not be finite)
+        v[i][e] = e < left(i) ? res[i][e] + k[i][e] * u : 0.f;
       }
-      if (residual_out) store_vec<T, V>(residual_out + base + c, v[i]);
-    }
-  }
-  const float q = inv_rms<L, I, V>(v, C, eps);
-  if (!live) return;
+    const bool live = r < rows;
+    if (residual_out)
 #pragma unroll
-  for (int i = 0; i < I; ++i) {
-    const int c = (lane + i * L) * V;
-    if (c < C) {
-      float o[V];
+      for (int i = 0; i < I; ++i)
+        if (live && left(i) > 0)
+          store_first<T, V>(residual_out + r * C + (lane + i * L) * V, to_bits<T, V>(v[i]), left(i));
+    const float q = inv_rms<L, I, V>(v, C, eps, turn);
 #pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = v[i][e] * q * weight[c + e];
-      store_vec<T, V>(y + base + c, o);
-    }
+    for (int i = 0; i < I; ++i)
+      if (live && left(i) > 0) {
+        float o[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = v[i][e] * q * w[i][e];
+        store_first<T, V>(y + r * C + (lane + i * L) * V, to_bits<T, V>(o), left(i));
+      }
   }
 }
 
@@ -158,16 +189,15 @@ void by_length(int n, F&& f) {
   else if (n <= 16) KDA_ROW(16, 1);
   else if (n <= 32) KDA_ROW(32, 1);
   else if (n <= 64) KDA_ROW(64, 1);
-  else if (n <= 128) KDA_ROW(64, 2);
+  else if (n <= 128) KDA_ROW(128, 1);
   else if (n <= 256) KDA_ROW(256, 1);
-  else if (n <= 512) KDA_ROW(256, 2);
-  else if (n <= 1024) KDA_ROW(256, 4);
+  else if (n <= 512) KDA_ROW(512, 1);
+  else if (n <= 1024) KDA_ROW(1024, 1);
   else if (V > 4 || n <= 2048) KDA_ROW(1024, 2);
-  else if (V > 1 || n <= 4096) KDA_ROW(1024, 4);
-  else KDA_ROW(1024, 16);
+  else KDA_ROW(1024, 4);
 #undef KDA_ROW
 }
-static_assert(KDA_NORM_MAX <= 1024 * 2 * 8 && KDA_NORM_MAX <= 1024 * 4 * 4 && KDA_NORM_MAX <= 1024 * 16, "longest rows");
+static_assert(KDA_NORM_MAX <= 1024 * 2 * 8 && KDA_NORM_MAX <= 1024 * 4 * 4, "longest rows");
 
 template <typename T, int V>
 void gated_t(const GatedNormArgs& a) {
@@ -183,52 +213,37 @@ template <typename T, int V>
 void residual_t(const ResidualNormArgs& a) {
   by_length<V>((a.C + V - 1) / V, [&](auto L, auto I) {
     constexpr int l = decltype(L)::value, i = decltype(I)::value, per = threads_of<l>() / l;
-    hipLaunchKernelGGL((residual_norm_kernel<T, V, l, i>), dim3((unsigned)(((int64_t)a.T + per - 1) / per)),
-                       dim3(threads_of<l>()), 0, a.stream, (const T*)a.x, (const T*)a.residual, (const T*)a.gate,
-                       a.weight, a.post_weight, a.scale, (int64_t)a.T, a.C, a.act, a.alpha, a.eps, (T*)a.residual_out,
-                       (T*)a.y);
+    int64_t groups = ((int64_t)a.T + per - 1) / per;
+    const int64_t most = kResidualThreads / threads_of<l>();
+    if (groups > most) groups = most;
+    hipLaunchKernelGGL((residual_norm_kernel<T, V, l, i>), dim3((unsigned)groups), dim3(threads_of<l>()), 0, a.stream,
+                       (const T*)a.x, (const T*)a.residual, (const T*)a.gate, a.weight, a.post_weight, a.scale,
+                       (int64_t)a.T, groups * per, a.C, a.act, a.alpha, a.eps, (T*)a.residual_out, (T*)a.y);
   });
 }
-
-int64_t row_threads(int64_t rows, int n, int v) {
+template <int V>
+int64_t row_threads(int64_t rows, int n) {
   int64_t t = 0;
-  auto f = [&](auto L, auto) { t = (rows + 255) * decltype(L)::value; };
-  if (v == 8) by_length<8>(n, f);
-  else if (v == 4) by_length<4>(n, f);
-  else by_length<1>(n, f);
+  by_length<V>(n, [&](auto L, auto) { t = (rows + 255) * decltype(L)::value; });
   return t;
-}
-int width_of(const GatedNormArgs& a) {
-  const int v = a.bf16 ? 8 : 4;
-  return a.D % v == 0 && a.x_stride % v == 0 && (!a.gate || a.gate_stride % v == 0) ? v : 1;
-}
-int width_of(const ResidualNormArgs& a) {
-  const int v = a.bf16 ? 8 : 4;
-  return a.C % v == 0 ? v : 1;
 }
 
 }  // namespace
 
 int64_t gated_threads(const GatedNormArgs& a) {
-  const int v = width_of(a);
-  return row_threads((int64_t)a.T * a.H, (a.D + v - 1) / v, v);
-}
-int64_t residual_threads(const ResidualNormArgs& a) {
-  const int v = width_of(a);
-  return row_threads(a.T, (a.C + v - 1) / v, v);
+  const int64_t rows = (int64_t)a.T * a.H;
+  return a.bf16 ? row_threads<8>(rows, (a.D + 7) / 8) : row_threads<4>(rows, (a.D + 3) / 4);
 }
 
 hipError_t launch_gated_norm(const GatedNormArgs& a) {
-  const bool vec = width_of(a) > 1;
-  if (a.bf16) vec ? gated_t<bf16_bits, 8>(a) : gated_t<bf16_bits, 1>(a);
-  else vec ? gated_t<float, 4>(a) : gated_t<float, 1>(a);
+  if (a.bf16) gated_t<bf16_bits, 8>(a);
+  else gated_t<float, 4>(a);
   return hipGetLastError();
 }
 
 hipError_t launch_residual_norm(const ResidualNormArgs& a) {
-  const bool vec = width_of(a) > 1;
-  if (a.bf16) vec ? residual_t<bf16_bits, 8>(a) : residual_t<bf16_bits, 1>(a);
-  else vec ? residual_t<float, 4>(a) : residual_t<float, 1>(a);
+  if (a.bf16) residual_t<bf16_bits, 8>(a);
+  else residual_t<float, 4>(a);
   return hipGetLastError();
 }
 

@@ -8,23 +8,94 @@
 
 namespace kda {
 
-// V consecutive elements, as one load or store of up to 16 bytes.
+// V consecutive elements as one load or store, at the elements' own alignment
+// (gfx950's global accesses need no more).
 template <typename T, int V>
-struct alignas(sizeof(T) * V) Pack {
-  T e[V];
+struct Bits {
+  static_assert(sizeof(T) * V == 16 || sizeof(T) * V == 8, "8 or 16 bytes");
+  typedef uint32_t type __attribute__((ext_vector_type(sizeof(T) * V / 4)));
+  typedef type unaligned __attribute__((aligned(sizeof(T))));
 };
 template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float (&out)[V]) {
-  const Pack<T, V> v = *(const Pack<T, V>*)p;
+using bits_t = typename Bits<T, V>::type;
+template <typename T, int V>
+__device__ __forceinline__ bits_t<T, V> load_bits(const T* p) {
+  return *(const typename Bits<T, V>::unaligned*)p;
+}
+// Outputs go past the caches (a prompt's are larger than they are, and who reads
+// them runs on other dies: a convolution of 8192 x 12288 bf16 92 -> 73 us; one of
+// 3001 x 777 fp32 takes the same 10.5 us).
+template <typename T, int V>
+__device__ __forceinline__ void store_bits(T* p, bits_t<T, V> v) {
+  __builtin_nontemporal_store(v, (typename Bits<T, V>::unaligned*)p);
+}
+template <typename T, int V>
+__device__ __forceinline__ void from_bits(bits_t<T, V> v, float (&out)[V]) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) out[i] = Elem<T>::load(&v.e[i]);
+  for (int i = 0; i < V; ++i) {
+    if constexpr (sizeof(T) == 4) out[i] = __uint_as_float(v[i]);
+    else out[i] = __uint_as_float(i % 2 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ bits_t<T, V> to_bits(const float (&x)[V]) {
+  bits_t<T, V> v;
+#pragma unroll
+  for (int i = 0; i < V * (int)sizeof(T) / 4; ++i) {
+    if constexpr (sizeof(T) == 4) v[i] = __float_as_uint(x[i]);
+    else v[i] = (uint32_t)f32_to_bf16_bits(x[2 * i]) | (uint32_t)f32_to_bf16_bits(x[2 * i + 1]) << 16;
+  }
+  return v;
+}
+template <typename T, int V>
+__device__ __forceinline__ void load_vec(const T* p, float (&out)[V]) {
+  from_bits<T, V>(load_bits<T, V>(p), out);
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, const float (&x)[V]) {
-  Pack<T, V> v;
+  store_bits<T, V>(p, to_bits<T, V>(x));
+}
+// The first n (at least 1) of V elements; the others are 0, or not written: the
+// end of a row that is not whole vectors.
+template <typename T, int V>
+__device__ __forceinline__ bits_t<T, V> load_first(const T* p, int n) {
+  if (n >= V) return load_bits<T, V>(p);
+  bits_t<T, V> v = {};
 #pragma unroll
-  for (int i = 0; i < V; ++i) Elem<T>::store(&v.e[i], x[i]);
-  *(Pack<T, V>*)p = v;
+  for (int i = 0; i < V - 1; ++i)
+    if (i < n) {
+      if constexpr (sizeof(T) == 4) v[i] = __float_as_uint(p[i]);
+      else v[i / 2] |= (uint32_t)p[i] << (i % 2 ? 16 : 0);
+    }
+  return v;
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_first(T* p, bits_t<T, V> v, int n) {
+  if (n >= V) {
+    store_bits<T, V>(p, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V - 1; ++i)
+    if (i < n) {
+      if constexpr (sizeof(T) == 4) p[i] = __uint_as_float(v[i]);
+      else p[i] = (T)(i % 2 ? v[i / 2] >> 16 : v[i / 2]);
+    }
+}
+// The first n of V fp32 parameters (`fill` for the others).
+template <int V>
+__device__ __forceinline__ void load_params(const float* p, int n, float fill, float (&out)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    if (n >= i + 4) {
+      const bits_t<float, 4> v = load_bits<float, 4>(p + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[i + e] = __uint_as_float(v[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[i + e] = i + e < n ? p[i + e] : fill;
+    }
+  }
 }
 
 // 1 / (1 + e^-x). bf16 outputs: hardware exp2 and reciprocal, a few units of

@@ -855,52 +855,63 @@ __global__ __launch_bounds__(kThreads) void ssm_front_kernel(SsmParams a, int bl
 }
 
 // One token: the state read and written once, a float4 of columns per thread
-// and 256 / (P / 4) rows at a time (the rest of the workgroup idles where P / 4
-// does not divide it).
+// and as many rows at a time as the workgroup has threads for (the rest idles
+// where P / 4 does not divide it). A workgroup takes the whole head, or where
+// that leaves compute units without one, a part of its columns.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void ssm_step_kernel(SsmParams a, int N) {
-  const int h = blockIdx.x % a.H, n = blockIdx.x / a.H;
-  const int vecs = a.P / 4, groups = kThreads / vecs;
-  const int tid = threadIdx.x, cv = tid % vecs, rg = tid / vecs;
+__global__ __launch_bounds__(kThreads) void ssm_step_kernel(SsmParams a, int N, int split) {
+  const int part_id = blockIdx.x % split, h = blockIdx.x / split % a.H, n = blockIdx.x / split / a.H;
+  const int cols = a.P / split, vecs = cols / 4, groups = kThreads / vecs;
+  const int tid = threadIdx.x, cv = tid % vecs, rg = tid / vecs, col = part_id * cols + cv * 4;
   const int grp = h / (a.H / a.G);
   __shared__ float sb[256], sc[256];
   __shared__ f32x4 part[kThreads];
+  const bool on = rg < groups;
+  float* S = a.final_state + ((size_t)n * a.H + h) * N * a.P + col;
+  // (the state's first rows are on their way while d and B are made)
+  constexpr int U = 8;
+  f32x4 s[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (on) s[u] = *(const f32x4*)(S + (size_t)min(rg + u * groups, N - 1) * a.P);
   const float d = step_size(a.dt[(size_t)n * a.H + h], a.dt_bias ? a.dt_bias[h] : 0.f, a.softplus);
   const float f = expf(d * a.a[h]);
   if (tid < N) {
     sb[tid] = d * Elem<T>::load((const T*)a.b + n * a.b_stride + grp * N + tid);
     sc[tid] = Elem<T>::load((const T*)a.c + n * a.c_stride + grp * N + tid);
   }
-  __syncthreads();
   float xv[4];
-  load_vec<T, 4>((const T*)a.x + n * a.x_stride + (int64_t)h * a.P + cv * 4, xv);
+  load_vec<T, 4>((const T*)a.x + n * a.x_stride + (int64_t)h * a.P + col, xv);
   const f32x4 x = {xv[0], xv[1], xv[2], xv[3]};
-  float* S = a.final_state + ((size_t)n * a.H + h) * N * a.P + cv * 4;
+  lds_barrier();
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  if (rg < groups) {
-    constexpr int U = 4;
-    for (int r0 = rg; r0 < N; r0 += U * groups) {
-      f32x4 s[U];
+  for (int r0 = rg; on && r0 < N; r0 += U * groups) {
+    if (r0 != rg)
 #pragma unroll
       for (int u = 0; u < U; ++u) s[u] = *(const f32x4*)(S + (size_t)min(r0 + u * groups, N - 1) * a.P);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = r0 + u * groups;
-        if (r < N) {
-          s[u] = f * s[u] + sb[r] * x;
-          o += sc[r] * s[u];
-          *(f32x4*)(S + (size_t)r * a.P) = s[u];
-        }
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * groups;
+      if (r < N) {
+        s[u] = f * s[u] + sb[r] * x;
+        o += sc[r] * s[u];
+        __builtin_nontemporal_store(s[u], (f32x4*)(S + (size_t)r * a.P));
       }
     }
-    part[tid] = o;
   }
-  __syncthreads();
+  // sums over the groups of rows, halved until one is left
+  for (int m = groups; m > 1;) {
+    part[tid] = o;
+    lds_barrier();
+    const int half = (m + 1) / 2;
+    if (rg + half < m) o += part[tid + half * vecs];
+    m = half;
+    lds_barrier();
+  }
   if (tid < vecs) {
-    for (int g = 1; g < groups; ++g) o += part[g * vecs + tid];
     if (a.skip) o += a.skip[h] * x;
     const float out[4] = {o[0], o[1], o[2], o[3]};
-    store_vec<T, 4>((T*)a.y + ((size_t)n * a.H + h) * a.P + cv * 4, out);
+    store_vec<T, 4>((T*)a.y + ((size_t)n * a.H + h) * a.P + col, out);
   }
 }
 
@@ -993,9 +1004,13 @@ hipError_t launch_ssm(const SsmArgs& a) {
 
 hipError_t launch_ssm_step(const SsmArgs& a) {
   SsmParams p = params_of(a, 1);
-  const dim3 grid((unsigned)((int64_t)a.seqs.num_seqs * a.H));
-  if (a.bf16) hipLaunchKernelGGL(ssm_step_kernel<bf16_bits>, grid, dim3(kThreads), 0, a.stream, p, a.N);
-  else hipLaunchKernelGGL(ssm_step_kernel<float>, grid, dim3(kThreads), 0, a.stream, p, a.N);
+  const int64_t heads = (int64_t)a.seqs.num_seqs * a.H;
+  // halves of the columns (of at least 16) until there are two workgroups a compute unit
+  int split = 1;
+  while (heads * split < 512 && a.P / split % 32 == 0) split *= 2;
+  const dim3 grid((unsigned)(heads * split));
+  if (a.bf16) hipLaunchKernelGGL(ssm_step_kernel<bf16_bits>, grid, dim3(kThreads), 0, a.stream, p, a.N, split);
+  else hipLaunchKernelGGL(ssm_step_kernel<float>, grid, dim3(kThreads), 0, a.stream, p, a.N, split);
   return hipGetLastError();
 }
 

@@ -646,7 +646,7 @@ kda_status kda_gated_norm(const void* x, int64_t x_stride, const void* gate, int
  *   weight, post_weight, scale  [C] fp32; post_weight and scale may be NULL
  *   residual_out  [T, C] dtype, or NULL to skip; may be residual itself
  *   y             [T, C] dtype
- * Errors as kda_gated_norm (C for D; alpha not finite). */
+ * Errors as kda_gated_norm (C for D, any T; alpha not finite). */
 kda_status kda_residual_norm(const void* x, const void* residual, const void* gate,
                              const float* weight, const float* post_weight, const float* scale,
                              kda_dtype dtype, int32_t T, int32_t C, int32_t activation, float alpha,

@@ -92,7 +92,7 @@ def test_conv_prefill_refuses(bad, status):
 
 @pytest.mark.parametrize("bad,status", [
     (dict(N=-1), BAD), (dict(state=None), BAD), (dict(state=at(5, 4)), BAD), (dict(state=at(1)), BAD),
-    (dict(y=at(5)), BAD), (dict(N=1 << 30, C=1 << 20, x_stride=1 << 20), BAD), (dict(N=0, x=None, y=None, state=None), OK),
+    (dict(y=at(5)), BAD), (dict(N=0, x=None, y=None, state=None), OK),
 ])
 def test_conv_step_refuses(bad, status):
     assert conv_step(**bad) == status
@@ -168,7 +168,6 @@ def test_gated_norm_refuses(bad, status):
     (dict(gate=at(3, 4)), BAD), (dict(post=at(5, 4)), BAD), (dict(scale=at(6, 4)), BAD), (dict(out=at(7, 4)), BAD),
     (dict(y=at(1)), BAD), (dict(y=at(2)), BAD), (dict(out=at(8)), BAD), (dict(out=at(2, 16)), BAD), (dict(out=at(1)), BAD),
     (dict(out=at(5)), BAD), (dict(T=0, x=None, y=None), OK),
-    (dict(T=1 << 22, C=16384, x=at(1 << 8), residual=at(1 << 9), gate=None, out=at(1 << 10), y=at(1 << 11)), BAD),
 ])
 def test_residual_norm_refuses(bad, status):
     assert residual(**bad) == status
