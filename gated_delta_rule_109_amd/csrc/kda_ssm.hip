@@ -88,23 +88,43 @@ __device__ __forceinline__ f32x4* front_of(const SsmParams& a, const Part& p, in
 // lane holds 8 values along the sum: taking rows 16 (2v) + 4g + i and
 // 16 (2v + 1) + 4g + i for them makes the accumulators of two tiles that operand
 // without a move. The other operands are read in the same order:
-//   sC, sB  [token][N], natural order (C's part of it as two 8-byte reads)
-//   sBT, sXT  [row of B or column of x][token], sMh, sMl  [token t][token s]: token
-//        32 v + 16 u + 4 g + i at 32 v + 8 g + 4 u + i, one 16-byte read each
-// No padding: blocks of 16 bytes are XORed with bits of their row, so that the 16
-// lanes an LDS instruction serves at a time (16 bytes a lane: lanes 0-3, 12-15,
-// 20-23, 24-27 and so on) meet all 64 banks, and the rows of [row][token] arrays
-// change places in pairs in every other tile of 16, for the same in the stores.
+//   sC, sB  [token][channel], sX [token][column]: as they come, but channel 32 v +
+//        16 u + 4 g + i of a row is kept at 32 v + 8 g + 4 u + i, so that an operand
+//        of sums over channels is one read of 16 bytes. Sums over tokens read 4 rows
+//        of 16 columns turned over (a lane: one column, 4 tokens), twice an operand.
+//   sMh, sMl  [token t][token s], s kept in the order of the channels
+// No padding: blocks of 16 bytes are XORed with bits of their row, so that the
+// lanes an LDS instruction serves at a time meet different banks: 16 rows at one
+// block (16 bytes a lane: lanes 0-3, 12-15, 20-23, 24-27 and so on), and 4 rows of
+// 16 columns (turned over: 16 lanes).
 constexpr int kL = KDA_SSM_CHUNK, kDies = 8;
 
-// In an array [..][64 tokens], block b (8 tokens) of row 16 k + l is b ^ (l >> 1),
-// and where rows change places (k odd) the row is 16 k + (l ^ 1); in an array [64
-// tokens][NP channels], block b (8 channels) of token 16 u + l is b ^ channel_mask(l).
-// A lane keeps one place in each array; others are that one XOR a constant (other
-// blocks) plus a constant (other tiles).
+// Block b of row 16 k + l is kept at b ^ row_mask(l), by the row's bf16 elements. A
+// lane keeps one place in each array; others are that one XOR a constant (other
+// blocks) plus a constant (other tiles). The mask: rows 4 j' + j of one j' in
+// different fours of blocks (as far as those are not different banks anyway), and
+// 0, 2, 3, 1 by j' in the four: { m(0), m(3), m(1) ^ 1, m(2) ^ 1 } are all of it.
 template <int NP>
-__device__ __forceinline__ constexpr int channel_mask(int l) {
-  return NP >= 128 ? l : NP == 64 ? l >> 1 : -(l >> 2) & 3;
+__device__ __forceinline__ constexpr int row_mask(int l) {
+  const int m = (l >> 2 & 1) << 1 ^ (l >> 3) * 3;
+  return NP >= 128 ? (l & 3) << 2 | m : NP == 64 ? (l >> 1 & 1) << 2 | m : m;
+}
+// Place in a row (row l of its tile) of channels 8 nv .. 8 nv + 7: the first four, in
+// one block; the others are in the next one.
+template <int NP>
+__device__ __forceinline__ int channel_place(int nv, int l) {
+  return (4 * (nv / 4) + 2 * (nv & 1) ^ row_mask<NP>(l)) * 8 + 4 * (nv / 2 & 1);
+}
+__device__ __forceinline__ void store_channels(bf16_bits* dst, int place, u32x4 v) {
+  *(uint2*)(dst + place) = uint2{v[0], v[1]};
+  *(uint2*)(dst + (place ^ 8)) = uint2{v[2], v[3]};
+}
+// 16 lanes, each with the place of 4 elements (lanes 4 j .. 4 j + 3: row j of 4, 16
+// columns): lane l gets column l of the 4 rows.
+__device__ __forceinline__ bf16x4 read_turned(const bf16_bits* p) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s16x4 lds;
+  return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds*)p));
 }
 // v, and the compiler does not know it: what is made of it is made where it is
 // used, not once and kept in registers (which spill).
@@ -120,33 +140,7 @@ __device__ __forceinline__ double lane_value(double x, int l) {
   return __builtin_bit_cast(double, make_uint2(__builtin_amdgcn_ds_bpermute(4 * l, v.x),
                                                __builtin_amdgcn_ds_bpermute(4 * l, v.y)));
 }
-// Nothing moves across it: keeps the reads of later products, which would take
-// registers that are not there, behind the products before them.
-__device__ __forceinline__ void stay() { __builtin_amdgcn_sched_barrier(0); }
-
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-
-struct Rows4 {  // 8 columns of 4 tokens
-  u32x4 r[4];
-};
-// Place of columns 8 cv .. 8 cv + 7 (the first of them), tokens 4 sr .. 4 sr + 3.
-__device__ __forceinline__ int transposed_place(int cv, int sr) {
-  const int block = 4 * (sr / 8) + (sr & 3), half = (sr / 4) & 1;
-  return (8 * cv + (cv / 2 & 1)) * kL + (block ^ 4 * (cv & 1)) * 8 + 4 * half;
-}
-__device__ __forceinline__ void store_transposed(bf16_bits* dst, int place, const Rows4& q) {
-  const u32x4 a = q.r[0], b = q.r[1], c = q.r[2], d = q.r[3];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint2 even, odd;   // columns 2 j, 2 j + 1 of the 8
-    even.x = __builtin_amdgcn_perm(b[j], a[j], 0x05040100u);
-    even.y = __builtin_amdgcn_perm(d[j], c[j], 0x05040100u);
-    odd.x = __builtin_amdgcn_perm(b[j], a[j], 0x07060302u);
-    odd.y = __builtin_amdgcn_perm(d[j], c[j], 0x07060302u);
-    *(uint2*)(dst + (place ^ 8 * j) + 2 * j * kL) = even;
-    *(uint2*)(dst + (place ^ (8 * j + kL)) + 2 * j * kL) = odd;
-  }
-}
 
 // x = h + m + l in bf16, each the rest of the one before rounded to nearest.
 __device__ __forceinline__ void split3(f32x4 x, bf16x4& h, bf16x4& m, bf16x4& l) {
@@ -208,10 +202,8 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
   const int grp = h / (a.H / a.G);
   const float av = a.a[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, skip = a.skip ? a.skip[h] : 0.f;
 
-  constexpr int kB = kL * NP, kM = 2 * kL * kL;
-  __shared__ __attribute__((aligned(16))) bf16_bits sC[kL * NP], sBM[kB > kM ? kB : kM], sBT[N * kL], sXT[kCols * kL];
+  __shared__ __attribute__((aligned(16))) bf16_bits sC[kL * NP], sB[kL * NP], sX[kL * kCols], sMh[kL * kL], sMl[kL * kL];
   __shared__ Decays<kL> dec[4];
-  bf16_bits *sB = sBM, *sMh = sBM, *sMl = sBM + kL * kL;  // (M overwrites B once it is used)
 
   // ---- state in front of the segment
   f32x4 s[NT];
@@ -235,105 +227,70 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
 #pragma unroll
     for (int k = 0; k < NT; ++k) front(0)[k * kThreads] = s[k];
 
-  // ---- loads of a chunk into registers, and from there into LDS. Runs of 4 tokens
-  // by 8 columns of x and then of B are shared out over the threads (run i: tokens
-  // 4 (i / 4 % 16), columns 8 (4 (i / 64) + i % 4): 64 bytes of a row together), and
-  // the rows of C after them.
-  constexpr int kXRuns = 2 * W * 16, kRuns = kXRuns + NV * 16, UR = (kRuns + kThreads - 1) / kThreads;
-  constexpr int kCUnits = kL * NV, UC = (kCUnits + kThreads - 1) / kThreads;
-  static_assert(kXRuns % kWave == 0 && kThreads % kWave == 0, "a wave's runs are of one array");
-  static_assert(kThreads % NV == 0, "units of C");
-  Rows4 rr[UR];
-  u32x4 rc[UC];
-  const u32x4 zero = {0u, 0u, 0u, 0u};
+  // ---- loads of a chunk into registers, and from there into LDS: 16 bytes each, two
+  // of x a thread, UB of B and of C.
+  constexpr int XV = 2 * W, kXRows = kThreads / XV, kRows = kThreads / NV, kUnits = kL * NV;
+  constexpr int UB = (kUnits + kThreads - 1) / kThreads;
+  static_assert(kXRows == kL / 2 && kThreads % NV == 0, "rows of a thread");
+  static_assert(kRows % 8 == 0, "a row's mask is that of its first row XOR that of the rows between");
+  u32x4 rx[2], rb[UB], rc[UB];
   // Byte offsets of a thread's rows from a chunk's first token (64 rows of at most
-  // KDA_SSM_MAX_STRIDE elements: below 2^31). What is the same for a wave is kept
-  // in scalars.
+  // KDA_SSM_MAX_STRIDE elements: below 2^31). What is the same for all is kept in
+  // scalars.
   const char* gx = (const char*)((const bf16_bits*)a.x + p.first * a.x_stride + (int64_t)h * a.P + col0);
   const char* gb = (const char*)((const bf16_bits*)a.b + p.first * a.b_stride + grp * N);
   const char* gc = (const char*)((const bf16_bits*)a.c + p.first * a.c_stride + grp * N);
-  const int64_t xs = 2 * a.x_stride, bs = 2 * a.b_stride, cs = 2 * a.c_stride;
-  constexpr int kBRun = NV < 4 ? NV : 4;                 // (columns of B in a wave's runs)
+  const uint32_t xs = 2 * (uint32_t)a.x_stride, bs = 2 * (uint32_t)a.b_stride, cs = 2 * (uint32_t)a.c_stride;
   const int uwave = __builtin_amdgcn_readfirstlane(wave);
-  // Run k of the thread: of x, or of B; its columns / 8 and tokens / 4; whether there
-  // is one. (A thread without one, or with columns behind the head's, reads the
-  // first columns: nothing is made of them.)
-  auto of_x = [&](int k) { return uwave * kWave + k * kThreads < kXRuns; };
-  auto run_col = [&](int k, uint32_t t) -> int {
-    const uint32_t id = t + k * kThreads, b = id - kXRuns;
-    return of_x(k) ? 4 * (id / 64) + id % 4 : kBRun * (b / (16 * kBRun)) + b % kBRun;
-  };
-  auto run_tok = [&](int k, uint32_t t) -> int { return (of_x(k) ? t / 4 : t / kBRun) % 16; };
-  uint32_t first[UR], off[UR];   // bytes from a chunk's first token to a run's columns, and to its first row of them
-  int place[UR];                 // of its columns in sXT or sBT
-#pragma unroll
-  for (int k = 0; k < UR; ++k) {
-    const int cv = run_col(k, tid), sr = run_tok(k, tid);
-    first[k] = (of_x(k) ? col0 + 8 * cv < a.P : tid + k * kThreads < kRuns) ? 16 * cv : 0;
-    off[k] = 4 * sr * (uint32_t)(of_x(k) ? xs : bs) + first[k];
-    place[k] = transposed_place(cv, sr);
-  }
+  // (columns behind the head's: the first ones again, nothing is made of them)
+  const uint32_t xcol = col0 + 8 * (tid % XV) < a.P ? 16 * (tid % XV) : 0, bcol = 16 * (tid % NV);
+  const uint32_t xoff = tid / XV * xs + xcol, boff = tid / NV * bs + bcol, coff = tid / NV * cs + bcol;
   // Of the last chunk of a segment, rows behind the end are read as its last row
   // (offsets grow with the row, so the smaller of two is the earlier row): their
   // step sizes are 0, so nothing is added by them, and no output is theirs.
   auto load = [&](int t0) __attribute__((always_inline)) {
     const uint32_t rows = min(p.count - t0, kL) - 1;
+    const uint32_t x1 = fresh(xcol) + rows * xs, b1 = fresh(bcol) + rows * bs;
 #pragma unroll
-    for (int k = 0; k < UR; ++k) {
-      const char* base = of_x(k) ? gx : gb;
-      const uint32_t step = (uint32_t)(of_x(k) ? xs : bs), at = fresh(off[k]), most = fresh(first[k]) + rows * step;
+    for (int k = 0; k < 2; ++k) rx[k] = *(const u32x4*)(gx + min(xoff + k * kXRows * xs, x1));
 #pragma unroll
-      for (int r = 0; r < 4; ++r) rr[k].r[r] = *(const u32x4*)(base + min(at + r * step, most));
-    }
-    gx += kL * xs;
-    gb += kL * bs;
+    for (int k = 0; k < UB; ++k) rb[k] = *(const u32x4*)(gb + min(boff + k * kRows * bs, b1));
+    gx += (int64_t)kL * xs;
+    gb += (int64_t)kL * bs;
   };
-  const uint32_t coff = tid / NV * (uint32_t)cs + tid % NV * 16;
   auto load_c = [&](int t0) __attribute__((always_inline)) {
-    const uint32_t rows = min(p.count - t0, kL) - 1, at = fresh(coff), most = fresh(threadIdx.x) % NV * 16 + rows * (uint32_t)cs;
+    const uint32_t rows = min(p.count - t0, kL) - 1, c1 = fresh(bcol) + rows * cs;
 #pragma unroll
-    for (int k = 0; k < UC; ++k) rc[k] = *(const u32x4*)(gc + min(at + k * (kThreads / NV) * (uint32_t)cs, most));
-    gc += kL * cs;
+    for (int k = 0; k < UB; ++k) rc[k] = *(const u32x4*)(gc + min(coff + k * kRows * cs, c1));
+    gc += (int64_t)kL * cs;
   };
+  const int xplace = tid / XV * kCols + (tid % XV ^ row_mask<kCols>(tid / XV % 16)) * 8;
+  const int bplace = tid / NV * NP + channel_place<NP>(tid % NV, tid / NV % 16);
   auto store = [&]() __attribute__((always_inline)) {
-    const uint32_t t = fresh(threadIdx.x);
 #pragma unroll
-    for (int k = 0; k < UR; ++k) {
-      const int at = fresh(place[k]);
-      if (of_x(k)) {
-        store_transposed(sXT, at, rr[k]);
-      } else if (kRuns % kThreads == 0 || t + k * kThreads < kRuns) {
-        store_transposed(sBT, at, rr[k]);
-        if (outputs) {
-          const int cv = run_col(k, t), sr = run_tok(k, t);
-          const int row = 4 * sr * NP + (cv ^ channel_mask<NP>(4 * (sr & 3))) * 8;
+    for (int k = 0; k < 2; ++k) *(u32x4*)(sX + xplace + k * kXRows * kCols) = rx[k];
+    const int at = fresh(bplace);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) *(u32x4*)(sB + (row ^ channel_mask<NP>(r) * 8) + r * NP) = rr[k].r[r];
-        }
-      }
-    }
-    if (outputs) {
-      constexpr int kRows = kThreads / NV;
-      static_assert(kRows % 16 == 0 || NP >= 128, "the mask is linear in the row");
-      const int cplace = t / NV * NP + (t % NV ^ channel_mask<NP>(t / NV % 16)) * 8;
-#pragma unroll
-      for (int k = 0; k < UC; ++k)
-        if (kCUnits % kThreads == 0 || t + k * kThreads < kCUnits)
-          *(u32x4*)(sC + (cplace ^ k * kRows % 16 * 8) + k * kRows * NP) = rc[k];
-    }
-    if (N < NP && outputs && tid < kL)                   // the half of a block of 32 channels that N = 16 leaves
-#pragma unroll
-      for (int b = NV; b < NP / 8; ++b) {
-        const int at = tid * NP + (b ^ channel_mask<NP>(tid % 16)) * 8;
-        *(u32x4*)(sB + at) = zero, *(u32x4*)(sC + at) = zero;
+    for (int k = 0; k < UB; ++k)
+      if (kUnits % kThreads == 0 || tid + k * kThreads < kUnits) {
+        store_channels(sB + k * kRows * NP, at ^ row_mask<NP>(k * kRows % 16) * 8, rb[k]);
+        if (outputs) store_channels(sC + k * kRows * NP, at ^ row_mask<NP>(k * kRows % 16) * 8, rc[k]);
       }
   };
-  // A lane's places as it reads: its row and block g of a tile of a [row][token]
-  // array (1: the row it changes places with), of a [token][channel] array, and the
-  // 4 channels 4 g of the latter.
-  const int token_read[2] = {l16 * kL + (g ^ l16 >> 1) * 8, (l16 ^ 1) * kL + (g ^ l16 >> 1) * 8};
-  const int channel_read = l16 * NP + (g ^ channel_mask<NP>(l16)) * 8;
-  const int half_read = l16 * NP + (g / 2 ^ channel_mask<NP>(l16)) * 8 + 4 * (g & 1);
+  if (N < NP && outputs && tid < kL)                     // the channels of a row of 32 that N = 16 leaves
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int at = tid * NP + (b ^ row_mask<NP>(tid % 16)) * 8 + 4;
+      *(uint2*)(sB + at) = uint2{0u, 0u}, *(uint2*)(sC + at) = uint2{0u, 0u};
+    }
+  // A lane's places as it reads: row l16 and block g of a tile of M and of B or C; and
+  // turned over, columns 4 (l16 % 4) of row 4 g + l16 / 4 of x (the wave's) and B.
+  const int turned = 4 * g + l16 / 4, quad = l16 % 4;
+  const int token_read = l16 * kL + (g ^ row_mask<kL>(l16)) * 8;
+  const int channel_read = l16 * NP + (g ^ row_mask<NP>(l16)) * 8;
+  const int x_turned = turned * kCols + (2 * wave + quad / 2 ^ row_mask<kCols>(turned)) * 8 + 4 * (quad & 1);
+  const int b_turned = turned * NP + (quad ^ row_mask<NP>(turned)) * 8;
+
   // Wave w, lane t: what becomes of dt in the w-th of the next four chunks.
   float rdt = 0.f;
   double sum = 0.0;                                      // of the segment's d a, in the four waves' parts
@@ -371,8 +328,7 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
       // ---- M, transposed (a lane: one t, 4 s each), in tiles of 16 t by 16 s: the
       // ten up to the diagonal and two of zeros, shared out over the waves
       constexpr int kTiles = 12, kPer = (kTiles + W - 1) / W;
-      bf16x4 mh[kPer], ml[kPer];
-      const int cr = fresh(channel_read), mr = fresh(token_read[0]);
+      const int cr = fresh(channel_read), mr = fresh(token_read);
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         const int id = uwave + k * W;
@@ -404,32 +360,26 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
             }
           }
         }
-        split_bf16(x, mh[k], ml[k]);
-        stay();
-      }
-      lds_barrier();                                     // B is used
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int id = uwave + k * W;
-        const int tt = id < 4 ? 3 : id < 7 ? 2 : id < 9 ? 1 : id < 11 ? 0 : 2;
-        const int u = id < 4 ? id : id < 7 ? id - 4 : id < 9 ? id - 7 : id < 11 ? id - 9 : 3;
+        bf16x4 mh, ml;
+        split_bf16(x, mh, ml);
         const int at = (mr ^ 32 * (u / 2)) + 16 * tt * kL + 4 * (u & 1);
         if (id < kTiles) {
-          *(bf16x4*)(sMh + at) = mh[k];
-          *(bf16x4*)(sMl + at) = ml[k];
+          *(bf16x4*)(sMh + at) = mh;
+          *(bf16x4*)(sMl + at) = ml;
         }
       }
       lds_barrier();
     }
     // ---- x of the wave's columns: operands of both products
     auto x_operand = [&](int v) __attribute__((always_inline)) {
-      return *(const bf16x8*)(sXT + (fresh(token_read[uwave & 1]) ^ 32 * v) + uwave * 16 * kL);
+const bf16_bits* at = sX + x_turned + 32 * v * kCols;
+      return cat(read_turned(at), read_turned(at + 16 * kCols));
     };
     bf16x8 xo[2] = {x_operand(0), x_operand(1)};
     if (outputs) {
       // ---- y, transposed (a lane: one t, 4 columns): the state's part first
       f32x4 y[4];
-      const int hr = fresh(half_read), mr = fresh(token_read[0]);
+      const int hr = fresh(channel_read), mr = fresh(token_read);
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) y[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -440,12 +390,10 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
         const bf16x8 sh = cat(h0, h1), sl = cat(l0, l1);
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
-          const bf16x8 c = cat(*(const bf16x4*)(sC + (hr ^ 32 * v) + 16 * tt * NP),
-                               *(const bf16x4*)(sC + (hr ^ (32 * v + 16)) + 16 * tt * NP));
+          const bf16x8 c = *(const bf16x8*)(sC + (hr ^ 32 * v) + 16 * tt * NP);
           y[tt] = mfma32(sl, c, y[tt]);
           y[tt] = mfma32(sh, c, y[tt]);
         }
-        stay();
       }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) y[tt] *= q.e[16 * tt + l16];
@@ -479,7 +427,6 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
           y[tt] = mfma32(xo[v], *(const bf16x8*)(sMl + at), y[tt]);
           y[tt] = mfma32(xo[v], *(const bf16x8*)(sMh + at), y[tt]);
         }
-      stay();
       if (any_bad) {
         const uint32_t ft = fresh(threadIdx.x);
 #pragma unroll
@@ -504,7 +451,7 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
     }
     // ---- the state behind the chunk
     const float total = q.total;
-    const int br[2] = {fresh(token_read[0]), fresh(token_read[1])};
+    const int br = fresh(b_turned);
 #pragma unroll
     for (int k = 0; k < NT; ++k) s[k] *= total;
 #pragma unroll
@@ -515,11 +462,11 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
       const bf16x8 xh = cat(h0, h1), xm = cat(m0, m1), xl = cat(l0, l1);
 #pragma unroll
       for (int k = 0; k < NT; ++k) {
-        const bf16x8 b = *(const bf16x8*)(sBT + (br[k & 1] ^ 32 * v) + 16 * k * kL);
+        const bf16_bits* at = sB + (br ^ 32 * (k / 2)) + 4 * (k & 1) + 32 * v * NP;
+        const bf16x8 b = cat(read_turned(at), read_turned(at + 16 * NP));
         s[k] = mfma32(b, xl, s[k]);
         s[k] = mfma32(b, xm, s[k]);
         s[k] = mfma32(b, xh, s[k]);
-        if (k % 4 == 3) stay();
       }
     }
     lds_barrier();                                       // the chunk is used
@@ -657,18 +604,18 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk32_kernel(SsmP
       if (outputs && !of_x(k))
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          *(f32x4*)(sB + (4 * sr + r) * N + (cv ^ channel_mask<2 * N>(4 * (sr & 3) + r)) * 4) = rr[k][r];
+          *(f32x4*)(sB + (4 * sr + r) * N + (cv ^ row_mask<2 * N>(4 * (sr & 3) + r)) * 4) = rr[k][r];
     }
     if (outputs)
 #pragma unroll
       for (int k = 0; k < UC; ++k) {
         const int row = t / NV + k * (kThreads / NV);
         if (kCUnits % kThreads == 0 || t + k * kThreads < kCUnits)
-          *(f32x4*)(sC + row * N + (t % NV ^ channel_mask<2 * N>(row % 16)) * 4) = rc[k];
+          *(f32x4*)(sC + row * N + (t % NV ^ row_mask<2 * N>(row % 16)) * 4) = rc[k];
       }
   };
   const int token_read[2] = {l16 * L + (g ^ l16 >> 1) * 4, (l16 ^ 1) * L + (g ^ l16 >> 1) * 4};
-  const int channel_read = l16 * N + (g ^ channel_mask<2 * N>(l16)) * 4;
+  const int channel_read = l16 * N + (g ^ row_mask<2 * N>(l16)) * 4;
 
   // Wave w, lane t: what becomes of dt in the 2 w-th and next of the next eight chunks.
   float rdt = 0.f;
