@@ -266,6 +266,22 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
   };
   const int xplace = tid / XV * kCols + (tid % XV ^ row_mask<kCols>(tid / XV % 16)) * 8;
   const int bplace = tid / NV * NP + channel_place<NP>(tid % NV, tid / NV % 16);
+  // The chunk in front leaves its outputs in the place of its x, and the threads that
+  // put x there write them out: whole rows, past the caches (so that they are not
+  // still in them when the kernel ends).
+  const int64_t yrow = 2 * (int64_t)a.H * a.P;
+  char* gy = (char*)((bf16_bits*)a.y + ((size_t)p.first * a.H + h) * a.P + col0);
+  const uint32_t yoff = tid / XV * (uint32_t)yrow + 16 * (tid % XV);
+  auto write_out = [&](int t0) __attribute__((always_inline)) {
+    const uint32_t t = fresh(threadIdx.x), at = fresh(yoff);
+    if (col0 + 8 * (int)(t % XV) < a.P)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (t0 + (int)(t / XV) + k * kXRows < p.count)
+          __builtin_nontemporal_store(*(const u32x4*)(sX + xplace + k * kXRows * kCols),
+                                      (u32x4*)(gy + k * kXRows * yrow + at));
+    gy += kL * yrow;
+  };
   auto store = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) *(u32x4*)(sX + xplace + k * kXRows * kCols) = rx[k];
@@ -289,6 +305,7 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
   const int token_read = l16 * kL + (g ^ row_mask<kL>(l16)) * 8;
   const int channel_read = l16 * NP + (g ^ row_mask<NP>(l16)) * 8;
   const int x_turned = turned * kCols + (2 * wave + quad / 2 ^ row_mask<kCols>(turned)) * 8 + 4 * (quad & 1);
+  const int ywrite = l16 * kCols + (2 * wave + g / 2 ^ row_mask<kCols>(l16)) * 8 + 4 * (g & 1);
   const int b_turned = turned * NP + (quad ^ row_mask<NP>(turned)) * 8;
 
   // Wave w, lane t: what becomes of dt in the w-th of the next four chunks.
@@ -306,9 +323,6 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
     if (!outputs) sum += end;
   };
 
-  // (as the loads: a scalar base, and a row of H P <= KDA_SSM_MAX_STRIDE elements a lane)
-  const int64_t yrow = 2 * (int64_t)a.H * a.P;
-  char* gy = (char*)((bf16_bits*)a.y + ((size_t)p.first * a.H + h) * a.P + col0);
   load_dt(0);
   if (p.count > 0) {
     load(0);
@@ -321,9 +335,11 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
       decays(t0);
       load_dt(t0 + 4 * kL);
     }
+    if (outputs && t0 > 0) write_out(t0 - kL);
     store();
     lds_barrier();
     if (t0 + kL < p.count) load(t0 + kL);
+    f32x4 y[4];
     if (outputs) {
       // ---- M, transposed (a lane: one t, 4 s each), in tiles of 16 t by 16 s: the
       // ten up to the diagonal and two of zeros, shared out over the waves
@@ -368,18 +384,9 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
           *(bf16x4*)(sMl + at) = ml;
         }
       }
-      lds_barrier();
-    }
-    // ---- x of the wave's columns: operands of both products
-    auto x_operand = [&](int v) __attribute__((always_inline)) {
-const bf16_bits* at = sX + x_turned + 32 * v * kCols;
-      return cat(read_turned(at), read_turned(at + 16 * kCols));
-    };
-    bf16x8 xo[2] = {x_operand(0), x_operand(1)};
-    if (outputs) {
       // ---- y, transposed (a lane: one t, 4 columns): the state's part first
-      f32x4 y[4];
-      const int hr = fresh(channel_read), mr = fresh(token_read);
+      // (it needs nothing of M, which the other waves finish meanwhile)
+      const int hr = fresh(channel_read);
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) y[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -397,6 +404,15 @@ const bf16_bits* at = sX + x_turned + 32 * v * kCols;
       }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) y[tt] *= q.e[16 * tt + l16];
+      lds_barrier();
+    }
+    // ---- x of the wave's columns: operands of both products
+    auto x_operand = [&](int v) __attribute__((always_inline)) {
+const bf16_bits* at = sX + x_turned + 32 * v * kCols;
+      return cat(read_turned(at), read_turned(at + 16 * kCols));
+    };
+    bf16x8 xo[2] = {x_operand(0), x_operand(1)};
+    if (outputs) {
       // A value that is not finite would reach earlier tokens through M's zeros:
       // it is taken out here, and its column made NaN from its token on.
       const u16x8 most = __builtin_elementwise_max(__builtin_bit_cast(u16x8, xo[0]) & (uint16_t)0x7fff,
@@ -419,6 +435,7 @@ const bf16_bits* at = sX + x_turned + 32 * v * kCols;
         from = min(from, __builtin_amdgcn_ds_bpermute(4 * (fresh(threadIdx.x) ^ 16), from));
         from = min(from, __builtin_amdgcn_ds_bpermute(4 * (fresh(threadIdx.x) ^ 32), from));
       }
+      const int mr = fresh(token_read);
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
@@ -439,14 +456,9 @@ const bf16_bits* at = sX + x_turned + 32 * v * kCols;
 #pragma unroll
         for (int v = 0; v < 2; ++v) xo[v] = x_operand(v);
       }
-      if (live) {
-        const int left = p.count - t0 - l16;
-        const uint32_t yoff = l16 * (uint32_t)yrow + 2 * (16 * uwave + 4 * g);
+      // (x of the wave's columns is in registers, and no other wave reads it)
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-          if (16 * tt < left) *(bf16x4*)(gy + 16 * tt * yrow + yoff) = to_bf16x4(y[tt]);
-      }
-      gy += kL * yrow;
+      for (int tt = 0; tt < 4; ++tt) *(bf16x4*)(sX + ywrite + 16 * tt * kCols) = to_bf16x4(y[tt]);
       if (t0 + kL < p.count) load_c(t0 + kL);            // (late: the registers are needed until here)
     }
     // ---- the state behind the chunk
@@ -471,6 +483,7 @@ const bf16_bits* at = sX + x_turned + 32 * v * kCols;
     }
     lds_barrier();                                       // the chunk is used
   }
+  if (outputs && p.count > 0) write_out((p.count - 1) / kL * kL);
 
   if (!outputs) {
 #pragma unroll
@@ -770,15 +783,10 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk32_kernel(SsmP
 // starts). vecs: vectors of a head's state.
 __global__ __launch_bounds__(kThreads) void ssm_front_kernel(SsmParams a, int blocks, int vecs) {
   const int b = blockIdx.x % blocks, h = blockIdx.x / blocks % a.H, at = blockIdx.x / blocks / a.H;
-  int lo = 0, hi = a.seqs.num_seqs;   // the last sequence that starts before (at + 1) len
-  while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    if (token_offset(a.seqs, mid) / a.len <= at) lo = mid;
-    else hi = mid;
-  }
   Part p;
-  p.start = token_offset(a.seqs, lo);
-  p.length = token_offset(a.seqs, lo + 1) - p.start;
+  p.n = last_sequence(a.seqs, a.len, 0, at);   // the last that starts before (at + 1) len
+  p.start = token_offset(a.seqs, p.n);
+  p.length = token_offset(a.seqs, p.n + 1) - p.start;
   const int i = b * kThreads + threadIdx.x;
   if (p.start / a.len != at || p.length <= 2 * a.len || i >= vecs) return;
   const int parts = (p.length - 1) / a.len + 1;

@@ -556,47 +556,51 @@ def state_load(cache: StateCache, slots=None, states=None):
 
 # ---- the layer around a recurrence: short convolution, state-space scan, norms ---------
 
-def _row_stride(t, name, lead_shape):
-    """Elements from one row of t [lead, ..] to the next; a row itself is
-    contiguous. (One row has no next one: its own length.)"""
-    if t.shape != lead_shape:
-        raise ValueError(f"{name}: expected shape {tuple(lead_shape)}, got {tuple(t.shape)}")
-    width = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != width:
-            raise ValueError(f"{name}: rows must be contiguous")
-        width *= size
-    if t.shape[0] <= 1:
+def _row_stride(t, name, shape, width):
+    """Elements from one row of t (its shape as given, `width` elements a row) to
+    the next; a row itself is contiguous. (One row has no next one: its own
+    length.)"""
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 or (len(st) == 3 and st[1] != shape[2]):
+        run = 1          # (dimensions of one element may have any stride)
+        for size, stride in zip(reversed(shape[1:]), reversed(st[1:])):
+            if size != 1 and stride != run:
+                raise ValueError(f"{name}: rows must be contiguous")
+            run *= size
+    if shape[0] <= 1:
         return width
-    if t.stride(0) < width:
+    if st[0] < width:
         raise ValueError(f"{name}: rows overlap")
-    return t.stride(0)
+    return st[0]
 
 
 def _storage_code(t, name):
-    if t.dtype is torch.bfloat16:
+    dt = t.dtype
+    if dt is torch.bfloat16:
         return KDA_BF16
-    if t.dtype is torch.float32:
+    if dt is torch.float32:
         return KDA_F32
-    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    raise TypeError(f"{name} must be bfloat16 or float32, got {dt}")
 
 
-def _check_rest(x, *specs):
-    """The given tensors (name, tensor or None, shape, dtype, whether its rows
-    may be strided) are right and on x's device, whose index is returned."""
-    dev = x.get_device()
-    for name, t, shape, dtype, strided in specs:
-        if t is None:
-            continue
-        if t.shape != shape or t.dtype is not dtype:
-            _expect(t, name, shape, dtype)
-        if not strided and not t.is_contiguous():
-            raise ValueError(f"{name}: tensors must be contiguous device tensors")
-        if t.get_device() != dev:
+def _check_rest(dev, *specs):
+    """The given tensors (name, tensor or None, shape, dtype) have their shape and
+    dtype, are contiguous and on device `dev`. One pass over what is right; the
+    first thing wrong is looked up after it."""
+    for _, t, shape, dtype in specs:
+        if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()
+                              or t.get_device() != dev):
+            break
+    else:
+        if dev >= 0:
+            return
+    for name, t, shape, dtype in specs:
+        _expect(t, name, shape, dtype)
+        if t is not None and (not t.is_contiguous() or t.get_device() != dev):
             raise ValueError(f"{name}: tensors must be contiguous device tensors, all on one device")
-    if dev < 0:
-        raise ValueError("tensors must be contiguous device tensors")
-    return dev
+    raise ValueError("tensors must be contiguous device tensors")
 
 
 def _num_seqs(cu_seqlens):
@@ -621,12 +625,11 @@ def conv_prefill(x, weight, bias=None, cu_seqlens=None, initial_state=None, acti
     N = _num_seqs(cu_seqlens)
     _check_int32(T, C, N)
     code = _storage_code(x, "x")
-    stride = _row_stride(x, "x", (T, C))
-    sshape = (N, K - 1, C)
-    dev = _check_rest(x, ("weight", weight, (C, K), torch.float32, False), ("bias", bias, (C,), torch.float32, False),
-                      ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, False),
-                      ("initial_state", initial_state, sshape, x.dtype, False),
-                      ("final_state", final_state, sshape, x.dtype, False), ("y", y, (T, C), x.dtype, False))
+    stride = _row_stride(x, "x", (T, C), C)
+    dev, sshape = x.get_device(), (N, K - 1, C)
+    _check_rest(dev, ("weight", weight, (C, K), torch.float32), ("bias", bias, (C,), torch.float32),
+                ("cu_seqlens", cu_seqlens, (N + 1,), torch.int32), ("initial_state", initial_state, sshape, x.dtype),
+                ("final_state", final_state, sshape, x.dtype), ("y", y, (T, C), x.dtype))
     if y is None:
         y = x.new_empty(T, C)
     if final_state is None and out_final_state:
@@ -643,11 +646,12 @@ def conv_step(x, weight, state, bias=None, activation=ACT_SILU, y=None):
     K = weight.shape[-1]
     _check_int32(N, C, K)
     code = _storage_code(x, "x")
-    stride = _row_stride(x, "x", (N, C))
+    stride = _row_stride(x, "x", (N, C), C)
     if state is None:
         raise ValueError("state is required")
-    dev = _check_rest(x, ("weight", weight, (C, K), torch.float32, False), ("bias", bias, (C,), torch.float32, False),
-                      ("state", state, (N, K - 1, C), x.dtype, False), ("y", y, (N, C), x.dtype, False))
+    dev = x.get_device()
+    _check_rest(dev, ("weight", weight, (C, K), torch.float32), ("bias", bias, (C,), torch.float32),
+                ("state", state, (N, K - 1, C), x.dtype), ("y", y, (N, C), x.dtype))
     if y is None:
         y = x.new_empty(N, C)
     _call(dev, "kda_conv_step", lib().kda_conv_step, x.data_ptr(), stride, weight.data_ptr(), _addr(bias), code,
@@ -664,19 +668,21 @@ def ssm_workspace(num_seqs: int, T: int, H: int, N: int, P: int, device) -> torc
 
 
 def _ssm_inputs(x, dt, a, b, c, skip, dt_bias, T):
-    """Sizes, strides and specifications of what a scan reads."""
-    H, P = x.shape[1:]
+    """Sizes, strides and (name, tensor, shape, dtype) of what a scan reads."""
     if b.dim() != 3:
         raise ValueError(f"b: expected shape [T, G, N], got {tuple(b.shape)}")
-    G, N = b.shape[1:]
+    _, H, P = x.shape
+    _, G, N = b.shape
     code = _storage_code(x, "x")
     if b.dtype is not x.dtype or c.dtype is not x.dtype:
         raise TypeError(f"b, c: expected {x.dtype}, got {b.dtype}, {c.dtype}")
-    strides = (_row_stride(x, "x", (T, H, P)), _row_stride(b, "b", (T, G, N)), _row_stride(c, "c", (T, G, N)))
-    specs = (("b", b, (T, G, N), x.dtype, True), ("c", c, (T, G, N), x.dtype, True),
-             ("dt", dt, (T, H), torch.float32, False), ("a", a, (H,), torch.float32, False),
-             ("skip", skip, (H,), torch.float32, False), ("dt_bias", dt_bias, (H,), torch.float32, False))
-    return (H, P, G, N), code, strides, specs
+    dev = x.get_device()
+    if b.get_device() != dev or c.get_device() != dev:
+        raise ValueError("b, c: tensors must be contiguous device tensors, all on one device")
+    bshape, f32 = (T, G, N), torch.float32
+    strides = (_row_stride(x, "x", (T, H, P), H * P), _row_stride(b, "b", bshape, G * N), _row_stride(c, "c", bshape, G * N))
+    return (H, P, G, N), code, dev, strides, (("dt", dt, (T, H), f32), ("a", a, (H,), f32), ("skip", skip, (H,), f32),
+                                              ("dt_bias", dt_bias, (H,), f32))
 
 
 def ssm_prefill(x, dt, a, b, c, skip=None, dt_bias=None, dt_softplus=False, cu_seqlens=None, initial_state=None,
@@ -690,15 +696,14 @@ def ssm_prefill(x, dt, a, b, c, skip=None, dt_bias=None, dt_softplus=False, cu_s
     no sequence are left as they were (of a y made here: not initialised).
     Returns (y [T,H,P], final_state or None)."""
     T = x.shape[0]
-    (H, P, G, N), code, (xs, bs, cs), specs = _ssm_inputs(x, dt, a, b, c, skip, dt_bias, T)
+    (H, P, G, N), code, dev, (xs, bs, cs), specs = _ssm_inputs(x, dt, a, b, c, skip, dt_bias, T)
     S = _num_seqs(cu_seqlens)
     _check_int32(T, H, S)
     sshape = (S, H, N, P)
-    dev = _check_rest(x, *specs, ("cu_seqlens", cu_seqlens, (S + 1,), torch.int32, False),
-                      ("initial_state", initial_state, sshape, torch.float32, False),
-                      ("final_state", final_state, sshape, torch.float32, False),
-                      ("y", y, (T, H, P), x.dtype, False),
-                      ("workspace", workspace, None if workspace is None else (workspace.numel(),), torch.uint8, False))
+    _check_rest(dev, *specs, ("cu_seqlens", cu_seqlens, (S + 1,), torch.int32),
+                ("initial_state", initial_state, sshape, torch.float32), ("final_state", final_state, sshape, torch.float32),
+                ("y", y, (T, H, P), x.dtype),
+                ("workspace", workspace, None if workspace is None else (workspace.numel(),), torch.uint8))
     if y is None:
         y = x.new_empty(T, H, P)
     if final_state is None and out_final_state:
@@ -716,12 +721,11 @@ def ssm_step(x, dt, a, b, c, state, skip=None, dt_bias=None, dt_softplus=False, 
     [S,G,N]; state [S,H,N,P] float32 updated in place. Otherwise as
     ssm_prefill. Returns y [S,H,P]."""
     S = x.shape[0]
-    (H, P, G, N), code, (xs, bs, cs), specs = _ssm_inputs(x, dt, a, b, c, skip, dt_bias, S)
+    (H, P, G, N), code, dev, (xs, bs, cs), specs = _ssm_inputs(x, dt, a, b, c, skip, dt_bias, S)
     _check_int32(S, H, G)
     if state is None:
         raise ValueError("state is required")
-    dev = _check_rest(x, *specs, ("state", state, (S, H, N, P), torch.float32, False),
-                      ("y", y, (S, H, P), x.dtype, False))
+    _check_rest(dev, *specs, ("state", state, (S, H, N, P), torch.float32), ("y", y, (S, H, P), x.dtype))
     if y is None:
         y = x.new_empty(S, H, P)
     _call(dev, "kda_ssm_step", lib().kda_ssm_step, x.data_ptr(), xs, dt.data_ptr(), a.data_ptr(), b.data_ptr(), bs,
@@ -738,12 +742,15 @@ def gated_norm(x, gate, weight, activation=ACT_SIGMOID, gate_first=False, eps=1e
     T, H, D = x.shape
     _check_int32(T, H, D)
     code = _storage_code(x, "x")
-    xs = _row_stride(x, "x", (T, H, D))
-    gs = 0 if gate is None else _row_stride(gate, "gate", (T, H, D))
+    shape, dev = (T, H, D), x.get_device()
+    xs, gs = _row_stride(x, "x", shape, H * D), 0
+    if gate is not None:
+        if gate.dtype is not x.dtype or gate.get_device() != dev:
+            _expect(gate, "gate", shape, x.dtype)
+            raise ValueError("gate: tensors must be contiguous device tensors, all on one device")
+        gs = _row_stride(gate, "gate", shape, H * D)
     per_head = weight.dim() == 2
-    dev = _check_rest(x, ("gate", gate, (T, H, D), x.dtype, True),
-                      ("weight", weight, (H, D) if per_head else (D,), torch.float32, False),
-                      ("y", y, (T, H, D), x.dtype, False))
+    _check_rest(dev, ("weight", weight, (H, D) if per_head else (D,), torch.float32), ("y", y, shape, x.dtype))
     if y is None:
         y = x.new_empty(T, H, D)
     _call(dev, "kda_gated_norm", lib().kda_gated_norm, x.data_ptr(), xs, _addr(gate), gs, weight.data_ptr(),
@@ -760,11 +767,10 @@ def residual_norm(x, residual, weight, post_weight=None, gate=None, activation=A
     T, C = x.shape
     _check_int32(T, C, C)
     code = _storage_code(x, "x")
-    dt, f32 = x.dtype, torch.float32
-    dev = _check_rest(x, ("x", x, (T, C), dt, False), ("residual", residual, (T, C), dt, False),
-                      ("weight", weight, (C,), f32, False), ("post_weight", post_weight, (C,), f32, False),
-                      ("gate", gate, (T, C), dt, False), ("scale", scale, (C,), f32, False),
-                      ("residual_out", residual_out, (T, C), dt, False), ("y", y, (T, C), dt, False))
+    dt, f32, rows, row, dev = x.dtype, torch.float32, (T, C), (C,), x.get_device()
+    _check_rest(dev, ("x", x, rows, dt), ("residual", residual, rows, dt), ("weight", weight, row, f32),
+                ("post_weight", post_weight, row, f32), ("gate", gate, rows, dt), ("scale", scale, row, f32),
+                ("residual_out", residual_out, rows, dt), ("y", y, rows, dt))
     if residual_out is None:
         residual_out = torch.empty_like(x)
     if y is None:
