@@ -7,6 +7,8 @@
 // matrix cores.
 #include "kda_pack.h"
 
+#include <math.h>
+
 namespace kda {
 namespace {
 
@@ -24,22 +26,34 @@ constexpr int kThreads = 256;
 // sequence that starts at token s is entry 2 (s / len) + j: a sequence of two or
 // more segments reaches over at least one multiple of len, and has at most one
 // segment more than it reaches over, so no two meet and there are 2 T / len.
+//
+// How long: a segment adds its state, written and read twice (about 2 us a segment
+// for 2 MB of states, 0.5 us for small ones), and takes its tokens' time off the
+// chain (about 6 us per 64 tokens in both launches together), least where len is the
+// root of (5 + 15 H N P / 2^19) T. Measured, bf16, 32 heads of 128 x 128: 512 tokens in
+// segments of 128 29 us, of 256 36, whole 40; 2048 tokens in segments of 128 56 us, of
+// 256 51, of 512 67. Never more segments than fill the GPU, and none of calls where the
+// two more launches cost more than they save (300 tokens of two sequences: whole 13 us,
+// in segments 19).
 struct Split {
   int columns;     // columns of a head one workgroup owns
   int target;      // workgroups that the segments of a call make up
-  int shortest;    // tokens of the shortest segment
+  int chunk;       // tokens: segments are whole chunks, at least two
+  int whole;       // calls of at most so many tokens are not split
 };
-constexpr Split kFullSplit = {64, 512, 128};         // fp32
+constexpr Split kFullSplit = {64, 512, 32, 160};      // fp32
 // (the chunks' workgroups have 8 waves where a head has more than 64 columns, else 4)
-constexpr Split kChunkSplit = {64, 512, 256}, kWideSplit = {128, 512, 256};
+constexpr Split kChunkSplit = {64, 512, KDA_SSM_CHUNK, 384}, kWideSplit = {128, 512, KDA_SSM_CHUNK, 384};
 const Split& split_of(bool bf16, int P) { return !bf16 ? kFullSplit : P <= 64 ? kChunkSplit : kWideSplit; }
 int column_blocks(const Split& s, int P) { return (P + s.columns - 1) / s.columns; }
 
-int segment_len(const Packed& s, int H, int P, const Split& sp) {
+int segment_len(const Packed& s, int H, int N, int P, const Split& sp) {
   const int64_t parts = sp.target / ((int64_t)H * column_blocks(sp, P));   // segments of all sequences together
-  if (parts < 2 || s.T < 2 * sp.shortest) return s.T > 0 ? s.T : 1;
-  const int64_t len = ((s.T + parts - 1) / parts + KDA_SSM_CHUNK - 1) / KDA_SSM_CHUNK * KDA_SSM_CHUNK;
-  return (int)(len > sp.shortest ? len : sp.shortest);
+  if (parts < 2 || s.T <= sp.whole) return s.T > 0 ? s.T : 1;
+  const double best = sqrt((5.0 + 15.0 * H * N * P / (1 << 19)) * s.T), filled = (double)s.T / parts;
+  const double len = best > filled ? best : filled;
+  const int64_t chunks = (int64_t)ceil(len / sp.chunk);
+  return (int)(chunks > 2 ? chunks : 2) * sp.chunk;
 }
 
 // d_t of one token and head.
@@ -891,14 +905,14 @@ size_t end_bytes(int H, int N, int P, const Split& sp) { return (size_t)H * colu
 // Workgroups: whole rounds of the dies (the last ones have no segment).
 int64_t launch_groups(const SsmArgs& a, const Split& sp) {
   const int64_t blocks = column_blocks(sp, a.P), round = kDies * (a.H / a.G * blocks);
-  const int64_t groups = part_slots(a.seqs, segment_len(a.seqs, a.H, a.P, sp)) * a.H * blocks;
+  const int64_t groups = part_slots(a.seqs, segment_len(a.seqs, a.H, a.N, a.P, sp)) * a.H * blocks;
   return (groups + round - 1) / round * round;
 }
 
 // All launches of a scan by a kernel (for states alone, and with outputs).
 template <typename K>
 hipError_t launch_passes(K states, K outputs, const SsmArgs& a, const Split& sp, int threads) {
-  const int len = segment_len(a.seqs, a.H, a.P, sp);
+  const int len = segment_len(a.seqs, a.H, a.N, a.P, sp);
   SsmParams p = params_of(a, len);
   const int64_t e = entries(a.seqs, len);
   p.ends = (float*)a.workspace;
@@ -922,7 +936,8 @@ hipError_t launch_n(const SsmArgs& a) {
 
 size_t workspace_of(int32_t T, int32_t H, int32_t N, int32_t P, const Split& sp) {
   const size_t by_target = (size_t)sp.target * ((size_t)sp.columns * N * 4 + 8);
-  const size_t by_length = (size_t)(T / sp.shortest) * (end_bytes(H, N, P, sp) + (size_t)H * 8);
+  const size_t by_length = (size_t)(T / (2 * sp.chunk)) * (end_bytes(H, N, P, sp) + (size_t)H * 8);
+  if (T <= sp.whole) return 0;
   return 2 * (by_target < by_length ? by_target : by_length);
 }
 
@@ -933,8 +948,8 @@ int64_t ssm_threads(const SsmArgs& a) {
   return launch_groups(a, sp) * 4 * sp.columns;
 }
 
-// At most 2 target / (H column blocks) entries, and at most two per `shortest`
-// tokens: both grow with the sizes. Any type, and heads narrow or wide: the
+// At most 2 target / (H column blocks) entries, and at most two per 2
+// chunks: both grow with the sizes. Any type, and heads narrow or wide: the
 // largest.
 size_t ssm_workspace(int32_t num_seqs, int32_t T, int32_t H, int32_t N, int32_t P) {
   (void)num_seqs;
