@@ -175,10 +175,14 @@ struct Decays {
 };
 // A wave's 64 tokens, one a lane (at: the lane): the decays of 64 / L chunks, with
 // the sums of the logarithms c = d a in fp64. Returns the last chunk's c_L in every
-// lane of it.
+// lane of it. One logarithm is no less than kLeast: e^kLeast and all that is
+// multiplied by it are 0 as it is, while a token that ends the state (d a = -1e12)
+// would take the digits of the sums behind it.
 template <int L>
 __device__ __forceinline__ double make_decays(float d, float a, int at, Decays<L>* dec) {
+  constexpr double kLeast = -(1 << 20);
   double c = (double)d * a;
+  c = c < kLeast ? kLeast : c;                           // (NaN stays)
 #pragma unroll
   for (int m = 1; m < L; m *= 2) {
     const double o = lane_value(c, at - m);

@@ -561,9 +561,9 @@ kda_status kda_conv_prefill(const void* x, int64_t x_stride, const float* weight
                             int32_t activation, const void* initial_state, void* final_state,
                             void* y, hipStream_t stream);
 
-/* One token of each of N sequences: x [N, C] (x_stride), y [N, C], state
- * [N, width - 1, C] dtype, read and updated in place. Otherwise as
- * kda_conv_prefill. */
+/* One token of each of N sequences (at most KDA_MAX_PACKED_TOKENS): x [N, C]
+ * (x_stride), y [N, C], state [N, width - 1, C] dtype, read and updated in place.
+ * Otherwise as kda_conv_prefill. */
 kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, const float* bias,
                          kda_dtype dtype, void* state, int32_t N, int32_t C, int32_t width,
                          int32_t activation, void* y, hipStream_t stream);
@@ -586,14 +586,16 @@ kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, c
  * and x are exact there, every fp32 factor is carried in two bf16 terms for
  * outputs (2^-16 of each product) and three for states (2^-24). fp32 tensors run
  * in chunks of half that length with products of fp32. The decays between two
- * tokens come from sums in fp64. Values that are not finite in x, b or dt make outputs non-finite from
- * their token on (of a value in x: in its column), as the recurrence does, and
- * no outputs before; a c that is not finite, those of its token.
+ * tokens come from sums in fp64 (a d_t a[h] below -2^20 counts as -2^20: the
+ * state in front of it is gone either way). Values that are not finite in x, b or dt make
+ * outputs non-finite from their token on (of a value in x: in its column), as the
+ * recurrence does, and no outputs before; a c that is not finite, those of its
+ * token.
  *   workspace  256-byte aligned device scratch of kda_ssm_workspace_size(num_seqs,
- *              T, H, N, P) bytes (0: may be NULL): the states of segments of long sequences, which
- *              run side by side. It needs no initialisation; sizes do not shrink
- *              as num_seqs, T, H or P grow, so that of the largest call serves
- *              smaller ones; calls that may overlap need one each.
+ *              T, H, N, P) bytes (0: may be NULL): the states of segments of long
+ *              sequences, which run side by side. It needs no initialisation; sizes
+ *              do not shrink as num_seqs, T, H or P grow, so that of the largest call
+ *              serves smaller ones; calls that may overlap need one each.
  * Errors: KDA_ERR_INVALID_ARG (as kda_conv_prefill; G < 1 or H % G), KDA_ERR_UNSUPPORTED
  * (dtype, N or P), KDA_ERR_WORKSPACE, KDA_ERR_HIP. */
 #define KDA_SSM_CHUNK 64

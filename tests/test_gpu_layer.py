@@ -96,6 +96,41 @@ def test_conv(lengths, outside, C, K, dtype, act, bias, cached, pad):
         assert torch.equal(state, end)
 
 
+@pytest.mark.parametrize("count", [65, 700, 5000])
+@pytest.mark.parametrize("kind", ["conv", "ssm"])
+def test_many_sequences(kind, count):
+    """More sequences than a wave has lanes, and than two and three steps of its
+    search tell apart; most are empty or short, some of several parts."""
+    rng = np.random.default_rng(count)
+    lengths = rng.integers(0, 3, count)
+    lengths[:count // 3] = 0
+    lengths[[0, count // 2, count - 2]] = 5, 90, 70
+    lengths = lengths.tolist()
+    if kind == "conv":
+        x, w, b, s, cu = conv_inputs(lengths, (1, 2), 8, 4, BF16, True, True, 0, count)
+        y, end = kda.conv_prefill(x, w, b, cu_seqlens=device_cu(cu), initial_state=s)
+        ref, bound, states = layer.conv(host(x), host(w), host(b), cu, host(s), 1)
+        assert np.array_equal(host(end), states)
+    else:
+        s, s0, cu = ssm_inputs(lengths, (1, 2), 1, 1, 16, 16, BF16, seed=count)
+        y, end = kda.ssm_prefill(**s, cu_seqlens=device_cu(cu), initial_state=s0)
+        ref, bound, states, sbound = ssm_reference(s, cu, s0, BF16)
+        check(end, states, sbound, "state")
+    check(y[cu[0]:cu[-1]], ref[cu[0]:cu[-1]], bound[cu[0]:cu[-1]], "y")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_ssm_many_sequences_in_segments(dtype):
+    """Segments and the states in front of them among many sequences."""
+    lengths = [0, 1, 2] * 30 + [1300] + [0] * 70 + [600, 1, 0, 450] + [3] * 80
+    s, s0, cu = ssm_inputs(lengths, (2, 0), 1, 1, 16, 32, dtype, seed=21, rate=0.3)
+    state = s0.clone()
+    y, _ = kda.ssm_prefill(**s, cu_seqlens=device_cu(cu), initial_state=state, final_state=state)
+    ref, bound, states, sbound = ssm_reference(s, cu, s0, dtype)
+    check(y[cu[0]:cu[-1]], ref[cu[0]:cu[-1]], bound[cu[0]:cu[-1]], "y")
+    check(state, states, sbound, "state")
+
+
 @pytest.mark.parametrize("dtype,C,K", [(BF16, 64, 4), (BF16, 9, 3), (F32, 20, 2), (F32, 3, 4)])
 def test_conv_in_parts_and_by_steps(dtype, C, K):
     """A prompt at once, cut in two, and token by token: the same bits."""
@@ -206,6 +241,21 @@ def test_ssm_growing_states_and_zero_steps(dtype):
     ref, bound, states, sbound = ssm_reference(s, cu, s0, dtype)
     check(y, ref, bound)
     check(end, states, sbound)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [100, 900])
+def test_ssm_after_steps_that_end_the_state(dtype, T):
+    """A step size of 1e12 leaves nothing of the state in front of it (its own x is 0
+    here); the decays between the tokens behind it keep their digits."""
+    s, s0, cu = ssm_inputs([T], (0, 0), 2, 1, 32, 32, dtype, soft=False, seed=12, rate=1.0)
+    for t in (7, 8, 50, T - 30):
+        s["dt"][t] = 1e12
+        s["x"][t] = 0
+    y, end = kda.ssm_prefill(**s, initial_state=s0)
+    ref, bound, states, sbound = ssm_reference(s, cu, s0, dtype)
+    check(y, ref, bound, "y")
+    check(end, states, sbound, "state")
 
 
 @pytest.mark.parametrize("dtype,T", [(BF16, 200), (F32, 200), (BF16, 700)])
