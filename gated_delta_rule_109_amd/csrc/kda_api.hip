@@ -619,7 +619,7 @@ kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, c
   kda::ConvArgs a;
   const kda_status st = conv_args(x, x_stride, weight, bias, dt, N, C, width, activation, y, stream, &a);
   if (st != KDA_OK) return st;
-  if (N < 0 || (N > 0 && !state) || !aligned16({state})) return KDA_ERR_INVALID_ARG;
+  if (N < 0 || N > KDA_MAX_PACKED_TOKENS || (N > 0 && !state) || !aligned16({state})) return KDA_ERR_INVALID_ARG;
   a.seqs = packed(nullptr, 1, 0);
   a.N = N;
   a.initial_state = state; a.final_state = state;

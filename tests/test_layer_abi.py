@@ -91,7 +91,7 @@ def test_conv_prefill_refuses(bad, status):
 
 
 @pytest.mark.parametrize("bad,status", [
-    (dict(N=-1), BAD), (dict(state=None), BAD), (dict(state=at(5, 4)), BAD), (dict(state=at(1)), BAD),
+    (dict(N=-1), BAD), (dict(N=(1 << 30) + 1), BAD), (dict(state=None), BAD), (dict(state=at(5, 4)), BAD), (dict(state=at(1)), BAD),
     (dict(y=at(5)), BAD), (dict(N=0, x=None, y=None, state=None), OK),
 ])
 def test_conv_step_refuses(bad, status):
