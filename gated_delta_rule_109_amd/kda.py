@@ -623,7 +623,7 @@ def conv_prefill(x, weight, bias=None, cu_seqlens=None, initial_state=None, acti
     T, C = x.shape
     K = weight.shape[-1]
     N = _num_seqs(cu_seqlens)
-    _check_int32(T, C, N)
+    _check_int32(T, C, N if N > K else K)
     code = _storage_code(x, "x")
     stride = _row_stride(x, "x", (T, C), C)
     dev, sshape = x.get_device(), (N, K - 1, C)
@@ -663,6 +663,7 @@ def ssm_workspace(num_seqs: int, T: int, H: int, N: int, P: int, device) -> torc
     """A workspace for ssm_prefill calls of these sizes and smaller ones (state
     size N), one after another."""
     _check_int32(num_seqs, T, H)
+    _check_int32(H, N, P)
     size = int(lib().kda_ssm_workspace_size(int(num_seqs), int(T), int(H), int(N), int(P)))
     return torch.empty(max(size, 256), dtype=torch.uint8, device=device)
 
@@ -673,6 +674,7 @@ def _ssm_inputs(x, dt, a, b, c, skip, dt_bias, T):
         raise ValueError(f"b: expected shape [T, G, N], got {tuple(b.shape)}")
     _, H, P = x.shape
     _, G, N = b.shape
+    _check_int32(P, G, N)
     code = _storage_code(x, "x")
     if b.dtype is not x.dtype or c.dtype is not x.dtype:
         raise TypeError(f"b, c: expected {x.dtype}, got {b.dtype}, {c.dtype}")

@@ -224,6 +224,13 @@ def test_step_and_norm_bindings_check():
         kda.residual_norm(t(3, 16), t(3, 16, dtype=BF16), t(16))
     with pytest.raises(ValueError, match="int32"):
         kda.conv_prefill(torch.empty(1, device="meta").expand(2 ** 31, 8), t(8, 4))
+    with pytest.raises(ValueError, match="int32"):
+        kda.conv_prefill(t(9, 1), torch.empty(1, device="meta").expand(1, 2 ** 32 + 4))
+    with pytest.raises(ValueError, match="int32"):
+        wide = torch.empty(1, device="meta").expand(9, 1, 2 ** 32 + 16)
+        kda.ssm_prefill(t(9, 4, 32), t(9, 4), t(4), wide, wide)
+    with pytest.raises(ValueError, match="int32"):
+        kda.ssm_workspace(1, 9, 4, 2 ** 32 + 16, 32, "cpu")
 
 
 def test_oracle_forms_agree():
