@@ -156,12 +156,35 @@ __device__ __forceinline__ double lane_value(double x, int l) {
 }
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 
-// x = h + m + l in bf16, each the rest of the one before rounded to nearest.
-__device__ __forceinline__ void split3(f32x4 x, bf16x4& h, bf16x4& m, bf16x4& l) {
+// x - h, h the bf16 nearest to x: exact, and one instruction a value, the sum of
+// products of a pair of bf16 with (-1, 0) or (0, -1), where the pair taken apart takes
+// two (8192 tokens of 32 heads: states 35.0 -> 33.7 us, outputs 76.8 -> 75.0). The factors come from registers: as
+// an instruction's own constant, -1 stands in the wrong half of its pair.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+struct Minus {
+  bf16x2 lo, hi;
+};
+__device__ __forceinline__ Minus minus_one() {
+  uint32_t lo = 0xbf80u, hi = 0xbf800000u;
+  asm("" : "+s"(lo), "+s"(hi));
+  return {__builtin_bit_cast(bf16x2, lo), __builtin_bit_cast(bf16x2, hi)};
+}
+__device__ __forceinline__ f32x4 rest_of(f32x4 x, bf16x4 h, const Minus& m) {
+  const uint2 p = __builtin_bit_cast(uint2, h);
+  const bf16x2 a = __builtin_bit_cast(bf16x2, p.x), b = __builtin_bit_cast(bf16x2, p.y);
+  return f32x4{__builtin_amdgcn_fdot2_f32_bf16(a, m.lo, x[0], false), __builtin_amdgcn_fdot2_f32_bf16(a, m.hi, x[1], false),
+               __builtin_amdgcn_fdot2_f32_bf16(b, m.lo, x[2], false), __builtin_amdgcn_fdot2_f32_bf16(b, m.hi, x[3], false)};
+}
+// x = h + l, and x = h + m + l in bf16, each the rest of the one before rounded to nearest.
+__device__ __forceinline__ void split2(f32x4 x, bf16x4& h, bf16x4& l, const Minus& one) {
   h = to_bf16x4(x);
-  const f32x4 r = x - from_bf16x4(h);
+  l = to_bf16x4(rest_of(x, h, one));
+}
+__device__ __forceinline__ void split3(f32x4 x, bf16x4& h, bf16x4& m, bf16x4& l, const Minus& one) {
+  h = to_bf16x4(x);
+  const f32x4 r = rest_of(x, h, one);
   m = to_bf16x4(r);
-  l = to_bf16x4(r - from_bf16x4(m));
+  l = to_bf16x4(rest_of(r, m, one));
 }
 
 // What the tokens of a chunk need of d and a.
@@ -260,6 +283,7 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
   const char* gc = (const char*)((const bf16_bits*)a.c + p.first * a.c_stride + grp * N);
   const uint32_t xs = 2 * (uint32_t)a.x_stride, bs = 2 * (uint32_t)a.b_stride, cs = 2 * (uint32_t)a.c_stride;
   const int uwave = __builtin_amdgcn_readfirstlane(wave);
+  const Minus one = minus_one();
   // (columns behind the head's: the first ones again, nothing is made of them)
   const uint32_t xcol = col0 + 8 * (tid % XV) < a.P ? 16 * (tid % XV) : 0, bcol = 16 * (tid % NV);
   const uint32_t xoff = tid / XV * xs + xcol, boff = tid / NV * bs + bcol, coff = tid / NV * cs + bcol;
@@ -395,7 +419,7 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
           }
         }
         bf16x4 mh, ml;
-        split_bf16(x, mh, ml);
+        split2(x, mh, ml, one);
         const int at = (mr ^ 32 * (u / 2)) + 16 * tt * kL + 4 * (u & 1);
         if (id < kTiles) {
           *(bf16x4*)(sMh + at) = mh;
@@ -410,8 +434,8 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
 #pragma unroll
       for (int v = 0; v < KS; ++v) {
         bf16x4 h0, l0, h1 = {}, l1 = {};
-        split_bf16(s[2 * v], h0, l0);
-        if constexpr (NT > 1) split_bf16(s[2 * v + 1], h1, l1);
+        split2(s[2 * v], h0, l0, one);
+        if constexpr (NT > 1) split2(s[2 * v + 1], h1, l1, one);
         const bf16x8 sh = cat(h0, h1), sl = cat(l0, l1);
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
@@ -487,8 +511,8 @@ const bf16_bits* at = sX + x_turned + 32 * v * kCols;
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       bf16x4 h0, m0, l0, h1, m1, l1;
-      split3(from_bf16x4(lo_half(xo[v])) * *(const f32x4*)&q.w[32 * v + 4 * g], h0, m0, l0);
-      split3(from_bf16x4(hi_half(xo[v])) * *(const f32x4*)&q.w[32 * v + 16 + 4 * g], h1, m1, l1);
+      split3(from_bf16x4(lo_half(xo[v])) * *(const f32x4*)&q.w[32 * v + 4 * g], h0, m0, l0, one);
+      split3(from_bf16x4(hi_half(xo[v])) * *(const f32x4*)&q.w[32 * v + 16 + 4 * g], h1, m1, l1, one);
       const bf16x8 xh = cat(h0, h1), xm = cat(m0, m1), xl = cat(l0, l1);
 #pragma unroll
       for (int k = 0; k < NT; ++k) {
