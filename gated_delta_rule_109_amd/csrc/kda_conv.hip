@@ -6,17 +6,22 @@
 // 2 K operations and the activation per element against 2 elements of traffic:
 // bound by HBM. A thread owns V consecutive channels (16 bytes, or what a row has
 // left) and walks along the tokens with the last K - 1 rows in registers, so every
-// row is read once but for the K - 1 rows in front of a thread's first token.
+// row is read once but for the K - 1 rows in front of a thread's first token; four
+// rows are on their way while four are worked on. 8192 x 12288 bf16: 89 us, 4.5 TB/s,
+// where a copy of the same bytes takes 75 (without the activation the same: it is not
+// arithmetic); nine sequences of 3001 x 777 fp32 8.4 us.
 #include "kda_pack.h"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-// Tokens a thread walks along: as many as leave kPromptThreads threads, so that the
-// rows in front of them are read seldom, and at least the K - 1 that read the state.
+// Tokens a thread walks along: as many as leave kPromptThreads threads (two waves a
+// SIMD), so that the rows in front of them are read seldom, and at least the K - 1
+// that read the state. 2048 tokens of 12288 channels, bf16: 22.9 us, with a wave a
+// SIMD 25.4, with four 25.3; 8192 tokens by 8 a thread 105, by 16 96, by 64 89.
 constexpr int kMinTokens = 4, kMostTokens = 64;
-constexpr int64_t kPromptThreads = 256 * 4 * 2 * 64;   // two waves a SIMD
+constexpr int64_t kPromptThreads = 256 * 4 * 2 * 64;
 
 // Threads along the channels; the rest of the workgroup takes further tokens.
 int channel_threads(int vecs) {
@@ -155,8 +160,10 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(const T* x, int64_t
   }
 }
 
-// Sequences apart that a thread of a step takes: about kStepThreads threads.
-constexpr int64_t kStepThreads = 256 * 4 * 2 * 64;   // two waves a SIMD
+// Sequences apart that a thread of a step takes: about kStepThreads threads, a wave a
+// SIMD. 256 sequences of 12288 channels, bf16: 10.9 us (4.6 TB/s), with twice the
+// threads 11.4, half of them 14.8, a thread for every sequence 15.1.
+constexpr int64_t kStepThreads = 256 * 4 * 64;
 int step_groups(const ConvArgs& a) {
   const int64_t g = kStepThreads / vecs_of(a);
   return (int)(g < 1 ? 1 : g < a.N ? g : a.N);

@@ -2,8 +2,10 @@
 //
 // Both read every element once, keep a row in registers between the sum of its
 // squares and its use, and write once: bound by HBM. A row belongs to L threads
-// (4 to 64 lanes of a wave, then 256 or 1024 threads), each with up to I vectors
-// of it, so that a wave holds several short rows and a long one fits.
+// (4 to 64 lanes of a wave, then 128 to 1024 threads), each with up to I vectors
+// of it, so that a wave holds several short rows and a long one fits. 8192 x 32 heads
+// of 128, bf16: 37.5 us, 5.4 TB/s; residual norm of 8192 x 4096 with gate: 66 us, 5.1
+// TB/s (a copy reaches 5.3 to 5.4).
 #include "kda_pack.h"
 
 namespace kda {
@@ -32,7 +34,9 @@ __device__ __forceinline__ float row_sum(float x, int& turn) {
   return x;
 }
 
-// Most threads of a residual norm: four waves a SIMD.
+// Most threads of a residual norm, whose workgroups then take several rows: four
+// waves a SIMD. 4096 rows of 16384, bf16: 139 us, with two waves a SIMD 204, with
+// eight 145, a workgroup for every row 180; 8192 of 4096: 65, 63, 69, 65.
 constexpr int64_t kResidualThreads = 256 * 4 * 4 * 64;
 
 // (a row of more than a wave has a workgroup to itself)

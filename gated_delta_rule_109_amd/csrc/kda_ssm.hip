@@ -1003,9 +1003,12 @@ hipError_t launch_ssm(const SsmArgs& a) {
 hipError_t launch_ssm_step(const SsmArgs& a) {
   SsmParams p = params_of(a, 1);
   const int64_t heads = (int64_t)a.seqs.num_seqs * a.H;
-  // halves of the columns (of at least 16) until there are two workgroups a compute unit
+  // Halves of the columns until there are two workgroups a compute unit: 32 heads of
+  // 128 x 128 whole 5.4 us, in quarters 4.3; of 8 sequences whole 9.6, in halves 8.8, in
+  // quarters 11.2. Of at least 32 columns, a row's part a whole line: in parts of 16
+  // three sequences take 9.0 us, in parts of 32 5.3.
   int split = 1;
-  while (heads * split < 512 && a.P / split % 32 == 0) split *= 2;
+  while (heads * split < 512 && a.P / split % 64 == 0) split *= 2;
   const dim3 grid((unsigned)(heads * split));
   if (a.bf16) hipLaunchKernelGGL(ssm_step_kernel<bf16_bits>, grid, dim3(kThreads), 0, a.stream, p, a.N, split);
   else hipLaunchKernelGGL(ssm_step_kernel<float>, grid, dim3(kThreads), 0, a.stream, p, a.N, split);
