@@ -41,10 +41,18 @@ struct Split {
   int chunk;       // tokens: segments are whole chunks, at least two
   int whole;       // calls of at most so many tokens are not split
 };
-constexpr Split kFullSplit = {64, 512, 32, 160};      // fp32
-// (the chunks' workgroups have 8 waves where a head has more than 64 columns, else 4)
-constexpr Split kChunkSplit = {64, 512, KDA_SSM_CHUNK, 384}, kWideSplit = {128, 512, KDA_SSM_CHUNK, 384};
-const Split& split_of(bool bf16, int P) { return !bf16 ? kFullSplit : P <= 64 ? kChunkSplit : kWideSplit; }
+// (the chunks' workgroups have 8 waves where a head has more than 64 columns, else 4.
+// Of states of 256 rows a compute unit holds one workgroup, where more of them run in
+// turns: 8192 tokens of 16 heads 256 x 128 in one round 99 us, in two 153. Of smaller
+// states it holds two and more; 3 or 4 for 64 columns gain nothing: 32 heads of
+// 16 x 64 49 us, with 1024 workgroups 54)
+enum Kind { kF32, kNarrow, kWide };
+Split split_of(Kind k, int N) {
+  const int target = N == 256 ? 256 : 512;
+  if (k == kF32) return {64, target, 32, 160};
+  return {k == kWide ? 128 : 64, target, KDA_SSM_CHUNK, 384};
+}
+Split split_of(bool bf16, int N, int P) { return split_of(!bf16 ? kF32 : P <= 64 ? kNarrow : kWide, N); }
 int column_blocks(const Split& s, int P) { return (P + s.columns - 1) / s.columns; }
 
 int segment_len(const Packed& s, int H, int N, int P, const Split& sp) {
@@ -111,7 +119,19 @@ __device__ __forceinline__ f32x4* front_of(const SsmParams& a, const Part& p, in
 // lanes an LDS instruction serves at a time meet different banks: 16 rows at one
 // block (16 bytes a lane: lanes 0-3, 12-15, 20-23, 24-27 and so on), and 4 rows of
 // 16 columns (turned over: 16 lanes).
-constexpr int kL = KDA_SSM_CHUNK, kDies = 8;
+constexpr int kL = KDA_SSM_CHUNK;
+
+// Workgroups go to the 8 dies in turn. They are numbered so that kShare of those that
+// share B and C (a group's heads in a segment) are on one die and meet in its L2; not
+// more, or a few segments of many heads leave dies without work (8192 tokens of 128
+// heads 128 x 64 in one group: all of a segment on a die 419 us, eight 220).
+constexpr int kDies = 8, kShare = 8;
+__host__ __device__ __forceinline__ int shared_groups(int heads, int blocks) {
+  return (int64_t)heads * blocks < kShare ? heads * blocks : kShare;
+}
+__device__ __forceinline__ int numbered(int share) {
+  return (blockIdx.x / (kDies * share) * kDies + blockIdx.x % kDies) * share + blockIdx.x / kDies % share;
+}
 
 // Block b of row 16 k + l is kept at b ^ row_mask(l), by the row's bf16 elements. A
 // lane keeps one place in each array; others are that one XOR a constant (other
@@ -228,10 +248,7 @@ template <int N, int W, bool outputs>
 __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_kernel(SsmParams a) {
   constexpr int kThreads = 64 * W, kCols = 16 * W, NP = N < 32 ? 32 : N, KS = NP / 32, NT = N / 16, NV = N / 8;
   const int pblocks = (a.P + kCols - 1) / kCols;
-  // Workgroups go to the 8 dies in turn: numbered so that those that share B and C
-  // (a group's heads in a segment) are on one die and meet in its L2.
-  const int share = a.H / a.G * pblocks;
-  const int id = (blockIdx.x / (kDies * share) * kDies + blockIdx.x % kDies) * share + blockIdx.x / kDies % share;
+  const int id = numbered(shared_groups(a.H / a.G, pblocks));
   const int pb = id % pblocks, h = id / pblocks % a.H;
   Part p;
   if (!find_part(a.seqs, a.len, id / pblocks / a.H, p)) return;
@@ -563,8 +580,7 @@ template <int N, bool outputs>
 __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk32_kernel(SsmParams a) {
   constexpr int kThreads = 256, kCols = 64, L = kL32, NT = N / 16, NV = N / 4;
   const int pblocks = (a.P + kCols - 1) / kCols;
-  const int share = a.H / a.G * pblocks;
-  const int id = (blockIdx.x / (kDies * share) * kDies + blockIdx.x % kDies) * share + blockIdx.x / kDies % share;
+  const int id = numbered(shared_groups(a.H / a.G, pblocks));
   const int pb = id % pblocks, h = id / pblocks % a.H;
   Part p;
   if (!find_part(a.seqs, a.len, id / pblocks / a.H, p)) return;
@@ -932,7 +948,7 @@ size_t end_bytes(int H, int N, int P, const Split& sp) { return (size_t)H * colu
 
 // Workgroups: whole rounds of the dies (the last ones have no segment).
 int64_t launch_groups(const SsmArgs& a, const Split& sp) {
-  const int64_t blocks = column_blocks(sp, a.P), round = kDies * (a.H / a.G * blocks);
+  const int64_t blocks = column_blocks(sp, a.P), round = kDies * shared_groups(a.H / a.G, blocks);
   const int64_t groups = part_slots(a.seqs, segment_len(a.seqs, a.H, a.N, a.P, sp)) * a.H * blocks;
   return (groups + round - 1) / round * round;
 }
@@ -957,7 +973,7 @@ hipError_t launch_passes(K states, K outputs, const SsmArgs& a, const Split& sp,
 }
 template <int N>
 hipError_t launch_n(const SsmArgs& a) {
-  const Split& sp = split_of(a.bf16, a.P);
+  const Split sp = split_of(a.bf16, a.N, a.P);
   if (!a.bf16) return launch_passes(ssm_chunk32_kernel<N, false>, ssm_chunk32_kernel<N, true>, a, sp, 4 * sp.columns);
   return a.P <= 64 ? launch_passes(ssm_chunk_kernel<N, 4, false>, ssm_chunk_kernel<N, 4, true>, a, sp, 4 * sp.columns) : launch_passes(ssm_chunk_kernel<N, 8, false>, ssm_chunk_kernel<N, 8, true>, a, sp, 4 * sp.columns);
 }
@@ -972,7 +988,7 @@ size_t workspace_of(int32_t T, int32_t H, int32_t N, int32_t P, const Split& sp)
 }  // namespace
 
 int64_t ssm_threads(const SsmArgs& a) {
-  const Split& sp = split_of(a.bf16, a.P);
+  const Split sp = split_of(a.bf16, a.N, a.P);
   return launch_groups(a, sp) * 4 * sp.columns;
 }
 
@@ -982,9 +998,9 @@ int64_t ssm_threads(const SsmArgs& a) {
 size_t ssm_workspace(int32_t num_seqs, int32_t T, int32_t H, int32_t N, int32_t P) {
   (void)num_seqs;
   size_t most = 0;
-  for (const Split* sp : {&kFullSplit, &kChunkSplit, &kWideSplit}) {
-    if (sp == &kWideSplit && P <= 64) continue;
-    const size_t w = workspace_of(T, H, N, P, *sp);
+  for (const Kind k : {kF32, kNarrow, kWide}) {
+    if (k == kWide && P <= 64) continue;
+    const size_t w = workspace_of(T, H, N, P, split_of(k, N));
     most = w > most ? w : most;
   }
   return most;

@@ -209,6 +209,9 @@ SSM = [
     ([300, 300], (0, 0), 3, 3, 16, 16, BF16, True, True, True, 0, 500.0),        # decays that underflow
     ([300, 300], (0, 0), 1, 1, 16, 16, F32, True, True, True, 0, 500.0),
     ([10] * 30, (0, 0), 2, 1, 16, 16, BF16, True, True, True, 0, 4.0),
+    ([420, 30], (0, 0), 26, 2, 16, 32, BF16, True, True, True, 0, 4.0),          # 13 heads share B and C
+    ([170, 30], (0, 0), 9, 1, 16, 144, F32, True, True, True, 0, 4.0),           # 9 heads of three column blocks
+    ([700, 500], (0, 0), 3, 1, 256, 80, BF16, True, True, True, 0, 0.5),
 ]
 
 
