@@ -73,17 +73,18 @@ __device__ __forceinline__ bits_t<T, V> conv_token(float (&past)[K - 1][V], bits
   return to_bits<T, V>(out);
 }
 
-template <typename T, int K>
+template <typename T, int K, bool whole>
 __global__ __launch_bounds__(kThreads) void conv_kernel(const T* x, int64_t x_stride, const float* weight,
                                                         const float* bias, Packed seqs, int C, int tokens,
                                                         int chan_threads, int chan_blocks, bool silu, const T* initial, T* final_state,
                                                         T* y) {
   constexpr int V = vec_of<T>();
   const int cb = blockIdx.x % chan_blocks, slot = blockIdx.x / chan_blocks;
-  const int c = (cb * chan_threads + (int)threadIdx.x % chan_threads) * V, n = min(V, C - c);
+  const VecAt<V, whole> at = vec_at<V, whole>(cb * chan_threads + (int)threadIdx.x % chan_threads, C);
+  const int c = at.c;
   const int row = threadIdx.x / chan_threads;     // which run of `tokens` tokens
   Part p;
-  if (!find_part(seqs, kThreads / chan_threads * tokens, slot, p) || n <= 0) return;
+  if (!find_part(seqs, kThreads / chan_threads * tokens, slot, p) || !at.on) return;
   const int first = p.first + row * tokens;
   const int count = min(tokens, p.first + p.count - first);
   // the rows in front: of the sequence, or of its state (row r of the state is
@@ -93,18 +94,18 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(const T* x, int64_t x_st
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
       const int t = first - (K - 1) + j;
-      if (t >= p.start) from_bits<T, V>(load_first<T, V>(x + t * x_stride + c, n), past[j]);
+      if (t >= p.start) from_bits<T, V>(load_row<whole, T, V>(x + t * x_stride + c, C), past[j]);
       else if (initial)
-        from_bits<T, V>(load_first<T, V>(initial + ((size_t)p.n * (K - 1) + t - p.start + K - 1) * C + c, n), past[j]);
+        from_bits<T, V>(load_row<whole, T, V>(initial + ((size_t)p.n * (K - 1) + t - p.start + K - 1) * C + c, C), past[j]);
     }
     float w[V * K], b[V];
-    load_weights<V, K>(weight, bias, c, n, w, b);
+    load_weights<V, K>(weight, bias, c, min(V, C), w, b);
     constexpr int U = 4;   // rows on their way while as many are worked on
     bits_t<T, V> rows[U], next[U];
     auto load = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        next[u] = load_first<T, V>(x + (int64_t)(first + min(t0 + u, count - 1)) * x_stride + c, n);
+        next[u] = load_row<whole, T, V>(x + (int64_t)(first + min(t0 + u, count - 1)) * x_stride + c, C);
     };
     load(0);
     for (int t0 = 0; t0 < count; t0 += U) {
@@ -114,20 +115,22 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(const T* x, int64_t x_st
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (t0 + u < count)
-          store_first<T, V>(y + (size_t)(first + t0 + u) * C + c, conv_token<T, V, K>(past, rows[u], w, b, silu), n);
+          store_row<whole, T, V>(y + (size_t)(first + t0 + u) * C + c, conv_token<T, V, K>(past, rows[u], w, b, silu), at.skip, C);
     }
   }
   // The state after the sequence, by the threads that alone read the state
-  // before it (the first K - 1 tokens are theirs): it may be the same array.
+  // before it (the first K - 1 tokens are theirs): it may be the same array. (A row's
+  // last vector also reads channels of the one in front, maybe after they are written;
+  // it writes nothing of them.)
   // Row i comes from row length + i of the state, not from a row before i.
   if (final_state && p.j == 0 && row == 0) {
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) {
       const int t = p.length - (K - 1) + i;
       bits_t<T, V> v = {};
-      if (t >= 0) v = load_first<T, V>(x + (int64_t)(p.start + t) * x_stride + c, n);
-      else if (initial) v = load_first<T, V>(initial + ((size_t)p.n * (K - 1) + p.length + i) * C + c, n);
-      store_first<T, V>(final_state + ((size_t)p.n * (K - 1) + i) * C + c, v, n);
+      if (t >= 0) v = load_row<whole, T, V>(x + (int64_t)(p.start + t) * x_stride + c, C);
+      else if (initial) v = load_row<whole, T, V>(initial + ((size_t)p.n * (K - 1) + p.length + i) * C + c, C);
+      store_row<whole, T, V>(final_state + ((size_t)p.n * (K - 1) + i) * C + c, v, at.skip, C);
     }
   }
 }
@@ -135,28 +138,29 @@ static_assert(kMinTokens >= KDA_CONV_MAX_WIDTH - 1, "the first K - 1 tokens are 
 
 // One token: a thread takes the sequences n, n + groups, .. for its channels, whose
 // weights (more bytes than a row and its state) it reads once.
-template <typename T, int K>
+template <typename T, int K, bool whole>
 __global__ __launch_bounds__(kThreads) void conv_step_kernel(const T* x, int64_t x_stride, const float* weight,
                                                              const float* bias, int N, int C, int vecs, int groups,
                                                              bool silu, T* state, T* y) {
   constexpr int V = vec_of<T>();
   const uint32_t id = blockIdx.x * kThreads + threadIdx.x;
   if (id >= (uint32_t)groups * vecs) return;
-  const int c = (int)(id % vecs) * V, m = min(V, C - c);
+  const VecAt<V, whole> at = vec_at<V, whole>(id % vecs, C);
+  const int c = at.c;
   float w[V * K], b[V];
-  load_weights<V, K>(weight, bias, c, m, w, b);
+  load_weights<V, K>(weight, bias, c, min(V, C), w, b);
   for (int n = id / vecs; n < N; n += groups) {
     T* s = state + (size_t)n * (K - 1) * C + c;
     bits_t<T, V> rows[K];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) rows[j] = load_first<T, V>(s + (size_t)j * C, m);
-    rows[K - 1] = load_first<T, V>(x + n * x_stride + c, m);
+    for (int j = 0; j < K - 1; ++j) rows[j] = load_row<whole, T, V>(s + (size_t)j * C, C);
+    rows[K - 1] = load_row<whole, T, V>(x + n * x_stride + c, C);
     float past[K - 1][V];
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) from_bits<T, V>(rows[j], past[j]);
-    store_first<T, V>(y + (size_t)n * C + c, conv_token<T, V, K>(past, rows[K - 1], w, b, silu), m);
+    store_row<whole, T, V>(y + (size_t)n * C + c, conv_token<T, V, K>(past, rows[K - 1], w, b, silu), at.skip, C);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) store_first<T, V>(s + (size_t)j * C, rows[j + 1], m);
+    for (int j = 0; j < K - 1; ++j) store_row<whole, T, V>(s + (size_t)j * C, rows[j + 1], at.skip, C);
   }
 }
 
@@ -169,31 +173,35 @@ int step_groups(const ConvArgs& a) {
   return (int)(g < 1 ? 1 : g < a.N ? g : a.N);
 }
 
-template <typename T, int K>
+template <typename T, int K, bool whole>
 hipError_t launch_k(const ConvArgs& a, bool step) {
   const int vecs = vecs_of(a);
   if (step) {
     const int groups = step_groups(a);
     const int64_t n = (int64_t)groups * vecs;
-    hipLaunchKernelGGL((conv_step_kernel<T, K>), dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+    hipLaunchKernelGGL((conv_step_kernel<T, K, whole>), dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0,
                        a.stream, (const T*)a.x, a.x_stride, a.weight, a.bias, a.N, a.C, vecs, groups, a.silu,
                        (T*)a.initial_state, (T*)a.y);
     return hipGetLastError();
   }
   const int tokens = tokens_of(a), ct = channel_threads(vecs), blocks = (vecs + ct - 1) / ct;
   const int64_t slots = part_slots(a.seqs, kThreads / ct * tokens);
-  hipLaunchKernelGGL((conv_kernel<T, K>), dim3((unsigned)(slots * blocks)), dim3(kThreads), 0, a.stream, (const T*)a.x,
+  hipLaunchKernelGGL((conv_kernel<T, K, whole>), dim3((unsigned)(slots * blocks)), dim3(kThreads), 0, a.stream, (const T*)a.x,
                      a.x_stride, a.weight, a.bias, a.seqs, a.C, tokens, ct, blocks, a.silu, (const T*)a.initial_state,
                      (T*)a.final_state, (T*)a.y);
   return hipGetLastError();
 }
+template <typename T, bool whole>
+hipError_t launch_w(const ConvArgs& a, bool step) {
+  switch (a.width) {
+    case 2: return launch_k<T, 2, whole>(a, step);
+    case 3: return launch_k<T, 3, whole>(a, step);
+    default: return launch_k<T, 4, whole>(a, step);
+  }
+}
 template <typename T>
 hipError_t launch_t(const ConvArgs& a, bool step) {
-  switch (a.width) {
-    case 2: return launch_k<T, 2>(a, step);
-    case 3: return launch_k<T, 3>(a, step);
-    default: return launch_k<T, 4>(a, step);
-  }
+  return a.C % vec_of<T>() == 0 ? launch_w<T, true>(a, step) : launch_w<T, false>(a, step);
 }
 
 }  // namespace

@@ -53,7 +53,7 @@ __device__ __forceinline__ float inv_rms(const float (&v)[I][V], int D, float ep
   return rsqrtf(row_sum<L>(s, turn) * (1.0f / (float)D) + eps);
 }
 
-template <typename T, int V, int L, int I>
+template <typename T, int V, bool whole, int L, int I>
 __global__ __launch_bounds__(threads_of<L>()) void gated_norm_kernel(const T* x, int64_t x_stride, const T* gate,
                                                                      int64_t gate_stride, const float* weight,
                                                                      bool per_head, int64_t rows, int H, int D, int act,
@@ -69,20 +69,24 @@ __global__ __launch_bounds__(threads_of<L>()) void gated_norm_kernel(const T* x,
   float v[I][V], g[I][V];
 #pragma unroll
   for (int i = 0; i < I; ++i) {
-    const int d = (lane + i * L) * V;
+    const VecAt<V, whole> at = vec_at<V, whole>(lane + i * L, D);
 #pragma unroll
     for (int e = 0; e < V; ++e) v[i][e] = 0.f, g[i][e] = 1.f;
-    if (live && d < D) {
-      from_bits<T, V>(load_first<T, V>(px + d, D - d), v[i]);
+    if (live && at.on) {
+      from_bits<T, V>(load_row<whole, T, V>(px + at.c, D), v[i]);
+      if (at.skip) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[i][e] = e < at.skip ? 0.f : v[i][e];
+      }
       if (pg) {
-        from_bits<T, V>(load_first<T, V>(pg + d, D - d), g[i]);
+        from_bits<T, V>(load_row<whole, T, V>(pg + at.c, D), g[i]);
 #pragma unroll
         for (int e = 0; e < V; ++e) g[i][e] = activate<T>(g[i][e], act);
       }
     }
     if (gate_first) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[i][e] *= g[i][e], g[i][e] = 1.f;
+      for (int e = 0; e < V; ++e) v[i][e] = e < at.skip ? 0.f : v[i][e] * g[i][e], g[i][e] = 1.f;
     }
   }
   int turn = 0;
@@ -92,21 +96,22 @@ __global__ __launch_bounds__(threads_of<L>()) void gated_norm_kernel(const T* x,
   T* py = y + r * D;
 #pragma unroll
   for (int i = 0; i < I; ++i) {
-    const int d = (lane + i * L) * V;
-    if (d < D) {
+    const VecAt<V, whole> at = vec_at<V, whole>(lane + i * L, D);
+    if (at.on) {
       float o[V];
-      load_params<V>(w + d, D - d, 0.f, o);
+      load_params<V>(w + at.c, min(V, D), 0.f, o);
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] *= v[i][e] * s * g[i][e];
-      store_first<T, V>(py + d, to_bits<T, V>(o), D - d);
+      store_row<whole, T, V>(py + at.c, to_bits<T, V>(o), at.skip, D);
     }
   }
 }
 
 // A workgroup takes rows `step` apart, with its columns' weights in registers for
 // all of them (they are fp32: a row's weights are more bytes than the row) and the
-// next row's loads on their way while it works on one.
-template <typename T, int V, int L, int I>
+// next row's loads on their way while it works on one. Rows of more than 8192 elements
+// leave no registers for the weights: they are read for each row.
+template <typename T, int V, bool whole, int L, int I>
 __global__ __launch_bounds__(threads_of<L>()) void residual_norm_kernel(const T* x, const T* residual, const T* gate,
                                                                         const float* weight, const float* post,
                                                                         const float* scale, int64_t rows, int64_t step,
@@ -114,34 +119,41 @@ __global__ __launch_bounds__(threads_of<L>()) void residual_norm_kernel(const T*
                                                                         T* residual_out, T* y) {
   const int lane = threadIdx.x % L;
   const int64_t r0 = (int64_t)blockIdx.x * (threads_of<L>() / L);
+  constexpr bool kKeep = I * V < 16;
   float w[I][V], pw[I][V], k[I][V];
   bits_t<T, V> nx[I] = {}, nr[I] = {}, ng[I] = {};
-  auto left = [&](int i) { return C - (lane + i * L) * V; };   // columns from a vector's first one on
+  auto vec = [&](int i) { return vec_at<V, whole>(lane + i * L, C); };
   // (threads without a row stay for the sums of their wave)
   auto load = [&](int64_t r) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < I; ++i)
-      if (r < rows && left(i) > 0) {
-        const int64_t at = r * C + (lane + i * L) * V;
-        nx[i] = load_first<T, V>(x + at, left(i));
-        if (residual) nr[i] = load_first<T, V>(residual + at, left(i));
-        if (gate) ng[i] = load_first<T, V>(gate + at, left(i));
+      if (r < rows && vec(i).on) {
+        const int64_t at = r * C + vec(i).c;
+        nx[i] = load_row<whole, T, V>(x + at, C);
+        if (residual) nr[i] = load_row<whole, T, V>(residual + at, C);
+        if (gate) ng[i] = load_row<whole, T, V>(gate + at, C);
       }
   };
   load(r0 + threadIdx.x / L);
+  auto params = [&](int i) __attribute__((always_inline)) {
+    const int c = vec(i).c;
 #pragma unroll
-  for (int i = 0; i < I; ++i) {
-    const int c = (lane + i * L) * V;
-#pragma unroll
-    for (int e = 0; e < V; ++e) w[i][e] = 0.f, pw[i][e] = k[i][e] = 1.f;
-    if (left(i) > 0) {
-      load_params<V>(weight + c, left(i), 0.f, w[i]);
-      if (post) load_params<V>(post + c, left(i), 0.f, pw[i]);
-      if (scale) load_params<V>(scale + c, left(i), 0.f, k[i]);
+    for (int e = 0; e < V; ++e) pw[i][e] = k[i][e] = 1.f;
+    if (vec(i).on) {
+      if (post) load_params<V>(post + c, min(V, C), 0.f, pw[i]);
+      if (scale) load_params<V>(scale + c, min(V, C), 0.f, k[i]);
     }
 #pragma unroll
     for (int e = 0; e < V; ++e) k[i][e] *= alpha;
-  }
+  };
+  auto weights = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[i][e] = 0.f;
+    if (vec(i).on) load_params<V>(weight + vec(i).c, min(V, C), 0.f, w[i]);
+  };
+  if (kKeep)
+#pragma unroll
+    for (int i = 0; i < I; ++i) params(i), weights(i);
   const int64_t mine = threadIdx.x / L;
   int turn = 0;
   for (int64_t rb = r0; rb < rows; rb += step) {
@@ -152,33 +164,41 @@ __global__ __launch_bounds__(threads_of<L>()) void residual_norm_kernel(const T*
       from_bits<T, V>(nx[i], v[i]);
       from_bits<T, V>(nr[i], res[i]);
       from_bits<T, V>(ng[i], g[i]);
+      const int skip = vec(i).skip;
+      if (skip) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[i][e] = e < skip ? 0.f : v[i][e];
+      }
     }
     load(r + step);
     const float s = post ? inv_rms<L, I, V>(v, C, eps, turn) : 1.f;
 #pragma unroll
-    for (int i = 0; i < I; ++i)
+    for (int i = 0; i < I; ++i) {
+      const VecAt<V, whole> at = vec(i);
+      if (!kKeep) params(i);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         float u = v[i][e];
         if (post) u = u * s * pw[i][e];
         if (gate) u *= activate<T>(g[i][e], act);
-        // (columns behind the row's last: residual and v are 0 there, and s may not be finite)
-        v[i][e] = e < left(i) ? res[i][e] + k[i][e] * u : 0.f;
+        // (columns of the vector in front, and behind the row's last, count for nothing)
+        v[i][e] = at.owns(e, C) ? res[i][e] + k[i][e] * u : 0.f;
       }
+    }
     const bool live = r < rows;
     if (residual_out)
 #pragma unroll
       for (int i = 0; i < I; ++i)
-        if (live && left(i) > 0)
-          store_first<T, V>(residual_out + r * C + (lane + i * L) * V, to_bits<T, V>(v[i]), left(i));
+        if (live && vec(i).on) store_row<whole, T, V>(residual_out + r * C + vec(i).c, to_bits<T, V>(v[i]), vec(i).skip, C);
     const float q = inv_rms<L, I, V>(v, C, eps, turn);
 #pragma unroll
     for (int i = 0; i < I; ++i)
-      if (live && left(i) > 0) {
+      if (live && vec(i).on) {
+        if (!kKeep) weights(i);
         float o[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] = v[i][e] * q * w[i][e];
-        store_first<T, V>(y + r * C + (lane + i * L) * V, to_bits<T, V>(o), left(i));
+        store_row<whole, T, V>(y + r * C + vec(i).c, to_bits<T, V>(o), vec(i).skip, C);
       }
   }
 }
@@ -198,29 +218,29 @@ void by_length(int n, F&& f) {
   else if (n <= 512) KDA_ROW(512, 1);
   else if (n <= 1024) KDA_ROW(1024, 1);
   else if (V > 4 || n <= 2048) KDA_ROW(1024, 2);
-  else KDA_ROW(1024, 4);
+  else if constexpr (V <= 4) KDA_ROW(1024, 4);
 #undef KDA_ROW
 }
 static_assert(KDA_NORM_MAX <= 1024 * 2 * 8 && KDA_NORM_MAX <= 1024 * 4 * 4, "longest rows");
 
-template <typename T, int V>
+template <typename T, int V, bool whole>
 void gated_t(const GatedNormArgs& a) {
   const int64_t rows = (int64_t)a.T * a.H;
   by_length<V>((a.D + V - 1) / V, [&](auto L, auto I) {
     constexpr int l = decltype(L)::value, i = decltype(I)::value, per = threads_of<l>() / l;
-    hipLaunchKernelGGL((gated_norm_kernel<T, V, l, i>), dim3((unsigned)((rows + per - 1) / per)),
+    hipLaunchKernelGGL((gated_norm_kernel<T, V, whole, l, i>), dim3((unsigned)((rows + per - 1) / per)),
                        dim3(threads_of<l>()), 0, a.stream, (const T*)a.x, a.x_stride, (const T*)a.gate, a.gate_stride,
                        a.weight, a.weight_per_head, rows, a.H, a.D, a.act, a.gate_first, a.eps, (T*)a.y);
   });
 }
-template <typename T, int V>
+template <typename T, int V, bool whole>
 void residual_t(const ResidualNormArgs& a) {
   by_length<V>((a.C + V - 1) / V, [&](auto L, auto I) {
     constexpr int l = decltype(L)::value, i = decltype(I)::value, per = threads_of<l>() / l;
     int64_t groups = ((int64_t)a.T + per - 1) / per;
     const int64_t most = kResidualThreads / threads_of<l>();
     if (groups > most) groups = most;
-    hipLaunchKernelGGL((residual_norm_kernel<T, V, l, i>), dim3((unsigned)groups), dim3(threads_of<l>()), 0, a.stream,
+    hipLaunchKernelGGL((residual_norm_kernel<T, V, whole, l, i>), dim3((unsigned)groups), dim3(threads_of<l>()), 0, a.stream,
                        (const T*)a.x, (const T*)a.residual, (const T*)a.gate, a.weight, a.post_weight, a.scale,
                        (int64_t)a.T, groups * per, a.C, a.act, a.alpha, a.eps, (T*)a.residual_out, (T*)a.y);
   });
@@ -240,14 +260,14 @@ int64_t gated_threads(const GatedNormArgs& a) {
 }
 
 hipError_t launch_gated_norm(const GatedNormArgs& a) {
-  if (a.bf16) gated_t<bf16_bits, 8>(a);
-  else gated_t<float, 4>(a);
+  if (a.bf16) a.D % 8 == 0 ? gated_t<bf16_bits, 8, true>(a) : gated_t<bf16_bits, 8, false>(a);
+  else a.D % 4 == 0 ? gated_t<float, 4, true>(a) : gated_t<float, 4, false>(a);
   return hipGetLastError();
 }
 
 hipError_t launch_residual_norm(const ResidualNormArgs& a) {
-  if (a.bf16) residual_t<bf16_bits, 8>(a);
-  else residual_t<float, 4>(a);
+  if (a.bf16) a.C % 8 == 0 ? residual_t<bf16_bits, 8, true>(a) : residual_t<bf16_bits, 8, false>(a);
+  else a.C % 4 == 0 ? residual_t<float, 4, true>(a) : residual_t<float, 4, false>(a);
   return hipGetLastError();
 }
 

@@ -64,6 +64,8 @@ CONV = [
     ([700], (0, 0), 777, 3, F32, 1, True, False, 0),
     ([64] * 40, (0, 0), 16, 4, F32, 0, False, True, 0),
     ([0, 0], (3, 4), 16, 4, BF16, 1, False, True, 0),
+    ([40, 1, 300, 2], (1, 1), 2059, 4, BF16, 1, True, True, 1),
+    ([40, 0, 300, 3], (0, 2), 1027, 3, F32, 1, True, True, 0),
 ]
 
 
@@ -147,7 +149,8 @@ def test_conv_in_parts_and_by_steps(dtype, C, K):
 
 @pytest.mark.parametrize("N,C,K,dtype,act,bias,pad", [
     (1, 1, 2, F32, 1, True, 0), (3, 12288, 4, BF16, 1, False, 8), (257, 40, 3, BF16, 0, True, 0),
-    (5, 777, 3, F32, 1, True, 1), (130, 17, 4, BF16, 1, True, 0)])
+    (5, 777, 3, F32, 1, True, 1), (130, 17, 4, BF16, 1, True, 0),
+    (300, 4099, 4, BF16, 1, True, 3), (9, 12285, 2, BF16, 1, False, 0)])
 def test_conv_step(N, C, K, dtype, act, bias, pad):
     x, w, b, s, cu = conv_inputs([1] * N, (0, 0), C, K, dtype, bias, True, pad, N)
     ref, bound, states = layer.conv(host(x), host(w), host(b), cu, host(s), act)
@@ -393,6 +396,42 @@ def test_norm_rows_stay_apart():
     assert torch.equal(y2[keep], y[keep]) and torch.isnan(y2[7, 1]).all() and (y2[8, 2] == 0).all()
     r, z = kda.residual_norm(x[:, 0].contiguous(), None, w, post_weight=w, eps=0.0)
     assert torch.isfinite(z).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_of_every_length_up_to_three_vectors(dtype):
+    """Rows shorter than a vector, whole vectors and every length of a last one; in
+    place where a call allows it, with guards behind the rows."""
+    rng = np.random.default_rng(4)
+    T = 67
+    for C in range(1, 26):
+        x, w, b, s, cu = conv_inputs([20, 0, T - 20], (0, 0), C, 3, dtype, True, True, 0, C)
+        ref, bound, states = layer.conv(host(x), host(w), host(b), cu, host(s), 1)
+        out = torch.full((T * C + 64,), 7.0, dtype=dtype, device=DEV)
+        y, state = out[:T * C].view(T, C), s.clone()
+        kda.conv_prefill(x, w, b, cu_seqlens=device_cu(cu), initial_state=state, final_state=state, y=y)
+        check(y, ref, bound, f"convolution of {C}")
+        assert np.array_equal(host(state), states) and (out[T * C:] == 7).all()
+        _, _, _, s, cu = conv_inputs([1] * T, (0, 0), C, 3, dtype, True, True, 0, C)
+        ref, bound, states = layer.conv(host(x), host(w), host(b), cu, host(s), 1)
+        kda.conv_step(x, w, s, b, y=y)
+        check(y, ref, bound, f"steps of {C}")
+        assert np.array_equal(host(s), states) and (out[T * C:] == 7).all()
+        g, r = dev(rng.normal(size=(T, C)), dtype), dev(rng.normal(size=(T, C)), dtype)
+        nw, p = dev(rng.normal(size=C)), dev(rng.normal(size=C))
+        for first in (False, True):
+            kda.gated_norm(x[:, None], g[:, None], nw, gate_first=first, y=y[:, None])
+            ref, bound = layer.gated_norm(host(x)[:, None], host(g)[:, None], host(nw), 2, first, float(np.float32(1e-6)))
+            check(y[:, None], ref, bound, f"gated norm of {C}")
+        res, rb, ref, bound = layer.residual_norm(host(x), host(r), host(nw), host(p), host(g), 2, host(nw), 0.5,
+                                                  float(np.float32(1e-6)))
+        same = torch.full((T * C + 64,), 7.0, dtype=dtype, device=DEV)
+        same[:T * C] = r.reshape(-1)
+        rows = same[:T * C].view(T, C)
+        kda.residual_norm(x, rows, nw, p, g, 2, nw, 0.5, residual_out=rows, y=y)
+        check(rows, res, rb, f"residual of {C}")
+        check(y, ref, bound, f"residual norm of {C}")
+        assert (out[T * C:] == 7).all() and (same[T * C:] == 7).all()
 
 
 # ---- streams, graphs, far offsets, whole layers --------------------------------------------
