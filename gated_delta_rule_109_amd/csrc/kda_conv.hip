@@ -165,8 +165,9 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(const T* x, int64_t
 }
 
 // Sequences apart that a thread of a step takes: about kStepThreads threads, a wave a
-// SIMD. 256 sequences of 12288 channels, bf16: 10.9 us (4.6 TB/s), with twice the
-// threads 11.4, half of them 14.8, a thread for every sequence 15.1.
+// SIMD. 256 sequences of 12288 channels, bf16: 10.4 us, 4.9 TB/s; before a step of
+// whole vectors had its own kernel 10.9, with twice the threads 11.4, half of them 14.8,
+// a thread for every sequence 15.1.
 constexpr int64_t kStepThreads = 256 * 4 * 64;
 int step_groups(const ConvArgs& a) {
   const int64_t g = kStepThreads / vecs_of(a);

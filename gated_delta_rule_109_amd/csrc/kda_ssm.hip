@@ -119,6 +119,15 @@ __device__ __forceinline__ f32x4* front_of(const SsmParams& a, const Part& p, in
 // lanes an LDS instruction serves at a time meet different banks: 16 rows at one
 // block (16 bytes a lane: lanes 0-3, 12-15, 20-23, 24-27 and so on), and 4 rows of
 // 16 columns (turned over: 16 lanes).
+//
+// 8192 tokens of 32 heads 128 x 128: states 34 us, fronts 13, outputs 75, where the
+// bytes take 32 (copies reach 5.35 TB/s) and the products as written 31 (98 a chunk
+// and wave in the outputs' launch, 48 in the other). Neither bounds it: vector
+// instructions, matrix instructions and LDS are at work for 33, 21 and 28 us of the
+// outputs' 75, four waves a SIMD that wait for each other at three barriers a chunk. A
+// third workgroup a compute unit (M in the place of C, 64 columns) changes nothing;
+// scaling the state as it is split spills, 80 us; eight waves of 128 columns share B,
+// C and M among twice the columns of four.
 constexpr int kL = KDA_SSM_CHUNK;
 
 // Workgroups go to the 8 dies in turn. They are numbered so that kShare of those that
@@ -192,8 +201,9 @@ __device__ __forceinline__ Minus minus_one() {
 __device__ __forceinline__ f32x4 rest_of(f32x4 x, bf16x4 h, const Minus& m) {
   const uint2 p = __builtin_bit_cast(uint2, h);
   const bf16x2 a = __builtin_bit_cast(bf16x2, p.x), b = __builtin_bit_cast(bf16x2, p.y);
-  return f32x4{__builtin_amdgcn_fdot2_f32_bf16(a, m.lo, x[0], false), __builtin_amdgcn_fdot2_f32_bf16(a, m.hi, x[1], false),
-               __builtin_amdgcn_fdot2_f32_bf16(b, m.lo, x[2], false), __builtin_amdgcn_fdot2_f32_bf16(b, m.hi, x[3], false)};
+  return f32x4{
+      __builtin_amdgcn_fdot2_f32_bf16(a, m.lo, x[0], false), __builtin_amdgcn_fdot2_f32_bf16(a, m.hi, x[1], false),
+      __builtin_amdgcn_fdot2_f32_bf16(b, m.lo, x[2], false), __builtin_amdgcn_fdot2_f32_bf16(b, m.hi, x[3], false)};
 }
 // x = h + l, and x = h + m + l in bf16, each the rest of the one before rounded to nearest.
 __device__ __forceinline__ void split2(f32x4 x, bf16x4& h, bf16x4& l, const Minus& one) {
@@ -467,7 +477,7 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
     }
     // ---- x of the wave's columns: operands of both products
     auto x_operand = [&](int v) __attribute__((always_inline)) {
-const bf16_bits* at = sX + x_turned + 32 * v * kCols;
+      const bf16_bits* at = sX + x_turned + 32 * v * kCols;
       return cat(read_turned(at), read_turned(at + 16 * kCols));
     };
     bf16x8 xo[2] = {x_operand(0), x_operand(1)};
@@ -567,7 +577,11 @@ const bf16_bits* at = sX + x_turned + 32 * v * kCols;
 // workgroup, 16 a wave. As operand a lane holds 4 values along the sum, each for
 // one of four products: the accumulators of a tile are that operand as they are
 // (rows 16 k + 4 g + i, i the product), and 4 channels or tokens are one read.
-// Layouts as above, with blocks of 4 fp32.
+// Layouts as above, with blocks of 4 fp32. 8192 tokens of 32 heads 128 x 128: 346 us,
+// of which the products take 139 at the rate of a large fp32 product (154 TFLOP/s) in
+// the launch with outputs, and 2/5 of that again in the one for states; nine sequences
+// of 3001 tokens, 6 heads 32 x 48: 23 us, four chunks after each other in each pass. By
+// tokens, a state in registers: 830 and 62 us.
 constexpr int kL32 = 32;
 
 __device__ __forceinline__ f32x4 mfma4(f32x4 a, f32x4 b, f32x4 c) {
@@ -838,7 +852,8 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk32_kernel(SsmP
 
 // The states in front of the segments of one sequence (a block per 256 vectors of
 // them and per multiple of len, where at most one sequence of several segments
-// starts). vecs: vectors of a head's state.
+// starts). vecs: vectors of a head's state. Bound by HBM: 16 segments of 32 heads
+// 128 x 128 are 64 MB read and written in 13 us, 4.9 TB/s.
 __global__ __launch_bounds__(kThreads) void ssm_front_kernel(SsmParams a, int blocks, int vecs) {
   const int b = blockIdx.x % blocks, h = blockIdx.x / blocks % a.H, at = blockIdx.x / blocks / a.H;
   Part p;
@@ -870,7 +885,8 @@ __global__ __launch_bounds__(kThreads) void ssm_front_kernel(SsmParams a, int bl
 // One token: the state read and written once, a float4 of columns per thread
 // and as many rows at a time as the workgroup has threads for (the rest idles
 // where P / 4 does not divide it). A workgroup takes the whole head, or where
-// that leaves compute units without one, a part of its columns.
+// that leaves compute units without one, a part of its columns. Bound by HBM: 256
+// sequences of 32 heads 128 x 128, 1.08 GB: 207 us, 5.2 TB/s.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ssm_step_kernel(SsmParams a, int N, int split) {
   const int part_id = blockIdx.x % split, h = blockIdx.x / split % a.H, n = blockIdx.x / split / a.H;
@@ -975,7 +991,8 @@ template <int N>
 hipError_t launch_n(const SsmArgs& a) {
   const Split sp = split_of(a.bf16, a.N, a.P);
   if (!a.bf16) return launch_passes(ssm_chunk32_kernel<N, false>, ssm_chunk32_kernel<N, true>, a, sp, 4 * sp.columns);
-  return a.P <= 64 ? launch_passes(ssm_chunk_kernel<N, 4, false>, ssm_chunk_kernel<N, 4, true>, a, sp, 4 * sp.columns) : launch_passes(ssm_chunk_kernel<N, 8, false>, ssm_chunk_kernel<N, 8, true>, a, sp, 4 * sp.columns);
+  if (a.P <= 64) return launch_passes(ssm_chunk_kernel<N, 4, false>, ssm_chunk_kernel<N, 4, true>, a, sp, 4 * sp.columns);
+  return launch_passes(ssm_chunk_kernel<N, 8, false>, ssm_chunk_kernel<N, 8, true>, a, sp, 4 * sp.columns);
 }
 
 size_t workspace_of(int32_t T, int32_t H, int32_t N, int32_t P, const Split& sp) {
