@@ -29,7 +29,8 @@
  *   - Every tensor pointer is DEVICE memory owned by the caller, row-major
  *     and contiguous, 16-byte aligned. Only the *_host arrays are host memory.
  *   - Supported head sizes: Dk == Dv == D with D in {16, 128}; anything else
- *     returns KDA_ERR_UNSUPPORTED.
+ *     returns KDA_ERR_UNSUPPORTED. (The calls around a recurrence, the last
+ *     section, have sizes of their own, and strides where their arguments say so.)
  *   - All work is enqueued on `stream` (NULL = the default stream) and the
  *     calls are asynchronous. The library allocates nothing and keeps no
  *     global state, with one exception: kda_prefill_chunked_noalloc's static
