@@ -120,14 +120,15 @@ __device__ __forceinline__ f32x4* front_of(const SsmParams& a, const Part& p, in
 // block (16 bytes a lane: lanes 0-3, 12-15, 20-23, 24-27 and so on), and 4 rows of
 // 16 columns (turned over: 16 lanes).
 //
-// 8192 tokens of 32 heads 128 x 128: states 34 us, fronts 13, outputs 75, where the
+// 8192 tokens of 32 heads 128 x 128: states 34 us, fronts 13, outputs 73, where the
 // bytes take 32 (copies reach 5.35 TB/s) and the products as written 31 (98 a chunk
-// and wave in the outputs' launch, 48 in the other). Neither bounds it: vector
-// instructions, matrix instructions and LDS are at work for 33, 21 and 28 us of the
-// outputs' 75, four waves a SIMD that wait for each other at three barriers a chunk. A
-// third workgroup a compute unit (M in the place of C, 64 columns) changes nothing;
-// scaling the state as it is split spills, 80 us; eight waves of 128 columns share B,
-// C and M among twice the columns of four.
+// and wave in the outputs' launch, 48 in the other). Neither bounds it: matrix
+// instructions, vector instructions and LDS are at work for about 20, 30 and 28 us of
+// the outputs' 73, by four waves a SIMD that wait for each other at three barriers a
+// chunk. A third workgroup a compute unit (M in the place of C, 64 columns) changes
+// nothing; scaling the state as it is split, and reads of LDS held ahead of the work
+// that hides them, spill (80 and 73 to 77 us); w x in two terms instead of three where
+// only outputs come of the state takes 71.
 constexpr int kL = KDA_SSM_CHUNK;
 
 // Workgroups go to the 8 dies in turn. They are numbered so that kShare of those that
@@ -183,7 +184,6 @@ __device__ __forceinline__ double lane_value(double x, int l) {
   return __builtin_bit_cast(double, make_uint2(__builtin_amdgcn_ds_bpermute(4 * l, v.x),
                                                __builtin_amdgcn_ds_bpermute(4 * l, v.y)));
 }
-typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 
 // x - h, h the bf16 nearest to x: exact, and one instruction a value, the sum of
 // products of a pair of bf16 with (-1, 0) or (0, -1), where the pair taken apart takes
@@ -484,11 +484,15 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
     if (outputs) {
       // A value that is not finite would reach earlier tokens through M's zeros:
       // it is taken out here, and its column made NaN from its token on.
-      const u16x8 most = __builtin_elementwise_max(__builtin_bit_cast(u16x8, xo[0]) & (uint16_t)0x7fff,
-                                                   __builtin_bit_cast(u16x8, xo[1]) & (uint16_t)0x7fff);
-      bool bad = false;
+      typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+      u16x2 most = {0, 0};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) bad |= most[i] >= 0x7f80;
+      for (int v = 0; v < 2; ++v) {
+        const u32x4 bits = __builtin_bit_cast(u32x4, xo[v]) & 0x7fff7fffu;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, (uint32_t)bits[i]));
+      }
+      const bool bad = most[0] >= 0x7f80 || most[1] >= 0x7f80;
       const bool any_bad = __any(bad);
       int from = kL;
       if (any_bad) {
