@@ -601,7 +601,7 @@ kda_status kda_conv_prefill(const void* x, int64_t x_stride, const float* weight
   a.seqs = packed(cu_seqlens, num_seqs, T);
   a.N = 0;
   a.initial_state = initial_state; a.final_state = final_state;
-  if (kda::conv_threads(a) > kda::kMaxThreads) return KDA_ERR_INVALID_ARG;
+  if (kda::conv_groups(a) > kda::kMaxConvGroups) return KDA_ERR_INVALID_ARG;
   const size_t e = elem(dt), state = (size_t)num_seqs * (width - 1) * C;
   const Span initial = initial_state == final_state ? Span{nullptr, 0} : flat(initial_state, state, e);
   if (!apart({rows(y, T, C, C, e), flat(final_state, state, e)},

@@ -7,7 +7,7 @@
 // bound by HBM. A thread owns V consecutive channels (16 bytes, or what a row has
 // left) and walks along the tokens with the last K - 1 rows in registers, so every
 // row is read once but for the K - 1 rows in front of a thread's first token; four
-// rows are on their way while four are worked on. 8192 x 12288 bf16: 89 us, 4.5 TB/s,
+// rows are on their way while four are worked on. 8192 x 12288 bf16: 88 us, 4.6 TB/s,
 // where a copy of the same bytes takes 75 (without the activation the same: it is not
 // arithmetic); nine sequences of 3001 x 777 fp32 8.4 us.
 #include "kda_pack.h"
@@ -15,18 +15,21 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
+// A prompt's workgroup is a wave: nothing in it waits for another one (8192 x 12288
+// bf16 88 us, by four waves 90; 24576 x 4096 81 and 85; 1 x 12288 3.5 and 4.4).
+constexpr int kGroup = kWave;
 // Tokens a thread walks along: as many as leave kPromptThreads threads (two waves a
 // SIMD), so that the rows in front of them are read seldom, and at least the K - 1
 // that read the state. 2048 tokens of 12288 channels, bf16: 22.9 us, with a wave a
-// SIMD 25.4, with four 25.3; 8192 tokens by 8 a thread 105, by 16 96, by 64 89.
+// SIMD 25.4, with four 25.3; 8192 tokens by 8 a thread 105, by 16 96, by 64 89 (all by
+// workgroups of four waves).
 constexpr int kMinTokens = 4, kMostTokens = 64;
 constexpr int64_t kPromptThreads = 256 * 4 * 2 * 64;
 
 // Threads along the channels; the rest of the workgroup takes further tokens.
 int channel_threads(int vecs) {
   int t = 1;
-  while (t < vecs && t < kThreads) t *= 2;
+  while (t < vecs && t < kGroup) t *= 2;
   return t;
 }
 
@@ -74,7 +77,7 @@ __device__ __forceinline__ bits_t<T, V> conv_token(float (&past)[K - 1][V], bits
 }
 
 template <typename T, int K, bool whole>
-__global__ __launch_bounds__(kThreads) void conv_kernel(const T* x, int64_t x_stride, const float* weight,
+__global__ __launch_bounds__(kGroup) void conv_kernel(const T* x, int64_t x_stride, const float* weight,
                                                         const float* bias, Packed seqs, int C, int tokens,
                                                         int chan_threads, int chan_blocks, bool silu, const T* initial, T* final_state,
                                                         T* y) {
@@ -84,7 +87,7 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(const T* x, int64_t x_st
   const int c = at.c;
   const int row = threadIdx.x / chan_threads;     // which run of `tokens` tokens
   Part p;
-  if (!find_part(seqs, kThreads / chan_threads * tokens, slot, p) || !at.on) return;
+  if (!find_part(seqs, kGroup / chan_threads * tokens, slot, p) || !at.on) return;
   const int first = p.first + row * tokens;
   const int count = min(tokens, p.first + p.count - first);
   // the rows in front: of the sequence, or of its state (row r of the state is
@@ -136,6 +139,8 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(const T* x, int64_t x_st
 }
 static_assert(kMinTokens >= KDA_CONV_MAX_WIDTH - 1, "the first K - 1 tokens are one thread's");
 
+constexpr int kThreads = 256;
+
 // One token: a thread takes the sequences n, n + groups, .. for its channels, whose
 // weights (more bytes than a row and its state) it reads once.
 template <typename T, int K, bool whole>
@@ -186,8 +191,8 @@ hipError_t launch_k(const ConvArgs& a, bool step) {
     return hipGetLastError();
   }
   const int tokens = tokens_of(a), ct = channel_threads(vecs), blocks = (vecs + ct - 1) / ct;
-  const int64_t slots = part_slots(a.seqs, kThreads / ct * tokens);
-  hipLaunchKernelGGL((conv_kernel<T, K, whole>), dim3((unsigned)(slots * blocks)), dim3(kThreads), 0, a.stream, (const T*)a.x,
+  const int64_t slots = part_slots(a.seqs, kGroup / ct * tokens);
+  hipLaunchKernelGGL((conv_kernel<T, K, whole>), dim3((unsigned)(slots * blocks)), dim3(kGroup), 0, a.stream, (const T*)a.x,
                      a.x_stride, a.weight, a.bias, a.seqs, a.C, tokens, ct, blocks, a.silu, (const T*)a.initial_state,
                      (T*)a.final_state, (T*)a.y);
   return hipGetLastError();
@@ -207,9 +212,9 @@ hipError_t launch_t(const ConvArgs& a, bool step) {
 
 }  // namespace
 
-int64_t conv_threads(const ConvArgs& a) {
+int64_t conv_groups(const ConvArgs& a) {
   const int vecs = vecs_of(a), ct = channel_threads(vecs);
-  return part_slots(a.seqs, kThreads / ct * tokens_of(a)) * ((vecs + ct - 1) / ct) * kThreads;
+  return part_slots(a.seqs, kGroup / ct * tokens_of(a)) * ((vecs + ct - 1) / ct);
 }
 
 hipError_t launch_conv(const ConvArgs& a) { return a.bf16 ? launch_t<bf16_bits>(a, false) : launch_t<float>(a, false); }

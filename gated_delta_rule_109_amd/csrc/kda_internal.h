@@ -210,7 +210,10 @@ hipError_t launch_residual_norm(const ResidualNormArgs& a);
 
 // Threads of a call's largest launch: fewer than 2^32.
 constexpr int64_t kMaxThreads = (1ll << 32) - 1;
-int64_t conv_threads(const ConvArgs& a);   // (a step takes a bounded number)
+// Workgroups of a convolution's launch: fewer than 2^24 (of a wave each; a step takes
+// a bounded number).
+constexpr int64_t kMaxConvGroups = (1 << 24) - 1;
+int64_t conv_groups(const ConvArgs& a);
 int64_t ssm_threads(const SsmArgs& a);
 int64_t gated_threads(const GatedNormArgs& a);
 

@@ -553,7 +553,7 @@ typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1, KDA_ACT_SIGMOID = 2 } kda_act
  * Errors: KDA_ERR_INVALID_ARG (null required pointer, misaligned or overlapping
  * arrays, T or num_seqs < 0, num_seqs != 1 without cu_seqlens, C outside
  * [1, KDA_CONV_MAX_CHANNELS], x_stride < C, width, activation; sizes whose
- * launch would take 2^32 threads), KDA_ERR_UNSUPPORTED (dtype), KDA_ERR_HIP. */
+ * launch would take 2^24 workgroups), KDA_ERR_UNSUPPORTED (dtype), KDA_ERR_HIP. */
 #define KDA_CONV_MAX_WIDTH 4
 #define KDA_CONV_MAX_CHANNELS (1 << 20)
 kda_status kda_conv_prefill(const void* x, int64_t x_stride, const float* weight,
@@ -597,8 +597,9 @@ kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, c
  *              sequences, which run side by side. It needs no initialisation; sizes
  *              do not shrink as num_seqs, T, H or P grow, so that of the largest call
  *              serves smaller ones; calls that may overlap need one each.
- * Errors: KDA_ERR_INVALID_ARG (as kda_conv_prefill; G < 1 or H % G), KDA_ERR_UNSUPPORTED
- * (dtype, N or P), KDA_ERR_WORKSPACE, KDA_ERR_HIP. */
+ * Errors: KDA_ERR_INVALID_ARG (as kda_conv_prefill; G < 1 or H % G; strides; T * H or
+ * num_seqs * H above INT32_MAX; sizes whose launch would take 2^32 threads),
+ * KDA_ERR_UNSUPPORTED (dtype, N or P), KDA_ERR_WORKSPACE, KDA_ERR_HIP. */
 #define KDA_SSM_CHUNK 64
 #define KDA_SSM_MAX_STRIDE (1 << 23)
 size_t kda_ssm_workspace_size(int32_t num_seqs, int32_t T, int32_t H, int32_t N, int32_t P);
