@@ -15,8 +15,9 @@
 namespace kda {
 namespace {
 
-// A prompt's workgroup is a wave: nothing in it waits for another one (8192 x 12288
-// bf16 88 us, by four waves 90; 24576 x 4096 81 and 85; 1 x 12288 3.5 and 4.4).
+// A workgroup is a wave: nothing in it waits for another one (prompts of 8192 x 12288
+// bf16 88 us, by four waves 90; 24576 x 4096 81 and 85; 1 x 12288 3.5 and 4.4; steps of
+// 256 x 12288 10.0 and 10.3, of 64 4.1 and 4.6).
 constexpr int kGroup = kWave;
 // Tokens a thread walks along: as many as leave kPromptThreads threads (two waves a
 // SIMD), so that the rows in front of them are read seldom, and at least the K - 1
@@ -139,16 +140,14 @@ __global__ __launch_bounds__(kGroup) void conv_kernel(const T* x, int64_t x_stri
 }
 static_assert(kMinTokens >= KDA_CONV_MAX_WIDTH - 1, "the first K - 1 tokens are one thread's");
 
-constexpr int kThreads = 256;
-
 // One token: a thread takes the sequences n, n + groups, .. for its channels, whose
 // weights (more bytes than a row and its state) it reads once.
 template <typename T, int K, bool whole>
-__global__ __launch_bounds__(kThreads) void conv_step_kernel(const T* x, int64_t x_stride, const float* weight,
+__global__ __launch_bounds__(kGroup) void conv_step_kernel(const T* x, int64_t x_stride, const float* weight,
                                                              const float* bias, int N, int C, int vecs, int groups,
                                                              bool silu, T* state, T* y) {
   constexpr int V = vec_of<T>();
-  const uint32_t id = blockIdx.x * kThreads + threadIdx.x;
+  const uint32_t id = blockIdx.x * kGroup + threadIdx.x;
   if (id >= (uint32_t)groups * vecs) return;
   const VecAt<V, whole> at = vec_at<V, whole>(id % vecs, C);
   const int c = at.c;
@@ -170,9 +169,9 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(const T* x, int64_t
 }
 
 // Sequences apart that a thread of a step takes: about kStepThreads threads, a wave a
-// SIMD. 256 sequences of 12288 channels, bf16: 10.4 us, 4.9 TB/s; before a step of
-// whole vectors had its own kernel 10.9, with twice the threads 11.4, half of them 14.8,
-// a thread for every sequence 15.1.
+// SIMD. 256 sequences of 12288 channels, bf16: 10.0 us, 5.0 TB/s; before whole vectors
+// had a kernel of their own 10.9, with twice the threads 11.4, half of them 14.8, a
+// thread for every sequence 15.1.
 constexpr int64_t kStepThreads = 256 * 4 * 64;
 int step_groups(const ConvArgs& a) {
   const int64_t g = kStepThreads / vecs_of(a);
@@ -185,7 +184,7 @@ hipError_t launch_k(const ConvArgs& a, bool step) {
   if (step) {
     const int groups = step_groups(a);
     const int64_t n = (int64_t)groups * vecs;
-    hipLaunchKernelGGL((conv_step_kernel<T, K, whole>), dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+    hipLaunchKernelGGL((conv_step_kernel<T, K, whole>), dim3((unsigned)((n + kGroup - 1) / kGroup)), dim3(kGroup), 0,
                        a.stream, (const T*)a.x, a.x_stride, a.weight, a.bias, a.N, a.C, vecs, groups, a.silu,
                        (T*)a.initial_state, (T*)a.y);
     return hipGetLastError();
