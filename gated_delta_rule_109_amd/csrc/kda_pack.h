@@ -160,19 +160,29 @@ struct Part {
 __device__ __forceinline__ int token_offset(const Packed& s, int n) {
   return s.cu ? min(max(s.cu[n], 0), s.T) : n * s.T;
 }
-// The last sequence n with offset(n) / len + n * each <= at (0: there is none), found
-// by a whole wave: each step looks at 64 places at once (a step is a load's latency,
-// and a prompt of a few sequences takes microseconds).
-__device__ __forceinline__ int last_sequence(const Packed& s, int len, int each, int at) {
+// The last sequence n with offset(n) / len + n * each <= at (0: there is none) and its
+// tokens, found by a whole wave: each step looks at 64 places at once (a step is a
+// load's latency, and a prompt of a few sequences takes microseconds), and the last
+// one has loaded what the sequence begins and ends at.
+__device__ __forceinline__ int last_sequence(const Packed& s, int len, int each, int at, int& start, int& end) {
+  if (s.num_seqs == 1) {
+    start = token_offset(s, 0), end = token_offset(s, 1);
+    return 0;
+  }
+  const int lane = threadIdx.x % kWave;
   int lo = 0, n = s.num_seqs;            // it is in [lo, lo + n)
-  while (n > 1) {
-    const int step = (n + kWave - 1) / kWave, d = (int)(threadIdx.x % kWave) * step;
+  while (n > kWave) {
+    const int step = (n + kWave - 1) / kWave, d = lane * step;
     const bool below = d < n && token_offset(s, lo + min(d, n - 1)) / len + (lo + d) * each <= at;
     const int last = max(__popcll(__ballot(below)) - 1, 0) * step;
     lo += last;
     n = min(step, n - last);
   }
-  return __builtin_amdgcn_readfirstlane(lo);
+  const int offset = token_offset(s, lo + min(lane, n));
+  const int i = max(__popcll(__ballot(lane < n && offset / len + (lo + lane) * each <= at)) - 1, 0);
+  start = __builtin_amdgcn_readlane(offset, i);
+  end = i + 1 < kWave ? __builtin_amdgcn_readlane(offset, i + 1) : token_offset(s, lo + kWave);
+  return __builtin_amdgcn_readfirstlane(lo + i);
 }
 // Parts are numbered without a table: part j of sequence n is slot
 // offset(n) / len + n + j. A sequence of L tokens has max(1, ceil(L / len))
@@ -180,9 +190,9 @@ __device__ __forceinline__ int last_sequence(const Packed& s, int len, int each,
 // collide and there are at most T / len + num_seqs. False: no part has this slot.
 // (All threads of a wave ask together.)
 __device__ __forceinline__ bool find_part(const Packed& s, int len, int slot, Part& p) {
-  p.n = last_sequence(s, len, 1, slot);
-  p.start = token_offset(s, p.n);
-  p.length = max(token_offset(s, p.n + 1) - p.start, 0);
+  int end;
+  p.n = last_sequence(s, len, 1, slot, p.start, end);
+  p.length = max(end - p.start, 0);
   p.j = slot - (p.start / len + p.n);
   p.parts = p.length ? (p.length - 1) / len + 1 : 1;
   if (p.j < 0 || p.j >= p.parts) return false;

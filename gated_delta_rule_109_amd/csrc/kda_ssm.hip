@@ -861,9 +861,9 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk32_kernel(SsmP
 __global__ __launch_bounds__(kThreads) void ssm_front_kernel(SsmParams a, int blocks, int vecs) {
   const int b = blockIdx.x % blocks, h = blockIdx.x / blocks % a.H, at = blockIdx.x / blocks / a.H;
   Part p;
-  p.n = last_sequence(a.seqs, a.len, 0, at);   // the last that starts before (at + 1) len
-  p.start = token_offset(a.seqs, p.n);
-  p.length = token_offset(a.seqs, p.n + 1) - p.start;
+  int end;
+  p.n = last_sequence(a.seqs, a.len, 0, at, p.start, end);   // the last that starts before (at + 1) len
+  p.length = end - p.start;
   const int i = b * kThreads + threadIdx.x;
   if (p.start / a.len != at || p.length <= 2 * a.len || i >= vecs) return;
   const int parts = (p.length - 1) / a.len + 1;
