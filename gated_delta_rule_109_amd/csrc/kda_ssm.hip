@@ -9,6 +9,8 @@
 
 #include <math.h>
 
+#include <algorithm>
+
 namespace kda {
 namespace {
 
@@ -27,14 +29,17 @@ constexpr int kThreads = 256;
 // more segments reaches over at least one multiple of len, and has at most one
 // segment more than it reaches over, so no two meet and there are 2 T / len.
 //
-// How long: a segment adds its state, written and read twice (about 2 us a segment
-// for 2 MB of states, 0.5 us for small ones), and takes its tokens' time off the
-// chain (about 6 us per 64 tokens in both launches together), least where len is the
-// root of (5 + 15 H N P / 2^19) T. Measured, bf16, 32 heads of 128 x 128: 512 tokens in
-// segments of 128 29 us, of 256 36, whole 40; 2048 tokens in segments of 128 56 us, of
-// 256 51, of 512 67. Never more segments than fill the GPU, and none of calls where the
-// two more launches cost more than they save (300 tokens of two sequences: whole 13 us,
-// in segments 19).
+// How long is estimated from what was measured (by `cost` below, in us): a chunk of both
+// launches takes its time on the chain of a segment's chunks, more of it where compute
+// units hold two workgroups or more; a segment adds its state, written and read twice,
+// and a step of the chain of its sequence's states. Compared are the lengths that fill
+// one and two rounds of workgroups, the least one that the target allows (at least
+// twice the average sequence where sequences alone fill the GPU), and those where
+// chain and segments balance. Of 38 calls of 700 to 8192 tokens the length taken is on
+// average 2 % slower than the best one, by the balance alone 5 % and up to 27 (3001
+// tokens of nine sequences, 8 heads 128 x 128 fp32: 320 workgroups 76 us, 432 of shorter
+// segments 60; of one sequence: 256 of them 59, 304 of shorter segments 70). Calls of
+// few tokens are not split: 300 tokens of two sequences whole 13 us, in segments 19.
 struct Split {
   int columns;     // columns of a head one workgroup owns
   int target;      // workgroups that the segments of a call make up
@@ -56,12 +61,32 @@ Split split_of(bool bf16, int N, int P) { return split_of(!bf16 ? kF32 : P <= 64
 int column_blocks(const Split& s, int P) { return (P + s.columns - 1) / s.columns; }
 
 int segment_len(const Packed& s, int H, int N, int P, const Split& sp) {
-  const int64_t parts = sp.target / ((int64_t)H * column_blocks(sp, P));   // segments of all sequences together
+  const int64_t groups = (int64_t)H * column_blocks(sp, P);   // workgroups a segment
+  const int64_t parts = sp.target / groups;                   // segments of all sequences together
   if (parts < 2 || s.T <= sp.whole) return s.T > 0 ? s.T : 1;
-  const double best = sqrt((5.0 + 15.0 * H * N * P / (1 << 19)) * s.T), filled = (double)s.T / parts;
-  const double len = best > filled ? best : filled;
-  const int64_t chunks = (int64_t)ceil(len / sp.chunk);
-  return (int)(chunks > 2 ? chunks : 2) * sp.chunk;
+  constexpr int kUnits = 256;
+  const double chunks = (double)s.T / sp.chunk, n = s.num_seqs > 1 ? s.num_seqs : 1;
+  const double chunk_us = sp.chunk == KDA_SSM_CHUNK ? 2 + N / 40.0 : 1.7 + N / 32.0;
+  const double segment_us = 0.35 / sqrt(n) + 1.4 * H * N * P / (1 << 19);
+  const double ends = n > 1 ? 0.6 * n : 0;                    // segments that are a sequence's rest
+  auto cost = [&](int64_t k) {                                // segments of k chunks
+    const double count = n > 1 ? std::max(chunks / k + ends, n) : ceil(chunks / k), held = count * groups / kUnits;
+    return chunk_us * k * (held <= 1 ? 1 : std::max(1.4, 0.8 * held)) + segment_us * chunks / k;
+  };
+  int64_t least = std::max<int64_t>(2, (int64_t)ceil(chunks / parts));
+  if (n * groups >= 0.9 * sp.target) least = std::max<int64_t>(least, (int64_t)ceil(2 * chunks / n));
+  const int64_t even = (int64_t)sqrt(segment_us * chunks / chunk_us);
+  int64_t best = least;
+  auto consider = [&](int64_t k) {
+    if (k > least && cost(k) < cost(best)) best = k;
+  };
+  consider(even);
+  consider(even + 1);
+  for (int rounds = 1; rounds <= 2; ++rounds) {
+    const double room = n > 1 ? (double)rounds * kUnits / groups - ends : (double)(rounds * kUnits / groups);
+    if (room >= 1) consider((int64_t)ceil(chunks / room));
+  }
+  return (int)(best * sp.chunk);
 }
 
 // d_t of one token and head.
