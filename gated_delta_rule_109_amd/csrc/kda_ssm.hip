@@ -609,8 +609,8 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
 // Layouts as above, with blocks of 4 fp32. 8192 tokens of 32 heads 128 x 128: 346 us,
 // of which the products take 139 at the rate of a large fp32 product (154 TFLOP/s) in
 // the launch with outputs, and 2/5 of that again in the one for states; nine sequences
-// of 3001 tokens, 6 heads 32 x 48: 23 us, four chunks after each other in each pass. By
-// tokens, a state in registers: 830 and 62 us.
+// of 3001 tokens, 6 heads 32 x 48: 20 us, three chunks after each other in each pass.
+// By tokens, a state in registers: 830 and 62 us.
 constexpr int kL32 = 32;
 
 __device__ __forceinline__ f32x4 mfma4(f32x4 a, f32x4 b, f32x4 c) {
