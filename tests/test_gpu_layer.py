@@ -6,6 +6,8 @@ Tolerances: element by element the oracle's bound on fp32 arithmetic
 The bf16 scan carries every fp32 factor of an output in two bf16 terms: PRODUCT
 of each product's size (the decayed weights of a chunk's tokens, and the state).
 Convolution states are exact."""
+import random
+
 import numpy as np
 import pytest
 import torch
@@ -432,6 +434,49 @@ def test_rows_of_every_length_up_to_three_vectors(dtype):
         check(rows, res, rb, f"residual of {C}")
         check(y, ref, bound, f"residual norm of {C}")
         assert (out[T * C:] == 7).all() and (same[T * C:] == 7).all()
+
+
+def drawn(seed):
+    """(test, arguments) over the ranges that the calls take, small enough for the oracle."""
+    rng = random.Random(seed)
+    dt, flag = rng.choice([BF16, F32]), lambda: rng.random() < 0.5  # noqa: E731
+    outside = rng.randint(0, 3), rng.randint(1, 3)
+
+    def lengths(total, most):
+        k = rng.randint(1, most)
+        return [rng.choice([0, 1, 2, rng.randint(0, 40), rng.randint(0, total // k), rng.randint(0, total) // max(1, k // 2)])
+                for _ in range(k)]
+
+    op = rng.choice(["ssm", "ssm", "conv", "steps", "gated", "residual"])
+    if op == "ssm":
+        G = rng.choice([1, 2, 3])
+        H, N, P = G * rng.choice([1, 2, 5]), rng.choice([16, 32, 64, 128, 256]), 16 * rng.choice([1, 2, 3, 4, 5, 8, 9, 16])
+        if H * N * P > 60000:
+            H, G, N = 1, 1, rng.choice([16, 64])
+        return test_ssm, (lengths(rng.choice([100, 500, 1200]), rng.choice([1, 3, 12])), outside, H, G, N, P, dt, flag(),
+                          flag(), flag(), rng.choice([0, 8]), rng.choice([0.1, 1.0, 4.0, 50.0]))
+    if op == "conv":
+        return test_conv, (lengths(rng.choice([50, 400]), rng.choice([1, 3, 20])), outside, rng.randint(1, rng.choice([40, 1200])),
+                           rng.choice([2, 3, 4]), dt, rng.choice([0, 1]), flag(), flag(), rng.choice([0, 8, rng.randint(1, 9)]))
+    if op == "steps":
+        G = rng.choice([1, 2])
+        return rng.choice([
+            (test_conv_step, (rng.randint(1, 300), rng.randint(1, 2000), rng.choice([2, 3, 4]), dt, rng.choice([0, 1]), flag(),
+                              rng.choice([0, 3]))),
+            (test_ssm_step, (rng.randint(1, 9), G * rng.choice([1, 3]), G, rng.choice([16, 32, 64, 128, 256]),
+                             16 * rng.randint(1, 16), dt))])
+    D = rng.choice([rng.randint(1, 70), rng.randint(1, 2000), rng.randint(2000, 16384)])
+    if op == "gated":
+        return test_gated_norm, (rng.randint(1, 40), rng.randint(1, 4), D, dt, rng.choice([0, 1, 2]), flag(), flag(), flag(),
+                                 rng.choice([0, 5]))
+    return test_residual_norm, (rng.randint(1, 60), D, dt, flag(), flag(), flag(), rng.choice([0, 1, 2]), flag(),
+                                rng.choice([1.0, -0.5]))
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_drawn(seed):
+    test, args = drawn(seed)
+    test(*args)
 
 
 # ---- streams, graphs, far offsets, whole layers --------------------------------------------
