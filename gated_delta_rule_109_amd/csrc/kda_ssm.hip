@@ -125,9 +125,11 @@ __device__ __forceinline__ f32x4* front_of(const SsmParams& a, const Part& p, in
 //     y_t = e^{c_t} C_t^T S + sum_{s <= t} M[t][s] x_s,  M[t][s] = e^{c_t - c_s} d_s (C_t . B_s), M[t][t] += skip
 //     S  <- e^{c_L} S + sum_s B_s (w_s x_s)^T,           w_s = e^{c_L - c_s} d_s
 // B, C and x are bf16 and enter the products as they are. The fp32 factor of
-// each product is split into bf16 terms, two for outputs (S and M) and three for
-// the state (w x): 2^-17 and 2^-26 of it are left out. Sums of d a are taken in
-// fp64 and handed on as two floats, so that their differences are exact to fp32.
+// each product (S, M and w x) is split into three bf16 terms, which hold its 24 bits.
+// (With two of S and M a call of 8192 tokens of 32 heads took 114 us, not 125, but its
+// outputs were off by 2^-17 of each product, which shows where products cancel.) Sums of
+// d a are taken in fp64 and handed on as two floats, so that their differences are exact
+// to fp32.
 //
 // A workgroup owns 16 W columns of a head, wave w the 16 columns from 16 w on,
 // with their whole state in accumulators: tile k holds rows 16 k + 4 g
@@ -139,21 +141,21 @@ __device__ __forceinline__ f32x4* front_of(const SsmParams& a, const Part& p, in
 //        16 u + 4 g + i of a row is kept at 32 v + 8 g + 4 u + i, so that an operand
 //        of sums over channels is one read of 16 bytes. Sums over tokens read 4 rows
 //        of 16 columns turned over (a lane: one column, 4 tokens), twice an operand.
-//   sMh, sMl  [token t][token s], s kept in the order of the channels
+//   sM   [term][token t][token s], s kept in the order of the channels
 // No padding: blocks of 16 bytes are XORed with bits of their row, so that the
 // lanes an LDS instruction serves at a time meet different banks: 16 rows at one
 // block (16 bytes a lane: lanes 0-3, 12-15, 20-23, 24-27 and so on), and 4 rows of
 // 16 columns (turned over: 16 lanes).
 //
-// 8192 tokens of 32 heads 128 x 128: states 34 us, fronts 13, outputs 73, where the
-// bytes take 32 (copies reach 5.35 TB/s) and the products as written 31 (98 a chunk
-// and wave in the outputs' launch, 48 in the other). Neither bounds it: matrix
-// instructions, vector instructions and LDS are at work for about 20, 30 and 28 us of
-// the outputs' 73, by four waves a SIMD that wait for each other at three barriers a
-// chunk. A third workgroup a compute unit (M in the place of C, 64 columns) changes
-// nothing; scaling the state as it is split, and reads of LDS held ahead of the work
-// that hides them, spill (80 and 73 to 77 us); w x in two terms instead of three where
-// only outputs come of the state takes 71.
+// 8192 tokens of 32 heads 128 x 128: states 34 us, fronts 13, outputs 84, where the
+// bytes take 32 (copies reach 5.35 TB/s) and the products as written 36 (120 a chunk
+// and wave in the outputs' launch, 48 in the other). Neither bounds it: four waves a
+// SIMD wait for each other at three barriers a chunk. With two terms of S and M, when
+// the outputs took 73 to 77, matrix instructions, vector instructions and LDS were at
+// work for about 20, 30 and 28 us of them; a third workgroup a compute unit (M in the
+// place of C, 64 columns) changed nothing; scaling the state as it is split, and reads of
+// LDS held ahead of the work that hides them, spilled (80 and 73 to 77 us); w x in two
+// terms where only outputs come of the state gained 2 us.
 constexpr int kL = KDA_SSM_CHUNK;
 
 // Workgroups go to the 8 dies in turn. They are numbered so that kShare of those that
@@ -230,11 +232,7 @@ __device__ __forceinline__ f32x4 rest_of(f32x4 x, bf16x4 h, const Minus& m) {
       __builtin_amdgcn_fdot2_f32_bf16(a, m.lo, x[0], false), __builtin_amdgcn_fdot2_f32_bf16(a, m.hi, x[1], false),
       __builtin_amdgcn_fdot2_f32_bf16(b, m.lo, x[2], false), __builtin_amdgcn_fdot2_f32_bf16(b, m.hi, x[3], false)};
 }
-// x = h + l, and x = h + m + l in bf16, each the rest of the one before rounded to nearest.
-__device__ __forceinline__ void split2(f32x4 x, bf16x4& h, bf16x4& l, const Minus& one) {
-  h = to_bf16x4(x);
-  l = to_bf16x4(rest_of(x, h, one));
-}
+// x = h + m + l in bf16, each the rest of the one before rounded to nearest.
 __device__ __forceinline__ void split3(f32x4 x, bf16x4& h, bf16x4& m, bf16x4& l, const Minus& one) {
   h = to_bf16x4(x);
   const f32x4 r = rest_of(x, h, one);
@@ -295,7 +293,7 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
   const int grp = h / (a.H / a.G);
   const float av = a.a[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, skip = a.skip ? a.skip[h] : 0.f;
 
-  __shared__ __attribute__((aligned(16))) bf16_bits sC[kL * NP], sB[kL * NP], sX[kL * kCols], sMh[kL * kL], sMl[kL * kL];
+  __shared__ __attribute__((aligned(16))) bf16_bits sC[kL * NP], sB[kL * NP], sX[kL * kCols], sM[3][kL * kL];
   __shared__ Decays<kL> dec[4];
 
   // ---- state in front of the segment
@@ -470,12 +468,13 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
             }
           }
         }
-        bf16x4 mh, ml;
-        split2(x, mh, ml, one);
+        bf16x4 mh, mm, ml;
+        split3(x, mh, mm, ml, one);
         const int at = (mr ^ 32 * (u / 2)) + 16 * tt * kL + 4 * (u & 1);
         if (id < kTiles) {
-          *(bf16x4*)(sMh + at) = mh;
-          *(bf16x4*)(sMl + at) = ml;
+          *(bf16x4*)(sM[0] + at) = mh;
+          *(bf16x4*)(sM[1] + at) = mm;
+          *(bf16x4*)(sM[2] + at) = ml;
         }
       }
       // ---- y, transposed (a lane: one t, 4 columns): the state's part first
@@ -485,14 +484,15 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
       for (int tt = 0; tt < 4; ++tt) y[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int v = 0; v < KS; ++v) {
-        bf16x4 h0, l0, h1 = {}, l1 = {};
-        split2(s[2 * v], h0, l0, one);
-        if constexpr (NT > 1) split2(s[2 * v + 1], h1, l1, one);
-        const bf16x8 sh = cat(h0, h1), sl = cat(l0, l1);
+        bf16x4 h0, m0, l0, h1 = {}, m1 = {}, l1 = {};
+        split3(s[2 * v], h0, m0, l0, one);
+        if constexpr (NT > 1) split3(s[2 * v + 1], h1, m1, l1, one);
+        const bf16x8 sh = cat(h0, h1), sm = cat(m0, m1), sl = cat(l0, l1);
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
           const bf16x8 c = *(const bf16x8*)(sC + (hr ^ 32 * v) + 16 * tt * NP);
           y[tt] = mfma32(sl, c, y[tt]);
+          y[tt] = mfma32(sm, c, y[tt]);
           y[tt] = mfma32(sh, c, y[tt]);
         }
       }
@@ -539,8 +539,8 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
 #pragma unroll
         for (int v = 0; v <= tt / 2; ++v) {
           const int at = (mr ^ 32 * v) + 16 * tt * kL;
-          y[tt] = mfma32(xo[v], *(const bf16x8*)(sMl + at), y[tt]);
-          y[tt] = mfma32(xo[v], *(const bf16x8*)(sMh + at), y[tt]);
+#pragma unroll
+          for (int k = 2; k >= 0; --k) y[tt] = mfma32(xo[v], *(const bf16x8*)(sM[k] + at), y[tt]);
         }
       if (any_bad) {
         const uint32_t ft = fresh(threadIdx.x);

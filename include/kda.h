@@ -584,14 +584,13 @@ kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, c
  *   N  16, 32, 64, 128 or 256;  P a multiple of 16 up to 256; the strides of x,
  *      b and c are multiples of 16 bytes, at most KDA_SSM_MAX_STRIDE elements
  * bf16 tensors run in chunks of KDA_SSM_CHUNK tokens on the matrix cores: b, c
- * and x are exact there, every fp32 factor is carried in two bf16 terms for
- * outputs (2^-16 of each product) and three for states (2^-24). fp32 tensors run
- * in chunks of half that length with products of fp32. The decays between two
- * tokens come from sums in fp64 (a d_t a[h] below -2^20 counts as -2^20: the
- * state in front of it is gone either way). Values that are not finite in x, b or dt make
- * outputs non-finite from their token on (of a value in x: in its column), as the
- * recurrence does, and no outputs before; a c that is not finite, those of its
- * token.
+ * and x are exact there, and every fp32 factor is carried in three bf16 terms, which
+ * hold its 24 bits. fp32 tensors run in chunks of half that length with products of
+ * fp32. The decays between two tokens come from sums in fp64 (a d_t a[h] below -2^20
+ * counts as -2^20: the state in front of it is gone either way). Values that are not
+ * finite in x, b or dt make outputs non-finite from their token on (of a value in x: in
+ * its column), as the recurrence does, and no outputs before; a c that is not finite,
+ * those of its token.
  *   workspace  256-byte aligned device scratch of kda_ssm_workspace_size(num_seqs,
  *              T, H, N, P) bytes (0: may be NULL): the states of segments of long
  *              sequences, which run side by side. It needs no initialisation; sizes
