@@ -212,7 +212,7 @@ __device__ __forceinline__ double lane_value(double x, int l) {
                                                __builtin_amdgcn_ds_bpermute(4 * l, v.y)));
 }
 
-// x - h, h the bf16 nearest to x: exact, and one instruction a value, the sum of
+// x - h, h bf16 terms of x: exact, and one instruction a value, the sum of
 // products of a pair of bf16 with (-1, 0) or (0, -1), where the pair taken apart takes
 // two (8192 tokens of 32 heads: states 35.0 -> 33.7 us, outputs 76.8 -> 75.0). The factors come from registers: as
 // an instruction's own constant, -1 stands in the wrong half of its pair.
@@ -232,11 +232,19 @@ __device__ __forceinline__ f32x4 rest_of(f32x4 x, bf16x4 h, const Minus& m) {
       __builtin_amdgcn_fdot2_f32_bf16(a, m.lo, x[0], false), __builtin_amdgcn_fdot2_f32_bf16(a, m.hi, x[1], false),
       __builtin_amdgcn_fdot2_f32_bf16(b, m.lo, x[2], false), __builtin_amdgcn_fdot2_f32_bf16(b, m.hi, x[3], false)};
 }
-// x = h + m + l in bf16, each the rest of the one before rounded to nearest.
+// The upper halves of four floats: bf16, rounded towards zero.
+__device__ __forceinline__ bf16x4 upper_halves(f32x4 x) {
+  const u32x4 v = __builtin_bit_cast(u32x4, x);
+  return __builtin_bit_cast(bf16x4, uint2{__builtin_amdgcn_perm(v[1], v[0], 0x07060302u),
+                                          __builtin_amdgcn_perm(v[3], v[2], 0x07060302u)});
+}
+// x = h + m + l in bf16, 8 bits each, each towards zero, the rest of the ones before: exact.
+// (To nearest, as many instructions, a finite x above the largest bf16 would become
+// infinite, and the rest of it NaN.)
 __device__ __forceinline__ void split3(f32x4 x, bf16x4& h, bf16x4& m, bf16x4& l, const Minus& one) {
-  h = to_bf16x4(x);
+  h = upper_halves(x);
   const f32x4 r = rest_of(x, h, one);
-  m = to_bf16x4(r);
+  m = upper_halves(r);
   l = to_bf16x4(rest_of(r, m, one));
 }
 

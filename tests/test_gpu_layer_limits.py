@@ -52,3 +52,25 @@ def test_ssm_factors_keep_24_bits(dtype, N, P, T):
     assert torch.equal(y, dev(want, dtype))
     s0[0, :, 5] = (d - e)[:, None]
     assert torch.equal(end, dev(s0))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [70, 900])
+def test_ssm_largest_finite_factors(dtype, T):
+    """A state and a step size near the largest finite number, which rounds to infinity in bf16:
+    what b, c and x make small, and what they leave out, is finite. Products by powers of 2: exact."""
+    N, P, big = 16, 16, float(np.finfo(np.float32).max)
+    s0 = np.zeros((1, 2, N, P))
+    s0[0, 0, 2], s0[0, 0, 3], s0[0, 1, 4] = big, -big, 1.5
+    x, b, c, dt = np.zeros((T, 2, P)), np.zeros((T, 1, N)), np.zeros((T, 1, N)), np.zeros((T, 2))
+    x[5], b[5, 0, 5], dt[5, 1] = 2.0 ** -10, 1, big
+    c[:, 0, 5] = 1
+    c[::2, 0, 5], c[::2, 0, 2], c[::2, 0, 4] = 0, 2.0 ** -10, 1
+    want = np.zeros((T, 2, P))
+    want[5:, 1] = big * 2.0 ** -10
+    want[::2, 0], want[::2, 1] = big * 2.0 ** -10, 1.5
+    y, end = kda.ssm_prefill(dev(x, dtype), dev(dt), torch.zeros(2, device=DEV), dev(b, dtype), dev(c, dtype),
+                             initial_state=dev(s0))
+    assert torch.equal(y, dev(want, dtype))
+    s0[0, 1, 5] = big * 2.0 ** -10
+    assert torch.equal(end, dev(s0))
