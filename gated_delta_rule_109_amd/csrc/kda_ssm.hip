@@ -96,6 +96,17 @@ __device__ __forceinline__ float step_size(float dt, float bias, bool softplus) 
   return softplus ? (v > 0.f ? v : v < 0.f ? 0.f : v) + log1pf(expf(-fabsf(v))) : v;
 }
 
+// A factor e^x in two, so that it does not overflow before what it multiplies has its say:
+// e^min(x, kMostGrowth), and with x above that e^(x - kMostGrowth) besides, which leaves a
+// state of 0 at 0 whatever it is.
+constexpr float kMostGrowth = 88.f;
+__device__ __forceinline__ f32x4 grown(f32x4 s, float x) {
+  const float f = expf(x - kMostGrowth);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] = s[i] == 0.f ? 0.f : s[i] * f;
+  return s;
+}
+
 struct SsmParams {
   const void *x, *b, *c;
   int64_t x_stride, b_stride, c_stride;
@@ -205,6 +216,15 @@ __device__ __forceinline__ T fresh(T v) {
   return v;
 }
 
+// What is the same in all lanes.
+__device__ __forceinline__ float uniform(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+}
+// Keeps an array in scratch memory.
+template <typename T>
+__device__ __forceinline__ void in_memory(T* p) {
+  asm volatile("" ::"v"((__attribute__((address_space(5))) T*)p) : "memory");
+}
 // The value of lane `l` (its low 6 bits).
 __device__ __forceinline__ double lane_value(double x, int l) {
   const uint2 v = __builtin_bit_cast(uint2, x);
@@ -250,23 +270,37 @@ __device__ __forceinline__ void split3(f32x4 x, bf16x4& h, bf16x4& m, bf16x4& l,
 
 // What the tokens of a chunk need of d and a.
 template <int L>
-struct Decays {
+struct alignas(16) Decays {
   float hi[L], lo[L];   // c_t log2 e
   float d[L];           // d_t
   float e[L];           // e^{c_t}
   float w[L];           // e^{c_L - c_t} d_t
   float total;          // e^{c_L}
+  int grows;            // the chunk is taken by tokens
 };
 // A wave's 64 tokens, one a lane (at: the lane): the decays of 64 / L chunks, with
 // the sums of the logarithms c = d a in fp64. Returns the last chunk's c_L in every
 // lane of it. One logarithm is no less than kLeast: e^kLeast and all that is
 // multiplied by it are 0 as it is, while a token that ends the state (d a = -1e12)
 // would take the digits of the sums behind it.
+//
+// Factors between tokens of a chunk that grow may overflow where the state that they
+// multiply is 0 or small. Of a chunk whose growing tokens alone make more than
+// kMostInChunk of a logarithm (about 2^63: as much is left for c . b d) the tokens are
+// taken one after the other (8192 tokens of 32 heads 128 x 128, every chunk so: bf16 7.6
+// ms, fp32 6.1).
 template <int L>
 __device__ __forceinline__ double make_decays(float d, float a, int at, Decays<L>* dec) {
-  constexpr double kLeast = -(1 << 20);
+  constexpr double kLeast = -(1 << 20), kMostInChunk = 44.0;
   double c = (double)d * a;
   c = c < kLeast ? kLeast : c;                           // (NaN stays)
+  int grows = 0;
+  if (__any(c > 0.0)) {
+    double up = c > 0.0 ? c : 0.0;
+#pragma unroll
+    for (int m = 1; m < L; m *= 2) up += lane_value(up, at ^ m);
+    grows = up > kMostInChunk;
+  }
 #pragma unroll
   for (int m = 1; m < L; m *= 2) {
     const double o = lane_value(c, at - m);
@@ -281,12 +315,17 @@ __device__ __forceinline__ double make_decays(float d, float a, int at, Decays<L
   q.d[at % L] = d;
   q.e[at % L] = __builtin_amdgcn_exp2f(hi);
   q.w[at % L] = __builtin_amdgcn_exp2f((float)((end - c) * kL2)) * d;
-  if (at % L == 0) q.total = __builtin_amdgcn_exp2f((float)(end * kL2));
+  if (at % L == 0) q.total = __builtin_amdgcn_exp2f((float)(end * kL2)), q.grows = grows;
   return end;
 }
 
+// Waves a SIMD that the registers leave room for: those of two workgroups a compute unit
+// (of states of 256 rows, with outputs, one), and in the launches for states, which need
+// less of LDS, as many as there.
+constexpr int waves_of(int N, int W, bool outputs) { return outputs ? (N == 256 ? W / 4 : W / 2) : (N == 256 ? 2 : 4); }
+
 template <int N, int W, bool outputs>
-__global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_kernel(SsmParams a) {
+__global__ __launch_bounds__(64 * W, waves_of(N, W, outputs)) void ssm_chunk_kernel(SsmParams a) {
   constexpr int kThreads = 64 * W, kCols = 16 * W, NP = N < 32 ? 32 : N, KS = NP / 32, NT = N / 16, NV = N / 8;
   const int pblocks = (a.P + kCols - 1) / kCols;
   const int id = numbered(shared_groups(a.H / a.G, pblocks));
@@ -423,171 +462,220 @@ __global__ __launch_bounds__(64 * W, N == 256 ? W / 4 : W / 2) void ssm_chunk_ke
     if (!outputs) sum += end;
   };
 
+  // A chunk that grows: the recurrence, as a step computes it. Outputs go to the place of
+  // x, which only this wave reads. The state rests in scratch memory, and the loads of it
+  // end here: in registers, or waited for behind this path, it costs the others 2 to 7 %.
+  auto by_tokens = [&](const Decays<kL>& q, int count) __attribute__((always_inline)) {
+    f32x4 states[NT];
+    in_memory(states);
+#pragma unroll
+    for (int k = 0; k < NT; ++k) states[k] = s[k];
+    const int ft = fresh(threadIdx.x), fg = ft / 16 % 4, c8 = 2 * wave + ft % 16 / 8;
+#pragma unroll 1
+    for (int t = 0; t < count; ++t) {
+      bf16_bits* const px = sX + t * kCols + (c8 ^ row_mask<kCols>(t % 16)) * 8 + ft % 8;
+      const int at = t * NP, mask = row_mask<NP>(t % 16);
+      const float x = bf16_to_f32(*px), d = uniform(q.d[t]), da = d * av, f = expf(da > kMostGrowth ? kMostGrowth : da);
+      float o = 0.f;
+#pragma unroll 1
+      for (int k = 0; k < NT; ++k) {
+        const int place = at + ((4 * (k / 2) + fg) ^ mask) * 8 + 4 * (k & 1);
+        f32x4 v = states[k];
+        if (da > kMostGrowth) v = grown(v, da);
+        v = f * v + d * from_bf16x4(*(const bf16x4*)(sB + place)) * x;
+        states[k] = v;
+        if (outputs) {
+          const f32x4 r = from_bf16x4(*(const bf16x4*)(sC + place)) * v;
+          o += (r[0] + r[1]) + (r[2] + r[3]);
+        }
+      }
+      if (outputs) {
+        o += __shfl_xor(o, 16);
+        o += __shfl_xor(o, 32);
+        if (a.skip) o += skip * x;
+        if (fg == 0) *px = f32_to_bf16_bits(o);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NT; ++k) s[k] = fresh(states[k]);
+  };
+
   load_dt(0);
   if (p.count > 0) {
     load(0);
     if (outputs) load_c(0);
   }
+  // Chunks from token t0 on, up to one that grows.
+  auto chunks = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll 1
-  for (int t0 = 0; t0 < p.count; t0 += kL) {
-    const Decays<kL>& q = dec[t0 / kL & 3];
-    if ((t0 / kL & 3) == 0) {
-      decays(t0);
-      load_dt(t0 + 4 * kL);
-    }
-    if (outputs && t0 > 0) write_out(t0 - kL);
-    store();
-    lds_barrier();
-    if (t0 + kL < p.count) load(t0 + kL);
-    f32x4 y[4];
-    if (outputs) {
-      // ---- M, transposed (a lane: one t, 4 s each), in tiles of 16 t by 16 s: the
-      // ten up to the diagonal and two of zeros, shared out over the waves
-      constexpr int kTiles = 12, kPer = (kTiles + W - 1) / W;
-      const int cr = fresh(channel_read), mr = fresh(token_read);
+    for (; t0 < p.count; t0 += kL) {
+      const Decays<kL>& q = dec[t0 / kL & 3];
+      if ((t0 / kL & 3) == 0) {
+        decays(t0);
+        load_dt(t0 + 4 * kL);
+      }
+      if (outputs && t0 > 0) write_out(t0 - kL);
+      store();
+      lds_barrier();
+      if (t0 + kL < p.count) load(t0 + kL);
+      if (__builtin_expect(__builtin_amdgcn_readfirstlane(q.grows), 0)) break;
+      f32x4 y[4];
+      if (outputs) {
+        // ---- M, transposed (a lane: one t, 4 s each), in tiles of 16 t by 16 s: the
+        // ten up to the diagonal and two of zeros, shared out over the waves
+        constexpr int kTiles = 12, kPer = (kTiles + W - 1) / W;
+        const int cr = fresh(channel_read), mr = fresh(token_read);
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int id = uwave + k * W;
-        // tiles (tt, u) by id: 0 .. 3 (3, u), 4 .. 6 (2, u), 7 (1, 0), 8 (1, 1), 9 (0, 0), 10 (0, 1), 11 (2, 3)
-        const int tt = id < 4 ? 3 : id < 7 ? 2 : id < 9 ? 1 : id < 11 ? 0 : 2;
-        const int u = id < 4 ? id : id < 7 ? id - 4 : id < 9 ? id - 7 : id < 11 ? id - 9 : 3;
-        f32x4 x = {0.f, 0.f, 0.f, 0.f};
-        if (id < 10) {
-          const int t = 16 * tt + l16;
-          bf16x8 b[KS], c[KS];
+        for (int k = 0; k < kPer; ++k) {
+          const int id = uwave + k * W;
+          // tiles (tt, u) by id: 0 .. 3 (3, u), 4 .. 6 (2, u), 7 (1, 0), 8 (1, 1), 9 (0, 0), 10 (0, 1), 11 (2, 3)
+          const int tt = id < 4 ? 3 : id < 7 ? 2 : id < 9 ? 1 : id < 11 ? 0 : 2;
+          const int u = id < 4 ? id : id < 7 ? id - 4 : id < 9 ? id - 7 : id < 11 ? id - 9 : 3;
+          f32x4 x = {0.f, 0.f, 0.f, 0.f};
+          if (id < 10) {
+            const int t = 16 * tt + l16;
+            bf16x8 b[KS], c[KS];
 #pragma unroll
-          for (int v = 0; v < KS; ++v) {
-            b[v] = *(const bf16x8*)(sB + (cr ^ 32 * v) + 16 * u * NP);
-            c[v] = *(const bf16x8*)(sC + (cr ^ 32 * v) + 16 * tt * NP);
-          }
+            for (int v = 0; v < KS; ++v) {
+              b[v] = *(const bf16x8*)(sB + (cr ^ 32 * v) + 16 * u * NP);
+              c[v] = *(const bf16x8*)(sC + (cr ^ 32 * v) + 16 * tt * NP);
+            }
 #pragma unroll
-          for (int v = 0; v < KS; ++v) x = mfma32(b[v], c[v], x);
-          const float thi = q.hi[t], tlo = q.lo[t];
-          const f32x4 shi = *(const f32x4*)&q.hi[16 * u + 4 * g], slo = *(const f32x4*)&q.lo[16 * u + 4 * g],
-                      sd = *(const f32x4*)&q.d[16 * u + 4 * g];
+            for (int v = 0; v < KS; ++v) x = mfma32(b[v], c[v], x);
+            const float thi = q.hi[t], tlo = q.lo[t];
+            const f32x4 shi = *(const f32x4*)&q.hi[16 * u + 4 * g], slo = *(const f32x4*)&q.lo[16 * u + 4 * g],
+                        sd = *(const f32x4*)&q.d[16 * u + 4 * g];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] *= __builtin_amdgcn_exp2f((thi - shi[i]) + (tlo - slo[i])) * sd[i];
-          if (u == tt) {
-            const int at = fresh(l16) - 4 * g;                // the diagonal's place among the lane's 4
+            for (int i = 0; i < 4; ++i) x[i] *= __builtin_amdgcn_exp2f((thi - shi[i]) + (tlo - slo[i])) * sd[i];
+            if (u == tt) {
+              const int at = fresh(l16) - 4 * g;                // the diagonal's place among the lane's 4
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float v = i == at ? x[i] + skip : x[i];
-              x[i] = i <= at ? v : 0.f;
+              for (int i = 0; i < 4; ++i) {
+                const float v = i == at ? x[i] + skip : x[i];
+                x[i] = i <= at ? v : 0.f;
+              }
             }
           }
+          bf16x4 mh, mm, ml;
+          split3(x, mh, mm, ml, one);
+          const int at = (mr ^ 32 * (u / 2)) + 16 * tt * kL + 4 * (u & 1);
+          if (id < kTiles) {
+            *(bf16x4*)(sM[0] + at) = mh;
+            *(bf16x4*)(sM[1] + at) = mm;
+            *(bf16x4*)(sM[2] + at) = ml;
+          }
         }
-        bf16x4 mh, mm, ml;
-        split3(x, mh, mm, ml, one);
-        const int at = (mr ^ 32 * (u / 2)) + 16 * tt * kL + 4 * (u & 1);
-        if (id < kTiles) {
-          *(bf16x4*)(sM[0] + at) = mh;
-          *(bf16x4*)(sM[1] + at) = mm;
-          *(bf16x4*)(sM[2] + at) = ml;
+        // ---- y, transposed (a lane: one t, 4 columns): the state's part first
+        // (it needs nothing of M, which the other waves finish meanwhile)
+        const int hr = fresh(channel_read);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) y[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < KS; ++v) {
+          bf16x4 h0, m0, l0, h1 = {}, m1 = {}, l1 = {};
+          split3(s[2 * v], h0, m0, l0, one);
+          if constexpr (NT > 1) split3(s[2 * v + 1], h1, m1, l1, one);
+          const bf16x8 sh = cat(h0, h1), sm = cat(m0, m1), sl = cat(l0, l1);
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt) {
+            const bf16x8 c = *(const bf16x8*)(sC + (hr ^ 32 * v) + 16 * tt * NP);
+            y[tt] = mfma32(sl, c, y[tt]);
+            y[tt] = mfma32(sm, c, y[tt]);
+            y[tt] = mfma32(sh, c, y[tt]);
+          }
         }
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) y[tt] *= q.e[16 * tt + l16];
+        lds_barrier();
       }
-      // ---- y, transposed (a lane: one t, 4 columns): the state's part first
-      // (it needs nothing of M, which the other waves finish meanwhile)
-      const int hr = fresh(channel_read);
+      // ---- x of the wave's columns: operands of both products
+      auto x_operand = [&](int v) __attribute__((always_inline)) {
+        const bf16_bits* at = sX + x_turned + 32 * v * kCols;
+        return cat(read_turned(at), read_turned(at + 16 * kCols));
+      };
+      bf16x8 xo[2] = {x_operand(0), x_operand(1)};
+      if (outputs) {
+        // A value that is not finite would reach earlier tokens through M's zeros:
+        // it is taken out here, and its column made NaN from its token on.
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        u16x2 most = {0, 0};
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) y[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int v = 0; v < 2; ++v) {
+          const u32x4 bits = __builtin_bit_cast(u32x4, xo[v]) & 0x7fff7fffu;
 #pragma unroll
-      for (int v = 0; v < KS; ++v) {
-        bf16x4 h0, m0, l0, h1 = {}, m1 = {}, l1 = {};
-        split3(s[2 * v], h0, m0, l0, one);
-        if constexpr (NT > 1) split3(s[2 * v + 1], h1, m1, l1, one);
-        const bf16x8 sh = cat(h0, h1), sm = cat(m0, m1), sl = cat(l0, l1);
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-          const bf16x8 c = *(const bf16x8*)(sC + (hr ^ 32 * v) + 16 * tt * NP);
-          y[tt] = mfma32(sl, c, y[tt]);
-          y[tt] = mfma32(sm, c, y[tt]);
-          y[tt] = mfma32(sh, c, y[tt]);
+          for (int i = 0; i < 4; ++i) most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, (uint32_t)bits[i]));
         }
-      }
+        const bool bad = most[0] >= 0x7f80 || most[1] >= 0x7f80;
+        const bool any_bad = __any(bad);
+        int from = kL;
+        if (any_bad) {
+          const int fg = fresh(threadIdx.x) / 16 % 4;
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) y[tt] *= q.e[16 * tt + l16];
-      lds_barrier();
-    }
-    // ---- x of the wave's columns: operands of both products
-    auto x_operand = [&](int v) __attribute__((always_inline)) {
-      const bf16_bits* at = sX + x_turned + 32 * v * kCols;
-      return cat(read_turned(at), read_turned(at + 16 * kCols));
-    };
-    bf16x8 xo[2] = {x_operand(0), x_operand(1)};
-    if (outputs) {
-      // A value that is not finite would reach earlier tokens through M's zeros:
-      // it is taken out here, and its column made NaN from its token on.
-      typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-      u16x2 most = {0, 0};
+          for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (!((float)xo[v][i] * 0.f == 0.f)) {
+                xo[v][i] = (__bf16)0.f;
+                from = min(from, 32 * v + 16 * (i / 4) + 4 * fg + i % 4);
+              }
+          from = min(from, __builtin_amdgcn_ds_bpermute(4 * (fresh(threadIdx.x) ^ 16), from));
+          from = min(from, __builtin_amdgcn_ds_bpermute(4 * (fresh(threadIdx.x) ^ 32), from));
+        }
+        const int mr = fresh(token_read);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+          for (int v = 0; v <= tt / 2; ++v) {
+            const int at = (mr ^ 32 * v) + 16 * tt * kL;
+#pragma unroll
+            for (int k = 2; k >= 0; --k) y[tt] = mfma32(xo[v], *(const bf16x8*)(sM[k] + at), y[tt]);
+          }
+        if (any_bad) {
+          const uint32_t ft = fresh(threadIdx.x);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int first = __builtin_amdgcn_ds_bpermute(4 * (ft / 16 % 4 * 4 + i), from);
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt)
+              if (16 * tt + (int)(ft % 16) >= first) y[tt][i] = __builtin_nanf("");
+          }
+#pragma unroll
+          for (int v = 0; v < 2; ++v) xo[v] = x_operand(v);
+        }
+        // (x of the wave's columns is in registers, and no other wave reads it)
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) *(bf16x4*)(sX + ywrite + 16 * tt * kCols) = to_bf16x4(y[tt]);
+        if (t0 + kL < p.count) load_c(t0 + kL);            // (late: the registers are needed until here)
+      }
+      // ---- the state behind the chunk
+      const float total = q.total;
+      const int br = fresh(b_turned);
+#pragma unroll
+      for (int k = 0; k < NT; ++k) s[k] *= total;
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        const u32x4 bits = __builtin_bit_cast(u32x4, xo[v]) & 0x7fff7fffu;
+        bf16x4 h0, m0, l0, h1, m1, l1;
+        split3(from_bf16x4(lo_half(xo[v])) * *(const f32x4*)&q.w[32 * v + 4 * g], h0, m0, l0, one);
+        split3(from_bf16x4(hi_half(xo[v])) * *(const f32x4*)&q.w[32 * v + 16 + 4 * g], h1, m1, l1, one);
+        const bf16x8 xh = cat(h0, h1), xm = cat(m0, m1), xl = cat(l0, l1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, (uint32_t)bits[i]));
-      }
-      const bool bad = most[0] >= 0x7f80 || most[1] >= 0x7f80;
-      const bool any_bad = __any(bad);
-      int from = kL;
-      if (any_bad) {
-        const int fg = fresh(threadIdx.x) / 16 % 4;
-#pragma unroll
-        for (int v = 0; v < 2; ++v)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (!((float)xo[v][i] * 0.f == 0.f)) {
-              xo[v][i] = (__bf16)0.f;
-              from = min(from, 32 * v + 16 * (i / 4) + 4 * fg + i % 4);
-            }
-        from = min(from, __builtin_amdgcn_ds_bpermute(4 * (fresh(threadIdx.x) ^ 16), from));
-        from = min(from, __builtin_amdgcn_ds_bpermute(4 * (fresh(threadIdx.x) ^ 32), from));
-      }
-      const int mr = fresh(token_read);
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-        for (int v = 0; v <= tt / 2; ++v) {
-          const int at = (mr ^ 32 * v) + 16 * tt * kL;
-#pragma unroll
-          for (int k = 2; k >= 0; --k) y[tt] = mfma32(xo[v], *(const bf16x8*)(sM[k] + at), y[tt]);
+        for (int k = 0; k < NT; ++k) {
+          const bf16_bits* at = sB + (br ^ 32 * (k / 2)) + 4 * (k & 1) + 32 * v * NP;
+          const bf16x8 b = cat(read_turned(at), read_turned(at + 16 * NP));
+          s[k] = mfma32(b, xl, s[k]);
+          s[k] = mfma32(b, xm, s[k]);
+          s[k] = mfma32(b, xh, s[k]);
         }
-      if (any_bad) {
-        const uint32_t ft = fresh(threadIdx.x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int first = __builtin_amdgcn_ds_bpermute(4 * (ft / 16 % 4 * 4 + i), from);
-#pragma unroll
-          for (int tt = 0; tt < 4; ++tt)
-            if (16 * tt + (int)(ft % 16) >= first) y[tt][i] = __builtin_nanf("");
-        }
-#pragma unroll
-        for (int v = 0; v < 2; ++v) xo[v] = x_operand(v);
       }
-      // (x of the wave's columns is in registers, and no other wave reads it)
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) *(bf16x4*)(sX + ywrite + 16 * tt * kCols) = to_bf16x4(y[tt]);
-      if (t0 + kL < p.count) load_c(t0 + kL);            // (late: the registers are needed until here)
+      lds_barrier();                                       // the chunk is used
     }
-    // ---- the state behind the chunk
-    const float total = q.total;
-    const int br = fresh(b_turned);
-#pragma unroll
-    for (int k = 0; k < NT; ++k) s[k] *= total;
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      bf16x4 h0, m0, l0, h1, m1, l1;
-      split3(from_bf16x4(lo_half(xo[v])) * *(const f32x4*)&q.w[32 * v + 4 * g], h0, m0, l0, one);
-      split3(from_bf16x4(hi_half(xo[v])) * *(const f32x4*)&q.w[32 * v + 16 + 4 * g], h1, m1, l1, one);
-      const bf16x8 xh = cat(h0, h1), xm = cat(m0, m1), xl = cat(l0, l1);
-#pragma unroll
-      for (int k = 0; k < NT; ++k) {
-        const bf16_bits* at = sB + (br ^ 32 * (k / 2)) + 4 * (k & 1) + 32 * v * NP;
-        const bf16x8 b = cat(read_turned(at), read_turned(at + 16 * NP));
-        s[k] = mfma32(b, xl, s[k]);
-        s[k] = mfma32(b, xm, s[k]);
-        s[k] = mfma32(b, xh, s[k]);
-      }
-    }
-    lds_barrier();                                       // the chunk is used
+    return t0;
+  };
+  // (a loop of its own, which keeps its registers)
+  for (int t0 = 0; (t0 = chunks(t0)) < p.count; t0 += kL) {
+    by_tokens(dec[t0 / kL & 3], min(p.count - t0, kL));
+    if (outputs && t0 + kL < p.count) load_c(t0 + kL);
+    lds_barrier();
   }
   if (outputs && p.count > 0) write_out((p.count - 1) / kL * kL);
 
@@ -628,7 +716,7 @@ __device__ __forceinline__ f32x4 mfma4(f32x4 a, f32x4 b, f32x4 c) {
 }
 
 template <int N, bool outputs>
-__global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk32_kernel(SsmParams a) {
+__global__ __launch_bounds__(256, waves_of(N, 4, outputs)) void ssm_chunk32_kernel(SsmParams a) {
   constexpr int kThreads = 256, kCols = 64, L = kL32, NT = N / 16, NV = N / 4;
   const int pblocks = (a.P + kCols - 1) / kCols;
   const int id = numbered(shared_groups(a.H / a.G, pblocks));
@@ -756,115 +844,160 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk32_kernel(SsmP
 
   const int64_t yrow = 4 * (int64_t)a.H * a.P;
   char* gy = (char*)((float*)a.y + ((size_t)p.first * a.H + h) * a.P + col0);
-  load_dt(0);
-  if (p.count > 0) load(0);
+  auto by_tokens = [&](const Decays<L>& q, int count) __attribute__((always_inline)) {
+    f32x4 states[NT];
+    in_memory(states);
+#pragma unroll
+    for (int k = 0; k < NT; ++k) states[k] = s[k];
+    const int ft = fresh(threadIdx.x), fg = ft / 16 % 4, fl = ft % 16;
 #pragma unroll 1
-  for (int t0 = 0; t0 < p.count; t0 += L) {
-    const Decays<L>& q = dec[t0 / L & 7];
-    if ((t0 / L & 7) == 0) {
-      decays(t0);
-      load_dt(t0 + 8 * L);
-    }
-    store();
-    lds_barrier();
-    if (t0 + L < p.count) load(t0 + L);
-    if (outputs) {
-      // ---- M: tiles (tt, u) = (0, 0), (1, 0), (1, 1), a wave each
-      const int tt = uwave > 0, u = uwave == 2;
-      f32x4 m = {0.f, 0.f, 0.f, 0.f};
-      const int cr = fresh(channel_read);
-      if (uwave < 3) {
-        const int t = 16 * tt + l16;
+    for (int t = 0; t < count; ++t) {
+      // (token t of row l of a tile: its four of tokens is at t / 4 ^ l / 2)
+      auto place = [&](int tile, int l) { return (16 * tile + (l ^ (tile & 1))) * L + (t / 4 ^ l >> 1) * 4 + t % 4; };
+      const float x = sXT[place(uwave, fl)], d = uniform(q.d[t]), da = d * av, f = expf(da > kMostGrowth ? kMostGrowth : da);
+      float o = 0.f;
+#pragma unroll 1
+      for (int k = 0; k < NT; ++k) {
+        f32x4 b, v = states[k];
 #pragma unroll
-        for (int k = 0; k < NT; ++k)
-          m = mfma4(*(const f32x4*)(sB + (cr ^ 16 * k) + 16 * u * N), *(const f32x4*)(sC + (cr ^ 16 * k) + 16 * tt * N), m);
-        const float thi = q.hi[t], tlo = q.lo[t];
-        const f32x4 shi = *(const f32x4*)&q.hi[16 * u + 4 * g], slo = *(const f32x4*)&q.lo[16 * u + 4 * g],
-                    sd = *(const f32x4*)&q.d[16 * u + 4 * g];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m[i] *= __builtin_amdgcn_exp2f((thi - shi[i]) + (tlo - slo[i])) * sd[i];
-        if (u == tt) {
-          const int at = fresh(l16) - 4 * g;             // the diagonal's place among the lane's 4
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float v = i == at ? m[i] + skip : m[i];
-            m[i] = i <= at ? v : 0.f;
-          }
+        for (int i = 0; i < 4; ++i) b[i] = sBT[place(k, 4 * fg + i)];
+        if (da > kMostGrowth) v = grown(v, da);
+        v = f * v + d * b * x;
+        states[k] = v;
+        if (outputs) {
+          const f32x4 r = *(const f32x4*)(sC + t * N + ((4 * k + fg) ^ row_mask<2 * N>(t % 16)) * 4) * v;
+          o += (r[0] + r[1]) + (r[2] + r[3]);
         }
       }
-      lds_barrier();                                     // B is used
-      if (uwave < 3) *(f32x4*)(sM + 16 * tt * L + (token_read[0] ^ 16 * u)) = m;
-      lds_barrier();
+      if (outputs) {
+        o += __shfl_xor(o, 16);
+        o += __shfl_xor(o, 32);
+        if (a.skip) o += skip * x;
+        if (live && fg == 0) *(float*)(gy + t * yrow + 4 * (16 * uwave + fl)) = o;
+      }
     }
-    auto x_operand = [&](int u) __attribute__((always_inline)) {
-      return *(const f32x4*)(sXT + (fresh(token_read[uwave & 1]) ^ 16 * u) + uwave * 16 * L);
-    };
-    f32x4 xo[2] = {x_operand(0), x_operand(1)};
-    if (outputs) {
-      f32x4 y[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      const int cr = fresh(channel_read);
+    gy += L * yrow;
 #pragma unroll
-      for (int k = 0; k < NT; ++k)
+    for (int k = 0; k < NT; ++k) s[k] = fresh(states[k]);
+  };
+
+  load_dt(0);
+  if (p.count > 0) load(0);
+  auto chunks = [&](int t0) __attribute__((always_inline)) {
+#pragma unroll 1
+    for (; t0 < p.count; t0 += L) {
+      const Decays<L>& q = dec[t0 / L & 7];
+      if ((t0 / L & 7) == 0) {
+        decays(t0);
+        load_dt(t0 + 8 * L);
+      }
+      store();
+      lds_barrier();
+      if (t0 + L < p.count) load(t0 + L);
+      if (__builtin_expect(__builtin_amdgcn_readfirstlane(q.grows), 0)) break;
+      if (outputs) {
+        // ---- M: tiles (tt, u) = (0, 0), (1, 0), (1, 1), a wave each
+        const int tt = uwave > 0, u = uwave == 2;
+        f32x4 m = {0.f, 0.f, 0.f, 0.f};
+        const int cr = fresh(channel_read);
+        if (uwave < 3) {
+          const int t = 16 * tt + l16;
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt) y[tt] = mfma4(s[k], *(const f32x4*)(sC + (cr ^ 16 * k) + 16 * tt * N), y[tt]);
+          for (int k = 0; k < NT; ++k)
+            m = mfma4(*(const f32x4*)(sB + (cr ^ 16 * k) + 16 * u * N), *(const f32x4*)(sC + (cr ^ 16 * k) + 16 * tt * N), m);
+          const float thi = q.hi[t], tlo = q.lo[t];
+          const f32x4 shi = *(const f32x4*)&q.hi[16 * u + 4 * g], slo = *(const f32x4*)&q.lo[16 * u + 4 * g],
+                      sd = *(const f32x4*)&q.d[16 * u + 4 * g];
 #pragma unroll
-      for (int tt = 0; tt < 2; ++tt) y[tt] *= q.e[16 * tt + l16];
-      // (values that are not finite: as above)
-      bool bad = false;
+          for (int i = 0; i < 4; ++i) m[i] *= __builtin_amdgcn_exp2f((thi - shi[i]) + (tlo - slo[i])) * sd[i];
+          if (u == tt) {
+            const int at = fresh(l16) - 4 * g;             // the diagonal's place among the lane's 4
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+            for (int i = 0; i < 4; ++i) {
+              const float v = i == at ? m[i] + skip : m[i];
+              m[i] = i <= at ? v : 0.f;
+            }
+          }
+        }
+        lds_barrier();                                     // B is used
+        if (uwave < 3) *(f32x4*)(sM + 16 * tt * L + (token_read[0] ^ 16 * u)) = m;
+        lds_barrier();
+      }
+      auto x_operand = [&](int u) __attribute__((always_inline)) {
+        return *(const f32x4*)(sXT + (fresh(token_read[uwave & 1]) ^ 16 * u) + uwave * 16 * L);
+      };
+      f32x4 xo[2] = {x_operand(0), x_operand(1)};
+      if (outputs) {
+        f32x4 y[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        const int cr = fresh(channel_read);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) bad |= !(fabsf(xo[u][i]) < __builtin_inff());
-      const bool any_bad = __any(bad);
-      int from = L;
-      if (any_bad) {
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+          for (int tt = 0; tt < 2; ++tt) y[tt] = mfma4(s[k], *(const f32x4*)(sC + (cr ^ 16 * k) + 16 * tt * N), y[tt]);
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) y[tt] *= q.e[16 * tt + l16];
+        // (values that are not finite: as above)
+        bool bad = false;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!(fabsf(xo[u][i]) < __builtin_inff())) {
-              xo[u][i] = 0.f;
-              from = min(from, 16 * u + 4 * g + i);
-            }
-        from = min(from, __shfl_xor(from, 16));
-        from = min(from, __shfl_xor(from, 32));
-      }
+          for (int i = 0; i < 4; ++i) bad |= !(fabsf(xo[u][i]) < __builtin_inff());
+        const bool any_bad = __any(bad);
+        int from = L;
+        if (any_bad) {
 #pragma unroll
-      for (int tt = 0; tt < 2; ++tt)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int u = 0; u <= tt; ++u)
-          y[tt] = mfma4(xo[u], *(const f32x4*)(sM + 16 * tt * L + (token_read[0] ^ 16 * u)), y[tt]);
-      if (any_bad) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int first_bad = __shfl(from, 4 * g + i);
-#pragma unroll
-          for (int tt = 0; tt < 2; ++tt)
-            if (16 * tt + l16 >= first_bad) y[tt][i] = __builtin_nanf("");
+            for (int i = 0; i < 4; ++i)
+              if (!(fabsf(xo[u][i]) < __builtin_inff())) {
+                xo[u][i] = 0.f;
+                from = min(from, 16 * u + 4 * g + i);
+              }
+          from = min(from, __shfl_xor(from, 16));
+          from = min(from, __shfl_xor(from, 32));
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) xo[u] = x_operand(u);
-      }
-      if (live) {
-        const int left = p.count - t0 - l16;
-        const uint32_t yoff = l16 * (uint32_t)yrow + 4 * (16 * uwave + 4 * g);
-#pragma unroll
         for (int tt = 0; tt < 2; ++tt)
-          if (16 * tt < left) *(f32x4*)(gy + 16 * tt * yrow + yoff) = y[tt];
+#pragma unroll
+          for (int u = 0; u <= tt; ++u)
+            y[tt] = mfma4(xo[u], *(const f32x4*)(sM + 16 * tt * L + (token_read[0] ^ 16 * u)), y[tt]);
+        if (any_bad) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int first_bad = __shfl(from, 4 * g + i);
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+              if (16 * tt + l16 >= first_bad) y[tt][i] = __builtin_nanf("");
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) xo[u] = x_operand(u);
+        }
+        if (live) {
+          const int left = p.count - t0 - l16;
+          const uint32_t yoff = l16 * (uint32_t)yrow + 4 * (16 * uwave + 4 * g);
+#pragma unroll
+          for (int tt = 0; tt < 2; ++tt)
+            if (16 * tt < left) *(f32x4*)(gy + 16 * tt * yrow + yoff) = y[tt];
+        }
+        gy += L * yrow;
       }
-      gy += L * yrow;
+      const float total = q.total;
+#pragma unroll
+      for (int k = 0; k < NT; ++k) s[k] *= total;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const f32x4 xw = xo[u] * *(const f32x4*)&q.w[16 * u + 4 * g];
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+          s[k] = mfma4(*(const f32x4*)(sBT + (token_read[k & 1] ^ 16 * u) + 16 * k * L), xw, s[k]);
+      }
+      lds_barrier();                                       // the chunk is used
     }
-    const float total = q.total;
-#pragma unroll
-    for (int k = 0; k < NT; ++k) s[k] *= total;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const f32x4 xw = xo[u] * *(const f32x4*)&q.w[16 * u + 4 * g];
-#pragma unroll
-      for (int k = 0; k < NT; ++k)
-        s[k] = mfma4(*(const f32x4*)(sBT + (token_read[k & 1] ^ 16 * u) + 16 * k * L), xw, s[k]);
-    }
-    lds_barrier();                                       // the chunk is used
+    return t0;
+  };
+  for (int t0 = 0; (t0 = chunks(t0)) < p.count; t0 += L) {
+    by_tokens(dec[t0 / L & 7], min(p.count - t0, L));
+    lds_barrier();
   }
 
   if (!outputs) {
@@ -912,7 +1045,9 @@ __global__ __launch_bounds__(kThreads) void ssm_front_kernel(SsmParams a, int bl
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (u < m) {
-        s = __builtin_amdgcn_exp2f((float)(a.sums[entry_of(a, p, h, j + u)] * 1.4426950408889634)) * s + e[u];
+        double sum = a.sums[entry_of(a, p, h, j + u)];
+        if (sum > kMostGrowth) s = grown(s, (float)sum), sum = kMostGrowth;
+        s = __builtin_amdgcn_exp2f((float)(sum * 1.4426950408889634)) * s + e[u];
         v[(size_t)(u + 1) * step] = s;
       }
     v += (size_t)m * step;
@@ -941,7 +1076,7 @@ __global__ __launch_bounds__(kThreads) void ssm_step_kernel(SsmParams a, int N, 
   for (int u = 0; u < U; ++u)
     if (on) s[u] = *(const f32x4*)(S + (size_t)min(rg + u * groups, N - 1) * a.P);
   const float d = step_size(a.dt[(size_t)n * a.H + h], a.dt_bias ? a.dt_bias[h] : 0.f, a.softplus);
-  const float f = expf(d * a.a[h]);
+  const float da = d * a.a[h], f = expf(da > kMostGrowth ? kMostGrowth : da);
   if (tid < N) {
     sb[tid] = d * Elem<T>::load((const T*)a.b + n * a.b_stride + grp * N + tid);
     sc[tid] = Elem<T>::load((const T*)a.c + n * a.c_stride + grp * N + tid);
@@ -951,20 +1086,25 @@ __global__ __launch_bounds__(kThreads) void ssm_step_kernel(SsmParams a, int N, 
   const f32x4 x = {xv[0], xv[1], xv[2], xv[3]};
   lds_barrier();
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  for (int r0 = rg; on && r0 < N; r0 += U * groups) {
-    if (r0 != rg)
+  auto rows = [&](auto grows) __attribute__((always_inline)) {
+    for (int r0 = rg; on && r0 < N; r0 += U * groups) {
+      if (r0 != rg)
 #pragma unroll
-      for (int u = 0; u < U; ++u) s[u] = *(const f32x4*)(S + (size_t)min(r0 + u * groups, N - 1) * a.P);
+        for (int u = 0; u < U; ++u) s[u] = *(const f32x4*)(S + (size_t)min(r0 + u * groups, N - 1) * a.P);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * groups;
-      if (r < N) {
-        s[u] = f * s[u] + sb[r] * x;
-        o += sc[r] * s[u];
-        __builtin_nontemporal_store(s[u], (f32x4*)(S + (size_t)r * a.P));
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + u * groups;
+        if (r < N) {
+          if constexpr (decltype(grows)::value) s[u] = grown(s[u], da);
+          s[u] = f * s[u] + sb[r] * x;
+          o += sc[r] * s[u];
+          __builtin_nontemporal_store(s[u], (f32x4*)(S + (size_t)r * a.P));
+        }
       }
     }
-  }
+  };
+  if (__builtin_expect(uniform(da) > kMostGrowth, 0)) rows(std::true_type{});
+  else rows(std::false_type{});
   // sums over the groups of rows, halved until one is left
   for (int m = groups; m > 1;) {
     part[tid] = o;

@@ -576,7 +576,10 @@ kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, c
  *     y_t = S_t^T c[t][j] + skip[h] x[t][h]
  *   x   [T, H, P] dtype, x_stride;  y [T, H, P] dtype
  *   b, c  [T, G, N] dtype, b_stride, c_stride; H % G == 0
- *   dt  [T, H] fp32;  a [H] fp32 (negative for a decay; any value is taken)
+ *   dt  [T, H] fp32;  a [H] fp32 (negative for a decay; any value is taken: where the
+ *       recurrence stays finite, growth does not overflow on its way. A chunk whose
+ *       growing tokens make more than e^44 is taken token by token, up to 50 times as
+ *       slow; the products of fewer, c . b d e^44, have to stay below FLT_MAX)
  *   skip, dt_bias  [H] fp32, or NULL (0)
  *   initial_state  [num_seqs, H, N, P] fp32 (row = state channel, P contiguous,
  *                  as the states of the delta rule), or NULL (zeros)

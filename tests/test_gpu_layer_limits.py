@@ -74,3 +74,102 @@ def test_ssm_largest_finite_factors(dtype, T):
     assert torch.equal(y, dev(want, dtype))
     s0[0, 1, 5] = big * 2.0 ** -10
     assert torch.equal(end, dev(s0))
+
+
+# ---- states that grow ---------------------------------------------------------------------
+
+def reference(s, cu, s0):
+    """The oracle with the bounds of fp32 arithmetic alone."""
+    return layer.ssm(host(s["x"]), host(s["dt"]), host(s["a"]), host(s["b"]), host(s["c"]), host(s["skip"]),
+                     host(s["dt_bias"]), s["dt_softplus"], cu, host(s0))
+
+
+def growing(kind, lengths, H, N, P, dtype, seed):
+    """Inputs whose decay rates are positive (1): a sequence's step sizes are its logarithms."""
+    s, s0, cu = layer_tests.ssm_inputs(lengths, (1, 2), H, 1, N, P, dtype, soft=False, seed=seed)
+    s["a"] = torch.ones(H, device=DEV)
+    for n, L in enumerate(lengths):
+        x, dt, first = s["x"][cu[n]:cu[n + 1]], s["dt"][cu[n]:cu[n + 1]], s0[n]
+        if kind == "zero until the end":          # e^2 a token; nothing to multiply but for the last 30
+            dt.fill_(2.0)
+            first.zero_()
+            x[:max(L - 30, 0)] = 0
+        elif kind == "small states":              # e^132 over the first tokens, then as it is
+            dt.zero_()
+            dt[:33] = 4.0
+            first *= 1e-32
+            x[:30] = 0
+        else:                                     # up and down, by at most e^36 from any token to any other
+            c = np.random.default_rng(seed + n).uniform(-18, 18, (L + 1, H))
+            dt.copy_(dev(np.diff(c, axis=0)))
+    return s, s0, cu
+
+
+GROWING = [([200, 3, 64], 2, 32, 48), ([150, 131], 2, 128, 128), ([140], 1, 256, 80), ([170], 2, 16, 16),
+           ([133], 1, 64, 144), ([900, 5, 450], 1, 16, 32), ([700], 1, 64, 16)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind", ["zero until the end", "small states", "up and down"])
+@pytest.mark.parametrize("lengths,H,N,P", GROWING)
+def test_ssm_states_that_grow_far(lengths, H, N, P, kind, dtype):
+    """Growth by more than e^88 within a chunk and within a segment: where the recurrence stays
+    finite, so do outputs and states, in place and apart."""
+    s, s0, cu = growing(kind, lengths, H, N, P, dtype, N + P)
+    state = s0.clone()
+    y, _ = kda.ssm_prefill(**s, cu_seqlens=device_cu(cu), initial_state=state, final_state=state)
+    ref, bound, states, sbound = reference(s, cu, s0)
+    check(y[cu[0]:cu[-1]], ref[cu[0]:cu[-1]], bound[cu[0]:cu[-1]], "y")
+    check(state, states, sbound, "state")
+    y2, end = kda.ssm_prefill(**s, cu_seqlens=device_cu(cu), initial_state=s0)
+    assert torch.equal(y2[cu[0]:cu[-1]], y[cu[0]:cu[-1]]) and torch.equal(end, state)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("form", ["prompt", "steps"])
+def test_ssm_single_tokens_that_grow_far(form, dtype):
+    """Factors of e^100 and e^150, which are infinite in fp32, on states of 0 and small ones."""
+    H, N, P, L = 2, 32, 48, 70
+    s, s0, _ = layer_tests.ssm_inputs([L], (0, 0), H, 1, N, P, dtype, soft=False, seed=3)
+    s["a"] = torch.ones(H, device=DEV)
+    s["dt"].mul_(0.05)
+    s["dt"][20], s["dt"][L - 1, 0] = 100.0, 150.0
+    s0 *= 1e-34
+    s0[:, :, ::2] = 0
+    s0[:, 0] = 0
+    s["x"][:L - 1] = 0
+    ref, bound, states, sbound = reference(s, [0, L], s0)
+    if form == "prompt":
+        y, state = kda.ssm_prefill(**s, initial_state=s0)
+    else:
+        state = s0.clone()
+        row = lambda t: {k: v[t:t + 1].clone() if k in ("x", "b", "c", "dt") else v for k, v in s.items()}  # noqa: E731
+        y = torch.cat([kda.ssm_step(state=state, **row(t)) for t in range(L)])
+    check(y, ref, bound, "y")
+    check(state, states, sbound, "state")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_ssm_growth_keeps_what_is_not_finite_from_earlier_tokens(dtype):
+    """As without growth: x spoils its column, b and dt their head, c its token."""
+    T, H, P = 150, 4, 48
+    s, s0, _ = layer_tests.ssm_inputs([T], (0, 0), H, 4, 32, P, dtype, soft=False, seed=8)
+    s["a"] = torch.ones(H, device=DEV)
+    s["dt"].fill_(0.5)
+    s0 *= 1e-20
+    s["x"] *= 1e-20
+    y, end = kda.ssm_prefill(**s, initial_state=s0)
+    s["x"][90, 0, 5], s["x"][91, 0, 20], s["x"][30, 0, 21] = float("nan"), float("inf"), float("-inf")
+    s["b"][100, 1, 3] = float("nan")
+    s["dt"][70, 2] = float("nan")
+    s["c"][33, 3, 9] = float("nan")
+    y2, end2 = kda.ssm_prefill(**s, initial_state=s0)
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[90:, 0, 5] = bad[91:, 0, 20] = bad[30:, 0, 21] = True
+    bad[100:, 1] = bad[70:, 2] = bad[33, 3] = True
+    assert (~torch.isfinite(y2[bad])).all()
+    assert torch.equal(y2[~bad], y[~bad])
+    sbad = torch.zeros_like(end, dtype=torch.bool)
+    sbad[:, 0, :, [5, 20, 21]] = sbad[:, 1, 3] = sbad[:, 2] = True
+    assert (~torch.isfinite(end2[sbad])).all()
+    assert torch.equal(end2[~sbad], end[~sbad])
