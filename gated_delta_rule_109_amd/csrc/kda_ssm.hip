@@ -278,7 +278,7 @@ struct alignas(16) Decays {
   float total;          // e^{c_L}
   int grows;            // the chunk is taken by tokens
 };
-// A wave's 64 tokens, one a lane (at: the lane): the decays of 64 / L chunks, with
+// A wave's 64 tokens, one a lane (at: the lane; on: it has one): the decays of 64 / L chunks, with
 // the sums of the logarithms c = d a in fp64. Returns the last chunk's c_L in every
 // lane of it. One logarithm is no less than kLeast: e^kLeast and all that is
 // multiplied by it are 0 as it is, while a token that ends the state (d a = -1e12)
@@ -290,9 +290,9 @@ struct alignas(16) Decays {
 // taken one after the other (8192 tokens of 32 heads 128 x 128, every chunk so: bf16 7.6
 // ms, fp32 6.1).
 template <int L>
-__device__ __forceinline__ double make_decays(float d, float a, int at, Decays<L>* dec) {
+__device__ __forceinline__ double make_decays(bool on, float d, float a, int at, Decays<L>* dec) {
   constexpr double kLeast = -(1 << 20), kMostInChunk = 44.0;
-  double c = (double)d * a;
+  double c = on ? (double)d * a : 0.0;                   // (an infinite a times the d of no token: NaN)
   c = c < kLeast ? kLeast : c;                           // (NaN stays)
   int grows = 0;
   if (__any(c > 0.0)) {
@@ -457,8 +457,9 @@ __global__ __launch_bounds__(64 * W, waves_of(N, W, outputs)) void ssm_chunk_ker
   auto decays = [&](int t0) __attribute__((always_inline)) {
     if (uwave >= 4 || t0 + kL * uwave >= p.count) return;
     const uint32_t t = fresh(threadIdx.x);
-    const float d = t0 + (int)t < p.count ? step_size(rdt, bias, a.softplus) : 0.f;
-    const double end = make_decays<kL>(d, av, t % kWave, dec + uwave);
+    const bool on = t0 + (int)t < p.count;
+    const float d = on ? step_size(rdt, bias, a.softplus) : 0.f;
+    const double end = make_decays<kL>(on, d, av, t % kWave, dec + uwave);
     if (!outputs) sum += end;
   };
 
@@ -837,8 +838,9 @@ __global__ __launch_bounds__(256, waves_of(N, 4, outputs)) void ssm_chunk32_kern
   auto decays = [&](int t0) __attribute__((always_inline)) {
     if (t0 + 2 * L * uwave >= p.count) return;
     const uint32_t t = fresh(threadIdx.x);
-    const float d = t0 + (int)t < p.count ? step_size(rdt, bias, a.softplus) : 0.f;
-    const double end = make_decays<L>(d, av, t % kWave, dec + 2 * uwave);
+    const bool on = t0 + (int)t < p.count;
+    const float d = on ? step_size(rdt, bias, a.softplus) : 0.f;
+    const double end = make_decays<L>(on, d, av, t % kWave, dec + 2 * uwave);
     if (!outputs) sum += end;                            // (a lane: of its half of the wave)
   };
 

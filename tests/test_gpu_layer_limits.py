@@ -173,3 +173,24 @@ def test_ssm_growth_keeps_what_is_not_finite_from_earlier_tokens(dtype):
     sbad[:, 0, :, [5, 20, 21]] = sbad[:, 1, 3] = sbad[:, 2] = True
     assert (~torch.isfinite(end2[sbad])).all()
     assert torch.equal(end2[~sbad], end[~sbad])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [1, 70, 900])
+def test_ssm_rates_of_minus_infinity(dtype, T):
+    """A rate of -infinity ends the state at every token, as the lowest finite rate does: the same
+    bits, finite outputs and final states, whether or not the last chunk is whole."""
+    s, s0, _ = layer_tests.ssm_inputs([T], (0, 0), 2, 1, 32, 48, dtype, soft=False, seed=T)
+    s["dt"] += 0.01
+    s["a"] = dev([-np.finfo(np.float32).max, -1.0])
+    y, end = kda.ssm_prefill(**s, initial_state=s0)
+    ref, bound, states, sbound = reference(s, [0, T], s0)
+    check(y, ref, bound, "y")
+    check(end, states, sbound, "state")
+    s["a"][0] = -float("inf")
+    y2, end2 = kda.ssm_prefill(**s, initial_state=s0)
+    assert torch.equal(y2, y) and torch.equal(end2, end)
+    if T == 1:
+        state = s0.clone()
+        check(kda.ssm_step(state=state, **s), ref, bound, "y of a step")
+        check(state, states, sbound, "state of a step")
