@@ -194,3 +194,158 @@ def test_ssm_rates_of_minus_infinity(dtype, T):
         state = s0.clone()
         check(kda.ssm_step(state=state, **s), ref, bound, "y of a step")
         check(state, states, sbound, "state of a step")
+
+
+# ---- long walks ----------------------------------------------------------------------------
+
+def cut(rng, T, n, outside):
+    """Offsets of n sequences, cut anywhere, some of them empty; rows in front and behind."""
+    inner = np.sort(rng.integers(outside[0], T - outside[1] + 1, n - 1))
+    inner[n // 2] = inner[n // 2 - 1]
+    return np.concatenate([[outside[0]], inner, [T - outside[1]]])
+
+
+def conv_rows(x, w, b, cu, state, act):
+    """layer.conv for long calls: the rows that each output needs, a shift at a time, in fp64 on
+    the device; the same bounds. (Rows of no sequence: anything.)"""
+    T, C = x.shape
+    K = w.shape[1]
+    t = torch.arange(T, device=DEV)
+    seq = (torch.searchsorted(device_cu(cu), t.int(), right=True) - 1).clamp(0, len(cu) - 2)
+    start = torch.tensor(cu, device=DEV)[seq]
+    s = torch.zeros(T, C, dtype=torch.float64, device=DEV) + (b.double() if b is not None else 0.0)
+    size = s.abs()
+    for j in range(K):
+        at = t - (K - 1) + j
+        rows = x[at.clamp(min=0)].double()
+        early = ((at < start) & (t >= start)).nonzero()[:, 0]
+        rows[early] = state[seq[early], (at - start)[early] + K - 1].double() if state is not None else 0.0
+        s += w[:, j].double() * rows
+        size += (w[:, j].double() * rows).abs()
+    bound = (K + 1) * layer.U * size
+    if act:
+        y = s * torch.sigmoid(s)
+        return y, 1.1 * bound + y.abs() * (2 * s.abs() + 12) * layer.U
+    return s, bound
+
+
+@pytest.mark.parametrize("T,C,K,dtype,n", [
+    (140001, 64, 4, BF16, 40), (800003, 12, 3, F32, 9), (36003, 1027, 4, BF16, 30), (16501, 4096, 4, BF16, 12),
+    (43301, 777, 2, F32, 300), (9001, 7800, 4, F32, 1), (70001, 129, 3, BF16, 70)])
+def test_conv_of_many_rows(T, C, K, dtype, n):
+    """Calls large enough that a thread walks along 8 to 64 tokens: ragged ends, sequences that
+    begin inside a walk, rows of every kind, states in place."""
+    rng = np.random.default_rng(C)
+    gen = torch.Generator(device=DEV).manual_seed(C)
+    x = torch.randn(T, C, generator=gen, device=DEV).to(dtype)
+    w, b = torch.randn(C, K, generator=gen, device=DEV) / 2, torch.randn(C, generator=gen, device=DEV)
+    cu = cut(rng, T, n, (2, 3)) if n > 1 else np.array([2, T - 3])
+    s = torch.randn(n, K - 1, C, generator=gen, device=DEV).to(dtype)
+    state, y = s.clone(), torch.full((T, C), 7.0, dtype=dtype, device=DEV)
+    kda.conv_prefill(x, w, b, cu_seqlens=device_cu(cu), initial_state=state, final_state=state, y=y)
+    ref, bound = conv_rows(x, w, b, cu, s, True)
+    inside = slice(int(cu[0]), int(cu[-1]))
+    step = 2.0 ** -8 if dtype is BF16 else 2.0 ** -24
+    err, tol = (y.double() - ref).abs(), bound * (1 + step) + step * ref.abs() + 1e-37
+    assert (err[inside] <= tol[inside]).all()
+    assert (y[:cu[0]] == 7).all() and (y[cu[-1]:] == 7).all()
+    for i in range(n):
+        rows = torch.cat([s[i], x[cu[i]:cu[i + 1]]])[-(K - 1):]
+        assert torch.equal(state[i], rows)
+
+
+@pytest.mark.parametrize("T,C,dtype,post,gate,scale", [
+    (40001, 128, BF16, True, True, True), (70003, 20, F32, True, False, True), (10007, 512, BF16, False, True, False),
+    (1301, 4096, BF16, True, True, True), (1027, 4099, BF16, True, True, True), (515, 8192, BF16, True, False, False),
+    (1500, 2500, F32, True, True, True), (701, 16384, BF16, True, True, True), (600, 16383, BF16, False, True, True),
+    (590, 16384, F32, True, True, True), (300, 5001, F32, True, False, True), (530, 16381, F32, True, True, False)])
+def test_residual_norm_of_many_rows(T, C, dtype, post, gate, scale):
+    """Calls in which a workgroup takes several rows, one after the other: in place and apart;
+    rows of NaN, of infinities and of zeros change no row but their own."""
+    gen = torch.Generator(device=DEV).manual_seed(C)
+    x, r, g = (torch.randn(T, C, generator=gen, device=DEV).to(dtype) for _ in range(3))
+    w, p, sc = (torch.randn(C, generator=gen, device=DEV) for _ in range(3))
+    g, p, sc = (v if on else None for v, on in ((g, gate), (p, post), (sc, scale)))
+    call = lambda x, r, **kw: kda.residual_norm(x, r, w, p, g, 2, sc, 0.5, 1e-5, **kw)  # noqa: E731
+    out, y = call(x, r)
+    ref, rb, yref, yb = layer.residual_norm(host(x), host(r), host(w), host(p), host(g), 2, host(sc), 0.5, float(np.float32(1e-5)))
+    check(out, ref, rb, "residual")
+    check(y, yref, yb, "y")
+    same = r.clone()
+    _, y2 = call(x, same, residual_out=same)
+    assert torch.equal(same, out) and torch.equal(y2, y)
+    x, r = x.clone(), r.clone()
+    odd = [0, T // 3, T // 2, T - 2]
+    x[odd[0]], x[odd[1]], r[odd[2]] = float("nan"), float("inf"), float("nan")
+    x[odd[3]], r[odd[3]] = 0, 0
+    out2, y2 = call(x, r)
+    keep = torch.ones(T, dtype=torch.bool, device=DEV)
+    keep[odd] = False
+    assert torch.equal(out2[keep], out[keep]) and torch.equal(y2[keep], y[keep])
+    assert torch.isnan(y2[odd[:3]]).any(1).all()
+    assert (out2[odd[3]] == 0).all() and (y2[odd[3]] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gated_norm_rows_stay_apart(dtype):
+    """As the residual norm's, in one workgroup and in others."""
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    for T, H, D in ((200, 3, 20), (40, 2, 512), (9, 3, 5000)):
+        x, g = (torch.randn(T, H, D, generator=gen, device=DEV).to(dtype) for _ in range(2))
+        w = torch.ones(D, device=DEV)
+        for first in (False, True):
+            y = kda.gated_norm(x, g, w, gate_first=first)
+            x2 = x.clone()
+            x2[T // 2, 1], x2[T // 2 + 1, 0], x2[T // 2 + 2, H - 1] = float("nan"), float("inf"), 0.0
+            y2 = kda.gated_norm(x2, g, w, gate_first=first)
+            keep = torch.ones(T, H, dtype=torch.bool, device=DEV)
+            keep[T // 2, 1] = keep[T // 2 + 1, 0] = keep[T // 2 + 2, H - 1] = False
+            assert torch.equal(y2[keep], y[keep]) and torch.isnan(y2[T // 2, 1]).all()
+            assert torch.isnan(y2[T // 2 + 1, 0]).any() and (y2[T // 2 + 2, H - 1] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lengths,H", [([700], 300), ([30, 620, 0, 330], 300), ([1500], 200), ([2, 1100, 500], 200)])
+def test_ssm_of_long_walks(lengths, H, dtype):
+    """Heads that fill the GPU: sequences of many chunks whole, or in segments of more than the 256
+    tokens whose decays are made at a time."""
+    s, s0, cu = layer_tests.ssm_inputs(lengths, (1, 2), H, 2, 16, 16, dtype, seed=H, rate=0.2)
+    state = s0.clone()
+    y, _ = kda.ssm_prefill(**s, cu_seqlens=device_cu(cu), initial_state=state, final_state=state)
+    ref, bound, states, sbound = reference(s, cu, s0)
+    check(y[cu[0]:cu[-1]], ref[cu[0]:cu[-1]], bound[cu[0]:cu[-1]], "y")
+    check(state, states, sbound, "state")
+
+
+def test_steps_and_residual_norm_past_32_bits():
+    """Rows and states whose elements lie behind 2^31: as the last rows alone."""
+    C, N = 1 << 20, 2100
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    rand = lambda *shape: torch.randn(*shape, generator=gen, device=DEV)  # noqa: E731
+    w = rand(C, 4)
+    x, state = torch.zeros(N, C, dtype=BF16, device=DEV), torch.zeros(N, 3, C, dtype=BF16, device=DEV)
+    x[-2:], state[-2:] = rand(2, C).to(BF16), rand(2, 3, C).to(BF16)
+    small = state[-2:].clone()
+    y = kda.conv_step(x, w, state)
+    assert torch.equal(y[-2:], kda.conv_step(x[-2:].clone(), w, small)) and torch.equal(state[-2:], small)
+    assert not y[:-2].any() and not state[1000].any()
+    del state, y
+    C, T = 16384, (1 << 31) // 16384 + 70
+    rows = x.view(-1)[:T * C].view(T, C)
+    rows.zero_()
+    rows[-3:] = rand(3, C).to(BF16)
+    w = rand(C)
+    out, y = kda.residual_norm(rows, rows, w, post_weight=w, gate=rows, scale=w)
+    tail = rows[-3:].clone()
+    out2, y2 = kda.residual_norm(tail, tail, w, post_weight=w, gate=tail, scale=w)
+    assert torch.equal(out[-3:], out2) and torch.equal(y[-3:], y2) and not y[-70:-3].any()
+    del out, y, x, rows
+    S, H, N, P = 1050, 32, 256, 256
+    state = torch.zeros(S, H, N, P, device=DEV)
+    state[-1] = rand(H, N, P)
+    small = state[-1:].clone()
+    x, b, c = rand(S, H, P).to(BF16), rand(S, 1, N).to(BF16), rand(S, 1, N).to(BF16)
+    dt, a = torch.rand(S, H, generator=gen, device=DEV), -torch.ones(H, device=DEV)
+    y = kda.ssm_step(x, dt, a, b, c, state)
+    assert torch.equal(y[-1:], kda.ssm_step(x[-1:].clone(), dt[-1:].clone(), a, b[-1:].clone(), c[-1:].clone(), small)) \
+        and torch.equal(state[-1:], small)
