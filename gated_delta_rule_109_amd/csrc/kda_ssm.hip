@@ -35,22 +35,23 @@ constexpr int kThreads = 256;
 // and a step of the chain of its sequence's states. Compared are the lengths that fill
 // one and two rounds of workgroups, the least one that the target allows (at least
 // twice the average sequence where sequences alone fill the GPU), and those where
-// chain and segments balance. Of 38 calls of 700 to 8192 tokens the length taken is on
-// average 2 % slower than the best one, by the balance alone 5 % and up to 27 (3001
-// tokens of nine sequences, 8 heads 128 x 128 fp32: 320 workgroups 76 us, 432 of shorter
-// segments 60; of one sequence: 256 of them 59, 304 of shorter segments 70). Calls of
-// few tokens are not split: 300 tokens of two sequences whole 13 us, in segments 19.
+// chain and segments balance. The constants are fitted by hand to measured calls: over 38
+// of 700 to 8192 tokens the length taken is on average 2.9 % slower than the best one, at
+// most 14 % (2048 tokens of six sequences, 20 heads 128 x 128 fp32: 97 us, 85 by longer
+// segments). Calls of few tokens are not split: 300 tokens of two sequences whole 13 us,
+// in segments 19.
 struct Split {
   int columns;     // columns of a head one workgroup owns
-  int target;      // workgroups that the segments of a call make up
+  int target;      // workgroups that the segments of a call make up, sequences' rests aside
   int chunk;       // tokens: segments are whole chunks, at least two
   int whole;       // calls of at most so many tokens are not split
 };
 // (the chunks' workgroups have 8 waves where a head has more than 64 columns, else 4.
 // Of states of 256 rows a compute unit holds one workgroup, where more of them run in
-// turns: 8192 tokens of 16 heads 256 x 128 in one round 99 us, in two 153. Of smaller
-// states it holds two and more; 3 or 4 for 64 columns gain nothing: 32 heads of
-// 16 x 64 49 us, with 1024 workgroups 54)
+// turns: 8192 tokens of 16 heads 256 x 128 in one round 108 us; when outputs had two terms
+// of S and M it took 100, and two rounds 153. Of smaller states it holds two and more; 3
+// or 4 for 64 columns gained nothing then: 32 heads of 16 x 64 49 us, with 1024
+// workgroups 54)
 enum Kind { kF32, kNarrow, kWide };
 Split split_of(Kind k, int N) {
   const int target = N == 256 ? 256 : 512;
@@ -172,7 +173,8 @@ constexpr int kL = KDA_SSM_CHUNK;
 // Workgroups go to the 8 dies in turn. They are numbered so that kShare of those that
 // share B and C (a group's heads in a segment) are on one die and meet in its L2; not
 // more, or a few segments of many heads leave dies without work (8192 tokens of 128
-// heads 128 x 64 in one group: all of a segment on a die 419 us, eight 220).
+// heads 128 x 64 in one group: eight 233 us; with outputs of two terms of S and M 220,
+// and all of a segment on a die 419).
 constexpr int kDies = 8, kShare = 8;
 __host__ __device__ __forceinline__ int shared_groups(int heads, int blocks) {
   return (int64_t)heads * blocks < kShare ? heads * blocks : kShare;
@@ -278,9 +280,9 @@ struct alignas(16) Decays {
   float total;          // e^{c_L}
   int grows;            // the chunk is taken by tokens
 };
-// A wave's 64 tokens, one a lane (at: the lane; on: it has one): the decays of 64 / L chunks, with
-// the sums of the logarithms c = d a in fp64. Returns the last chunk's c_L in every
-// lane of it. One logarithm is no less than kLeast: e^kLeast and all that is
+// A wave's 64 tokens, one a lane (at: the lane; on: it has one): the decays of 64 / L
+// chunks, with the sums of the logarithms c = d a in fp64. Returns the last chunk's c_L
+// in every lane of it. One logarithm is no less than kLeast: e^kLeast and all that is
 // multiplied by it are 0 as it is, while a token that ends the state (d a = -1e12)
 // would take the digits of the sums behind it.
 //
@@ -703,7 +705,7 @@ __global__ __launch_bounds__(64 * W, waves_of(N, W, outputs)) void ssm_chunk_ker
 // workgroup, 16 a wave. As operand a lane holds 4 values along the sum, each for
 // one of four products: the accumulators of a tile are that operand as they are
 // (rows 16 k + 4 g + i, i the product), and 4 channels or tokens are one read.
-// Layouts as above, with blocks of 4 fp32. 8192 tokens of 32 heads 128 x 128: 346 us,
+// Layouts as above, with blocks of 4 fp32. 8192 tokens of 32 heads 128 x 128: 351 us,
 // of which the products take 139 at the rate of a large fp32 product (154 TFLOP/s) in
 // the launch with outputs, and 2/5 of that again in the one for states; nine sequences
 // of 3001 tokens, 6 heads 32 x 48: 20 us, three chunks after each other in each pass.

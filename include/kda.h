@@ -579,7 +579,7 @@ kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, c
  *   dt  [T, H] fp32;  a [H] fp32 (negative for a decay; any value is taken: where the
  *       recurrence stays finite, growth does not overflow on its way. A chunk whose
  *       growing tokens make more than e^44 is taken token by token, up to 50 times as
- *       slow; the products of fewer, c . b d e^44, have to stay below FLT_MAX)
+ *       slow)
  *   skip, dt_bias  [H] fp32, or NULL (0)
  *   initial_state  [num_seqs, H, N, P] fp32 (row = state channel, P contiguous,
  *                  as the states of the delta rule), or NULL (zeros)
@@ -590,7 +590,9 @@ kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, c
  * and x are exact there, and every fp32 factor is carried in three bf16 terms, which
  * hold its 24 bits. fp32 tensors run in chunks of half that length with products of
  * fp32. The decays between two tokens come from sums in fp64 (a d_t a[h] below -2^20
- * counts as -2^20: the state in front of it is gone either way). Values that are not
+ * counts as -2^20: the state in front of it is gone either way). c . b d and the products
+ * of c with the state in front of a chunk are formed before the decays that they meet:
+ * they have to stay below FLT_MAX, with growth below FLT_MAX e^-44. Values that are not
  * finite in x, b or dt make outputs non-finite from their token on (of a value in x: in
  * its column), as the recurrence does, and no outputs before; a c that is not finite,
  * those of its token.
