@@ -260,7 +260,8 @@ __device__ __forceinline__ bf16x4 upper_halves(f32x4 x) {
   return __builtin_bit_cast(bf16x4, uint2{__builtin_amdgcn_perm(v[1], v[0], 0x07060302u),
                                           __builtin_amdgcn_perm(v[3], v[2], 0x07060302u)});
 }
-// x = h + m + l in bf16, 8 bits each, each towards zero, the rest of the ones before: exact.
+// x = h + m + l in bf16, 8 bits each, each towards zero, the rest of the ones before: exact
+// (but for rests below 2^-126, which are taken as 0).
 // (To nearest, as many instructions, a finite x above the largest bf16 would become
 // infinite, and the rest of it NaN.)
 __device__ __forceinline__ void split3(f32x4 x, bf16x4& h, bf16x4& m, bf16x4& l, const Minus& one) {

@@ -588,8 +588,8 @@ kda_status kda_conv_step(const void* x, int64_t x_stride, const float* weight, c
  *      b and c are multiples of 16 bytes, at most KDA_SSM_MAX_STRIDE elements
  * bf16 tensors run in chunks of KDA_SSM_CHUNK tokens on the matrix cores: b, c
  * and x are exact there, and every fp32 factor is carried in three bf16 terms, which
- * hold its 24 bits. fp32 tensors run in chunks of half that length with products of
- * fp32. The decays between two tokens come from sums in fp64 (a d_t a[h] below -2^20
+ * hold its 24 bits (as far as they are at least 2^-126). fp32 tensors run in chunks of
+ * half that length with products of fp32. The decays between two tokens come from sums in fp64 (a d_t a[h] below -2^20
  * counts as -2^20: the state in front of it is gone either way). c . b d and the products
  * of c with the state in front of a chunk are formed before the decays that they meet:
  * they have to stay below FLT_MAX, with growth below FLT_MAX e^-44. Values that are not
